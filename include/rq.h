@@ -17,6 +17,11 @@
  *                       launch, the rotated activations never reaching HBM.
  *   rq_attn_decode      attention of decode queries over the rotated INT4 KV
  *                       cache that rq_kv_rotate_quant writes;
+ *   rq_rope             rotary positions on Q and K;
+ *   rq_kv_append, rq_kv_read  the paged rotated INT4 cache: rows quantised as they
+ *                       are written (with their rotary positions), read back dense;
+ *   rq_attn_tree        attention of trees of drafted tokens (or of one token per
+ *                       sequence) over the paged cache, grouped-query heads;
  *   rq_w4a8_gemm        the W4A8 variant of the linear layer (INT8 activations),
  *                       with per-channel or per-group weight scales.
  *
@@ -100,6 +105,10 @@ enum { RQ_E4M3_CODES = 16u, RQ_A_E4M3 = 16u };
 
 /* rq_fwht_quant code mode: the default INT4 codes, one int8 byte each. */
 enum { RQ_INT4_BYTES = 32u };
+
+/* rq_kv_read: leave the rows in the rotated basis.  rq_rope, rq_kv_append: pairs of
+ * neighbouring elements; rq_rope: the transposed turn. */
+enum { RQ_KV_ROTATED_OUT = 2u, RQ_ROPE_INTERLEAVED = 4u, RQ_ROPE_INVERSE = 8u };
 
 /* Smallest / largest supported Hadamard size (row length n, head_dim). */
 #define RQ_MIN_N 32
@@ -317,6 +326,104 @@ rq_status rq_fwht_quant_gemm(const void *x, rq_dtype x_dtype, int64_t M, int64_t
 rq_status rq_attn_decode(const void *q, rq_dtype q_dtype, int64_t M, int64_t heads, int64_t head_dim,
                          const uint8_t *kq, const float *ks, const uint8_t *vq, const float *vs, int64_t tokens,
                          uint64_t seed, uint32_t flags, float softmax_scale, float *out, void *stream);
+
+/*
+ * rq_rope -- rotary positions on the rows of Q and K, in one launch.
+ *
+ *   The first rot_dim elements of a head are pairs (a, b): elements (i, i + rot_dim/2),
+ *   or (2i, 2i + 1) with RQ_ROPE_INTERLEAVED.  Pair i of a token at position t becomes
+ *     (a cos - b sin, a sin + b cos) * mscale,   angle = t * w_i
+ *   (sin negated with RQ_ROPE_INVERSE: the transposed turn, which is the gradient of
+ *   the forward one).  The other head_dim - rot_dim elements are copied.  Computed in
+ *   fp32 and rounded once.
+ *
+ *   q, k     [tokens][heads][head_dim] elements of dtype, with token and head strides
+ *            in elements and unit stride inside a head; either may have 0 heads.  Rows
+ *            at 16-byte boundaries (pointers, strides, rot_dim/2) are moved 16 bytes at
+ *            a time, others element by element.
+ *   q_out, k_out  the same shapes, own strides; may be the input itself (in place).
+ *   head_dim even, <= 256; rot_dim even, in [2, head_dim]; q_heads + k_heads <= 4096.
+ *   positions [tokens] int64, any value.
+ *   turns    [rot_dim/2] uint64: w_i / (2 pi), in turns per position, as a binary
+ *            fraction (times 2^64).  position * turns modulo 2^64 is the angle, exact
+ *            for every position; scaled frequencies for long contexts are folded in.
+ *   flags    RQ_ROPE_INTERLEAVED, RQ_ROPE_INVERSE.
+ */
+rq_status rq_rope(const void *q, int64_t q_heads, int64_t q_token_stride, int64_t q_head_stride, void *q_out,
+                  int64_t q_out_token_stride, int64_t q_out_head_stride, const void *k, int64_t k_heads,
+                  int64_t k_token_stride, int64_t k_head_stride, void *k_out, int64_t k_out_token_stride,
+                  int64_t k_out_head_stride, rq_dtype dtype, int64_t tokens, int64_t head_dim, int64_t rot_dim,
+                  const int64_t *positions, const uint64_t *turns, float mscale, uint32_t flags, void *stream);
+
+/*
+ * The paged cache.  A page holds page_size tokens (a power of two, 16 to 256) of every
+ * KV head: codes kq, vq [pages][heads][page_size][head_dim/2], scales ks, vs
+ * [pages][heads][page_size] fp32.  Slot page * page_size + row names a token's place.
+ * A sequence's block table lists its pages in order.  head_dim is 32, 64, 128 or 256.
+ *
+ * rq_kv_append -- [QR] §End-to-end flow, "The KV cache": quantise rows as they are
+ *   written.  k, v [tokens][heads][head_dim] (strides in elements, 16-byte multiples)
+ *   are rotated by the head-wise R, quantised with one scale per (token, head), and
+ *   written to slots[token]; tokens whose slot is outside the cache (negative: padding)
+ *   are skipped.  No two tokens may name one slot.  With turns, the keys first take
+ *   their rotary positions as in rq_rope, without leaving fp32 (rot_dim a multiple of
+ *   16, or of 8 with RQ_ROPE_INTERLEAVED).  A row that holds a NaN or an infinity gets
+ *   scale NaN.
+ *   flags    RQ_SIGNS_FIRST, RQ_ROPE_INTERLEAVED.
+ */
+rq_status rq_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                       int64_t v_token_stride, int64_t v_head_stride, rq_dtype dtype, int64_t tokens, int64_t heads,
+                       int64_t head_dim, const int64_t *slots, const int64_t *positions, const uint64_t *turns,
+                       int64_t rot_dim, float mscale, uint64_t seed, uint32_t flags, uint8_t *kq, float *ks,
+                       uint8_t *vq, float *vs, int64_t pages, int64_t page_size, void *stream);
+
+/*
+ * rq_kv_read -- the cache back as dense rows: (code * scale) R^T, or code * scale with
+ *   RQ_KV_ROTATED_OUT.
+ *   block_table [seqs][table_width] int32 page numbers; starts [seqs] int32, the first
+ *   token wanted of each sequence (NULL: 0); offsets [seqs + 1] int32, the output row
+ *   its first token goes to (sequence b has offsets[b+1] - offsets[b] rows).
+ *   k_out, v_out [total][heads][head_dim] contiguous, of dtype; rows at or past
+ *   offsets[seqs] are not written.  A token past the table, or on a page number outside
+ *   the cache, reads as zeros.
+ *   flags    RQ_SIGNS_FIRST (as given to rq_kv_append), RQ_KV_ROTATED_OUT.
+ */
+rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, const float *vs, int64_t pages,
+                     int64_t heads, int64_t page_size, int64_t head_dim, const int32_t *block_table,
+                     int64_t table_width, const int32_t *starts, const int32_t *offsets, int64_t seqs, int64_t total,
+                     uint64_t seed, uint32_t flags, void *k_out, void *v_out, rq_dtype dtype, void *stream);
+
+/*
+ * rq_attn_tree -- attention of trees of drafted tokens over the paged cache (a tree of
+ *   one node is a plain decode step).
+ *
+ *   Sequence b has context_lens[b] tokens before its tree and n = offsets[b+1] -
+ *   offsets[b] nodes (<= max_nodes; more are ignored), whose keys and values are in the
+ *   cache at the next n places.  Node i sees every token of the context and the nodes j
+ *   with tree_mask[offsets[b] + i][j] != 0 (itself only if the mask says so); without a
+ *   mask, the nodes j <= i.
+ *     out = softmax(softmax_scale (q R) . k^) v^ R^T
+ *   in fp32, with q~ and the weights rounded to fp16 on the way into the tensor cores
+ *   (fp32 queries: split into two fp16 parts); a row that sees nothing is 0.  Tokens on
+ *   a page number outside the cache, or past the table, are not seen.  What a cache row
+ *   that a query does not see holds (NaN and infinite scales too) does not reach it.
+ *
+ *   q        [rows][q_heads][head_dim] of dtype, strides in elements (16-byte
+ *            multiples); q head h reads KV head h / (q_heads / kv_heads).
+ *   out      [rows][q_heads][head_dim] contiguous, of dtype.
+ *   tree_mask [rows][mask_stride] bytes, mask_stride >= max_nodes, or NULL.
+ *   workspace, workspace_bytes: scratch of the call, at least
+ *            rq_attn_tree_workspace(head_dim) bytes; nothing is kept in it between calls.
+ *   flags    RQ_SIGNS_FIRST (as given to rq_kv_append), RQ_ATTN_ROTATED_OUT.
+ *   RQ_ERR_UNSUPPORTED: pages * kv_heads * page_size or table_width * page_size past 2^31.
+ */
+int64_t rq_attn_tree_workspace(int64_t head_dim);
+rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_stride, rq_dtype dtype, int64_t rows,
+                       int64_t q_heads, int64_t head_dim, const uint8_t *kq, const float *ks, const uint8_t *vq,
+                       const float *vs, int64_t pages, int64_t kv_heads, int64_t page_size, const int32_t *block_table,
+                       int64_t table_width, const int32_t *context_lens, const int32_t *offsets, int64_t seqs,
+                       int64_t max_nodes, const uint8_t *tree_mask, int64_t mask_stride, uint64_t seed, uint32_t flags,
+                       float softmax_scale, void *out, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * rq_w4a8_gemm -- the W4A8 linear layer with per-channel or per-group weight scales.

@@ -8,6 +8,7 @@ library's kernels; a non-OK status raises :class:`RQError`.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -22,6 +23,9 @@ RQ_GROUP_SCALES = 8
 RQ_E4M3_CODES = 16      # rq_fwht_quant: INT4 codes as the product's E4M3 operand bytes
 RQ_INT4_BYTES = 32      # rq_fwht_quant: INT4 codes, one int8 byte each (the W4A8 product's A operand)
 RQ_A_E4M3 = 16          # rq_w4a4_gemm: a_q holds those bytes
+RQ_KV_ROTATED_OUT = 2     # rq_kv_read: rows left in the rotated basis
+RQ_ROPE_INTERLEAVED = 4   # rq_rope, rq_kv_append: pairs of neighbouring elements
+RQ_ROPE_INVERSE = 8       # rq_rope: the transposed turn
 
 _STATUS = {0: "RQ_OK", 1: "RQ_ERR_INVALID_ARG", 2: "RQ_ERR_UNSUPPORTED", 3: "RQ_ERR_MISALIGNED",
            4: "RQ_ERR_CUDA", 5: "RQ_ERR_TIMEOUT"}
@@ -63,6 +67,19 @@ def load_library() -> ctypes.CDLL:
     lib.rq_w4a8_gemm.argtypes = [P, P, P, P, i64, i64, i64, i64, P, i32, P]
     lib.rq_attn_decode.restype = i32
     lib.rq_attn_decode.argtypes = [P, i32, i64, i64, i64, P, P, P, P, i64, u64, u32, ctypes.c_float, P, P]
+    f32 = ctypes.c_float
+    lib.rq_rope.restype = i32
+    lib.rq_rope.argtypes = [P, i64, i64, i64, P, i64, i64] * 2 + [i32, i64, i64, i64, P, P, f32, u32, P]
+    lib.rq_kv_append.restype = i32
+    lib.rq_kv_append.argtypes = [P, i64, i64, P, i64, i64, i32, i64, i64, i64, P, P, P, i64, f32, u64, u32,
+                                 P, P, P, P, i64, i64, P]
+    lib.rq_kv_read.restype = i32
+    lib.rq_kv_read.argtypes = [P, P, P, P, i64, i64, i64, i64, P, i64, P, P, i64, i64, u64, u32, P, P, i32, P]
+    lib.rq_attn_tree_workspace.restype = i64
+    lib.rq_attn_tree_workspace.argtypes = [i64]
+    lib.rq_attn_tree.restype = i32
+    lib.rq_attn_tree.argtypes = [P, i64, i64, i32, i64, i64, i64, P, P, P, P, i64, i64, i64, P, i64, P, P, i64, i64,
+                                 P, i64, u64, u32, f32, P, P, i64, P]
     lib.rq_sync_status.restype = i32
     lib.rq_sync_status.argtypes = [P]
     lib.rq_selftest_wait_timeout.restype = i32
@@ -338,6 +355,280 @@ def w4a8_gemm(a_q: torch.Tensor, a_scales, w_q: torch.Tensor, w_scales, *, out_d
         st = lib.rq_w4a8_gemm(_ptr(a_q), _ptr(a_scales), _ptr(w_q), _ptr(w_scales), M, N, K, group, _ptr(out),
                               _DTYPES[out.dtype], _stream(stream))
     _check("rq_w4a8_gemm", st)
+    return out
+
+
+# ---- rotary positions, the paged cache and the attention over it ----
+
+def _call(fn, name, device, *args, stream=None):
+    """Call a C entry point on `device` and its current (or the given) stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream.cuda_stream)
+    if st != 0:
+        raise RQError(name, st)
+
+
+def _expect_heads(t, name: str, dtype=None, tokens=None):
+    """A [tokens][heads][head_dim] tensor: any token and head strides, unit stride inside a head."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] with unit stride in the last dimension")
+    if t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if tokens is not None and t.shape[0] != tokens:
+        raise ValueError(f"{name}: expected {tokens} tokens, got {t.shape[0]}")
+
+
+def rope_turns(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+               original_length: int = 8192, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Rotary frequencies for :func:`rope` and :func:`kv_append`: ``(turns, mscale)``, turns an int64 tensor of
+    rot_dim/2 frequencies in 2^-64 turns per position, mscale the factor the rotated values are multiplied by.
+
+    w_i = base^(-2i/rot_dim) radians per position, scaled for contexts `factor` times longer:
+
+    * ``"none"``: w_i;
+    * ``"linear"``: w_i / factor (positions interpolated);
+    * ``"base"``: base * factor^(rot_dim / (rot_dim - 2)), which leaves the fastest pair and interpolates the slowest;
+    * ``"parts"``: pairs that turn more than `fast` times within original_length stay, those below `slow` turns
+      are interpolated, with a ramp in the turns in between; mscale = 0.1 ln(factor) + 1 (Peng et al. 2023,
+      "YaRN: Efficient Context Window Extension of Large Language Models");
+    * ``"smooth"``: the same frequencies with mscale 1 (fast = 4, slow = 1 are usual there).
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    if factor <= 0 or base <= 0 or not fast > slow:
+        raise ValueError("factor and base must be positive, fast above slow")
+    half, mscale = rot_dim // 2, 1.0
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("scaling 'base' needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    w = [base ** (-i / half) for i in range(half)]
+    if scaling == "linear":
+        w = [x / factor for x in w]
+    elif scaling in ("parts", "smooth"):
+        def kept(x):
+            return min(1.0, max(0.0, (original_length * x / (2 * math.pi) - slow) / (fast - slow)))
+        w = [x * kept(x) + x / factor * (1.0 - kept(x)) for x in w]
+        if scaling == "parts" and factor > 1.0:
+            mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    turns = [int(round(x / (2 * math.pi) * 2.0**64)) % (1 << 64) for x in w]
+    return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device), mscale
+
+
+def rope(q, k, positions: torch.Tensor, turns: torch.Tensor, *, interleaved: bool = False, inverse: bool = False,
+         mscale: float = 1.0, out=None, stream=None):
+    """Rotary positions on q and k ([tokens][heads][head_dim], strided views welcome; either may be None): the first
+    2 * len(turns) elements of each head turn by positions[token] * turns, the others pass.  Returns (q', k'), new
+    contiguous tensors or the pair given as `out` (which may be (q, k): in place).  ``inverse=True`` is the transposed
+    turn, the gradient of the forward one.  turns and mscale come from :func:`rope_turns`."""
+    lib = load_library()
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q and k cannot both be None")
+    T, D = ref.shape[0], ref.shape[-1]
+    oq, ok = (None, None) if out is None else out
+    args = []
+    for name, x, o in (("q", q, oq), ("k", k, ok)):
+        if x is None:
+            args.append(None)
+            continue
+        _expect_heads(x, name, ref.dtype, T)
+        if x.shape[2] != D:
+            raise ValueError("q and k must have one head_dim")
+        if o is None:
+            o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _expect_heads(o, f"out ({name})", ref.dtype, T)
+            if o.shape != x.shape:
+                raise ValueError(f"out ({name}): expected shape {tuple(x.shape)}, got {tuple(o.shape)}")
+        args.append((x, o))
+    if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int64 tensor with one entry per token")
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError("turns must be a contiguous 1-D int64 tensor (rope_turns)")
+    rot = 2 * turns.shape[0]
+    if not 2 <= rot <= D:
+        raise ValueError(f"turns rotate {rot} of {D} elements")
+    flat, tensors = [], [positions, turns]
+    for pair in args:
+        if pair is None:
+            flat += [None, 0, 0, 0, None, 0, 0]
+        else:
+            x, o = pair
+            tensors += pair
+            xs, os = x.stride(), o.stride()
+            flat += [x.data_ptr(), x.shape[1], xs[0], xs[1], o.data_ptr(), os[0], os[1]]
+    dev = _dev(*tensors)
+    flags = (RQ_ROPE_INTERLEAVED if interleaved else 0) | (RQ_ROPE_INVERSE if inverse else 0)
+    _call(lib.rq_rope, "rq_rope", dev, *flat, _DTYPES[ref.dtype], T, D, rot, positions.data_ptr(), turns.data_ptr(),
+          mscale, flags, stream=stream)
+    return tuple(None if pair is None else pair[1] for pair in args)
+
+
+def kv_cache(pages: int, heads: int, head_dim: int, page_size: int = 64, device="cuda") -> dict:
+    """An empty paged cache: dict(kq, ks, vq, vs) with codes [pages][heads][page_size][head_dim/2] uint8 and scales
+    [pages][heads][page_size] fp32."""
+    cache = {}
+    for n in "kv":
+        cache[n + "q"] = torch.zeros(pages, heads, page_size, head_dim // 2, dtype=torch.uint8, device=device)
+        cache[n + "s"] = torch.zeros(pages, heads, page_size, dtype=torch.float32, device=device)
+    return cache
+
+
+def _cache_parts(cache, head_dim=None):
+    kq, ks, vq, vs = cache["kq"], cache["ks"], cache["vq"], cache["vs"]
+    shape = kq.shape
+    if len(shape) != 4 or (head_dim is not None and shape[3] * 2 != head_dim):
+        raise ValueError(f"cache['kq']: expected [pages][heads][page_size][head_dim/2], got {tuple(shape)}")
+    if kq.dtype != torch.uint8 or vq.dtype != torch.uint8 or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise ValueError("cache: codes are uint8 and scales float32")
+    if vq.shape != shape or ks.shape != shape[:3] or vs.shape != shape[:3]:
+        raise ValueError("cache: kq and vq, ks and vs must agree in shape")
+    if not (kq.is_contiguous() and ks.is_contiguous() and vq.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("cache tensors must be contiguous")
+    return kq, ks, vq, vs
+
+
+def _expect_int32(t, name, shape):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+
+
+def kv_append(k, v, cache: dict, slots: torch.Tensor, seed: int, flags: int = RQ_SIGNS_FIRST, *, positions=None,
+              turns=None, interleaved: bool = False, mscale: float = 1.0, stream=None) -> dict:
+    """Quantise k and v ([tokens][heads][head_dim], strided views welcome) into the paged cache: row t goes to slot
+    slots[t] = page * page_size + row (int64; outside the cache: skipped).  With positions and turns the keys take
+    their rotary positions on the way (see :func:`rope`).  Returns the cache."""
+    lib = load_library()
+    _expect_heads(k, "k")
+    T, H, D = k.shape
+    _expect_heads(v, "v", k.dtype, T)
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    kq, ks, vq, vs = _cache_parts(cache, D)
+    if kq.shape[1] != H:
+        raise ValueError(f"cache holds {kq.shape[1]} heads, k has {H}")
+    if slots.dtype != torch.int64 or slots.shape != (T,) or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 tensor with one entry per token")
+    if (positions is None) != (turns is None):
+        raise ValueError("positions and turns go together")
+    rot = 0
+    if turns is not None:
+        if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int64 tensor with one entry per token")
+        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+            raise ValueError("turns must be a contiguous 1-D int64 tensor (rope_turns)")
+        rot = 2 * turns.shape[0]
+        if not 2 <= rot <= D:
+            raise ValueError(f"turns rotate {rot} of {D} elements")
+    dev = _dev(k, v, kq, ks, vq, vs, slots, positions, turns)
+    kst, vst = k.stride(), v.stride()
+    _call(lib.rq_kv_append, "rq_kv_append", dev, k.data_ptr(), kst[0], kst[1], v.data_ptr(), vst[0], vst[1],
+          _DTYPES[k.dtype], T, H, D, slots.data_ptr(), None if turns is None else positions.data_ptr(),
+          None if turns is None else turns.data_ptr(), rot, mscale, seed,
+          flags | (RQ_ROPE_INTERLEAVED if interleaved else 0), kq.data_ptr(), ks.data_ptr(), vq.data_ptr(),
+          vs.data_ptr(), kq.shape[0], kq.shape[2], stream=stream)
+    return cache
+
+
+def kv_read(cache: dict, block_table: torch.Tensor, starts, offsets: torch.Tensor, total: int, seed: int,
+            flags: int = RQ_SIGNS_FIRST, *, dtype=torch.bfloat16, out=None, stream=None):
+    """Sequences of the paged cache as dense rows (k, v), [total][heads][head_dim] of `dtype` (or the pair `out`), in
+    the original basis, or the rotated one with RQ_KV_ROTATED_OUT in flags.  block_table [seqs][width] int32; starts
+    [seqs] int32 (first token wanted; None: 0); offsets [seqs + 1] int32: sequence b fills rows offsets[b] to
+    offsets[b + 1] - 1; rows at or past offsets[seqs] are left as they are."""
+    lib = load_library()
+    kq, ks, vq, vs = _cache_parts(cache)
+    pages, H, page, half = kq.shape
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [seqs][width]")
+    B, W = block_table.shape
+    _expect_int32(block_table, "block_table", (B, W))
+    _expect_int32(offsets, "offsets", (B + 1,))
+    if starts is not None:
+        _expect_int32(starts, "starts", (B,))
+    if dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError("dtype must be float32, bfloat16 or float16")
+    if out is None:
+        out = (torch.empty(total, H, 2 * half, dtype=dtype, device=kq.device),
+               torch.empty(total, H, 2 * half, dtype=dtype, device=kq.device))
+    ko, vo = out
+    _expect(ko, "out (k)", (total, H, 2 * half), dtype)
+    _expect(vo, "out (v)", (total, H, 2 * half), dtype)
+    dev = _dev(kq, ks, vq, vs, block_table, starts, offsets, ko, vo)
+    _call(lib.rq_kv_read, "rq_kv_read", dev, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages, H, page,
+          2 * half, block_table.data_ptr(), W, None if starts is None else starts.data_ptr(), offsets.data_ptr(), B,
+          total, seed, flags, ko.data_ptr(), vo.data_ptr(), _DTYPES[dtype], stream=stream)
+    return ko, vo
+
+
+def attn_tree_workspace(head_dim: int) -> int:
+    """Bytes of scratch that :func:`attn_tree` needs on the current device."""
+    return int(load_library().rq_attn_tree_workspace(head_dim))
+
+
+def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_lens: torch.Tensor,
+              offsets: torch.Tensor, seed: int, flags: int = RQ_SIGNS_FIRST, *, tree_mask=None, max_nodes=None,
+              softmax_scale=None, out=None, workspace=None, stream=None):
+    """Attention of trees of drafted tokens over the paged cache.  Rows offsets[b] .. offsets[b + 1] - 1 of q
+    ([rows][q_heads][head_dim], strided views welcome) are the nodes of sequence b, whose keys and values lie in the
+    cache at places context_lens[b], context_lens[b] + 1, ...  A node sees the context and the nodes that its row of
+    tree_mask (bool [rows][width], width >= the largest tree) names; without a mask, itself and those before it.
+    max_nodes bounds the nodes of a sequence (default: the mask's width, or the number of rows).  One node per sequence
+    is a plain decode step.  Returns [rows][q_heads][head_dim] of q's dtype; rows that see nothing are 0."""
+    lib = load_library()
+    _expect_heads(q, "q")
+    N, Hq, D = q.shape
+    kq, ks, vq, vs = _cache_parts(cache, D)
+    pages, H, page, _ = kq.shape
+    if Hq % H:
+        raise ValueError(f"{Hq} query heads do not divide over {H} KV heads")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [seqs][width]")
+    B, W = block_table.shape
+    _expect_int32(block_table, "block_table", (B, W))
+    _expect_int32(context_lens, "context_lens", (B,))
+    _expect_int32(offsets, "offsets", (B + 1,))
+    mask_ptr, mask_stride = None, 0
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.bool or tree_mask.dim() != 2 or tree_mask.shape[0] != N or tree_mask.stride(1) != 1:
+            raise ValueError("tree_mask must be bool [rows][width] with unit stride in the last dimension")
+        mask_ptr, mask_stride = tree_mask.data_ptr(), tree_mask.stride(0)
+        if max_nodes is None:
+            max_nodes = tree_mask.shape[1]
+        elif max_nodes > tree_mask.shape[1]:
+            raise ValueError("tree_mask is narrower than max_nodes")
+        if N <= 1:
+            mask_stride = tree_mask.shape[1]      # one row: its stride says nothing
+    elif max_nodes is None:
+        max_nodes = N
+    if out is None:
+        out = torch.empty(N, Hq, D, dtype=q.dtype, device=q.device)
+    else:
+        _expect(out, "out", (N, Hq, D), q.dtype)
+    dev = _dev(q, kq, ks, vq, vs, block_table, context_lens, offsets, tree_mask, out, workspace)
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = lib.rq_attn_tree_workspace(D)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    qs = q.stride()
+    _call(lib.rq_attn_tree, "rq_attn_tree", dev, q.data_ptr(), qs[0], qs[1], _DTYPES[q.dtype], N, Hq, D, kq.data_ptr(),
+          ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages, H, page, block_table.data_ptr(), W,
+          context_lens.data_ptr(), offsets.data_ptr(), B, max_nodes, mask_ptr, mask_stride, seed, flags, softmax_scale,
+          out.data_ptr(), workspace.data_ptr(), workspace.numel(), stream=stream)
     return out
 
 

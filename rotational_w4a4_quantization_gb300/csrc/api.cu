@@ -63,6 +63,20 @@ cudaError_t launch_w4a4_gemm(const GemmArgs &g, cudaStream_t stream) {
 
 }  // namespace rq
 
+namespace {
+// What the paged-cache entry points ask of a cache.
+rq_status check_cache(const rq::PagedCache &c, int64_t head_dim) {
+    if (c.pages < 0 || c.heads <= 0 || head_dim <= 0 || c.page_size <= 0) return RQ_ERR_INVALID_ARG;
+    if (!rq::attn_decode_supported(head_dim)) return RQ_ERR_UNSUPPORTED;
+    if (!rq::pow2(c.page_size) || c.page_size < 16 || c.page_size > 256 || c.heads > 4096 || c.pages > 0x7fffffff)
+        return RQ_ERR_UNSUPPORTED;
+    if (!c.kq || !c.ks || !c.vq || !c.vs) return RQ_ERR_INVALID_ARG;
+    if (!rq::aligned16(c.kq) || !rq::aligned16(c.ks) || !rq::aligned16(c.vq) || !rq::aligned16(c.vs))
+        return RQ_ERR_MISALIGNED;
+    return RQ_OK;
+}
+}  // namespace
+
 extern "C" {
 
 rq_status rq_fwht_quant(const void *x, rq_dtype x_dtype, int64_t rows, int64_t n, int64_t ld_x,
@@ -190,6 +204,118 @@ rq_status rq_attn_decode(const void *q, rq_dtype q_dtype, int64_t M, int64_t hea
     if (heads > 65535 / 8 || M > 65535) return RQ_ERR_UNSUPPORTED;   // grid limits: 8 CTAs per head, M rows
     cudaError_t e = rq::launch_attn_decode(q, (int)q_dtype, M, heads, head_dim, kq, ks, vq, vs, tokens, seed, flags,
                                            softmax_scale, out, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+rq_status rq_rope(const void *q, int64_t q_heads, int64_t q_token_stride, int64_t q_head_stride, void *q_out,
+                  int64_t q_out_token_stride, int64_t q_out_head_stride, const void *k, int64_t k_heads,
+                  int64_t k_token_stride, int64_t k_head_stride, void *k_out, int64_t k_out_token_stride,
+                  int64_t k_out_head_stride, rq_dtype dtype, int64_t tokens, int64_t head_dim, int64_t rot_dim,
+                  const int64_t *positions, const uint64_t *turns, float mscale, uint32_t flags, void *stream) {
+    if (tokens < 0 || q_heads < 0 || k_heads < 0 || head_dim <= 0 || rot_dim <= 0) return RQ_ERR_INVALID_ARG;
+    if (flags & ~uint32_t(RQ_ROPE_INTERLEAVED | RQ_ROPE_INVERSE)) return RQ_ERR_INVALID_ARG;
+    if (!rq::is_rot_input(dtype)) return RQ_ERR_UNSUPPORTED;
+    if (rot_dim > head_dim || rot_dim % 2 != 0) return RQ_ERR_INVALID_ARG;
+    if (head_dim > 256 || head_dim % 2 != 0 || q_heads + k_heads > 4096) return RQ_ERR_UNSUPPORTED;
+    if (tokens == 0 || q_heads + k_heads == 0) return RQ_OK;
+    if ((q_heads && (!q || !q_out)) || (k_heads && (!k || !k_out)) || !positions || !turns) return RQ_ERR_INVALID_ARG;
+    const uintptr_t es = rq::elem_size(dtype);
+    const void *ptrs[4] = {q, q_out, k, k_out};
+    for (const void *p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) % es) return RQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(turns)) & 7u) return RQ_ERR_MISALIGNED;
+    const rq::RopeView qv{q, q_out, q_heads, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride};
+    const rq::RopeView kv{k, k_out, k_heads, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride};
+    cudaError_t e = rq::launch_rope(qv, kv, (int)dtype, tokens, head_dim, rot_dim, positions, turns, mscale,
+                                    (flags & RQ_ROPE_INTERLEAVED) != 0, (flags & RQ_ROPE_INVERSE) != 0,
+                                    static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+rq_status rq_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                       int64_t v_token_stride, int64_t v_head_stride, rq_dtype dtype, int64_t tokens, int64_t heads,
+                       int64_t head_dim, const int64_t *slots, const int64_t *positions, const uint64_t *turns,
+                       int64_t rot_dim, float mscale, uint64_t seed, uint32_t flags, uint8_t *kq, float *ks,
+                       uint8_t *vq, float *vs, int64_t pages, int64_t page_size, void *stream) {
+    if (tokens < 0) return RQ_ERR_INVALID_ARG;
+    if (flags & ~uint32_t(RQ_SIGNS_FIRST | RQ_ROPE_INTERLEAVED)) return RQ_ERR_INVALID_ARG;
+    if (!rq::is_rot_input(dtype)) return RQ_ERR_UNSUPPORTED;
+    const rq::PagedCache c{kq, ks, vq, vs, pages, heads, page_size};
+    if (rq_status st = check_cache(c, head_dim)) return st;
+    if (turns) {
+        if (rot_dim <= 0 || rot_dim > head_dim) return RQ_ERR_INVALID_ARG;
+        if (rot_dim % ((flags & RQ_ROPE_INTERLEAVED) ? 8 : 16) != 0) return RQ_ERR_UNSUPPORTED;
+    }
+    if (tokens == 0) return RQ_OK;
+    if (!k || !v || !slots || (turns && !positions)) return RQ_ERR_INVALID_ARG;
+    const int64_t es = rq::elem_size(dtype);
+    if (!rq::aligned16(k) || !rq::aligned16(v) || k_token_stride * es % 16 || k_head_stride * es % 16 ||
+        v_token_stride * es % 16 || v_head_stride * es % 16)
+        return RQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(turns)) & 7u)
+        return RQ_ERR_MISALIGNED;
+    cudaError_t e = rq::launch_kv_append({k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}, (int)dtype,
+                                         tokens, head_dim, c, slots, positions, turns, turns ? rot_dim : 0, mscale,
+                                         (flags & RQ_ROPE_INTERLEAVED) != 0, seed, flags,
+                                         static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, const float *vs, int64_t pages,
+                     int64_t heads, int64_t page_size, int64_t head_dim, const int32_t *block_table,
+                     int64_t table_width, const int32_t *starts, const int32_t *offsets, int64_t seqs, int64_t total,
+                     uint64_t seed, uint32_t flags, void *k_out, void *v_out, rq_dtype dtype, void *stream) {
+    if (total < 0 || seqs < 0 || table_width < 0) return RQ_ERR_INVALID_ARG;
+    if (flags & ~uint32_t(RQ_SIGNS_FIRST | RQ_KV_ROTATED_OUT)) return RQ_ERR_INVALID_ARG;
+    if (!rq::is_rot_input(dtype)) return RQ_ERR_UNSUPPORTED;
+    const rq::PagedCache c{const_cast<uint8_t *>(kq), const_cast<float *>(ks), const_cast<uint8_t *>(vq),
+                           const_cast<float *>(vs), pages, heads, page_size};
+    if (rq_status st = check_cache(c, head_dim)) return st;
+    if (seqs > 0x7fffffff) return RQ_ERR_UNSUPPORTED;
+    if (total == 0 || seqs == 0) return RQ_OK;
+    if (!block_table || !offsets || !k_out || !v_out) return RQ_ERR_INVALID_ARG;
+    if (!rq::aligned16(k_out) || !rq::aligned16(v_out)) return RQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(offsets)) & 3u)
+        return RQ_ERR_MISALIGNED;
+    cudaError_t e = rq::launch_kv_read(c, head_dim, block_table, table_width, starts, offsets, seqs, total, seed, flags,
+                                       k_out, v_out, (int)dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+int64_t rq_attn_tree_workspace(int64_t head_dim) {
+    return rq::attn_decode_supported(head_dim) ? rq::attn_tree_workspace(head_dim) : 0;
+}
+
+rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_stride, rq_dtype dtype, int64_t rows,
+                       int64_t q_heads, int64_t head_dim, const uint8_t *kq, const float *ks, const uint8_t *vq,
+                       const float *vs, int64_t pages, int64_t kv_heads, int64_t page_size, const int32_t *block_table,
+                       int64_t table_width, const int32_t *context_lens, const int32_t *offsets, int64_t seqs,
+                       int64_t max_nodes, const uint8_t *tree_mask, int64_t mask_stride, uint64_t seed, uint32_t flags,
+                       float softmax_scale, void *out, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (rows < 0 || q_heads <= 0 || seqs < 0 || max_nodes < 0 || table_width < 0) return RQ_ERR_INVALID_ARG;
+    if (flags & ~uint32_t(RQ_SIGNS_FIRST | RQ_ATTN_ROTATED_OUT)) return RQ_ERR_INVALID_ARG;
+    if (!rq::is_rot_input(dtype)) return RQ_ERR_UNSUPPORTED;
+    const rq::PagedCache c{const_cast<uint8_t *>(kq), const_cast<float *>(ks), const_cast<uint8_t *>(vq),
+                           const_cast<float *>(vs), pages, kv_heads, page_size};
+    if (rq_status st = check_cache(c, head_dim)) return st;
+    if (q_heads % kv_heads != 0 || (tree_mask && mask_stride < max_nodes)) return RQ_ERR_INVALID_ARG;
+    // the row index of a page is a TMA coordinate, a row of the tree an int
+    if (pages * kv_heads * page_size > 0x7fffffffll || seqs > 0x7fffffffll || max_nodes * q_heads > 0x3fffffffll ||
+        table_width * page_size > 0x7fffff00ll)
+        return RQ_ERR_UNSUPPORTED;
+    if (rows == 0 || seqs == 0 || max_nodes == 0) return RQ_OK;
+    if (table_width < 1 || !q || !block_table || !context_lens || !offsets || !out) return RQ_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < rq::attn_tree_workspace(head_dim)) return RQ_ERR_INVALID_ARG;
+    const int64_t es = rq::elem_size(dtype);
+    if (!rq::aligned16(q) || !rq::aligned16(out) || !rq::aligned16(workspace) || q_token_stride * es % 16 ||
+        q_head_stride * es % 16)
+        return RQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens) | reinterpret_cast<uintptr_t>(offsets)) & 3u)
+        return RQ_ERR_MISALIGNED;
+    const rq::TreeCall call{q, (int)dtype, rows, q_heads, head_dim, q_token_stride, q_head_stride, c, block_table,
+                            table_width, context_lens, offsets, seqs, max_nodes, tree_mask, mask_stride, seed, flags,
+                            softmax_scale, out, workspace};
+    cudaError_t e = rq::launch_attn_tree(call, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }
 

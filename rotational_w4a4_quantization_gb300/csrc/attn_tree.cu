@@ -1,0 +1,561 @@
+// attn_tree.cu -- attention of trees of drafted tokens (or of single tokens) over
+// the paged rotated INT4 cache (sm_103a): blocks of 16 query rows on mma.sync.
+//
+//   q~ = q R;  e_t = softmax_scale (q~ . k^_t) over the context and the visible
+//   nodes;  p = softmax(e);  out = (sum_t p_t v^_t) R^T
+// with k^_t = ks_t * codes, v^_t = vs_t * codes.  The G query heads of a KV head and
+// the nodes of a sequence together are the rows of one product, so the cache is read
+// once per 16 rows.
+//
+//  * A block of 4 warps streams tiles of 64 tokens through a TMA ring; each warp
+//    takes 16 of them.  A tile is codes of K and V (rows of D/2 bytes, swizzled by
+//    the TMA so that the reads below are free of bank conflicts) and their scales.
+//  * S = Q K^T: a lane reads the codes of a token straight into the B operand: the
+//    nibbles of a word, taken 4 bits apart, are pairs of fp16 (0x6400 | code + 8 is
+//    1024 + code + 8; one subtraction leaves the code, exactly).  The order of the
+//    dims is the same permutation on both sides and drops out.
+//  * softmax on the fragments, base 2, with a lazy reference: it moves only when a
+//    score passes it by 8, so the accumulators are rarely rescaled.
+//  * O += (P vs) V: ldmatrix.trans pairs the codes of two tokens in a register, which
+//    is the B operand after the same nibble step.  P vs is rounded to fp16 (11 bits,
+//    below the rounding of 16-bit outputs), vs relative to a power of two that moves
+//    like the softmax's reference.
+//  * fp32 queries: q~ and P vs are split into two fp16 halves (22 bits) and the
+//    products run twice; codes are exact in either.
+#include "rq.h"
+#include "rq_internal.h"
+#include "tree_device.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int kRows = 16, kTT = 64, kStages = 4, kCWarps = 4;
+constexpr int kMThreads = 32 * (kCWarps + 1);
+
+template <int IN, int D>
+struct MSmem {
+    static constexpr int RB = D / 2;
+    static constexpr int HALVES = IN == IN_F32 ? 2 : 1;
+    static constexpr int QS = D + 8;                 // row stride of q~ in halves
+    alignas(1024) uint8_t kq[kStages][kTT * RB];
+    alignas(1024) uint8_t vq[kStages][kTT * RB];
+    alignas(16) float ks[kStages][kTT];
+    alignas(16) float vs[kStages][kTT];
+    alignas(16) __half q[HALVES][kRows * QS];
+    float acc[2][kRows][D + 4];                      // the warps' sums, joined two by two
+    float ref[kCWarps][kRows], sum[kCWarps][kRows], rscale[kRows];
+    int vexp[kCWarps];
+    int64_t prefix[kScan + 1];
+    alignas(8) uint64_t full[kStages], empty[kStages];
+    uint32_t valid[kStages];
+    volatile int abort_flag;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// nibbles j and j + 4 of x (codes with the sign bit flipped) as two fp16 codes
+__device__ __forceinline__ uint32_t nibble_pair(uint32_t x, int j) {
+    const uint32_t t = ((x >> (4 * j)) & 0x000f000fu) | 0x64006400u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&t), __half2half2(__ushort_as_half(0x6408)));   // 1032
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// byte address of 16-byte chunk `ch` of row `row` in a tile written by TMA
+template <int RB>
+__device__ __forceinline__ uint32_t tile_chunk(int row, int ch) {
+    if constexpr (RB == 128) ch ^= row & 7;
+    else if constexpr (RB == 64) ch ^= (row >> 1) & 3;
+    else if constexpr (RB == 32) ch ^= (row >> 2) & 1;
+    return (uint32_t)(row * RB + ch * 16);
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
+
+template <int IN, int D>
+__global__ void __launch_bounds__(kMThreads, IN == IN_F32 || D == 256 ? 1 : 2)
+attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                     const __grid_constant__ TreeParams p) {
+    using S = MSmem<IN, D>;
+    constexpr int RB = D / 2, WPT = D / 32, E = D / 32, HV = S::HALVES;
+    constexpr int NQ = D / 32;                        // 16-byte chunks of a code row
+    constexpr bool kQRegs = D <= 128;                 // q~ fragments kept in registers
+    extern __shared__ uint8_t raw[];
+    S &s = *reinterpret_cast<S *>(raw + ((1024u - (t_smem(raw) & 1023u)) & 1023u));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            t_mbar_init(&s.full[i], 1);
+            t_mbar_init(&s.empty[i], kCWarps);
+        }
+        s.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tree_scan<kRows, kTT>(p, s.prefix);               // ends with a block barrier
+    const int64_t total = s.prefix[kScan];
+    const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
+    int st = 0;
+    uint32_t ph = 0;
+
+    if (warp == kCWarps) {
+        // ---------------- producer: one lane per page piece of a tile ----------------
+        const int bt = min(kTT, 1 << p.log_page), pieces = kTT / bt;
+        for (int64_t at = begin; at < end;) {
+            const TreeWork w = tree_work<kRows, kTT>(p, s.prefix, at, end);
+            at += w.t1 - w.t0;
+            auto page_of = [&](int tile) -> int64_t {
+                const int t = tile * kTT + lane * bt;
+                if (lane >= pieces || t >= w.s.len) return -1;
+                const int64_t pg = p.table[w.b * p.width + (t >> p.log_page)];
+                return pg >= 0 && pg < p.pages ? pg : -1;
+            };
+            int64_t pg = page_of(w.t0);
+            for (int tile = w.t0; tile < w.t1; ++tile) {
+                const int64_t next = tile + 1 < w.t1 ? page_of(tile + 1) : -1;
+                const bool go = t_mbar_wait(&s.empty[st], ph ^ 1, &s.abort_flag, p.err);
+                const uint32_t valid = __ballot_sync(0xffffffffu, pg >= 0 && go);
+                if (lane == 0) {
+                    s.valid[st] = valid;
+                    t_mbar_expect(&s.full[st], __popc(valid) * bt * (2 * RB + 8));
+                }
+                __syncwarp();
+                if ((valid >> lane) & 1) {
+                    const int t = tile * kTT + lane * bt;
+                    const int64_t row = ((pg * p.kv_heads + w.h) << p.log_page) + (t & ((1 << p.log_page) - 1));
+                    t_tma_2d(s.kq[st] + lane * bt * RB, &tmk, &s.full[st], (int)row);
+                    t_bulk(&s.ks[st][lane * bt], p.ks + row, bt * 4, &s.full[st]);
+                    t_tma_2d(s.vq[st] + lane * bt * RB, &tmv, &s.full[st], (int)row);
+                    t_bulk(&s.vs[st][lane * bt], p.vs + row, bt * 4, &s.full[st]);
+                }
+                pg = next;
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        // no copy outlives the block, also when it gave up
+        if (s.abort_flag) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < 20000000ll) __nanosleep(1000);
+        }
+        return;
+    }
+
+    // ---------------- consumers ----------------
+    const int g = lane >> 2, c = lane & 3;
+    auto cta_sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    float sg[E];
+    lane_signs<E>(sg, lane, p.seed);
+    const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;
+
+    for (int64_t at = begin; at < end;) {
+        const TreeWork w = tree_work<kRows, kTT>(p, s.prefix, at, end);
+        at += w.t1 - w.t0;
+        const int rows = min(kRows, w.s.n * p.group - w.mt * kRows);
+
+        // ---- q~ of the block's rows: rotated in fp32, scaled by a power of two to below
+        // 1 (its inverse goes into the row's score factor), rounded to fp16 once ----
+#pragma unroll 1
+        for (int i = 0; i < kRows / kCWarps; ++i) {
+            const int r = warp * (kRows / kCWarps) + i, gr = w.mt * kRows + r;
+            float v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = 0.f;
+            if (r < rows) {
+                const char *src = static_cast<const char *>(p.q) +
+                                  ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head) *
+                                      (IN == IN_F32 ? 4 : 2);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = load_elem<IN>(src, lane * E + e);
+                warp_rotate<E>(v, sg, lane, signs_first, inv_sqrt_dim<D>());
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^ex > top, within what a float's exponent holds
+            int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 126;
+            ex = max(-100, min(ex, 120));
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+            if (lane == 0) s.rscale[r] = up * p.score_scale;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int d = lane * E + e;
+                const int at_q = r * S::QS + (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1);   // 0 4 1 5 2 6 3 7
+                const float x = v[e] * down;
+                const __half hi = __float2half_rn(x);
+                s.q[0][at_q] = hi;
+                if constexpr (HV == 2) s.q[1][at_q] = __float2half_rn(x - __half2float(hi));
+            }
+        }
+        cta_sync();
+
+        // fragments of q~: word wd of lane column c covers dims base .. base + 7
+        auto q_frag = [&](int half, int wd, uint32_t (&a)[2][4]) {
+            const int base = (D == 256 ? (wd < 4 ? c * 32 : (c + 4) * 32) + 8 * (wd & 3) : c * (D / 4) + 8 * wd);
+            const uint4 x = *reinterpret_cast<const uint4 *>(&s.q[half][g * S::QS + base]);
+            const uint4 y = *reinterpret_cast<const uint4 *>(&s.q[half][(g + 8) * S::QS + base]);
+            a[0][0] = x.x; a[0][2] = x.y; a[1][0] = x.z; a[1][2] = x.w;
+            a[0][1] = y.x; a[0][3] = y.y; a[1][1] = y.z; a[1][3] = y.w;
+        };
+        uint32_t qa[kQRegs ? HV : 1][kQRegs ? WPT : 1][2][4];
+        if constexpr (kQRegs) {
+#pragma unroll
+            for (int hv = 0; hv < HV; ++hv)
+#pragma unroll
+                for (int wd = 0; wd < WPT; ++wd) q_frag(hv, wd, qa[hv][wd]);
+        }
+        const float rs0 = s.rscale[g], rs1 = s.rscale[g + 8];
+
+        float acc[NQ * 4][4];
+#pragma unroll
+        for (int i = 0; i < NQ * 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f, l0 = 0.f, l1 = 0.f;   // z: finite reference
+        int ve = -100;
+        float vf = __uint_as_float((uint32_t)(127 + 100) << 23);                          // 2^-ve
+
+        for (int tile = w.t0; tile < w.t1; ++tile) {
+            const bool ok = __all_sync(0xffffffffu, t_mbar_wait(&s.full[st], ph, &s.abort_flag, p.err));
+            const int tk = warp * 16;                                 // this warp's tokens of the tile
+            const int t_first = tile * kTT + tk;
+            if (ok && t_first < w.s.len) {
+                // ---- S = Q K^T ----
+                float sc[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[t][k] = 0.f;
+                    const int row = tk + t * 8 + g;
+                    uint32_t kw[WPT];
+                    if constexpr (D == 32) {
+                        kw[0] = *reinterpret_cast<const uint32_t *>(s.kq[st] + row * RB + 4 * c);
+                    } else if constexpr (D == 64) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(s.kq[st] + tile_chunk<RB>(row, c >> 1) + 8 * (c & 1));
+                        kw[0] = x.x; kw[1] = x.y;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < WPT / 4; ++i) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(s.kq[st] + tile_chunk<RB>(row, c + 4 * i));
+                            kw[4 * i] = x.x; kw[4 * i + 1] = x.y; kw[4 * i + 2] = x.z; kw[4 * i + 3] = x.w;
+                        }
+                    }
+#pragma unroll
+                    for (int wd = 0; wd < WPT; ++wd) {
+                        const uint32_t x = kw[wd] ^ 0x88888888u;
+                        const uint32_t b[4] = {nibble_pair(x, 0), nibble_pair(x, 1), nibble_pair(x, 2), nibble_pair(x, 3)};
+#pragma unroll
+                        for (int hv = 0; hv < HV; ++hv) {
+                            if constexpr (kQRegs) {
+                                mma16816(sc[t], qa[hv][wd][0], b[0], b[1]);
+                                mma16816(sc[t], qa[hv][wd][1], b[2], b[3]);
+                            } else {
+                                uint32_t a[2][4];
+                                q_frag(hv, wd, a);
+                                mma16816(sc[t], a[0], b[0], b[1]);
+                                mma16816(sc[t], a[1], b[2], b[3]);
+                            }
+                        }
+                    }
+                }
+                // ---- scales, mask ----
+                float kscale[2][2], vscale[2][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float2 a = *reinterpret_cast<const float2 *>(&s.ks[st][tk + 8 * t + 2 * c]);
+                    const float2 b = *reinterpret_cast<const float2 *>(&s.vs[st][tk + 8 * t + 2 * c]);
+                    kscale[t][0] = a.x; kscale[t][1] = a.y;
+                    vscale[t][0] = b.x; vscale[t][1] = b.y;
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[t][k] *= kscale[t][k & 1] * (k < 2 ? rs0 : rs1);
+                const int bt = min(kTT, 1 << p.log_page);
+                const uint32_t valid = s.valid[st];
+                if (t_first + 16 > w.s.ctx || valid != (uint32_t)((1ull << (kTT / bt)) - 1)) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        bool any[2] = {false, false};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int tl = tk + 8 * t + 2 * c + (k & 1);
+                            const bool sees = ((valid >> (tl / bt)) & 1) &&
+                                              tree_sees<kRows>(p, w, g + (k < 2 ? 0 : 8), tile * kTT + tl);
+                            any[k & 1] |= sees;
+                            if (!sees) sc[t][k] = -INFINITY;
+                        }
+                        // a value row that none of this lane's two query rows sees must not reach
+                        // them, whatever its scale holds
+                        if (!any[0]) vscale[t][0] = 0.f;
+                        if (!any[1]) vscale[t][1] = 0.f;
+                    }
+                }
+                // ---- lazy references ----
+                float up0 = -INFINITY, up1 = -INFINITY, vtop = 0.f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    up0 = fmaxf(up0, fmaxf(sc[t][0], sc[t][1]));
+                    up1 = fmaxf(up1, fmaxf(sc[t][2], sc[t][3]));
+                    vtop = fmaxf(vtop, fmaxf(vscale[t][0], vscale[t][1]));
+                }
+                if (__any_sync(0xffffffffu, up0 > m0 + 8.f || up1 > m1 + 8.f || vtop * vf > 64.f)) {
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) {
+                        up0 = fmaxf(up0, __shfl_xor_sync(0xffffffffu, up0, o));
+                        up1 = fmaxf(up1, __shfl_xor_sync(0xffffffffu, up1, o));
+                    }
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+                    const float n0 = fmaxf(m0, up0), n1 = fmaxf(m1, up1);
+                    const float zn0 = n0 == -INFINITY ? 0.f : n0, zn1 = n1 == -INFINITY ? 0.f : n1;
+                    float f0 = m0 == -INFINITY ? 1.f : ex2(m0 - zn0), f1 = m1 == -INFINITY ? 1.f : ex2(m1 - zn1);
+                    m0 = n0; m1 = n1; z0 = zn0; z1 = zn1;
+                    l0 *= f0; l1 *= f1;
+                    if (vtop * vf > 64.f) {
+                        const int nv = max(-100, min((int)(__float_as_uint(vtop) >> 23) - 127, 100));
+                        const float dv = ve - nv < -126 ? 0.f : __uint_as_float((uint32_t)(127 + ve - nv) << 23);
+                        ve = nv;
+                        vf = __uint_as_float((uint32_t)(127 - ve) << 23);
+                        f0 *= dv; f1 *= dv;
+                    }
+#pragma unroll
+                    for (int i = 0; i < NQ * 4; ++i) {
+                        acc[i][0] *= f0; acc[i][1] *= f0;
+                        acc[i][2] *= f1; acc[i][3] *= f1;
+                    }
+                }
+                // ---- weights ----
+                uint32_t pa[HV][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float p0 = ex2(sc[t][0] - z0), p1 = ex2(sc[t][1] - z0);
+                    const float p2 = ex2(sc[t][2] - z1), p3 = ex2(sc[t][3] - z1);
+                    l0 += p0 + p1;
+                    l1 += p2 + p3;
+                    const float v0 = vscale[t][0] * vf, v1 = vscale[t][1] * vf;
+                    float w0 = p0 * v0, w1 = p1 * v1, w2 = p2 * v0, w3 = p3 * v1;
+                    // a masked weight is zero, also where the value's scale is not finite
+                    if (sc[t][0] == -INFINITY) w0 = 0.f;
+                    if (sc[t][1] == -INFINITY) w1 = 0.f;
+                    if (sc[t][2] == -INFINITY) w2 = 0.f;
+                    if (sc[t][3] == -INFINITY) w3 = 0.f;
+                    pa[0][2 * t] = pack_h2(w0, w1);
+                    pa[0][2 * t + 1] = pack_h2(w2, w3);
+                    if constexpr (HV == 2) {
+                        const float2 a = unpack_h2(pa[0][2 * t]), b = unpack_h2(pa[0][2 * t + 1]);
+                        pa[1][2 * t] = pack_h2(w0 - a.x, w1 - a.y);
+                        pa[1][2 * t + 1] = pack_h2(w2 - b.x, w3 - b.y);
+                    }
+                }
+                // ---- O += (P vs) V ----
+                auto pv = [&](int q, uint32_t x, uint32_t y) {
+                    x ^= 0x88888888u;
+                    y ^= 0x88888888u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t b0 = nibble_pair(x, j), b1 = nibble_pair(y, j);
+#pragma unroll
+                        for (int hv = 0; hv < HV; ++hv) mma16816(acc[4 * q + j], pa[hv], b0, b1);
+                    }
+                };
+                const uint32_t vbase = t_smem(s.vq[st]);
+                const int mrow = tk + ((lane >> 3) & 1) * 8 + (lane & 7);
+                if constexpr (NQ == 1) {
+                    uint32_t x, y;
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+                                 : "=r"(x), "=r"(y) : "r"(vbase + tile_chunk<RB>(mrow, 0)) : "memory");
+                    pv(0, x, y);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NQ; q += 2) {
+                        uint32_t x[4];
+                        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(vbase + tile_chunk<RB>(mrow, q + (lane >> 4))) : "memory");
+                        pv(q, x[0], x[1]);
+                        pv(q + 1, x[2], x[3]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) t_mbar_arrive(&s.empty[st]);
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+
+        // ---- join the warps: references first, then the sums two by two ----
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+        }
+        if (m0 == -INFINITY && !(l0 == 0.f)) m0 = 0.f;      // nothing but NaN seen
+        if (m1 == -INFINITY && !(l1 == 0.f)) m1 = 0.f;
+        if (c == 0) {
+            s.ref[warp][g] = m0;
+            s.ref[warp][g + 8] = m1;
+            s.sum[warp][g] = l0;
+            s.sum[warp][g + 8] = l1;
+        }
+        cta_sync();
+        auto joined = [&](int r, float &top, float &sum) {
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kCWarps; ++i) top = fmaxf(top, s.ref[i][r]);
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kCWarps; ++i)
+                if (s.ref[i][r] != -INFINITY) sum += s.sum[i][r] * ex2(s.ref[i][r] - top);
+        };
+        float top0, top1, sum0, sum1;
+        joined(g, top0, sum0);
+        joined(g + 8, top1, sum1);
+        const float vup = __uint_as_float((uint32_t)(127 + ve) << 23);
+        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - top0) * vup, f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top1) * vup;
+        // accumulator (chunk q, j) of lane column c: dims 32 q + 8 c + j and + 4 + j
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+            if ((warp >> 1) == 1 - step) {                  // warps 2, 3 write, then 0, 1 add
+                float(*dst)[D + 4] = s.acc[warp & 1];
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = g + (k < 2 ? 0 : 8);
+                        const float f = k < 2 ? f0 : f1;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float *x = &dst[r][32 * q + 8 * c + 4 * (k & 1) + j];
+                            const float val = f == 0.f ? 0.f : acc[4 * q + j][k] * f;
+                            *x = step == 0 ? val : *x + val;
+                        }
+                    }
+            }
+            cta_sync();
+        }
+        // ---- rows out: finished, or as a partial ----
+        float *part = p.part, *ml = p.part + (int64_t)2 * p.ctas * kRows * D;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (at - (w.t1 - w.t0) == begin ? 0 : 1);
+#pragma unroll 1
+        for (int i = 0; i < kRows / kCWarps; ++i) {
+            const int r = warp * (kRows / kCWarps) + i, gr = w.mt * kRows + r;
+            if (r >= rows) break;
+            float top, sum, v[E];
+            joined(r, top, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = s.acc[0][r][lane * E + e] + s.acc[1][r][lane * E + e];
+            if (!w.whole) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) part[(slot * kRows + r) * D + lane * E + e] = v[e];
+                if (lane == 0) *reinterpret_cast<float2 *>(ml + (slot * kRows + r) * 2) = make_float2(top, sum);
+                continue;
+            }
+            const float il = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] *= il;
+            if (!(p.flags & RQ_ATTN_ROTATED_OUT)) warp_rotate<E>(v, sg, lane, !signs_first, inv_sqrt_dim<D>());
+            const int64_t o = ((w.s.row0 + gr / p.group) * p.kv_heads + w.h) * p.group + gr % p.group;
+#pragma unroll
+            for (int e = 0; e < E; ++e) store_elem<IN>(p.out, o * D + lane * E + e, v[e]);
+        }
+        cta_sync();                                          // s.acc and s.q are free again
+    }
+}
+
+template <int IN, int D>
+cudaError_t launch_tree_d(TreeParams &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
+    auto kern = attn_tree_mma_kernel<IN, D>;
+    const size_t smem = sizeof(MSmem<IN, D>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.ctas, kMThreads, smem, stream>>>(mk, mv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int bph = (int)(((int64_t)p.max_nodes * p.group + kRows - 1) / kRows);
+    const int64_t units = (int64_t)p.seqs * p.kv_heads * bph;
+    if (units > 0x7fffffffll) return cudaErrorInvalidValue;
+    attn_tree_join_kernel<IN, D, kRows, kTT><<<dim3((unsigned)units, 1), 32 * kJoinWarps, 0, stream>>>(p, bph);
+    return cudaGetLastError();
+}
+
+template <int IN>
+cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
+    switch (d) {
+        case 32: return launch_tree_d<IN, 32>(p, mk, mv, stream);
+        case 64: return launch_tree_d<IN, 64>(p, mk, mv, stream);
+        case 128: return launch_tree_d<IN, 128>(p, mk, mv, stream);
+        default: return launch_tree_d<IN, 256>(p, mk, mv, stream);
+    }
+}
+
+}  // namespace
+
+int64_t attn_tree_workspace(int64_t head_dim) {
+    const int64_t ctas = 2 * (int64_t)device_sm_count();
+    return 2 * ctas * kRows * (head_dim + 2) * (int64_t)sizeof(float);
+}
+
+cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
+    TreeParams p{};
+    p.q = c.q;
+    p.q_token = c.q_token;
+    p.q_head = c.q_head;
+    p.ks = c.cache.ks;
+    p.vs = c.cache.vs;
+    p.table = c.table;
+    p.contexts = c.contexts;
+    p.offsets = c.offsets;
+    p.mask = c.mask;
+    p.mask_stride = c.mask_stride;
+    p.width = c.width;
+    p.rows = c.rows;
+    p.pages = c.cache.pages;
+    p.seqs = (int)c.seqs;
+    p.kv_heads = (int)c.cache.heads;
+    p.group = (int)(c.q_heads / c.cache.heads);
+    while ((int64_t(1) << p.log_page) < c.cache.page_size) ++p.log_page;
+    p.max_nodes = (int)c.max_nodes;
+    p.seed = c.seed;
+    p.flags = c.flags;
+    p.score_scale = (float)((double)c.softmax_scale * 1.4426950408889634);
+    p.out = c.out;
+    p.part = static_cast<float *>(c.workspace);
+    p.err = error_word_device_ptr();
+    if (!p.err) return cudaErrorUnknown;
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorUnknown;
+    const int per_sm = c.in_type == IN_F32 || c.head_dim == 256 ? 1 : 2;
+    const int64_t bph = (c.max_nodes * p.group + kRows - 1) / kRows;
+    const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTT - 1) / kTT);
+    p.ctas = (int)(max_tiles < per_sm * sms ? max_tiles : per_sm * sms);
+    const int64_t rows = c.cache.pages * c.cache.heads * c.cache.page_size;
+    const int rb = (int)(c.head_dim / 2), box = (int)(c.cache.page_size < kTT ? c.cache.page_size : kTT);
+    const CUtensorMapSwizzle sw = rb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : rb == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                             : CU_TENSOR_MAP_SWIZZLE_NONE;
+    CUtensorMap mk, mv;
+    if (!make_tma_map_u8(&mk, c.cache.kq, rows, rb, rb, box, sw) || !make_tma_map_u8(&mv, c.cache.vq, rows, rb, rb, box, sw))
+        return cudaErrorInvalidValue;
+    switch (c.in_type) {
+        case IN_F32: return launch_tree_in<IN_F32>(p, c.head_dim, mk, mv, stream);
+        case IN_BF16: return launch_tree_in<IN_BF16>(p, c.head_dim, mk, mv, stream);
+        default: return launch_tree_in<IN_F16>(p, c.head_dim, mk, mv, stream);
+    }
+}
+
+}  // namespace rq

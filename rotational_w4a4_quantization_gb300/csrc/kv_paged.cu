@@ -1,0 +1,358 @@
+// kv_paged.cu -- the paged rotated INT4 KV cache: quantising rows as they are
+// written to their slots, and reading sequences back dense (sm_103a).
+//
+// "End-to-end flow" (The KV cache) of the QuaRot page: keys (after their rotary
+// positions) and values are rotated head by head and stored in four bits.
+//   write: y = x R, scale = max|y| / 7, code = round_half_even(y / scale)
+//   read:  x^ = (code * scale) R^T, or code * scale where the rotated basis is kept
+// A page holds page_size tokens of every head, head-major: codes
+// [page][head][row][D/2], scales [page][head][row].
+//
+// Both are bound by moving the rows once (D elements on one side, D/2 + 4 bytes on
+// the other).  A row is spread over 4 lanes (8 for D = 256), 32 elements each at
+// D = 128, interleaved in 8-element chunks so that every load and store covers whole
+// lines: 5 of the 7 butterfly stages run in registers as f32x2 operations, 2 as
+// shuffles, and no shared memory is passed through.
+#include "rq.h"
+#include "rq_internal.h"
+#include "paged_device.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int kPThreads = 128;
+constexpr int kMaxTok = 16;          // tokens per block
+
+struct AppendParams {
+    const void *x[2];                // K, V
+    int64_t token_stride[2], head_stride[2];
+    uint8_t *codes[2];
+    float *scales[2];
+    const int64_t *slots, *positions;
+    const uint64_t *turns;
+    int64_t tokens, slots_total;     // pages * page_size
+    int heads, log_page, half, tb;
+    uint64_t seed;
+    uint32_t flags;
+    float mscale;
+};
+
+// This lane's chunk `ch` (elements 8 ch ..) of a key row with its rotary turn: half
+// layout pairs i with i + half, so the partner chunk is read as well (its lines are
+// being read by the neighbouring lanes); half is a multiple of 8.
+template <int IN, bool INTER>
+__device__ __forceinline__ void load_turned(const char *row, int ch, const float2 *c, int half, pair_t (&v)[4]) {
+    constexpr int ES = IN == IN_F32 ? 4 : 2;
+    load8<IN>(row + ch * 8 * ES, v);
+    const int e0 = 8 * ch;
+    if (e0 >= 2 * half) return;
+    if constexpr (INTER) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 w = c[4 * ch + k];
+            const float a = lo2(v[k]), b = hi2(v[k]);
+            v[k] = mk2(a * w.x - b * w.y, a * w.y + b * w.x);
+        }
+    } else {
+        const bool first = e0 < half;
+        const float sg = first ? -1.f : 1.f;
+        pair_t o[4];
+        load8<IN>(row + (first ? e0 + half : e0 - half) * ES, o);
+        const float4 *cp = reinterpret_cast<const float4 *>(c + (first ? e0 : e0 - half));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 w = cp[k];                       // cos, sin of the pair's two elements
+            v[k] = mk2(lo2(v[k]) * w.x + sg * (lo2(o[k]) * w.y), hi2(v[k]) * w.z + sg * (hi2(o[k]) * w.w));
+        }
+    }
+}
+
+template <int IN, int D, bool ROPE, bool INTER>
+__global__ void __launch_bounds__(kPThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    using L = RowLanes<D>;
+    constexpr int ES = IN == IN_F32 ? 4 : 2;
+    constexpr int RPP = kPThreads / L::LPR;              // rows at a time
+    extern __shared__ __align__(16) float2 cs[];         // [tb][half] when ROPE
+    __shared__ uint32_t sign_words[8];
+    __shared__ int64_t slot_of[kMaxTok];
+    const int64_t tok0 = (int64_t)blockIdx.x * p.tb;
+    const int nt = (int)min((int64_t)p.tb, p.tokens - tok0);
+    block_sign_words<D>(sign_words, p.seed);
+    if (threadIdx.x < nt) slot_of[threadIdx.x] = p.slots[tok0 + threadIdx.x];
+    if constexpr (ROPE) {
+        for (int i = threadIdx.x; i < nt * p.half; i += kPThreads) {
+            const int tk = i / p.half, pr = i - tk * p.half;
+            cs[i] = rotary_cos_sin(p.positions[tok0 + tk], p.turns[pr], p.mscale);
+        }
+    }
+    __syncthreads();
+    const int rl = threadIdx.x % L::LPR, r0 = threadIdx.x / L::LPR;
+    pair_t sg[L::NP];
+    row_sign_pairs<D>(sg, sign_words, rl);
+    const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;
+    constexpr float isd = inv_sqrt_dim<D>();
+
+    const int rows = nt * 2 * p.heads;
+    // the shuffles name whole warps: every lane runs every pass, rows past the end idle
+    for (int base = 0; base < rows; base += RPP) {
+        const int r = base + r0;
+        const int tk = r / (2 * p.heads);
+        const int rest = r - tk * 2 * p.heads;
+        const bool is_v = rest >= p.heads;
+        const int h = is_v ? rest - p.heads : rest;
+        const int64_t slot = r < rows ? slot_of[tk] : -1;
+        const bool live = slot >= 0 && slot < p.slots_total;   // others are padding
+        pair_t v[L::NP];
+        const char *row = static_cast<const char *>(p.x[is_v]) +
+                          ((tok0 + tk) * p.token_stride[is_v] + h * p.head_stride[is_v]) * ES;
+#pragma unroll
+        for (int i = 0; i < L::NCH; ++i) {
+            pair_t c[4] = {0ull, 0ull, 0ull, 0ull};
+            const int ch = rl + L::LPR * i;
+            if (live) {
+                if (ROPE && !is_v) load_turned<IN, INTER>(row, ch, cs + tk * p.half, p.half, c);
+                else load8<IN>(row + ch * 8 * ES, c);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * i + k] = c[k];
+        }
+        if (signs_first) {
+#pragma unroll
+            for (int i = 0; i < L::NP; ++i) v[i] ^= sg[i];
+        }
+        row_fwht<D>(v, rl);
+        if (!signs_first) {
+#pragma unroll
+            for (int i = 0; i < L::NP; ++i) v[i] ^= sg[i];
+        }
+        float top = pairs_absmax(v);
+#pragma unroll
+        for (int m = 1; m < L::LPR; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        // A row that holds a NaN or an infinity rotates to nothing but those: its
+        // scale becomes NaN, so that it reads back as NaN.
+        const float probe = lo2(v[0]);
+        const bool bad = !(top < INFINITY) || probe != probe;
+        const float inv = top > 0.f && !bad ? fminf(7.0f / top, 3.4028234e38f) : 0.f;
+        const pair_t inv2 = mk2(inv, inv), magic = mk2(12582912.f, 12582912.f);   // 1.5 2^23: rounds to nearest even
+        if (!live) continue;
+        const int64_t at = (((slot >> p.log_page) * p.heads + h) << p.log_page) + (slot & ((1ll << p.log_page) - 1));
+        uint32_t *codes = reinterpret_cast<uint32_t *>(p.codes[is_v] + at * (D / 2));
+#pragma unroll
+        for (int i = 0; i < L::NCH; ++i) {
+            uint32_t c[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const pair_t q = fma2(bad ? 0ull : v[4 * i + k], inv2, magic);
+                c[2 * k] = (uint32_t)q;
+                c[2 * k + 1] = (uint32_t)(q >> 32);
+            }
+            codes[rl + L::LPR * i] = pack8(c);
+        }
+        if (rl == 0) p.scales[is_v][at] = bad ? __int_as_float(0x7fffffff) : (top / 7.0f) * isd;
+    }
+}
+
+struct ReadParams {
+    const uint8_t *codes[2];
+    const float *scales[2];
+    void *out[2];
+    const int32_t *table, *starts, *offsets;
+    int64_t total, pages, width;
+    int heads, log_page, seqs, tb;
+    uint64_t seed;
+    uint32_t flags;
+};
+
+template <int OUT, int D>
+__global__ void __launch_bounds__(kPThreads) kv_read_kernel(const __grid_constant__ ReadParams p) {
+    using L = RowLanes<D>;
+    constexpr int ES = OUT == IN_F32 ? 4 : 2;
+    constexpr int RPP = kPThreads / L::LPR;
+    __shared__ uint32_t sign_words[8];
+    __shared__ int64_t at_of[kMaxTok];       // cache row of head 0; -1: no such page (reads zeros); -2: not asked for
+    const int64_t n0 = (int64_t)blockIdx.x * p.tb;
+    const int nt = (int)min((int64_t)p.tb, p.total - n0);
+    block_sign_words<D>(sign_words, p.seed);
+    if (threadIdx.x < nt) {
+        const int64_t n = n0 + threadIdx.x;
+        int lo = 0, hi = p.seqs;             // the last sequence whose first row is at or before n
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.offsets[mid] <= n) lo = mid;
+            else hi = mid;
+        }
+        int64_t at = -2;
+        if (n >= p.offsets[lo] && n < p.offsets[lo + 1]) {
+            const int64_t pos = n - p.offsets[lo] + (p.starts ? p.starts[lo] : 0);
+            const int64_t blk = pos >> p.log_page;
+            at = -1;
+            if (pos >= 0 && blk < p.width) {
+                const int64_t page = p.table[lo * p.width + blk];
+                if (page >= 0 && page < p.pages)
+                    at = ((page * p.heads) << p.log_page) + (pos & ((1ll << p.log_page) - 1));
+            }
+        }
+        at_of[threadIdx.x] = at;
+    }
+    __syncthreads();
+    const int rl = threadIdx.x % L::LPR, r0 = threadIdx.x / L::LPR;
+    pair_t sg[L::NP];
+    row_sign_pairs<D>(sg, sign_words, rl);
+    const bool rotated = (p.flags & RQ_KV_ROTATED_OUT) != 0;
+    const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;   // of R: R^T has them last
+    constexpr float isd = inv_sqrt_dim<D>();
+
+    // rows in the order (head, K or V, token): consecutive rows lie next to each other in a page
+    const int rows = nt * 2 * p.heads;
+    for (int base = 0; base < rows; base += RPP) {
+        const int r = base + r0;
+        const int hs = r / nt, tk = r - hs * nt;
+        const int h = hs >> 1, is_v = hs & 1;
+        const int64_t at0 = r < rows ? at_of[tk] : -2;
+        const int64_t at = at0 + ((int64_t)h << p.log_page);
+        pair_t v[L::NP];
+        float scale = 0.f;
+        if (at0 >= 0) scale = p.scales[is_v][at];
+        const uint32_t *codes = reinterpret_cast<const uint32_t *>(p.codes[is_v] + at * (D / 2));
+#pragma unroll
+        for (int i = 0; i < L::NCH; ++i) {
+            const uint32_t w = at0 >= 0 ? codes[rl + L::LPR * i] : 0u;
+            pair_t c[4];
+            codes_to_pairs(w, c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * i + k] = c[k];
+        }
+        if (!rotated) {
+            if (!signs_first) {
+#pragma unroll
+                for (int i = 0; i < L::NP; ++i) v[i] ^= sg[i];
+            }
+            row_fwht<D>(v, rl);
+            if (signs_first) {
+#pragma unroll
+                for (int i = 0; i < L::NP; ++i) v[i] ^= sg[i];
+            }
+            scale *= isd;
+        }
+        if (at0 < -1) continue;
+        const pair_t s2 = mk2(scale, scale);
+        char *out = static_cast<char *>(p.out[is_v]) + ((n0 + tk) * p.heads + h) * D * ES;
+#pragma unroll
+        for (int i = 0; i < L::NCH; ++i) {
+            pair_t c[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = fma2(v[4 * i + k], s2, 0ull);
+            store8<OUT>(out + (rl + L::LPR * i) * 8 * ES, c);
+        }
+    }
+}
+
+template <int IN, int D>
+cudaError_t launch_append_d(const AppendParams &p, bool rope, bool inter, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)((p.tokens + p.tb - 1) / p.tb);
+    const size_t smem = rope ? sizeof(float2) * p.tb * p.half : 0;
+    if (!rope) kv_append_kernel<IN, D, false, false><<<blocks, kPThreads, 0, stream>>>(p);
+    else if (inter) kv_append_kernel<IN, D, true, true><<<blocks, kPThreads, smem, stream>>>(p);
+    else kv_append_kernel<IN, D, true, false><<<blocks, kPThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+template <int IN>
+cudaError_t launch_append_in(const AppendParams &p, int64_t d, bool rope, bool inter, cudaStream_t stream) {
+    switch (d) {
+        case 32: return launch_append_d<IN, 32>(p, rope, inter, stream);
+        case 64: return launch_append_d<IN, 64>(p, rope, inter, stream);
+        case 128: return launch_append_d<IN, 128>(p, rope, inter, stream);
+        default: return launch_append_d<IN, 256>(p, rope, inter, stream);
+    }
+}
+template <int OUT>
+cudaError_t launch_read_out(const ReadParams &p, int64_t d, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)((p.total + p.tb - 1) / p.tb);
+    switch (d) {
+        case 32: kv_read_kernel<OUT, 32><<<blocks, kPThreads, 0, stream>>>(p); break;
+        case 64: kv_read_kernel<OUT, 64><<<blocks, kPThreads, 0, stream>>>(p); break;
+        case 128: kv_read_kernel<OUT, 128><<<blocks, kPThreads, 0, stream>>>(p); break;
+        default: kv_read_kernel<OUT, 256><<<blocks, kPThreads, 0, stream>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+int log2_of(int64_t n) {
+    int l = 0;
+    while ((int64_t(1) << l) < n) ++l;
+    return l;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvRows &k, const KvRows &v, int in_type, int64_t tokens, int64_t head_dim,
+                             const PagedCache &c, const int64_t *slots, const int64_t *positions,
+                             const uint64_t *turns, int64_t rot, float mscale, bool inter, uint64_t seed,
+                             uint32_t flags, cudaStream_t stream) {
+    AppendParams p{};
+    p.x[0] = k.x;
+    p.x[1] = v.x;
+    p.token_stride[0] = k.token_stride;
+    p.token_stride[1] = v.token_stride;
+    p.head_stride[0] = k.head_stride;
+    p.head_stride[1] = v.head_stride;
+    p.codes[0] = c.kq;
+    p.codes[1] = c.vq;
+    p.scales[0] = c.ks;
+    p.scales[1] = c.vs;
+    p.slots = slots;
+    p.positions = positions;
+    p.turns = turns;
+    p.tokens = tokens;
+    p.slots_total = c.pages * c.page_size;
+    p.heads = (int)c.heads;
+    p.log_page = log2_of(c.page_size);
+    p.half = (int)(rot / 2);
+    p.seed = seed;
+    p.flags = flags;
+    p.mscale = mscale;
+    // about two passes of the block's 32 rows (16 at D = 256) per block, more blocks while SMs would idle
+    p.tb = (int)((64 + 2 * c.heads - 1) / (2 * c.heads));
+    if (p.tb > kMaxTok) p.tb = kMaxTok;
+    while (p.tb > 1 && tokens / p.tb < 2 * device_sm_count()) p.tb /= 2;
+    if ((tokens + p.tb - 1) / p.tb > 0x7fffffffll) return cudaErrorInvalidValue;
+    const bool rope = turns != nullptr;
+    switch (in_type) {
+        case IN_F32: return launch_append_in<IN_F32>(p, head_dim, rope, inter, stream);
+        case IN_BF16: return launch_append_in<IN_BF16>(p, head_dim, rope, inter, stream);
+        default: return launch_append_in<IN_F16>(p, head_dim, rope, inter, stream);
+    }
+}
+
+cudaError_t launch_kv_read(const PagedCache &c, int64_t head_dim, const int32_t *table, int64_t width,
+                           const int32_t *starts, const int32_t *offsets, int64_t seqs, int64_t total, uint64_t seed,
+                           uint32_t flags, void *k_out, void *v_out, int out_type, cudaStream_t stream) {
+    ReadParams p{};
+    p.codes[0] = c.kq;
+    p.codes[1] = c.vq;
+    p.scales[0] = c.ks;
+    p.scales[1] = c.vs;
+    p.out[0] = k_out;
+    p.out[1] = v_out;
+    p.table = table;
+    p.starts = starts;
+    p.offsets = offsets;
+    p.total = total;
+    p.pages = c.pages;
+    p.width = width;
+    p.heads = (int)c.heads;
+    p.log_page = log2_of(c.page_size);
+    p.seqs = (int)seqs;
+    p.seed = seed;
+    p.flags = flags;
+    p.tb = kMaxTok;
+    while (p.tb > 1 && total / p.tb < 2 * device_sm_count()) p.tb /= 2;
+    if ((total + p.tb - 1) / p.tb > 0x7fffffffll) return cudaErrorInvalidValue;
+    switch (out_type) {
+        case IN_F32: return launch_read_out<IN_F32>(p, head_dim, stream);
+        case IN_BF16: return launch_read_out<IN_BF16>(p, head_dim, stream);
+        default: return launch_read_out<IN_F16>(p, head_dim, stream);
+    }
+}
+
+}  // namespace rq

@@ -7,6 +7,7 @@
 
 #include "rq_internal.h"
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cstdint>
@@ -198,6 +199,72 @@ __device__ __forceinline__ K4Addr k4_addr(int t) {
     return a;
 }
 __host__ __device__ constexpr int k4_k3(int s, int h) { return (2 * s + h) ^ ((s >> 2) & 1); }
+
+template <int IN>
+__device__ __forceinline__ float load_elem(const void *base, int64_t i) {
+    if constexpr (IN == IN_F32) return static_cast<const float *>(base)[i];
+    else if constexpr (IN == IN_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[i]);
+    else return __half2float(static_cast<const __half *>(base)[i]);
+}
+
+// Warp-wide rotation of a D-vector held as E = D/32 values per lane (element
+// lane * E + e): signs (before or after), Sylvester butterflies over the e bits in
+// registers and over the lane bits by shuffles, then a scale.
+template <int E>
+__device__ __forceinline__ void lane_signs(float (&sg)[E], int lane, uint64_t seed) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        sg[e] = (splitmix64_at(seed, (uint64_t)(lane * E + e)) >> 63) ? -1.f : 1.f;
+}
+template <int E>
+__device__ __forceinline__ void warp_rotate(float (&v)[E], const float (&sg)[E], int lane, bool signs_before,
+                                            float scale) {
+    if (signs_before) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= sg[e];
+    }
+#pragma unroll
+    for (int st = 1; st < E; st <<= 1)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (!(e & st)) {
+                const float a = v[e], b = v[e + st];
+                v[e] = a + b;
+                v[e + st] = a - b;
+            }
+#pragma unroll
+    for (int lm = 1; lm < 32; lm <<= 1)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float o = __shfl_xor_sync(0xffffffffu, v[e], lm);
+            v[e] = (lane & lm) ? o - v[e] : v[e] + o;
+        }
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = (signs_before ? v[e] : v[e] * sg[e]) * scale;
+}
+
+// 8 codes of a packed word -> four fp32 pairs (codes 2k, 2k+1): byte permutes
+// into 2^23 + (q + 8), then one f32x2 add of -(2^23 + 8).
+__device__ __forceinline__ void codes_to_pairs(uint32_t w, pair_t (&c)[4]) {
+    const uint32_t x = w ^ 0x88888888u;
+    const uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
+    const uint32_t magic = 0x4b000000u;
+    const pair_t bias = mk2(-8388616.0f, -8388616.0f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t e0 = __byte_perm(lo, magic, 0x7650u + k);
+        const uint32_t e1 = __byte_perm(hi, magic, 0x7650u + k);
+        c[k] = add2(((pair_t)e1 << 32) | (pair_t)e0, bias);
+    }
+}
+
+// 2^x by the hardware approximation (relative error below 2^-22; flushes to 0
+// far below the running maximum, as the softmax wants).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 }  // namespace
 }  // namespace rq

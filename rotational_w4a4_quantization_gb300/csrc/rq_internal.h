@@ -75,6 +75,58 @@ cudaError_t launch_attn_decode(const void *q, int in_type, int64_t M, int64_t he
                                int64_t tokens, uint64_t seed, uint32_t flags, float softmax_scale, float *out,
                                cudaStream_t stream);
 
+// Rows of heads with free token and head strides (elements); heads 0: absent.
+struct RopeView {
+    const void *src;
+    void *dst;
+    int64_t heads, src_token, src_head, dst_token, dst_head;
+};
+cudaError_t launch_rope(const RopeView &q, const RopeView &k, int in_type, int64_t tokens, int64_t head_dim,
+                        int64_t rot, const int64_t *positions, const uint64_t *turns, float mscale, bool inter,
+                        bool inverse, cudaStream_t stream);
+
+// The paged rotated INT4 cache: codes [pages][heads][page_size][D/2], scales
+// [pages][heads][page_size].
+struct PagedCache {
+    uint8_t *kq;
+    float *ks;
+    uint8_t *vq;
+    float *vs;
+    int64_t pages, heads, page_size;
+};
+struct KvRows {
+    const void *x;
+    int64_t token_stride, head_stride;
+};
+// turns NULL: no rotary positions on the keys.
+cudaError_t launch_kv_append(const KvRows &k, const KvRows &v, int in_type, int64_t tokens, int64_t head_dim,
+                             const PagedCache &c, const int64_t *slots, const int64_t *positions,
+                             const uint64_t *turns, int64_t rot, float mscale, bool inter, uint64_t seed,
+                             uint32_t flags, cudaStream_t stream);
+cudaError_t launch_kv_read(const PagedCache &c, int64_t head_dim, const int32_t *table, int64_t width,
+                           const int32_t *starts, const int32_t *offsets, int64_t seqs, int64_t total, uint64_t seed,
+                           uint32_t flags, void *k_out, void *v_out, int out_type, cudaStream_t stream);
+
+// Attention of trees of drafted tokens over the paged cache.
+struct TreeCall {
+    const void *q;
+    int in_type;
+    int64_t rows, q_heads, head_dim, q_token, q_head;
+    PagedCache cache;
+    const int32_t *table;
+    int64_t width;
+    const int32_t *contexts, *offsets;
+    int64_t seqs, max_nodes;
+    const uint8_t *mask;
+    int64_t mask_stride;
+    uint64_t seed;
+    uint32_t flags;
+    float softmax_scale;
+    void *out, *workspace;
+};
+int64_t attn_tree_workspace(int64_t head_dim);
+cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream);
+
 // W4A8 product: INT8 activations, INT4 weights, per-channel (group == K) or
 // per-group (group == 128) weight scales.  Per-channel scales with more than 64
 // tokens run on the tensor cores (launch_w4a8_gemm_tc), the rest on mma.sync.

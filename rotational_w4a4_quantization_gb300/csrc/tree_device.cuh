@@ -1,0 +1,279 @@
+// tree_device.cuh -- what the tree-attention kernels share: parameters, the
+// schedule of tiles over CTAs, and where partial results lie.  Internal linkage.
+//
+// A unit is (sequence, KV head, block of ROWS query rows); its tokens are cut into
+// tiles of TT.  All tiles of all units form one line, unit after unit, and CTA c of
+// G takes the stretch [c T / G, (c + 1) T / G): every CTA has the same number of
+// tiles whatever the lengths, long sequences spread over many CTAs, and a unit that
+// lies inside one stretch is finished there.  A unit that spans CTAs leaves one
+// partial per CTA: slot 2c for the unit the stretch begins in, 2c + 1 for the last.
+#pragma once
+
+#include "paged_device.cuh"
+
+namespace rq {
+namespace {
+
+struct TreeParams {
+    const void *q;
+    int64_t q_token, q_head;            // strides in elements
+    const float *ks, *vs;
+    const int32_t *table, *contexts, *offsets;
+    const uint8_t *mask;                // [rows][mask_stride], NULL: causal among the nodes
+    int64_t mask_stride, width, pages, rows;
+    int seqs, kv_heads, group, log_page, max_nodes;
+    uint64_t seed;
+    uint32_t flags;
+    float score_scale;                  // softmax_scale * log2(e)
+    void *out;
+    float *part;                        // [2 G][ROWS][D] fp32, then [2 G][ROWS][2] (reference, sum)
+    int ctas;                           // G
+    int *err;
+};
+
+struct TreeSeq {
+    int64_t row0;      // first query row
+    int ctx, n, len;   // tokens before the tree, nodes, tokens in all
+    int mt, nt;        // row blocks, tiles
+};
+
+template <int ROWS, int TT>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
+    TreeSeq s;
+    const int64_t o0 = p.offsets[b], o1 = min((int64_t)p.offsets[b + 1], p.rows);
+    s.row0 = o0;
+    s.n = o0 < 0 ? 0 : (int)max((int64_t)0, min(o1 - o0, (int64_t)p.max_nodes));
+    const int64_t cap = p.width << p.log_page;
+    s.ctx = max(0, p.contexts[b]);
+    s.len = (int)min((int64_t)s.ctx + s.n, cap);
+    s.mt = (s.n * p.group + ROWS - 1) / ROWS;
+    s.nt = s.mt ? (s.len + TT - 1) / TT : 0;
+    return s;
+}
+
+constexpr int kScan = 128;              // stretches of sequences whose tile counts are scanned
+
+// Exclusive prefix sums of the tile counts of kScan stretches of sequences, the
+// total in prefix[kScan].  Threads 0..kScan-1 of the block take part; the caller's
+// barrier follows.  Needs __syncthreads in between, so every thread calls it.
+template <int ROWS, int TT>
+__device__ __forceinline__ void tree_scan(const TreeParams &p, int64_t *prefix) {
+    const int per = (p.seqs + kScan - 1) / kScan;
+    if (threadIdx.x < kScan) {
+        int64_t sum = 0;
+        for (int b = threadIdx.x * per; b < min(p.seqs, ((int)threadIdx.x + 1) * per); ++b) {
+            const TreeSeq s = tree_seq<ROWS, TT>(p, b);
+            sum += (int64_t)p.kv_heads * s.mt * s.nt;
+        }
+        prefix[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int64_t v[kScan / 32], run = 0;
+#pragma unroll
+        for (int i = 0; i < kScan / 32; ++i) {
+            v[i] = prefix[threadIdx.x * (kScan / 32) + i];
+            run += v[i];
+        }
+        int64_t incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (threadIdx.x >= o) incl += x;
+        }
+        int64_t at = incl - run;
+#pragma unroll
+        for (int i = 0; i < kScan / 32; ++i) {
+            prefix[threadIdx.x * (kScan / 32) + i] = at;
+            at += v[i];
+        }
+        if (threadIdx.x == 31) prefix[kScan] = at;
+    }
+    __syncthreads();
+}
+
+// One stretch of a unit, as one CTA works on it.
+struct TreeWork {
+    TreeSeq s;
+    int b, h, mt;          // sequence, KV head, row block
+    int t0, t1;            // the CTA's tiles of the unit
+    bool whole;            // the unit lies in this CTA alone
+};
+
+template <int ROWS, int TT>
+__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const int64_t *prefix, int64_t tile, int64_t end) {
+    int lo = 0, hi = kScan;
+    while (hi - lo > 1) {                    // the last stretch that begins at or before the tile
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= tile) lo = mid;
+        else hi = mid;
+    }
+    const int per = (p.seqs + kScan - 1) / kScan;
+    int64_t at = prefix[lo];
+    TreeWork w;
+    w.b = lo * per;
+    while (true) {
+        w.s = tree_seq<ROWS, TT>(p, w.b);
+        const int64_t tiles = (int64_t)p.kv_heads * w.s.mt * w.s.nt;
+        if (tile < at + tiles || w.b + 1 >= p.seqs) break;
+        at += tiles;
+        ++w.b;
+    }
+    const int64_t off = tile - at, u = off / w.s.nt;
+    w.t0 = (int)(off - u * w.s.nt);
+    w.h = (int)(u / w.s.mt);
+    w.mt = (int)(u - (int64_t)w.h * w.s.mt);
+    w.t1 = (int)min((int64_t)w.s.nt, w.t0 + (end - tile));
+    w.whole = w.t0 == 0 && w.t1 == w.s.nt;
+    return w;
+}
+
+__device__ __forceinline__ int64_t tree_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
+
+// May query row `r` of the row block see token `t` of the sequence?  Rows past the
+// sequence's last see nothing.
+template <int ROWS>
+__device__ __forceinline__ bool tree_sees(const TreeParams &p, const TreeWork &w, int r, int t) {
+    const int i = (w.mt * ROWS + r) / p.group;
+    if (i >= w.s.n || t >= w.s.len) return false;
+    if (t < w.s.ctx) return true;
+    const int j = t - w.s.ctx;
+    return p.mask ? p.mask[(w.s.row0 + i) * p.mask_stride + j] != 0 : j <= i;
+}
+
+__device__ __forceinline__ uint32_t t_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void t_mbar_init(uint64_t *b, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(t_smem(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void t_mbar_arrive(uint64_t *b) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(t_smem(b)) : "memory");
+}
+__device__ __forceinline__ void t_mbar_expect(uint64_t *b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(t_smem(b)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool t_mbar_try(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(t_smem(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+constexpr long long kTreeWaitLimit = 4000000000ll;   // ~2 s at 2 GHz
+
+// Bounded wait.  On expiry it raises the error word and the CTA's abort flag; the
+// caller goes on through its loops (whose later waits return at once), so that
+// barriers between warps still meet.
+__device__ __forceinline__ bool t_mbar_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag, int *err) {
+    if (t_mbar_try(b, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (t_mbar_try(b, parity)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kTreeWaitLimit) {
+            *abort_flag = 1;
+            atomicExch(err, 1);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void t_tma_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            t_smem(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(t_smem(bar))
+        : "memory");
+}
+__device__ __forceinline__ void t_bulk(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     t_smem(dst)),
+                 "l"(src), "r"(bytes), "r"(t_smem(bar))
+                 : "memory");
+}
+
+// Joins the partials of the units that span CTAs: per row, in the order of the
+// CTAs (so results do not change from run to run), the largest reference, the
+// rescaled sums, then normalisation, R^T and the one rounding to the output type.
+// One warp per row.
+constexpr int kJoinWarps = 16;
+template <int IN, int D, int ROWS, int TT>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const __grid_constant__ TreeParams p,
+                                                                         int blocks_per_head) {
+    constexpr int E = D / 32;
+    __shared__ int64_t prefix[kScan + 1];
+    tree_scan<ROWS, TT>(p, prefix);
+    const int64_t total = prefix[kScan];
+    const int per_seq = p.kv_heads * blocks_per_head;
+    const int b = blockIdx.x / per_seq, hm = blockIdx.x - b * per_seq;
+    const int h = hm / blocks_per_head, mt = hm - h * blocks_per_head;
+    const TreeSeq s = tree_seq<ROWS, TT>(p, b);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.y * kJoinWarps + warp, gr = mt * ROWS + row;
+    if (mt >= s.mt || gr >= s.n * p.group) return;
+    const int per = (p.seqs + kScan - 1) / kScan;
+    int64_t first = prefix[b / per];
+    for (int i = b / per * per; i < b; ++i) {
+        const TreeSeq x = tree_seq<ROWS, TT>(p, i);
+        first += (int64_t)p.kv_heads * x.mt * x.nt;
+    }
+    first += ((int64_t)h * s.mt + mt) * s.nt;
+    // CTA of a tile: the last c with total c / ctas <= tile
+    const int c0 = (int)(((first + 1) * p.ctas - 1) / total), c1 = (int)(((first + s.nt) * p.ctas - 1) / total);
+    if (c0 == c1) return;                                   // finished in its CTA
+    const float *ml = p.part + (int64_t)2 * p.ctas * ROWS * D;
+    auto slot = [&](int c) { return (int64_t)(tree_begin(total, p.ctas, c) >= first ? 2 * c : 2 * c + 1); };
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        if (tree_begin(total, p.ctas, c) == tree_begin(total, p.ctas, c + 1)) continue;   // an empty stretch
+        top = fmaxf(top, ml[(slot(c) * ROWS + row) * 2]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float acc[E], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int base = c0; base <= c1; base += 32) {
+        const int c = base + lane;
+        float f = 0.f, l = 0.f;
+        int64_t sl = 0;
+        bool there = c <= c1 && tree_begin(total, p.ctas, c) != tree_begin(total, p.ctas, c + 1);
+        if (there) {
+            sl = slot(c);
+            const float2 x = *reinterpret_cast<const float2 *>(ml + (sl * ROWS + row) * 2);
+            there = x.x != -INFINITY;                      // an empty partial adds nothing
+            if (there) {
+                f = ex2(x.x - top);
+                l = x.y;
+            }
+        }
+        sum += l * f;
+        unsigned live = __ballot_sync(0xffffffffu, there);
+        while (live) {
+            const int k = __ffs(live) - 1;
+            live &= live - 1;
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const int64_t sk = __shfl_sync(0xffffffffu, sl, k);
+            const float *a = p.part + (sk * ROWS + row) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += fk * a[e];
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float il = sum == 0.f ? 0.f : 1.f / sum;          // nothing visible: zeros
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= il;
+    if (!(p.flags & RQ_ATTN_ROTATED_OUT)) {
+        float sg[E];
+        lane_signs<E>(sg, lane, p.seed);
+        warp_rotate<E>(acc, sg, lane, !(p.flags & RQ_SIGNS_FIRST), inv_sqrt_dim<D>());
+    }
+    const int64_t at = ((s.row0 + gr / p.group) * p.kv_heads + h) * p.group + gr % p.group;
+#pragma unroll
+    for (int e = 0; e < E; ++e) store_elem<IN>(p.out, at * D + lane * E + e, acc[e]);
+}
+
+}  // namespace
+}  // namespace rq

@@ -360,29 +360,70 @@ def w4a8_gemm(a_q: torch.Tensor, a_scales, w_q: torch.Tensor, w_scales, *, out_d
 
 # ---- rotary positions, the paged cache and the attention over it ----
 
-def _call(fn, name, device, *args, stream=None):
-    """Call a C entry point on `device` and its current (or the given) stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+# Small calls cost what their checks cost, so these entry points ask for a tensor's
+# properties once, compare device numbers, and take the raw stream handle.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def _call(fn, name, dev: int, stream, *args):
+    """Call a C entry point on device `dev` and its current (or the given) stream."""
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == _current_device():
+        st = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
     if st != 0:
         raise RQError(name, st)
 
 
+def _empty(shape, dtype, device, stream):
+    """New memory that a call on `stream` (None: the current one) writes: it has to come from that stream's pool, where
+    earlier uses are ordered before the call and later ones behind it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _one_device(*tensors) -> int:
+    dev = tensors[0].get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
 def _expect_heads(t, name: str, dtype=None, tokens=None):
-    """A [tokens][heads][head_dim] tensor: any token and head strides, unit stride inside a head."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+    """A [tokens][heads][head_dim] tensor: any token and head strides, unit stride inside a head.  Returns its shape."""
+    shape = t.shape
+    if len(shape) != 3 or (t.stride(2) != 1 and shape[2] != 1):
         raise ValueError(f"{name} must be [tokens][heads][head_dim] with unit stride in the last dimension")
-    if t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    if t.dtype not in _FLOATS:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if tokens is not None and t.shape[0] != tokens:
-        raise ValueError(f"{name}: expected {tokens} tokens, got {t.shape[0]}")
+    if tokens is not None and shape[0] != tokens:
+        raise ValueError(f"{name}: expected {tokens} tokens, got {shape[0]}")
+    return shape
+
+
+def _expect_vector(t, name: str, dtype, n: int, what: str):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {what}")
+
+
+def _expect_turns(turns, head_dim: int) -> int:
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError("turns must be a contiguous 1-D int64 tensor (rope_turns)")
+    rot = 2 * turns.shape[0]
+    if not 2 <= rot <= head_dim:
+        raise ValueError(f"turns rotate {rot} of {head_dim} elements")
+    return rot
 
 
 def rope_turns(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -430,48 +471,38 @@ def rope(q, k, positions: torch.Tensor, turns: torch.Tensor, *, interleaved: boo
     2 * len(turns) elements of each head turn by positions[token] * turns, the others pass.  Returns (q', k'), new
     contiguous tensors or the pair given as `out` (which may be (q, k): in place).  ``inverse=True`` is the transposed
     turn, the gradient of the forward one.  turns and mscale come from :func:`rope_turns`."""
-    lib = load_library()
+    lib = _lib or load_library()
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k cannot both be None")
-    T, D = ref.shape[0], ref.shape[-1]
-    oq, ok = (None, None) if out is None else out
-    args = []
-    for name, x, o in (("q", q, oq), ("k", k, ok)):
+    T, _, D = _expect_heads(ref, "q" if q is not None else "k")
+    dtype, dev = ref.dtype, ref.get_device()
+    flat, outs = [], []
+    for i, x in enumerate((q, k)):
         if x is None:
-            args.append(None)
+            flat += (None, 0, 0, 0, None, 0, 0)
+            outs.append(None)
             continue
-        _expect_heads(x, name, ref.dtype, T)
-        if x.shape[2] != D:
+        name = "qk"[i]
+        shape = _expect_heads(x, name, dtype, T)
+        if shape[2] != D:
             raise ValueError("q and k must have one head_dim")
+        o = None if out is None else out[i]
         if o is None:
-            o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _expect_heads(o, f"out ({name})", ref.dtype, T)
-            if o.shape != x.shape:
-                raise ValueError(f"out ({name}): expected shape {tuple(x.shape)}, got {tuple(o.shape)}")
-        args.append((x, o))
-    if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous int64 tensor with one entry per token")
-    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
-        raise ValueError("turns must be a contiguous 1-D int64 tensor (rope_turns)")
-    rot = 2 * turns.shape[0]
-    if not 2 <= rot <= D:
-        raise ValueError(f"turns rotate {rot} of {D} elements")
-    flat, tensors = [], [positions, turns]
-    for pair in args:
-        if pair is None:
-            flat += [None, 0, 0, 0, None, 0, 0]
-        else:
-            x, o = pair
-            tensors += pair
-            xs, os = x.stride(), o.stride()
-            flat += [x.data_ptr(), x.shape[1], xs[0], xs[1], o.data_ptr(), os[0], os[1]]
-    dev = _dev(*tensors)
-    flags = (RQ_ROPE_INTERLEAVED if interleaved else 0) | (RQ_ROPE_INVERSE if inverse else 0)
-    _call(lib.rq_rope, "rq_rope", dev, *flat, _DTYPES[ref.dtype], T, D, rot, positions.data_ptr(), turns.data_ptr(),
-          mscale, flags, stream=stream)
-    return tuple(None if pair is None else pair[1] for pair in args)
+            o = _empty(shape, dtype, x.device, stream)
+        elif _expect_heads(o, f"out ({name})", dtype, T) != shape:
+            raise ValueError(f"out ({name}): expected shape {tuple(shape)}, got {tuple(o.shape)}")
+        if x.get_device() != dev or o.get_device() != dev:
+            raise ValueError("tensors must be on one device")
+        xs, os = x.stride(), o.stride()
+        flat += (x.data_ptr(), shape[1], xs[0], xs[1], o.data_ptr(), os[0], os[1])
+        outs.append(o)
+    _expect_vector(positions, "positions", torch.int64, T, "int64 tensor with one entry per token")
+    rot = _expect_turns(turns, D)
+    _one_device(positions, turns, ref)
+    _call(lib.rq_rope, "rq_rope", dev, stream, *flat, _DTYPES[dtype], T, D, rot, positions.data_ptr(), turns.data_ptr(),
+          mscale, (RQ_ROPE_INTERLEAVED if interleaved else 0) | (RQ_ROPE_INVERSE if inverse else 0))
+    return tuple(outs)
 
 
 def kv_cache(pages: int, heads: int, head_dim: int, page_size: int = 64, device="cuda") -> dict:
@@ -485,22 +516,24 @@ def kv_cache(pages: int, heads: int, head_dim: int, page_size: int = 64, device=
 
 
 def _cache_parts(cache, head_dim=None):
+    """The cache's tensors and its shape [pages][heads][page_size][head_dim/2]."""
     kq, ks, vq, vs = cache["kq"], cache["ks"], cache["vq"], cache["vs"]
     shape = kq.shape
     if len(shape) != 4 or (head_dim is not None and shape[3] * 2 != head_dim):
         raise ValueError(f"cache['kq']: expected [pages][heads][page_size][head_dim/2], got {tuple(shape)}")
     if kq.dtype != torch.uint8 or vq.dtype != torch.uint8 or ks.dtype != torch.float32 or vs.dtype != torch.float32:
         raise ValueError("cache: codes are uint8 and scales float32")
-    if vq.shape != shape or ks.shape != shape[:3] or vs.shape != shape[:3]:
+    if vq.shape != shape or ks.shape != shape[:3] or vs.shape != ks.shape:
         raise ValueError("cache: kq and vq, ks and vs must agree in shape")
     if not (kq.is_contiguous() and ks.is_contiguous() and vq.is_contiguous() and vs.is_contiguous()):
         raise ValueError("cache tensors must be contiguous")
-    return kq, ks, vq, vs
+    return kq, ks, vq, vs, shape
 
 
-def _expect_int32(t, name, shape):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+def _expect_table(t):
+    if t.dim() != 2 or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 tensor [seqs][width]")
+    return t.shape
 
 
 def kv_append(k, v, cache: dict, slots: torch.Tensor, seed: int, flags: int = RQ_SIGNS_FIRST, *, positions=None,
@@ -508,35 +541,27 @@ def kv_append(k, v, cache: dict, slots: torch.Tensor, seed: int, flags: int = RQ
     """Quantise k and v ([tokens][heads][head_dim], strided views welcome) into the paged cache: row t goes to slot
     slots[t] = page * page_size + row (int64; outside the cache: skipped).  With positions and turns the keys take
     their rotary positions on the way (see :func:`rope`).  Returns the cache."""
-    lib = load_library()
-    _expect_heads(k, "k")
-    T, H, D = k.shape
-    _expect_heads(v, "v", k.dtype, T)
-    if v.shape != k.shape:
+    lib = _lib or load_library()
+    T, H, D = _expect_heads(k, "k")
+    dtype = k.dtype
+    if _expect_heads(v, "v", dtype, T) != k.shape:
         raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    kq, ks, vq, vs = _cache_parts(cache, D)
-    if kq.shape[1] != H:
-        raise ValueError(f"cache holds {kq.shape[1]} heads, k has {H}")
-    if slots.dtype != torch.int64 or slots.shape != (T,) or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous int64 tensor with one entry per token")
+    kq, ks, vq, vs, shape = _cache_parts(cache, D)
+    if shape[1] != H:
+        raise ValueError(f"cache holds {shape[1]} heads, k has {H}")
+    _expect_vector(slots, "slots", torch.int64, T, "int64 tensor with one entry per token")
     if (positions is None) != (turns is None):
         raise ValueError("positions and turns go together")
-    rot = 0
+    rot, pp, tp = 0, None, None
     if turns is not None:
-        if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous int64 tensor with one entry per token")
-        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
-            raise ValueError("turns must be a contiguous 1-D int64 tensor (rope_turns)")
-        rot = 2 * turns.shape[0]
-        if not 2 <= rot <= D:
-            raise ValueError(f"turns rotate {rot} of {D} elements")
-    dev = _dev(k, v, kq, ks, vq, vs, slots, positions, turns)
+        _expect_vector(positions, "positions", torch.int64, T, "int64 tensor with one entry per token")
+        rot, pp, tp = _expect_turns(turns, D), positions.data_ptr(), turns.data_ptr()
+    dev = _one_device(k, v, kq, ks, vq, vs, slots, positions, turns)
     kst, vst = k.stride(), v.stride()
-    _call(lib.rq_kv_append, "rq_kv_append", dev, k.data_ptr(), kst[0], kst[1], v.data_ptr(), vst[0], vst[1],
-          _DTYPES[k.dtype], T, H, D, slots.data_ptr(), None if turns is None else positions.data_ptr(),
-          None if turns is None else turns.data_ptr(), rot, mscale, seed,
-          flags | (RQ_ROPE_INTERLEAVED if interleaved else 0), kq.data_ptr(), ks.data_ptr(), vq.data_ptr(),
-          vs.data_ptr(), kq.shape[0], kq.shape[2], stream=stream)
+    _call(lib.rq_kv_append, "rq_kv_append", dev, stream, k.data_ptr(), kst[0], kst[1], v.data_ptr(), vst[0], vst[1],
+          _DTYPES[dtype], T, H, D, slots.data_ptr(), pp, tp, rot, mscale, seed,
+          flags | RQ_ROPE_INTERLEAVED if interleaved else flags, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(),
+          vs.data_ptr(), shape[0], shape[2])
     return cache
 
 
@@ -546,29 +571,30 @@ def kv_read(cache: dict, block_table: torch.Tensor, starts, offsets: torch.Tenso
     the original basis, or the rotated one with RQ_KV_ROTATED_OUT in flags.  block_table [seqs][width] int32; starts
     [seqs] int32 (first token wanted; None: 0); offsets [seqs + 1] int32: sequence b fills rows offsets[b] to
     offsets[b + 1] - 1; rows at or past offsets[seqs] are left as they are."""
-    lib = load_library()
-    kq, ks, vq, vs = _cache_parts(cache)
-    pages, H, page, half = kq.shape
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [seqs][width]")
-    B, W = block_table.shape
-    _expect_int32(block_table, "block_table", (B, W))
-    _expect_int32(offsets, "offsets", (B + 1,))
+    lib = _lib or load_library()
+    kq, ks, vq, vs, shape = _cache_parts(cache)
+    pages, H, page, half = shape
+    B, W = _expect_table(block_table)
+    _expect_vector(offsets, "offsets", torch.int32, B + 1, "int32 tensor [seqs + 1]")
     if starts is not None:
-        _expect_int32(starts, "starts", (B,))
-    if dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        _expect_vector(starts, "starts", torch.int32, B, "int32 tensor [seqs]")
+    if dtype not in _FLOATS:
         raise ValueError("dtype must be float32, bfloat16 or float16")
     if out is None:
-        out = (torch.empty(total, H, 2 * half, dtype=dtype, device=kq.device),
-               torch.empty(total, H, 2 * half, dtype=dtype, device=kq.device))
-    ko, vo = out
-    _expect(ko, "out (k)", (total, H, 2 * half), dtype)
-    _expect(vo, "out (v)", (total, H, 2 * half), dtype)
-    dev = _dev(kq, ks, vq, vs, block_table, starts, offsets, ko, vo)
-    _call(lib.rq_kv_read, "rq_kv_read", dev, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages, H, page,
-          2 * half, block_table.data_ptr(), W, None if starts is None else starts.data_ptr(), offsets.data_ptr(), B,
-          total, seed, flags, ko.data_ptr(), vo.data_ptr(), _DTYPES[dtype], stream=stream)
+        ko = _empty((total, H, 2 * half), dtype, kq.device, stream)
+        vo = _empty((total, H, 2 * half), dtype, kq.device, stream)
+    else:
+        ko, vo = out
+        _expect(ko, "out (k)", (total, H, 2 * half), dtype)
+        _expect(vo, "out (v)", (total, H, 2 * half), dtype)
+    dev = _one_device(kq, ks, vq, vs, block_table, starts, offsets, ko, vo)
+    _call(lib.rq_kv_read, "rq_kv_read", dev, stream, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages,
+          H, page, 2 * half, block_table.data_ptr(), W, None if starts is None else starts.data_ptr(),
+          offsets.data_ptr(), B, total, seed, flags, ko.data_ptr(), vo.data_ptr(), _DTYPES[dtype])
     return ko, vo
+
+
+_workspace_bytes: dict = {}     # by device and head_dim: a size, asked for once
 
 
 def attn_tree_workspace(head_dim: int) -> int:
@@ -585,50 +611,47 @@ def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_l
     tree_mask (bool [rows][width], width >= the largest tree) names; without a mask, itself and those before it.
     max_nodes bounds the nodes of a sequence (default: the mask's width, or the number of rows).  One node per sequence
     is a plain decode step.  Returns [rows][q_heads][head_dim] of q's dtype; rows that see nothing are 0."""
-    lib = load_library()
-    _expect_heads(q, "q")
-    N, Hq, D = q.shape
-    kq, ks, vq, vs = _cache_parts(cache, D)
-    pages, H, page, _ = kq.shape
-    if Hq % H:
-        raise ValueError(f"{Hq} query heads do not divide over {H} KV heads")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [seqs][width]")
-    B, W = block_table.shape
-    _expect_int32(block_table, "block_table", (B, W))
-    _expect_int32(context_lens, "context_lens", (B,))
-    _expect_int32(offsets, "offsets", (B + 1,))
+    lib = _lib or load_library()
+    N, Hq, D = _expect_heads(q, "q")
+    dtype = q.dtype
+    kq, ks, vq, vs, shape = _cache_parts(cache, D)
+    if Hq % shape[1]:
+        raise ValueError(f"{Hq} query heads do not divide over {shape[1]} KV heads")
+    B, W = _expect_table(block_table)
+    _expect_vector(context_lens, "context_lens", torch.int32, B, "int32 tensor [seqs]")
+    _expect_vector(offsets, "offsets", torch.int32, B + 1, "int32 tensor [seqs + 1]")
     mask_ptr, mask_stride = None, 0
     if tree_mask is not None:
-        if tree_mask.dtype != torch.bool or tree_mask.dim() != 2 or tree_mask.shape[0] != N or tree_mask.stride(1) != 1:
+        ms = tree_mask.shape
+        if tree_mask.dtype != torch.bool or len(ms) != 2 or ms[0] != N or (tree_mask.stride(1) != 1 and ms[1] > 1):
             raise ValueError("tree_mask must be bool [rows][width] with unit stride in the last dimension")
-        mask_ptr, mask_stride = tree_mask.data_ptr(), tree_mask.stride(0)
+        mask_ptr = tree_mask.data_ptr()
+        mask_stride = tree_mask.stride(0) if N > 1 else ms[1]     # the stride of a single row says nothing
         if max_nodes is None:
-            max_nodes = tree_mask.shape[1]
-        elif max_nodes > tree_mask.shape[1]:
+            max_nodes = ms[1]
+        elif max_nodes > ms[1]:
             raise ValueError("tree_mask is narrower than max_nodes")
-        if N <= 1:
-            mask_stride = tree_mask.shape[1]      # one row: its stride says nothing
     elif max_nodes is None:
         max_nodes = N
     if out is None:
-        out = torch.empty(N, Hq, D, dtype=q.dtype, device=q.device)
+        out = _empty((N, Hq, D), dtype, q.device, stream)
     else:
-        _expect(out, "out", (N, Hq, D), q.dtype)
-    dev = _dev(q, kq, ks, vq, vs, block_table, context_lens, offsets, tree_mask, out, workspace)
-    if softmax_scale is None:
-        softmax_scale = D ** -0.5
+        _expect(out, "out", (N, Hq, D), dtype)
+    dev = _one_device(q, kq, ks, vq, vs, block_table, context_lens, offsets, tree_mask, out, workspace)
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = lib.rq_attn_tree_workspace(D)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        need = _workspace_bytes.get((dev, D))
+        if need is None:
+            with torch.cuda.device(dev):
+                need = _workspace_bytes[dev, D] = lib.rq_attn_tree_workspace(D)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     qs = q.stride()
-    _call(lib.rq_attn_tree, "rq_attn_tree", dev, q.data_ptr(), qs[0], qs[1], _DTYPES[q.dtype], N, Hq, D, kq.data_ptr(),
-          ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages, H, page, block_table.data_ptr(), W,
-          context_lens.data_ptr(), offsets.data_ptr(), B, max_nodes, mask_ptr, mask_stride, seed, flags, softmax_scale,
-          out.data_ptr(), workspace.data_ptr(), workspace.numel(), stream=stream)
+    _call(lib.rq_attn_tree, "rq_attn_tree", dev, stream, q.data_ptr(), qs[0], qs[1], _DTYPES[dtype], N, Hq, D,
+          kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2],
+          block_table.data_ptr(), W, context_lens.data_ptr(), offsets.data_ptr(), B, max_nodes, mask_ptr, mask_stride,
+          seed, flags, D ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
     return out
 
 

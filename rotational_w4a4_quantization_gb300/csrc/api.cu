@@ -34,8 +34,13 @@ bool is_rot_input(rq_dtype t) { return t == RQ_F32 || t == RQ_BF16 || t == RQ_F1
 }  // namespace
 
 int *error_word_device_ptr() {
+    static std::atomic<int *> known[kMaxDevices];   // the word's address on each device
+    int dev = 0;
     int *p = nullptr;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    if (dev < kMaxDevices && (p = known[dev].load(std::memory_order_relaxed))) return p;
     if (cudaGetSymbolAddress(reinterpret_cast<void **>(&p), g_error_word) != cudaSuccess) return nullptr;
+    if (dev < kMaxDevices) known[dev].store(p, std::memory_order_relaxed);
     return p;
 }
 

@@ -480,7 +480,8 @@ template <int IN, int D>
 cudaError_t launch_tree_d(TreeParams &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
     auto kern = attn_tree_mma_kernel<IN, D>;
     const size_t smem = sizeof(MSmem<IN, D>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_smem((const void *)kern, smem, allowed);
     if (e != cudaSuccess) return e;
     kern<<<p.ctas, kMThreads, smem, stream>>>(mk, mv, p);
     e = cudaGetLastError();
@@ -506,51 +507,24 @@ cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, cons
 
 int64_t attn_tree_workspace(int64_t head_dim) {
     const int64_t ctas = 2 * (int64_t)device_sm_count();
-    return 2 * ctas * kRows * (head_dim + 2) * (int64_t)sizeof(float);
+    const int64_t small = 2 * ctas * kRows * (head_dim + 2) * (int64_t)sizeof(float);
+    const int64_t wide = attn_tree_tc_workspace(head_dim);
+    return small > wide ? small : wide;
 }
 
 cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
-    TreeParams p{};
-    p.q = c.q;
-    p.q_token = c.q_token;
-    p.q_head = c.q_head;
-    p.ks = c.cache.ks;
-    p.vs = c.cache.vs;
-    p.table = c.table;
-    p.contexts = c.contexts;
-    p.offsets = c.offsets;
-    p.mask = c.mask;
-    p.mask_stride = c.mask_stride;
-    p.width = c.width;
-    p.rows = c.rows;
-    p.pages = c.cache.pages;
-    p.seqs = (int)c.seqs;
-    p.kv_heads = (int)c.cache.heads;
-    p.group = (int)(c.q_heads / c.cache.heads);
-    while ((int64_t(1) << p.log_page) < c.cache.page_size) ++p.log_page;
-    p.max_nodes = (int)c.max_nodes;
-    p.seed = c.seed;
-    p.flags = c.flags;
-    p.score_scale = (float)((double)c.softmax_scale * 1.4426950408889634);
-    p.out = c.out;
-    p.part = static_cast<float *>(c.workspace);
-    p.err = error_word_device_ptr();
-    if (!p.err) return cudaErrorUnknown;
+    if (attn_tree_tc_supported(c.in_type, c.head_dim, c.max_nodes * (c.q_heads / c.cache.heads)))
+        return launch_attn_tree_tc(c, stream);
+    TreeParams p;
+    if (!tree_params(c, p)) return cudaErrorUnknown;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorUnknown;
     const int per_sm = c.in_type == IN_F32 || c.head_dim == 256 ? 1 : 2;
     const int64_t bph = (c.max_nodes * p.group + kRows - 1) / kRows;
     const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTT - 1) / kTT);
     p.ctas = (int)(max_tiles < per_sm * sms ? max_tiles : per_sm * sms);
-    const int64_t rows = c.cache.pages * c.cache.heads * c.cache.page_size;
-    const int rb = (int)(c.head_dim / 2), box = (int)(c.cache.page_size < kTT ? c.cache.page_size : kTT);
-    const CUtensorMapSwizzle sw = rb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                  : rb == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                             : CU_TENSOR_MAP_SWIZZLE_NONE;
     CUtensorMap mk, mv;
-    if (!make_tma_map_u8(&mk, c.cache.kq, rows, rb, rb, box, sw) || !make_tma_map_u8(&mv, c.cache.vq, rows, rb, rb, box, sw))
-        return cudaErrorInvalidValue;
+    if (!tree_maps(c, kTT, mk, mv)) return cudaErrorInvalidValue;
     switch (c.in_type) {
         case IN_F32: return launch_tree_in<IN_F32>(p, c.head_dim, mk, mv, stream);
         case IN_BF16: return launch_tree_in<IN_BF16>(p, c.head_dim, mk, mv, stream);

@@ -314,7 +314,8 @@ cudaError_t launch_kv_append(const KvRows &k, const KvRows &v, int in_type, int6
     // about two passes of the block's 32 rows (16 at D = 256) per block, more blocks while SMs would idle
     p.tb = (int)((64 + 2 * c.heads - 1) / (2 * c.heads));
     if (p.tb > kMaxTok) p.tb = kMaxTok;
-    while (p.tb > 1 && tokens / p.tb < 2 * device_sm_count()) p.tb /= 2;
+    const int64_t want = 8 * (int64_t)device_sm_count();
+    while (p.tb > 1 && tokens / p.tb < want) p.tb /= 2;
     if ((tokens + p.tb - 1) / p.tb > 0x7fffffffll) return cudaErrorInvalidValue;
     const bool rope = turns != nullptr;
     switch (in_type) {
@@ -346,7 +347,8 @@ cudaError_t launch_kv_read(const PagedCache &c, int64_t head_dim, const int32_t 
     p.seed = seed;
     p.flags = flags;
     p.tb = kMaxTok;
-    while (p.tb > 1 && total / p.tb < 2 * device_sm_count()) p.tb /= 2;
+    const int64_t want = 8 * (int64_t)device_sm_count();
+    while (p.tb > 1 && total / p.tb < want) p.tb /= 2;
     if ((total + p.tb - 1) / p.tb > 0x7fffffffll) return cudaErrorInvalidValue;
     switch (out_type) {
         case IN_F32: return launch_read_out<IN_F32>(p, head_dim, stream);

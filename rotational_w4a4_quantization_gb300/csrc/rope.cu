@@ -53,55 +53,70 @@ __global__ void __launch_bounds__(kRThreads) rope_kernel(const __grid_constant__
     // element offsets of this thread's piece(s) in a row
     const int ea = turn ? it * VE : 2 * p.half + (it - p.rot_items) * VE;
     const int eb = ea + p.half;
-    for (int r = r0; r < nt * heads; r += rpp) {
-        const int tk = r / heads;
-        int h = r - tk * heads;
-        const bool second = h >= p.t[0].heads;
-        const RopeView &v = p.t[second];
-        if (second) h -= (int)p.t[0].heads;
-        const char *src = static_cast<const char *>(v.src) + ((tok0 + tk) * v.src_token + h * v.src_head) * ES;
-        char *dst = static_cast<char *>(v.dst) + ((tok0 + tk) * v.dst_token + h * v.dst_head) * ES;
-        const float2 *c = cs + tk * p.half;
+    const int rows = nt * heads;
+    constexpr int U = VEC ? 4 : 1;                        // rows in flight per thread
+    for (int rb = r0; rb < rows; rb += U * rpp) {
+        const char *src[U];
+        char *dst[U];
+        const float2 *c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = rb + u * rpp;
+            const int tk = r / heads;
+            int h = r - tk * heads;
+            const bool second = h >= p.t[0].heads;
+            const RopeView &v = p.t[second];
+            if (second) h -= (int)p.t[0].heads;
+            src[u] = static_cast<const char *>(v.src) + ((tok0 + tk) * v.src_token + h * v.src_head) * ES;
+            dst[u] = static_cast<char *>(v.dst) + ((tok0 + tk) * v.dst_token + h * v.dst_head) * ES;
+            c[u] = cs + tk * p.half;
+        }
         if constexpr (VEC) {
-            if (!turn) {
-                *reinterpret_cast<uint4 *>(dst + ea * ES) = *reinterpret_cast<const uint4 *>(src + ea * ES);
-                continue;
-            }
-            // the piece's elements as fp32 (fp32 rows: 4 elements of the 8 slots)
-            float a[VE], b[VE];
-            const uint4 ra = *reinterpret_cast<const uint4 *>(src + ea * ES);
-            unpack16<IN>(ra, a);
-            if constexpr (!INTER) {
-                unpack16<IN>(*reinterpret_cast<const uint4 *>(src + eb * ES), b);
-                float oa[VE], ob[VE];
+            uint4 ra[U], rc[U];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    const float2 w = c[ea + e];
-                    oa[e] = a[e] * w.x - b[e] * w.y;
-                    ob[e] = a[e] * w.y + b[e] * w.x;
+            for (int u = 0; u < U; ++u)
+                if (rb + u * rpp < rows) {
+                    ra[u] = *reinterpret_cast<const uint4 *>(src[u] + ea * ES);
+                    if (!INTER && turn) rc[u] = *reinterpret_cast<const uint4 *>(src[u] + eb * ES);
                 }
-                *reinterpret_cast<uint4 *>(dst + ea * ES) = pack16<IN>(oa);
-                *reinterpret_cast<uint4 *>(dst + eb * ES) = pack16<IN>(ob);
-            } else {
 #pragma unroll
-                for (int e = 0; e < VE; e += 2) {
-                    const float2 w = c[(ea + e) / 2];
-                    b[e] = a[e] * w.x - a[e + 1] * w.y;
-                    b[e + 1] = a[e] * w.y + a[e + 1] * w.x;
+            for (int u = 0; u < U; ++u) {
+                if (rb + u * rpp >= rows) break;
+                if (!turn) {
+                    *reinterpret_cast<uint4 *>(dst[u] + ea * ES) = ra[u];
+                    continue;
                 }
-                *reinterpret_cast<uint4 *>(dst + ea * ES) = pack16<IN>(b);
+                float a[VE], b[VE], oa[VE], ob[VE];
+                unpack16<IN>(ra[u], a);
+                if constexpr (!INTER) {
+                    unpack16<IN>(rc[u], b);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float2 w = c[u][ea + e];
+                        oa[e] = a[e] * w.x - b[e] * w.y;
+                        ob[e] = a[e] * w.y + b[e] * w.x;
+                    }
+                    *reinterpret_cast<uint4 *>(dst[u] + ea * ES) = pack16<IN>(oa);
+                    *reinterpret_cast<uint4 *>(dst[u] + eb * ES) = pack16<IN>(ob);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VE; e += 2) {
+                        const float2 w = c[u][(ea + e) / 2];
+                        oa[e] = a[e] * w.x - a[e + 1] * w.y;
+                        oa[e + 1] = a[e] * w.y + a[e + 1] * w.x;
+                    }
+                    *reinterpret_cast<uint4 *>(dst[u] + ea * ES) = pack16<IN>(oa);
+                }
             }
+        } else if (!turn) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) store_elem<IN>(dst[0], ea + e, load_elem<IN>(src[0], ea + e));
         } else {
-            if (!turn) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) store_elem<IN>(dst, ea + e, load_elem<IN>(src, ea + e));
-                continue;
-            }
             const int ia = ea, ib = INTER ? ea + 1 : eb;
-            const float a = load_elem<IN>(src, ia), b = load_elem<IN>(src, ib);
-            const float2 w = c[it];
-            store_elem<IN>(dst, ia, a * w.x - b * w.y);
-            store_elem<IN>(dst, ib, a * w.y + b * w.x);
+            const float a = load_elem<IN>(src[0], ia), b = load_elem<IN>(src[0], ib);
+            const float2 w = c[0][it];
+            store_elem<IN>(dst[0], ia, a * w.x - b * w.y);
+            store_elem<IN>(dst[0], ib, a * w.y + b * w.x);
         }
     }
 }
@@ -112,10 +127,11 @@ cudaError_t launch_rope_in(RParams &p, bool inter, bool vec, int rot, cudaStream
     p.rot_items = (inter ? rot : rot / 2) / ve;
     p.items = p.rot_items + (p.head_dim - rot) / ve;
     // as many tokens per block as there are threads for their pairs, fewer while
-    // the grid would leave SMs idle
-    p.tb = p.half ? kRThreads / p.half : 4;
+    // that leaves SMs without a full set of blocks
+    const int64_t want = 8 * (int64_t)device_sm_count();
+    p.tb = kRThreads / p.half;
     if (p.tb < 1) p.tb = 1;
-    while (p.tb > 1 && p.tokens / p.tb < 2 * device_sm_count()) p.tb /= 2;
+    while (p.tb > 1 && p.tokens / p.tb < want) p.tb /= 2;
     const int64_t blocks = (p.tokens + p.tb - 1) / p.tb;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     const size_t smem = sizeof(float2) * p.tb * p.half;

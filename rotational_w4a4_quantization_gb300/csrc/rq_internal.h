@@ -2,11 +2,26 @@
 // translation units.  Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace rq {
+
+constexpr int kMaxDevices = 64;   // devices whose attributes are remembered; others are asked each time
+
+// Allows a kernel `bytes` of dynamic shared memory: once per device, remembered in
+// `done` (one per kernel, one bit per device).
+inline cudaError_t allow_smem(const void *kern, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices && (done.load(std::memory_order_relaxed) >> dev) & 1) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < kMaxDevices) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
 
 // Element types of rotation inputs (values match rq_dtype).
 enum InType : int { IN_F32 = 0, IN_BF16 = 1, IN_F16 = 2 };
@@ -126,6 +141,11 @@ struct TreeCall {
 };
 int64_t attn_tree_workspace(int64_t head_dim);
 cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream);
+// Blocks of 128 or 256 rows on the tensor cores: 16-bit queries, head_dim 64 or 128,
+// more than 16 rows (nodes x query heads per KV head).
+bool attn_tree_tc_supported(int in_type, int64_t head_dim, int64_t rows);
+int64_t attn_tree_tc_workspace(int64_t head_dim);
+cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream);
 
 // W4A8 product: INT8 activations, INT4 weights, per-channel (group == K) or
 // per-group (group == 128) weight scales.  Per-channel scales with more than 64

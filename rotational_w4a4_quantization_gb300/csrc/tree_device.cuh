@@ -31,6 +31,46 @@ struct TreeParams {
     int *err;
 };
 
+// Host side: the parameters that do not depend on the kernel, and TMA maps whose boxes
+// are whole pages, or a tile's worth of a larger page.
+inline bool tree_params(const TreeCall &c, TreeParams &p) {
+    p = TreeParams{};
+    p.q = c.q;
+    p.q_token = c.q_token;
+    p.q_head = c.q_head;
+    p.ks = c.cache.ks;
+    p.vs = c.cache.vs;
+    p.table = c.table;
+    p.contexts = c.contexts;
+    p.offsets = c.offsets;
+    p.mask = c.mask;
+    p.mask_stride = c.mask_stride;
+    p.width = c.width;
+    p.rows = c.rows;
+    p.pages = c.cache.pages;
+    p.seqs = (int)c.seqs;
+    p.kv_heads = (int)c.cache.heads;
+    p.group = (int)(c.q_heads / c.cache.heads);
+    while ((int64_t(1) << p.log_page) < c.cache.page_size) ++p.log_page;
+    p.max_nodes = (int)c.max_nodes;
+    p.seed = c.seed;
+    p.flags = c.flags;
+    p.score_scale = (float)((double)c.softmax_scale * 1.4426950408889634);
+    p.out = c.out;
+    p.part = static_cast<float *>(c.workspace);
+    p.err = error_word_device_ptr();
+    return p.err != nullptr;
+}
+inline bool tree_maps(const TreeCall &c, int tile, CUtensorMap &mk, CUtensorMap &mv) {
+    const int64_t rows = c.cache.pages * c.cache.heads * c.cache.page_size;
+    const int rb = (int)(c.head_dim / 2), box = (int)(c.cache.page_size < tile ? c.cache.page_size : tile);
+    const CUtensorMapSwizzle sw = rb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : rb == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                             : CU_TENSOR_MAP_SWIZZLE_NONE;
+    return make_tma_map_u8(&mk, c.cache.kq, rows, rb, rb, box, sw) && make_tma_map_u8(&mv, c.cache.vq, rows, rb, rb, box, sw);
+}
+
 struct TreeSeq {
     int64_t row0;      // first query row
     int ctx, n, len;   // tokens before the tree, nodes, tokens in all

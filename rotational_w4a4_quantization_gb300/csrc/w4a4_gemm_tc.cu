@@ -79,6 +79,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstring>
 
 namespace rq {
@@ -1222,11 +1223,14 @@ bool make_map(CUtensorMap *map, const void *base, int64_t rows, int64_t row_byte
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// SM count of the current device (0 on error).
+// SM count of the current device (0 on error), asked for once per device.
 int sm_count() {
+    static std::atomic<int> known[kMaxDevices];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 

@@ -108,3 +108,30 @@ def tree_mask(counts, generator, width=None):
             m[at + i, i] = True
         at += n
     return m
+
+
+def attention_blocks(q, cache, table, contexts, offsets, seed, flags, scale, mask=None):
+    """attention() for larger cases: a sequence at a time, all heads and nodes at once.  Needs valid pages and at least
+    one visible token in every row.  Returns (out, spread, delta) as attention() does."""
+    q = q.double()
+    N, Hq, D = q.shape
+    H, page = cache["kq"].shape[1], cache["kq"].shape[2]
+    R = rotation(D, seed, flags & 1).to(q.device)
+    out, spread, delta = torch.zeros_like(q), torch.zeros_like(q), torch.zeros(N, Hq, dtype=torch.float64, device=q.device)
+    for b in range(table.shape[0]):
+        r0, r1, c = int(offsets[b]), int(offsets[b + 1]), int(contexts[b])
+        n, L = r1 - r0, c + r1 - r0
+        if n == 0:
+            continue
+        pg, row = (x.to(q.device) for x in places(table, page, b, L))
+        k = decode(cache["kq"][pg, :, row], cache["ks"][pg, :, row]).transpose(0, 1)      # [H][L][D]
+        v = decode(cache["vq"][pg, :, row], cache["vs"][pg, :, row]).transpose(0, 1)
+        seen = torch.ones(n, L, dtype=torch.bool, device=q.device)
+        seen[:, c:] = torch.ones(n, n, dtype=torch.bool).tril().to(q.device) if mask is None else mask[r0:r1, :n].to(q.device)
+        qr = (q[r0:r1] @ R).view(n, H, Hq // H, D)
+        s = torch.einsum("nhgd,hld->nhgl", qr, k) * scale
+        p = torch.softmax(s.masked_fill(~seen[:, None, None, :], -math.inf), -1)
+        out[r0:r1] = (torch.einsum("nhgl,hld->nhgd", p, v) @ R.T).reshape(n, Hq, D)
+        spread[r0:r1] = torch.einsum("nhgl,hld->nhgd", p, v.abs()).reshape(n, Hq, D)
+        delta[r0:r1] = (torch.einsum("nhgd,hld->nhgl", qr ** 2, k ** 2).amax(-1).sqrt() * abs(scale)).reshape(n, Hq)
+    return out, spread, delta

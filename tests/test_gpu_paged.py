@@ -503,3 +503,34 @@ def test_verification_step_end_to_end():
         want = torch.softmax(s.masked_fill(~seen, -np.inf), -1) @ vd[:, h // G].double()
         err = (out[:, h].double() - want).norm(dim=-1) / want.norm(dim=-1)
         assert err.max() < 6e-3           # bf16 rounding up to 2^-8 of each element, weights 2^-11
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,H,G,n,context,D,page", [
+    (64, 8, 2, 10, 200, 128, 16),      # whole blocks of rows and pieces of them in one thread block
+    (16, 8, 2, 12, 1300, 64, 32),      # stretches of many tiles
+    (5, 4, 8, 40, 1500, 128, 64),      # more than 256 rows
+    (24, 2, 4, 33, 700, 128, 256),     # a little more than 128 rows
+    (40, 8, 1, 3, 900, 64, 64),        # few rows
+    (9, 4, 4, 1, 5000, 128, 128),      # single tokens
+])
+def test_tree_many_tiles(dtype, B, H, G, n, context, D, page):
+    """More tiles than thread blocks: stretches that begin and end inside sequences, heads and row blocks."""
+    g = gen(150 + B)
+    contexts = (torch.rand(B, generator=g) * context).to(torch.int32).tolist()
+    counts = torch.randint(max(1, n - 3), n + 1, (B,), generator=g).tolist()
+    counts[0] = n
+    cache, table = paged([c + k for c, k in zip(contexts, counts)], H, page, D, 151)
+    cache, table = dev_cache(cache), table.to(DEV)
+    mask = ref.tree_mask(counts, g).to(DEV)
+    q = randn(sum(counts), H * G, D, seed=152, dtype=dtype).to(DEV)
+    offsets = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device=DEV)
+    ctx = torch.tensor(contexts, dtype=torch.int32, device=DEV)
+    want, spread, delta = ref.attention_blocks(q, cache, table, contexts, offsets, SEED, 1, D ** -0.5, mask)
+    got = rq.attn_tree(q, cache, table, ctx, offsets, SEED, 1, tree_mask=mask)
+    part = 2.0**-22 if dtype == torch.float32 else 2.0**-12
+    eps = 8e-6 + 2 * part + 2 * (4 / 3) * part * delta
+    bound = eps * spread.norm(dim=-1) + ref.UNIT[dtype] * want.norm(dim=-1) + (2.0**-25 * D**0.5 if dtype == torch.float16 else 0)
+    err = (got.double() - want).norm(dim=-1)
+    assert (err <= bound).all(), float((err / bound).max())
+    assert torch.equal(got, rq.attn_tree(q, cache, table, ctx, offsets, SEED, 1, tree_mask=mask))

@@ -12,11 +12,11 @@
 //   NT = 1: 128 rows; team w takes the tiles of parity w with an accumulator of its
 //           own, and the two are joined at the end.
 //
-// Roles (20 warps, one block per SM):
+// Roles (16 warps, one block per SM):
 //   warp 0       TMA: packed code tiles (8 KB each at D = 128) and scales
 //   warp 1       tensor memory, all MMAs (one lane)
 //   warps 4-11   softmax teams
-//   warps 12-19  converters: packed codes -> fp16 codes (exact) in the 128-byte-
+//   warps 12-15  converters: packed codes -> fp16 codes (exact) in the 128-byte-
 //                swizzled operand layout.  One layout serves both products: rows of
 //                64 dims per token are K-major for Q K^T and MN-major for P V.
 // Tensor memory, 512 columns: S0 S1 (128 each; P overwrites the first half of its S)
@@ -40,7 +40,7 @@ namespace {
 constexpr int kTcTT = 128;               // tokens per tile
 constexpr int kOps = 3;                  // operand slots
 constexpr int kSc = 4;                   // scale slots
-constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kTcThreads = 32 * (4 + kSoftWarps + kConvWarps);
 
 template <int D, int NT, int HV>
@@ -54,7 +54,7 @@ struct TSmem {
     alignas(1024) uint8_t rawt[RAW][kTcTT * RB];
     alignas(16) float ks[kSc][kTcTT];
     alignas(16) float vs[kSc][kTcTT];
-    float rscale[NT * 128];
+    float2 rfac[NT * 128];                                  // a row's factors: s = (a S + b) ks
     float ref[2][128], sum[2][128];                         // NT = 1: the teams' references and sums
     int64_t prefix[kScan + 1];
     alignas(8) uint64_t raw_full[RAW], raw_empty[RAW];
@@ -111,6 +111,9 @@ __device__ __forceinline__ void tm_ld32(uint32_t t, uint32_t *r) {
                  "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
                  : RQ_R8(r, 0), RQ_R8(r, 8), RQ_R8(r, 16), RQ_R8(r, 24) : "r"(t));
 }
+__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), RQ_W8(r, 0) : "memory");
+}
 __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
                  RQ_W8(r, 0), RQ_W8(r, 8) : "memory");
@@ -159,10 +162,32 @@ __device__ __forceinline__ int item_of_k(int k) { return NT == 2 ? 2 * k : (k ==
 template <int NT>
 __device__ __forceinline__ int item_of_v(int k, int T) { return NT == 2 ? 2 * k + 1 : (k == T - 1 ? 2 * T - 1 : 2 * k + 2); }
 
-__device__ __forceinline__ uint32_t nibbles_fp16(uint32_t x, int j) {
-    const uint32_t t = ((x >> (4 * j)) & 0x000f000fu) | 0x64006400u;       // 1024 + code + 8, twice
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&t), __half2half2(__ushort_as_half(0x6408)));
-    return *reinterpret_cast<const uint32_t *>(&h);
+// A word of 8 codes as 8 fp16 operands, in the order of the dims 0 4 1 5 2 6 3 7.
+// Values: 0x6400 | u is 1024 + u, so nibbles 0 and 4 (u = code + 8 after the sign bit's
+// flip) lose 1032, nibbles 1 and 5, which stay four bits up, are 1024 + 16 u: times
+// 1/16, less 72.  Exact.
+__device__ __forceinline__ uint4 v_operands(uint32_t x) {
+    const __half2 m0 = __half2half2(__ushort_as_half(0xe408)), r16 = __half2half2(__ushort_as_half(0x2c00)),
+                  m1 = __half2half2(__ushort_as_half(0xd480));             // -1032, 1/16, -72
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        const uint32_t y = x >> (4 * j);
+        const uint32_t a = (y & 0x000f000fu) ^ 0x64086408u, b = (y & 0x00f000f0u) ^ 0x64806480u;
+        const __half2 ha = __hadd2(*reinterpret_cast<const __half2 *>(&a), m0);
+        const __half2 hb = __hfma2(*reinterpret_cast<const __half2 *>(&b), r16, m1);
+        r[j] = *reinterpret_cast<const uint32_t *>(&ha);
+        r[j + 1] = *reinterpret_cast<const uint32_t *>(&hb);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// Keys: no arithmetic.  u = code + 8 as the subnormal u 2^-24 (nibbles 1, 3, 5, 7:
+// 16 u 2^-24, and q~ holds a sixteenth there); the softmax takes 2^24 and 8 sum q~ out
+// again with the row's factors.  The sums are short (D terms), so nothing is lost.
+__device__ __forceinline__ uint4 k_operands(uint32_t x) {
+    const uint32_t y = x >> 8;
+    return make_uint4((x ^ 0x00080008u) & 0x000f000fu, (x ^ 0x00800080u) & 0x00f000f0u,
+                      (y ^ 0x00080008u) & 0x000f000fu, (y ^ 0x00800080u) & 0x00f000f0u);
 }
 __device__ __forceinline__ float lg2(float x) {
     float y;
@@ -171,8 +196,167 @@ __device__ __forceinline__ float lg2(float x) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+// t_mbar_wait by a whole warp, with one answer
+__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag, int *err) {
+    return __all_sync(0xffffffffu, t_mbar_wait(b, parity, abort_flag, err));
+}
+
 // position p of an 8-group of operand columns holds dim kPerm(p) of the group
 __device__ __forceinline__ constexpr int perm8(int p) { return (p & 1) * 4 + (p >> 1); }
+
+// Which of the tokens t .. t + 15 (rows at .. of a tile with page pieces `valid`) a node
+// sees, as bits.  The mask bytes are loaded all at once.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 16 ? 0xffffu : (1u << n) - 1u); }
+__device__ __forceinline__ uint32_t tree_visible(const TreeParams &p, const TreeWork &w, int node, int t, int at, uint32_t valid) {
+    if (node >= w.s.n || !((valid >> (at >> min(p.log_page, 7))) & 1)) return 0u;
+    const uint32_t there = below(w.s.len - t);
+    const int j0 = t - w.s.ctx;                                   // the node at token t
+    if (!p.mask) return there & below(node + 1 - j0);
+    uint32_t seen = below(-j0);
+    if (j0 + 16 > 0 && j0 < w.s.n) {
+        const uint8_t *m = p.mask + (w.s.row0 + node) * p.mask_stride + j0;
+        uint8_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = (unsigned)(j0 + i) < (unsigned)w.s.n ? m[i] : (uint8_t)0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) seen |= x[i] ? 1u << i : 0u;
+    }
+    return there & seen;
+}
+
+constexpr int kCW = 16;                  // scores that a row works on at a time: more of them spill
+
+// A row's kCW raw scores -> s - M, with s = (a S + b) ks.
+__device__ __forceinline__ void soft_scores(const uint32_t (&sr)[kCW], const float *ks, float2 fac, float M,
+                                            float2 (&t)[kCW / 2]) {
+    const float2 a2 = make_float2(fac.x, fac.x), b2 = make_float2(fac.y, fac.y), nm = make_float2(-M, -M);
+    const float4 *k4 = reinterpret_cast<const float4 *>(ks);
+#pragma unroll
+    for (int i = 0; i < kCW / 4; ++i) {
+        const float4 k = k4[i];
+        const float2 x = make_float2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1]));
+        const float2 y = make_float2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3]));
+        t[2 * i] = __ffma2_rn(__ffma2_rn(x, a2, b2), make_float2(k.x, k.y), nm);
+        t[2 * i + 1] = __ffma2_rn(__ffma2_rn(y, a2, b2), make_float2(k.z, k.w), nm);
+    }
+}
+// Weights of kCW scores: p = 2^t (their sum is returned), w = p vs as fp16 pairs.
+__device__ __forceinline__ float soft_weights(const float2 (&t)[kCW / 2], const float *vs, uint32_t (&pk)[kCW / 2]) {
+    const float4 *v4 = reinterpret_cast<const float4 *>(vs);
+    float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int i = 0; i < kCW / 4; ++i) {
+        const float4 v = v4[i];
+        const float2 p0 = make_float2(ex2(t[2 * i].x), ex2(t[2 * i].y));
+        const float2 p1 = make_float2(ex2(t[2 * i + 1].x), ex2(t[2 * i + 1].y));
+        sum[0] = __fadd2_rn(sum[0], p0);
+        sum[1] = __fadd2_rn(sum[1], p1);
+        const float2 w0 = __fmul2_rn(p0, make_float2(v.x, v.y)), w1 = __fmul2_rn(p1, make_float2(v.z, v.w));
+        const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
+        pk[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
+        pk[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+    }
+    const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+    return s2.x + s2.y;
+}
+
+// One row's state: the reference M (-inf: nothing seen yet), the sum l, and the factor
+// F that the sums of earlier tiles still need.
+struct SoftRow {
+    float M, l, F;
+};
+
+// Chunk c of a tile with everything that is rare: masks (the low bits of `vis` name the
+// visible tokens), the first reference, a reference that has to move.  A masked weight
+// is zero whatever the value's scale holds.  The chunk's scores lie in tensor memory,
+// the tile's earlier weights over the scores before them.
+__device__ __forceinline__ void soft_careful(uint32_t tS, int c, const float *ks, const float *vs, float2 fac, uint32_t vis,
+                                             SoftRow &r) {
+    uint32_t sr[kCW];
+    float2 t[kCW / 2];
+    tm_ld16(tS + kCW * c, sr);
+    tc_wait_ld16(sr);
+    soft_scores(sr, ks, fac, r.M == -INFINITY ? 0.f : r.M, t);
+    float cand = -INFINITY, tmax = -INFINITY;                     // log2 of the largest w and p, against M
+#pragma unroll
+    for (int i = 0; i < kCW / 2; ++i) {
+        const float2 v = reinterpret_cast<const float2 *>(vs)[i];
+        const bool s0 = (vis >> (2 * i)) & 1, s1 = (vis >> (2 * i + 1)) & 1;
+        t[i] = make_float2(s0 ? t[i].x : -INFINITY, s1 ? t[i].y : -INFINITY);
+        if (s0) cand = fmaxf(cand, t[i].x + lg2(v.x));
+        if (s1) cand = fmaxf(cand, t[i].y + lg2(v.y));
+        tmax = max3(tmax, t[i].x, t[i].y);
+    }
+    cand = fmaxf(cand, tmax - 100.f);                             // rows of zero values: keeps p itself finite
+    float up = 0.f, f = 1.f;
+    if (r.M == -INFINITY) {
+        if (vis) r.M = up = cand == -INFINITY ? 0.f : cand;       // nothing but NaN seen: any reference
+    } else if (cand > 8.f) {
+        up = cand;
+        f = ex2(-up);
+        r.M += up;
+        r.l *= f;
+        r.F *= f;
+    }
+    if (__any_sync(0xffffffffu, f != 1.f)) {
+        const __half2 fh = __half2half2(__float2half_rn(f));
+        for (int cc = 0; cc < c; ++cc) {                          // this tile's earlier weights
+            uint32_t x[8];
+            tm_ld8(tS + kCW / 2 * cc, x);
+            tc_wait_ld8(x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[i]), fh);
+                x[i] = *reinterpret_cast<const uint32_t *>(&y);
+            }
+            tm_st8(tS + kCW / 2 * cc, x);
+        }
+        tc_wait_st();
+    }
+#pragma unroll
+    for (int i = 0; i < kCW / 2; ++i) t[i] = make_float2(t[i].x - up, t[i].y - up);
+    uint32_t pk[kCW / 2];
+    r.l += soft_weights(t, vs, pk);
+#pragma unroll
+    for (int i = 0; i < kCW / 2; ++i)
+        pk[i] &= ((vis >> (2 * i)) & 1 ? 0x0000ffffu : 0u) | ((vis >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+    tm_st8(tS + kCW / 2 * c, pk);
+}
+
+// One row's 128 scores of a tile that every row sees whole; the next kCW are on their
+// way while these are worked on.  Whether a weight leaves fp16's range is seen from the
+// sum of kCW p (needed anyway) times their largest vs: it is at most kCW times the
+// largest w, so below 2^13 all is well, and only a w above 2^9 can pass that.  Returns
+// the number of chunks done: the rest, from the first that is not well, need care.
+__device__ __forceinline__ int soft_tile(uint32_t tS, const float *ks, const float *vs, float2 fac, SoftRow &r) {
+    uint32_t sr[2][kCW];
+    tm_ld16(tS, sr[0]);
+    const float4 v = reinterpret_cast<const float4 *>(vs)[threadIdx.x & 31];
+    float vtop = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));         // each kCW / 4 lanes: a chunk's largest vs
+#pragma unroll
+    for (int o = 1; o < kCW / 4; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+#pragma unroll
+    for (int c = 0; c < kTcTT / kCW; ++c) {
+        const float vmax = __shfl_sync(0xffffffffu, vtop, kCW / 4 * c);
+        float2 t[kCW / 2];
+        tc_wait_ld16(sr[c & 1]);
+        // the next columns are overwritten after chunk 2 c + 1 at the earliest
+        if (c + 1 < kTcTT / kCW) tm_ld16(tS + kCW * (c + 1), sr[(c + 1) & 1]);
+        soft_scores(sr[c & 1], ks + kCW * c, fac, r.M, t);
+        uint32_t pk[kCW / 2];
+        const float add = soft_weights(t, vs + kCW * c, pk);
+        // also where r.M = -inf: add is infinite or NaN
+        if (__any_sync(0xffffffffu, !(add * vmax <= 8192.f && add <= 1e30f))) return c;
+        r.l += add;
+        tm_st8(tS + kCW / 2 * c, pk);
+    }
+    return kTcTT / kCW;
+}
 
 template <int IN, int D, int NT, int HV>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -264,55 +448,63 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
         }
     } else if (warp == 1) {
         // ---------------- MMA ----------------
-        if (lane == 0) {
-            uint32_t base = 0, unit = 0, pc[2] = {0, 0};     // items of earlier stretches; stretches; P tiles per team
-            constexpr uint32_t id_qk = idesc_f16(kTcTT, false), id_pv = idesc_f16(D, true);
-            bool ok = true;
-            for (int64_t at = begin; at < end && ok; ++unit) {
-                const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
-                const int T = w.t1 - w.t0, J = NT * T;
-                at += T;
-                ok = t_mbar_wait(&s.q_full, unit & 1, &s.abort_flag, p.err);
+        // The whole warp runs the loop, so that descriptors stay in uniform registers;
+        // one lane issues (16 MMAs of 64 cycles each per tile leave no time for more).
+        const bool one = elect_one();
+        uint32_t base = 0, unit = 0, pc[2] = {0, 0};         // items of earlier stretches; stretches; P tiles per team
+        constexpr uint32_t id_qk = idesc_f16(kTcTT, false), id_pv = idesc_f16(D, true);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = op_desc(t_smem(s.q[0]), 16), dk = op_desc(t_smem(s.op[0]), 16);
+        const uint64_t dv = op_desc(t_smem(s.op[0]), S::PANEL);
+        bool ok = true;
+        for (int64_t at = begin; at < end && ok; ++unit) {
+            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
+            const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), J = NT * T;
+            at += T;
+            ok = warp_wait(&s.q_full, unit & 1, &s.abort_flag, p.err);
+            auto qk = [&](int j) {
+                const int k = NT == 2 ? j >> 1 : j, t = j & 1;
+                const uint32_t i = base + item_of_k<NT>(k), slot = i % kOps;
+                if (NT == 1 || t == 0) ok = ok && warp_wait(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
+                if (!ok) return;
                 tc_fence_after();
-                auto qk = [&](int j) {
-                    const int k = NT == 2 ? j >> 1 : j, t = j & 1;
-                    const uint32_t i = base + item_of_k<NT>(k), slot = i % kOps;
-                    if (NT == 1 || t == 0) ok = ok && t_mbar_wait(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t b = t_smem(s.op[slot]);
+                const uint64_t b = dk + slot * (S::TILE >> 4);
+                const uint64_t a = dq + (NT == 2 ? t * (S::TILE >> 4) : 0);
+                if (one) {
 #pragma unroll
-                    for (int hv = 0; hv < HV; ++hv) {
-                        const uint32_t a = t_smem(s.q[NT == 2 ? t : hv]);
+                    for (int hv = 0; hv < HV; ++hv)
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
-                            const uint32_t off = (c >> 2) * S::PANEL + (c & 3) * 32;
-                            mma_ss(tS[t], op_desc(a + off, 16), op_desc(b + off, 16), id_qk, hv + c > 0);
+                            const uint32_t off = ((c >> 2) * S::PANEL + (c & 3) * 32) >> 4;
+                            mma_ss(tm + 128 * t, a + hv * (S::TILE >> 4) + off, b + off, id_qk, hv + c > 0);
                         }
-                    }
                     if (NT == 1 || t == 1) tc_commit(&s.op_empty[slot]);
                     tc_commit(&s.s_full[t]);
-                };
-                qk(0);
-                if (J > 1) qk(1);
-                for (int j = 0; j < J && ok; ++j) {
-                    const int k = NT == 2 ? j >> 1 : j, t = j & 1;
-                    const uint32_t i = base + item_of_v<NT>(k, T), slot = i % kOps;
-                    if (NT == 1 || t == 0) ok = ok && t_mbar_wait(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
-                    ok = ok && t_mbar_wait(&s.p_full[t], pc[t] & 1, &s.abort_flag, p.err);
-                    ++pc[t];
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t b = t_smem(s.op[slot]);
+                }
+                __syncwarp();
+            };
+            qk(0);
+            if (J > 1) qk(1);
+            for (int j = 0; j < J && ok; ++j) {
+                const int k = NT == 2 ? j >> 1 : j, t = j & 1;
+                const uint32_t i = base + item_of_v<NT>(k, T), slot = i % kOps;
+                if (NT == 1 || t == 0) ok = ok && warp_wait(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
+                ok = ok && warp_wait(&s.p_full[t], pc[t] & 1, &s.abort_flag, p.err);
+                ++pc[t];
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t b = dv + slot * (S::TILE >> 4);
+                if (one) {
 #pragma unroll
                     for (int c = 0; c < kTcTT / 16; ++c)
-                        mma_ts(tO[t], tS[t] + 8 * c, op_desc(b + c * 2048, S::PANEL), id_pv, j >= 2 || c > 0);
+                        mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * c, b + c * (2048 >> 4), id_pv, j >= 2 || c > 0);
                     if (NT == 1 || t == 1) tc_commit(&s.op_empty[slot]);
-                    if (j + 2 < J) qk(j + 2);
-                    else tc_commit(&s.o_full[t]);
+                    if (j + 2 >= J) tc_commit(&s.o_full[t]);
                 }
-                base += 2 * T;
+                __syncwarp();
+                if (j + 2 < J) qk(j + 2);
             }
+            base += 2 * T;
         }
     } else if (warp >= 4 && warp < 4 + kSoftWarps) {
         // ---------------- softmax teams ----------------
@@ -329,40 +521,64 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
 
             // ---- q~: each warp 32 (NT = 2) or 16 rows of the block's ----
             {
-                constexpr int RW = ROWS / kSoftWarps;
+                constexpr int RW = ROWS / kSoftWarps, U = 8;         // U rows in flight
                 float sg[E];
                 lane_signs<E>(sg, lane, p.seed);
-#pragma unroll 2
-                for (int i = 0; i < RW; ++i) {
-                    const int r = (warp - 4) * RW + i, gr = w.mt * ROWS + r;
-                    float v[E];
+#pragma unroll 1
+                for (int i = 0; i < RW; i += U) {
+                    const int r0 = (warp - 4) * RW + i;
+                    float v[U][E], top[U], sum[U];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] = 0.f;
-                    if (r < rows) {
+                    for (int u = 0; u < U; ++u) {
+                        const int gr = w.mt * ROWS + r0 + u;
                         const char *src = static_cast<const char *>(p.q) +
                                           ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head) * 2;
 #pragma unroll
-                        for (int e = 0; e < E; ++e) v[e] = load_elem<IN>(src, lane * E + e);
+                        for (int e = 0; e < E; ++e) v[u][e] = r0 + u < rows ? load_elem<IN>(src, lane * E + e) : 0.f;
                     }
-                    warp_rotate<E>(v, sg, lane, signs_first, inv_sqrt_dim<D>());
-                    float top = 0.f;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
+                    for (int u = 0; u < U; ++u) {
+                        warp_rotate<E>(v[u], sg, lane, signs_first, inv_sqrt_dim<D>());
+                        top[u] = 0.f;
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 126;      // top < 2^ex
-                    ex = max(-100, min(ex, 120));
-                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                    if (lane == 0) s.rscale[r] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.score_scale;
+                        for (int e = 0; e < E; ++e) top[u] = fmaxf(top[u], fabsf(v[u][e]));
+                    }
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const int d = lane * E + e, rr = r & 127;
-                        const int pos = ((d & 3) << 1) + ((d >> 2) & 1);
-                        const uint32_t off = (uint32_t)((d >> 6) * S::PANEL + rr * 128 + ((((d & 63) >> 3) ^ (rr & 7)) << 4) + pos * 2);
-                        const float x = v[e] * down;
-                        const __half hi = __float2half_rn(x);
-                        *reinterpret_cast<__half *>(s.q[NT == 2 ? r >> 7 : 0] + off) = hi;
-                        if constexpr (HV == 2) *reinterpret_cast<__half *>(s.q[1] + off) = __float2half_rn(x - __half2float(hi));
+                    for (int o = 16; o; o >>= 1)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int r = r0 + u, rr = r & 127;
+                        int ex = (int)((__float_as_uint(top[u]) >> 23) & 255u) - 126;      // top < 2^ex
+                        ex = max(-100, min(ex, 104));
+                        top[u] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.score_scale;
+                        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                        sum[u] = 0.f;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int d = lane * E + e;
+                            const int pos = ((d & 3) << 1) + ((d >> 2) & 1);
+                            const uint32_t off = (uint32_t)((d >> 6) * S::PANEL + rr * 128 + ((((d & 63) >> 3) ^ (rr & 7)) << 4) + pos * 2);
+                            const float x = v[u][e] * down * (d & 1 ? 0.0625f : 1.f);
+                            const __half hi = __float2half_rn(x);
+                            float got = __half2float(hi);
+                            *reinterpret_cast<__half *>(s.q[NT == 2 ? r >> 7 : 0] + off) = hi;
+                            if constexpr (HV == 2) {
+                                const __half lo = __float2half_rn(x - got);
+                                got += __half2float(lo);
+                                *reinterpret_cast<__half *>(s.q[1] + off) = lo;
+                            }
+                            sum[u] += got * (d & 1 ? 16.f : 1.f);
+                        }
+                    }
+#pragma unroll
+                    for (int o = 16; o; o >>= 1)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+                    if (lane == 0) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) s.rfac[r0 + u] = make_float2(top[u] * 16777216.f, -8.f * sum[u] * top[u]);
                     }
                 }
             }
@@ -371,14 +587,11 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
             if (lane == 0) t_mbar_arrive(&s.q_full);
             both_sync();
             const int brow = (NT == 2 ? team * 128 : 0) + row;               // row of the block
-            const float a = s.rscale[brow];
-            const pair_t a2 = mk2(a, a);
+            const float2 fac = s.rfac[brow];
             const bool idle = (NT == 2 ? team * 128 : 0) + quarter * 32 >= rows;     // no row of this warp exists
             const int node = (w.mt * ROWS + brow) / p.group;
-            const int bt = min(kTcTT, 1 << p.log_page);
-            const uint32_t all = (uint32_t)((1ull << (kTcTT / bt)) - 1);
-
-            float M = -INFINITY, l = 0.f;
+            const uint32_t all = (uint32_t)((1ull << (kTcTT / min(kTcTT, 1 << p.log_page))) - 1);
+            SoftRow r{-INFINITY, 0.f, 1.f};
             bool first = true;
             for (int k = NT == 2 ? 0 : team; k < T; k += NT == 2 ? 1 : 2, ++uses) {
                 const uint32_t scs = (sc + k) % kSc;
@@ -390,115 +603,21 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
                     const int t0 = (w.t0 + k) * kTcTT;
                     const uint32_t valid = s.valid[scs];
                     const bool masked = t0 + kTcTT > w.s.ctx || valid != all;
-                    float F = 1.f;                                            // rescaling of earlier tiles
+                    r.F = 1.f;
+                    const int fast = masked ? 0 : soft_tile(tS[team] + lanes, s.ks[scs], s.vs[scs], fac, r);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t sr[32];
-                        tm_ld32(tS[team] + lanes + 32 * c, sr);
-                        uint32_t vis = 0xffffffffu;
-                        if (masked) {
-                            vis = 0;
-                            if (node < w.s.n) {
-                                const int tc = t0 + 32 * c;
-                                const uint8_t *m = p.mask ? p.mask + (w.s.row0 + node) * p.mask_stride : nullptr;
-                                for (int i = 0; i < 32; ++i) {
-                                    const int t = tc + i;
-                                    if (t >= w.s.len || !((valid >> ((32 * c + i) / bt)) & 1)) continue;
-                                    const int j = t - w.s.ctx;
-                                    if (j < 0 || (m ? m[j] != 0 : j <= node)) vis |= 1u << i;
-                                }
-                            }
-                        }
-                        tc_wait_ld32(sr);
-                        const float Mz = M == -INFINITY ? 0.f : M;
-                        const pair_t nm = mk2(-Mz, -Mz);
-                        pair_t t2[16];
-                        const float4 *k4 = reinterpret_cast<const float4 *>(&s.ks[scs][32 * c]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 kk = k4[i];
-                            const pair_t x0 = fma2(mk2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1])), mk2(kk.x, kk.y), 0ull);
-                            const pair_t x1 = fma2(mk2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3])), mk2(kk.z, kk.w), 0ull);
-                            t2[2 * i] = fma2(x0, a2, nm);
-                            t2[2 * i + 1] = fma2(x1, a2, nm);
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                t2[i] = mk2((vis >> (2 * i)) & 1 ? lo2(t2[i]) : -INFINITY, (vis >> (2 * i + 1)) & 1 ? hi2(t2[i]) : -INFINITY);
-                        }
-                        const float4 *v4 = reinterpret_cast<const float4 *>(&s.vs[scs][32 * c]);
-                        uint32_t pk[16];
-                        float add = 0.f, wtop = 0.f;
-                        auto weigh = [&] {
-                            pair_t sum2 = 0ull;
-                            wtop = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 vv = v4[i];
-                                const pair_t p0 = mk2(ex2(lo2(t2[2 * i])), ex2(hi2(t2[2 * i])));
-                                const pair_t p1 = mk2(ex2(lo2(t2[2 * i + 1])), ex2(hi2(t2[2 * i + 1])));
-                                sum2 = add2(sum2, add2(p0, p1));
-                                pair_t w0 = fma2(p0, mk2(vv.x, vv.y), 0ull), w1 = fma2(p1, mk2(vv.z, vv.w), 0ull);
-                                if (masked) {        // a masked weight is zero whatever the value's scale holds
-                                    w0 = mk2((vis >> (4 * i)) & 1 ? lo2(w0) : 0.f, (vis >> (4 * i + 1)) & 1 ? hi2(w0) : 0.f);
-                                    w1 = mk2((vis >> (4 * i + 2)) & 1 ? lo2(w1) : 0.f, (vis >> (4 * i + 3)) & 1 ? hi2(w1) : 0.f);
-                                }
-                                wtop = max3(wtop, max3(lo2(w0), hi2(w0), lo2(w1)), hi2(w1));
-                                const __half2 h0 = __floats2half2_rn(lo2(w0), hi2(w0)), h1 = __floats2half2_rn(lo2(w1), hi2(w1));
-                                pk[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
-                                pk[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
-                            }
-                            add = lo2(sum2) + hi2(sum2);
-                        };
-                        weigh();
-                        if (__any_sync(0xffffffffu, wtop > 256.f || (M == -INFINITY && vis != 0))) {
-                            // move the reference of the rows that need it
-                            float cand = -INFINITY, tmax = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 vv = reinterpret_cast<const float2 *>(v4)[i];
-                                const bool s0 = (vis >> (2 * i)) & 1, s1 = (vis >> (2 * i + 1)) & 1;
-                                if (s0) cand = fmaxf(cand, lo2(t2[i]) + lg2(vv.x));
-                                if (s1) cand = fmaxf(cand, hi2(t2[i]) + lg2(vv.y));
-                                tmax = max3(tmax, lo2(t2[i]), hi2(t2[i]));
-                            }
-                            if (cand == -INFINITY) cand = tmax;                // zero values only
-                            float delta = 0.f;
-                            if (M == -INFINITY ? cand != -INFINITY : wtop > 256.f) delta = cand;
-                            const float f = M == -INFINITY ? 1.f : ex2(-delta);
-                            if (M != -INFINITY || cand != -INFINITY) M = Mz + delta;
-                            const pair_t d2 = mk2(-delta, -delta);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) t2[i] = add2(t2[i], d2);
-                            l *= f;
-                            F *= f;
-                            const __half2 fh = __half2half2(__float2half_rn(f));
-                            for (int cc = 0; cc < c; ++cc) {                   // this tile's earlier weights
-                                uint32_t x[16];
-                                tm_ld16(tS[team] + lanes + 16 * cc, x);
-                                tc_wait_ld16(x);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[i]), fh);
-                                    x[i] = *reinterpret_cast<const uint32_t *>(&y);
-                                }
-                                tm_st16(tS[team] + lanes + 16 * cc, x);
-                            }
-                            tc_wait_st();
-                            weigh();
-                        }
-                        l += add;
-                        tm_st16(tS[team] + lanes + 16 * c, pk);
+                    for (int c = fast; c < kTcTT / kCW; ++c) {
+                        const uint32_t vis = masked ? tree_visible(p, w, node, t0 + kCW * c, kCW * c, valid) : 0xffffu;
+                        soft_careful(tS[team] + lanes, c, s.ks[scs] + kCW * c, s.vs[scs] + kCW * c, fac, vis, r);
                     }
-                    if (!first && __any_sync(0xffffffffu, F != 1.f)) {
+                    if (!first && __any_sync(0xffffffffu, r.F != 1.f)) {
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t x[32];
                             tm_ld32(tO[team] + lanes + 32 * c, x);
                             tc_wait_ld32(x);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * F);
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * r.F);
                             tm_st32(tO[team] + lanes + 32 * c, x);
                         }
                     }
@@ -521,7 +640,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
                 ++units;
             }
             tc_fence_after();
-            if (M == -INFINITY && !(l == 0.f)) M = 0.f;                       // nothing but NaN seen
+            float M = r.M, l = r.l;
             l = fminf(l, 3.4028234e38f) + (l != l ? l : 0.f);                 // keeps NaN, bounds infinity
             float fa = 1.f, fb = 0.f;                                         // factors of the teams' accumulators
             if constexpr (NT == 1) {
@@ -655,7 +774,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
         }
     } else if (warp >= 4 + kSoftWarps) {
         // ---------------- converters ----------------
-        const int ct = threadIdx.x - 32 * (4 + kSoftWarps);                  // 0 .. 255
+        const int ct = threadIdx.x - 32 * (4 + kSoftWarps);                  // 0 .. 127
         uint32_t it = 0;
         for (int64_t at = begin; at < end;) {
             const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
@@ -663,24 +782,33 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
             at += T;
             for (int i = 0; i < 2 * T; ++i, ++it) {
                 const int st = it % RAW, slot = it % kOps;
+                int k;
+                bool is_v;
+                item_at<NT>(i, T, k, is_v);
                 bool ok = t_mbar_wait(&s.raw_full[st], (it / RAW) & 1, &s.abort_flag, p.err);
                 ok = t_mbar_wait(&s.op_empty[slot], ((it / kOps) & 1) ^ 1, &s.abort_flag, p.err) && ok;
                 if (ok) {
                     // 16 bytes of codes: 32 dims of one token -> four 16-byte pieces of the operand.
                     // 8 lanes take 8 rows of one chunk: no bank conflicts on either side.
+                    constexpr int CH = RB / 16, N = kTcTT * CH / (32 * kConvWarps);
+                    uint4 x[N];
 #pragma unroll
-                    for (int u = ct; u < kTcTT * RB / 16; u += 32 * kConvWarps) {
-                        const int r = (u & 7) | ((u / (8 * (RB / 16))) << 3), ch = (u >> 3) % (RB / 16);
-                        const int sw = RB == 64 ? ch ^ ((r >> 1) & 3) : ch ^ ((r >> 2) & 1);
-                        const uint4 x = *reinterpret_cast<const uint4 *>(s.rawt[st] + r * RB + sw * 16);
-                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                    for (int n = 0; n < N; ++n) {
+                        const int u = ct + n * 32 * kConvWarps;
+                        const int r = (u & 7) | ((u / (8 * CH)) << 3), ch = (u >> 3) % CH;
+                        const int sw = CH == 4 ? ch ^ ((r >> 1) & 3) : ch ^ ((r >> 2) & 1);
+                        x[n] = *reinterpret_cast<const uint4 *>(s.rawt[st] + r * RB + sw * 16);
+                    }
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        const int u = ct + n * 32 * kConvWarps;
+                        const int r = (u & 7) | ((u / (8 * CH)) << 3), ch = (u >> 3) % CH;
+                        const uint32_t xw[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
                         uint8_t *dst = s.op[slot] + (ch >> 1) * S::PANEL + r * 128;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t y = xw[q] ^ 0x88888888u;
+                        for (int q = 0; q < 4; ++q)
                             *reinterpret_cast<uint4 *>(dst + ((((ch & 1) * 4 + q) ^ (r & 7)) << 4)) =
-                                make_uint4(nibbles_fp16(y, 0), nibbles_fp16(y, 1), nibbles_fp16(y, 2), nibbles_fp16(y, 3));
-                        }
+                                is_v ? v_operands(xw[q]) : k_operands(xw[q]);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

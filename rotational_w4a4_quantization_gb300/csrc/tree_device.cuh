@@ -193,11 +193,13 @@ __device__ __forceinline__ void t_mbar_expect(uint64_t *b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(t_smem(b)), "r"(bytes)
                  : "memory");
 }
+// The hint lets the hardware suspend the thread for up to 20 us: waiting warps then
+// leave their issue slots to the others.
 __device__ __forceinline__ bool t_mbar_try(uint64_t *b, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(t_smem(b)), "r"(parity) : "memory");
+                 : "=r"(ok) : "r"(t_smem(b)), "r"(parity), "r"(20000u) : "memory");
     return ok != 0;
 }
 constexpr long long kTreeWaitLimit = 4000000000ll;   // ~2 s at 2 GHz

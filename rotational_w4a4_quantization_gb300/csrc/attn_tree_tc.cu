@@ -12,24 +12,34 @@
 //   NT = 1: 128 rows; team w takes the tiles of parity w with an accumulator of its
 //           own, and the two are joined at the end.
 //
-// Roles (16 warps, one block per SM):
-//   warp 0       TMA: packed code tiles (8 KB each at D = 128) and scales
+// Roles (20 warps of which two idle, one block per SM):
+//   warp 0       scales of each tile: their units, and the scales themselves where they
+//                are not folded in
 //   warp 1       tensor memory, all MMAs (one lane)
 //   warps 4-11   softmax teams
-//   warps 12-15  converters: packed codes -> fp16 codes (exact) in the 128-byte-
-//                swizzled operand layout.  One layout serves both products: rows of
-//                64 dims per token are K-major for Q K^T and MN-major for P V.
+//   warps 12-19  converters, two teams in turn: packed codes, loaded two operands ahead
+//                straight into registers, -> fp16 in the 128-byte-swizzled operand
+//                layout.  One layout serves both products: rows of 64 dims per token
+//                are K-major for Q K^T and MN-major for P V.
 // Tensor memory, 512 columns: S0 S1 (128 each; P overwrites the first half of its S)
 // and O0 O1 (D each).
 //
-// Weights: w = 2^(s - M) vs is what the MMA sees, rounded to fp16; the sum l adds
-// 2^(s - M) in fp32.  O / l does not depend on M, so M only has to keep w in range: it
-// follows the largest s + log2 vs, and moves only when some w passes 2^8 (the
-// accumulator is then rescaled in place, between the commit that delivers S and the
-// arrival that delivers P, when no MMA touches it).
-// The scales of K stay out of the product: s = (q~ . code) ks in fp32.
-// fp16 queries: q~ carries 22 bits (two fp16 parts, Q K^T twice), as their outputs
-// resolve the rounding of q~ to 11 bits.
+// Scales.  In a tile that every row sees whole (all but the last ones of a sequence)
+// they are folded into the operands: k^ and v^ as fp16(code * scale), scales relative to
+// a power of two per tile, one rounding (the scale enters in two fp16 parts).  The
+// softmax then reads nothing but its scores: broadcasting scales from shared memory
+// costs 4 cycles per 16 bytes and warp, and bound the kernel (8 warps x 64 loads per
+// tile; measured 2,150 cycles per tile for that softmax alone, against 2,048 of MMAs).
+// Tiles with masks keep exact codes and apply the scales to scores and weights, so that
+// what an unseen token holds (a NaN scale, say) reaches nobody.  fp16 queries, whose
+// outputs resolve an 11-bit rounding of q~ and k^, keep q~ in two fp16 parts (Q K^T runs
+// twice) and the scales of K out of the operand.
+//
+// Weights: P = 2^(s - M + ev) (2^ev the tile's unit of vs) is what the MMA sees, rounded
+// to fp16; the sum l adds 2^(s - M) in fp32.  O / l does not depend on M, so M only has
+// to keep P in range: it moves only when some P would pass 2^8 (the accumulator is then
+// rescaled in place, between the commit that delivers S and the arrival that delivers
+// P, when no MMA touches it).
 #include "rq.h"
 #include "rq_internal.h"
 #include "tree_device.cuh"
@@ -38,30 +48,27 @@ namespace rq {
 namespace {
 
 constexpr int kTcTT = 128;               // tokens per tile
-constexpr int kOps = 3;                  // operand slots
+constexpr int kOps = 4;                  // operand slots
 constexpr int kSc = 4;                   // scale slots
-constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kSoftWarps = 8, kConvTeams = 2, kTeamWarps = 4, kConvWarps = kConvTeams * kTeamWarps;
 constexpr int kTcThreads = 32 * (4 + kSoftWarps + kConvWarps);
 
 template <int D, int NT, int HV>
 struct TSmem {
-    static constexpr int RB = D / 2;                        // packed bytes of a token
-    static constexpr int RAW = NT * HV == 2 ? 6 : 8;        // packed tiles in flight
     static constexpr int PANEL = 128 * 128;                 // 128 rows x 64 dims of fp16
     static constexpr int TILE = D / 64 * PANEL;
     alignas(1024) uint8_t q[NT * HV][TILE];
     alignas(1024) uint8_t op[kOps][TILE];
-    alignas(1024) uint8_t rawt[RAW][kTcTT * RB];
     alignas(16) float ks[kSc][kTcTT];
     alignas(16) float vs[kSc][kTcTT];
-    float2 rfac[NT * 128];                                  // a row's factors: s = (a S + b) ks
-    float ref[2][128], sum[2][128];                         // NT = 1: the teams' references and sums
+    float2 unit[kSc];                                       // a tile's 2^ek and ev; 0 and 0: masked, scales not folded in
+    float rfac[NT * 128];                                   // s = rfac S (times ks)
+    float ref[2][NT == 1 ? 128 : 1], sum[2][NT == 1 ? 128 : 1];   // NT = 1: the teams' references and sums
     int64_t prefix[kScan + 1];
-    alignas(8) uint64_t raw_full[RAW], raw_empty[RAW];
-    uint64_t sc_full[kSc], sc_empty[kSc];
+    alignas(8) uint64_t sc_full[kSc], sc_empty[kSc];
     uint64_t op_full[kOps], op_empty[kOps];
     uint64_t q_full, s_full[2], p_full[2], o_full[2];
-    uint32_t valid[kSc];
+    uint32_t valid[kSc];                                    // bit c: tokens 16 c .. lie on a page of the cache
     uint32_t sign_words[8];
     uint32_t tmem_base;
     volatile int abort_flag;
@@ -114,10 +121,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t t, uint32_t *r) {
 __device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), RQ_W8(r, 0) : "memory");
 }
-__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-                 RQ_W8(r, 0), RQ_W8(r, 8) : "memory");
-}
 __device__ __forceinline__ void tm_st32(uint32_t t, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
                  "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
@@ -162,11 +165,11 @@ __device__ __forceinline__ int item_of_k(int k) { return NT == 2 ? 2 * k : (k ==
 template <int NT>
 __device__ __forceinline__ int item_of_v(int k, int T) { return NT == 2 ? 2 * k + 1 : (k == T - 1 ? 2 * T - 1 : 2 * k + 2); }
 
-// A word of 8 codes as 8 fp16 operands, in the order of the dims 0 4 1 5 2 6 3 7.
-// Values: 0x6400 | u is 1024 + u, so nibbles 0 and 4 (u = code + 8 after the sign bit's
-// flip) lose 1032, nibbles 1 and 5, which stay four bits up, are 1024 + 16 u: times
-// 1/16, less 72.  Exact.
-__device__ __forceinline__ uint4 v_operands(uint32_t x) {
+// A word of 8 codes as 8 fp16 operands code * (hi + lo), rounded once, in the order of
+// the dims 0 4 1 5 2 6 3 7.  0x6400 | u is 1024 + u, so nibbles 0 and 4 (u = code + 8
+// after the sign bit's flip) lose 1032; nibbles 1 and 5, which stay four bits up, are
+// 1024 + 16 u: times 1/16, less 72.  Both exact.
+__device__ __forceinline__ uint4 operands(uint32_t x, __half2 hi, __half2 lo) {
     const __half2 m0 = __half2half2(__ushort_as_half(0xe408)), r16 = __half2half2(__ushort_as_half(0x2c00)),
                   m1 = __half2half2(__ushort_as_half(0xd480));             // -1032, 1/16, -72
     uint32_t r[4];
@@ -174,20 +177,26 @@ __device__ __forceinline__ uint4 v_operands(uint32_t x) {
     for (int j = 0; j < 4; j += 2) {
         const uint32_t y = x >> (4 * j);
         const uint32_t a = (y & 0x000f000fu) ^ 0x64086408u, b = (y & 0x00f000f0u) ^ 0x64806480u;
-        const __half2 ha = __hadd2(*reinterpret_cast<const __half2 *>(&a), m0);
-        const __half2 hb = __hfma2(*reinterpret_cast<const __half2 *>(&b), r16, m1);
+        const __half2 ca = __hadd2(*reinterpret_cast<const __half2 *>(&a), m0);
+        const __half2 cb = __hfma2(*reinterpret_cast<const __half2 *>(&b), r16, m1);
+        const __half2 ha = __hfma2(ca, hi, __hmul2(ca, lo)), hb = __hfma2(cb, hi, __hmul2(cb, lo));
         r[j] = *reinterpret_cast<const uint32_t *>(&ha);
         r[j + 1] = *reinterpret_cast<const uint32_t *>(&hb);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
-// Keys: no arithmetic.  u = code + 8 as the subnormal u 2^-24 (nibbles 1, 3, 5, 7:
-// 16 u 2^-24, and q~ holds a sixteenth there); the softmax takes 2^24 and 8 sum q~ out
-// again with the row's factors.  The sums are short (D terms), so nothing is lost.
-__device__ __forceinline__ uint4 k_operands(uint32_t x) {
-    const uint32_t y = x >> 8;
-    return make_uint4((x ^ 0x00080008u) & 0x000f000fu, (x ^ 0x00800080u) & 0x00f000f0u,
-                      (y ^ 0x00080008u) & 0x000f000fu, (y ^ 0x00800080u) & 0x00f000f0u);
+// The exponent e with 2^e above the largest of a tile's 128 scales (0 where all are 0):
+// one warp, four scales a lane.  Scales are not negative, so their bits order them.
+__device__ __forceinline__ int tile_exponent(const float4 &x) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(__float_as_uint(x.x), __float_as_uint(x.y)),
+                                                            max(__float_as_uint(x.z), __float_as_uint(x.w))));
+    return top == 0 ? 0 : max(-100, min((int)((top >> 23) & 255u) - 126, 100));
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // |e| <= 126
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
 __device__ __forceinline__ float lg2(float x) {
     float y;
@@ -209,176 +218,206 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile
 // position p of an 8-group of operand columns holds dim kPerm(p) of the group
 __device__ __forceinline__ constexpr int perm8(int p) { return (p & 1) * 4 + (p >> 1); }
 
-// Which of the tokens t .. t + 15 (rows at .. of a tile with page pieces `valid`) a node
-// sees, as bits.  The mask bytes are loaded all at once.
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 16 ? 0xffffu : (1u << n) - 1u); }
-__device__ __forceinline__ uint32_t tree_visible(const TreeParams &p, const TreeWork &w, int node, int t, int at, uint32_t valid) {
-    if (node >= w.s.n || !((valid >> (at >> min(p.log_page, 7))) & 1)) return 0u;
-    const uint32_t there = below(w.s.len - t);
-    const int j0 = t - w.s.ctx;                                   // the node at token t
-    if (!p.mask) return there & below(node + 1 - j0);
-    uint32_t seen = below(-j0);
-    if (j0 + 16 > 0 && j0 < w.s.n) {
-        const uint8_t *m = p.mask + (w.s.row0 + node) * p.mask_stride + j0;
-        uint8_t x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = (unsigned)(j0 + i) < (unsigned)w.s.n ? m[i] : (uint8_t)0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) seen |= x[i] ? 1u << i : 0u;
-    }
-    return there & seen;
+// Cache row of token t of a work's KV head, -1 past the sequence or off the cache.
+__device__ __forceinline__ int64_t tree_row(const TreeParams &p, const TreeWork &w, int t) {
+    if (t >= w.s.len) return -1;
+    const int64_t pg = p.table[w.b * p.width + (t >> p.log_page)];
+    if (pg < 0 || pg >= p.pages) return -1;
+    return ((pg * p.kv_heads + w.h) << p.log_page) + (t & ((1 << p.log_page) - 1));
 }
 
 constexpr int kCW = 16;                  // scores that a row works on at a time: more of them spill
 
-// A row's kCW raw scores -> s - M, with s = (a S + b) ks.
-__device__ __forceinline__ void soft_scores(const uint32_t (&sr)[kCW], const float *ks, float2 fac, float M,
-                                            float2 (&t)[kCW / 2]) {
-    const float2 a2 = make_float2(fac.x, fac.x), b2 = make_float2(fac.y, fac.y), nm = make_float2(-M, -M);
-    const float4 *k4 = reinterpret_cast<const float4 *>(ks);
-#pragma unroll
-    for (int i = 0; i < kCW / 4; ++i) {
-        const float4 k = k4[i];
-        const float2 x = make_float2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1]));
-        const float2 y = make_float2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3]));
-        t[2 * i] = __ffma2_rn(__ffma2_rn(x, a2, b2), make_float2(k.x, k.y), nm);
-        t[2 * i + 1] = __ffma2_rn(__ffma2_rn(y, a2, b2), make_float2(k.z, k.w), nm);
-    }
-}
-// Weights of kCW scores: p = 2^t (their sum is returned), w = p vs as fp16 pairs.
-__device__ __forceinline__ float soft_weights(const float2 (&t)[kCW / 2], const float *vs, uint32_t (&pk)[kCW / 2]) {
-    const float4 *v4 = reinterpret_cast<const float4 *>(vs);
-    float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-    for (int i = 0; i < kCW / 4; ++i) {
-        const float4 v = v4[i];
-        const float2 p0 = make_float2(ex2(t[2 * i].x), ex2(t[2 * i].y));
-        const float2 p1 = make_float2(ex2(t[2 * i + 1].x), ex2(t[2 * i + 1].y));
-        sum[0] = __fadd2_rn(sum[0], p0);
-        sum[1] = __fadd2_rn(sum[1], p1);
-        const float2 w0 = __fmul2_rn(p0, make_float2(v.x, v.y)), w1 = __fmul2_rn(p1, make_float2(v.z, v.w));
-        const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
-        pk[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
-        pk[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
-    }
-    const float2 s2 = __fadd2_rn(sum[0], sum[1]);
-    return s2.x + s2.y;
-}
-
-// One row's state: the reference M (-inf: nothing seen yet), the sum l, and the factor
-// F that the sums of earlier tiles still need.
+// One row's state: the reference M (-inf: nothing seen yet) and the sum l.
 struct SoftRow {
-    float M, l, F;
+    float M, l;
 };
 
-// Chunk c of a tile with everything that is rare: masks (the low bits of `vis` name the
-// visible tokens), the first reference, a reference that has to move.  A masked weight
-// is zero whatever the value's scale holds.  The chunk's scores lie in tensor memory,
-// the tile's earlier weights over the scores before them.
-__device__ __forceinline__ void soft_careful(uint32_t tS, int c, const float *ks, const float *vs, float2 fac, uint32_t vis,
-                                             SoftRow &r) {
-    uint32_t sr[kCW];
-    float2 t[kCW / 2];
-    tm_ld16(tS + kCW * c, sr);
-    tc_wait_ld16(sr);
-    soft_scores(sr, ks, fac, r.M == -INFINITY ? 0.f : r.M, t);
-    float cand = -INFINITY, tmax = -INFINITY;                     // log2 of the largest w and p, against M
+// One row's 128 scores of a tile -> weights over them in tensor memory.  Two passes over
+// the scores, the next kCW always on their way: the largest first, so that M is settled
+// once for the tile and the second pass has neither votes nor branches (settling it per
+// chunk cost 200 cycles each); returns the factor that earlier tiles' sums need.
+//   s = a S (times ks where KS);  weight = 2^(s - M + ev)
+template <bool KS>
+__device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a, float ev, SoftRow &r) {
+    constexpr int C = kTcTT / kCW;
+    uint32_t s0[kCW], s1[kCW];
+    tm_ld16(tS, s0);
+    float top0 = -INFINITY, top1 = -INFINITY;
+    auto largest = [&](const uint32_t (&x)[kCW], int c) {
 #pragma unroll
-    for (int i = 0; i < kCW / 2; ++i) {
-        const float2 v = reinterpret_cast<const float2 *>(vs)[i];
-        const bool s0 = (vis >> (2 * i)) & 1, s1 = (vis >> (2 * i + 1)) & 1;
-        t[i] = make_float2(s0 ? t[i].x : -INFINITY, s1 ? t[i].y : -INFINITY);
-        if (s0) cand = fmaxf(cand, t[i].x + lg2(v.x));
-        if (s1) cand = fmaxf(cand, t[i].y + lg2(v.y));
-        tmax = max3(tmax, t[i].x, t[i].y);
-    }
-    cand = fmaxf(cand, tmax - 100.f);                             // rows of zero values: keeps p itself finite
-    float up = 0.f, f = 1.f;
-    if (r.M == -INFINITY) {
-        if (vis) r.M = up = cand == -INFINITY ? 0.f : cand;       // nothing but NaN seen: any reference
-    } else if (cand > 8.f) {
-        up = cand;
-        f = ex2(-up);
-        r.M += up;
-        r.l *= f;
-        r.F *= f;
-    }
-    if (__any_sync(0xffffffffu, f != 1.f)) {
-        const __half2 fh = __half2half2(__float2half_rn(f));
-        for (int cc = 0; cc < c; ++cc) {                          // this tile's earlier weights
-            uint32_t x[8];
-            tm_ld8(tS + kCW / 2 * cc, x);
-            tc_wait_ld8(x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[i]), fh);
-                x[i] = *reinterpret_cast<const uint32_t *>(&y);
+        for (int i = 0; i < kCW; i += 4) {
+            float4 v = make_float4(__uint_as_float(x[i]), __uint_as_float(x[i + 1]), __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+            if constexpr (KS) {
+                const float4 k = *reinterpret_cast<const float4 *>(ks + kCW * c + i);
+                v.x *= k.x;
+                v.y *= k.y;
+                v.z *= k.z;
+                v.w *= k.w;
             }
-            tm_st8(tS + kCW / 2 * cc, x);
+            top0 = max3(top0, v.x, v.y);
+            top1 = max3(top1, v.z, v.w);
         }
-        tc_wait_st();
+    };
+#pragma unroll
+    for (int c = 0; c < C; c += 2) {
+        tc_wait_ld16(s0);
+        tm_ld16(tS + kCW * (c + 1), s1);
+        largest(s0, c);
+        tc_wait_ld16(s1);
+        tm_ld16(tS + kCW * ((c + 2) % C), s0);                    // at the end: the first again
+        largest(s1, c + 1);
     }
+    const float best = fmaxf(top0, top1) * a + ev;                // a > 0
+    float f = 1.f;
+    if (best > r.M + 8.f) {                                       // also the first time, where M = -inf
+        if (r.M != -INFINITY) f = ex2(r.M - best);
+        r.M = best;
+        r.l *= f;
+    }
+    const float Mz = (r.M == -INFINITY ? 0.f : r.M) - ev;
+    const float2 a2 = make_float2(a, a), nm = make_float2(-Mz, -Mz);
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+    auto weigh = [&](const uint32_t (&x)[kCW], int c) {
+        uint32_t pk[kCW / 2];
 #pragma unroll
-    for (int i = 0; i < kCW / 2; ++i) t[i] = make_float2(t[i].x - up, t[i].y - up);
-    uint32_t pk[kCW / 2];
-    r.l += soft_weights(t, vs, pk);
+        for (int i = 0; i < kCW / 2; i += 2) {
+            float2 t0 = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            float2 t1 = make_float2(__uint_as_float(x[2 * i + 2]), __uint_as_float(x[2 * i + 3]));
+            if constexpr (KS) {
+                const float4 k = *reinterpret_cast<const float4 *>(ks + kCW * c + 2 * i);
+                t0 = __ffma2_rn(__fmul2_rn(t0, a2), make_float2(k.x, k.y), nm);
+                t1 = __ffma2_rn(__fmul2_rn(t1, a2), make_float2(k.z, k.w), nm);
+            } else {
+                t0 = __ffma2_rn(t0, a2, nm);
+                t1 = __ffma2_rn(t1, a2, nm);
+            }
+            const float2 p0 = make_float2(ex2(t0.x), ex2(t0.y)), p1 = make_float2(ex2(t1.x), ex2(t1.y));
+            sum0 = __fadd2_rn(sum0, p0);
+            sum1 = __fadd2_rn(sum1, p1);
+            const __half2 h0 = __floats2half2_rn(p0.x, p0.y), h1 = __floats2half2_rn(p1.x, p1.y);
+            pk[i] = *reinterpret_cast<const uint32_t *>(&h0);
+            pk[i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+        }
+        tm_st8(tS + kCW / 2 * c, pk);
+    };
+    // the columns of a chunk are overwritten by the weights of twice its number at the earliest
 #pragma unroll
-    for (int i = 0; i < kCW / 2; ++i)
-        pk[i] &= ((vis >> (2 * i)) & 1 ? 0x0000ffffu : 0u) | ((vis >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
-    tm_st8(tS + kCW / 2 * c, pk);
+    for (int c = 0; c < C; c += 2) {
+        tc_wait_ld16(s0);
+        tm_ld16(tS + kCW * (c + 1), s1);
+        weigh(s0, c);
+        tc_wait_ld16(s1);
+        if (c + 2 < C) tm_ld16(tS + kCW * (c + 2), s0);
+        weigh(s1, c + 1);
+    }
+    const float2 s2 = __fadd2_rn(sum0, sum1);
+    r.l += (s2.x + s2.y) * ex2(-ev);
+    return f;
 }
 
-// One row's 128 scores of a tile that every row sees whole; the next kCW are on their
-// way while these are worked on.  Whether a weight leaves fp16's range is seen from the
-// sum of kCW p (needed anyway) times their largest vs: it is at most kCW times the
-// largest w, so below 2^13 all is well, and only a w above 2^9 can pass that.  Returns
-// the number of chunks done: the rest, from the first that is not well, need care.
-__device__ __forceinline__ int soft_tile(uint32_t tS, const float *ks, const float *vs, float2 fac, SoftRow &r) {
-    uint32_t sr[2][kCW];
-    tm_ld16(tS, sr[0]);
-    const float4 v = reinterpret_cast<const float4 *>(vs)[threadIdx.x & 31];
-    float vtop = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));         // each kCW / 4 lanes: a chunk's largest vs
-#pragma unroll
-    for (int o = 1; o < kCW / 4; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-#pragma unroll
+// The same for a tile with masks and exact codes: s = a S ks, weight = 2^(s - M) vs.  M
+// follows the largest s + log2 vs, the weight's exponent.  A masked weight is zero
+// whatever its scales hold.  Few tiles of a sequence come here, and their time is the
+// fetching of code that ran for none before: the loops stay rolled (unrolled, a masked
+// tile took 44,000 cycles, most of them instruction misses; now about 10,000).
+//   node: this row's, node0, node1: the warp's first and last; valid: bit c says that
+//   tokens 16 c .. lie on a page of the cache.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+__device__ __forceinline__ float soft_masked(const TreeParams &p, const TreeSeq &q, uint32_t tS, const float *ks, const float *vs,
+                                             float a, int node, int node0, int node1, int t0, uint32_t valid, SoftRow &r) {
+    // the tokens that this row's node sees, a bit each: a warp reads a node's 32 mask bytes
+    // together, and the rows of that node keep the ballot
+    const int lane = threadIdx.x & 31;
+    uint32_t vis[4] = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+        const int t = t0 + 32 * g, j = t + lane - q.ctx;
+        uint32_t seen = 0;
+        if (!p.mask) {
+            seen = below(node + 1 + q.ctx - t);
+        } else if (t + 32 <= q.ctx) {
+            seen = 0xffffffffu;
+        } else if (t < q.len) {
+            const uint8_t *m = p.mask + q.row0 * p.mask_stride + j;
+            const bool in = j >= 0 && j < q.n;
+#pragma unroll 4
+            for (int nd = node0; nd <= node1; ++nd) {
+                const uint32_t b = __ballot_sync(0xffffffffu, j < 0 || (in && m[nd * p.mask_stride] != 0));
+                if (nd == node) seen = b;
+            }
+        }
+        const uint32_t v = valid >> (2 * g);
+        seen &= below(q.len - t) & ((v & 1 ? 0xffffu : 0u) | (v & 2 ? 0xffff0000u : 0u));
+        vis[0] = vis[1];
+        vis[1] = vis[2];
+        vis[2] = vis[3];
+        vis[3] = node < q.n ? seen : 0u;
+    }
+    uint32_t x[kCW];
+    float best = -INFINITY, only = -INFINITY;
+#pragma unroll 1
     for (int c = 0; c < kTcTT / kCW; ++c) {
-        const float vmax = __shfl_sync(0xffffffffu, vtop, kCW / 4 * c);
-        float2 t[kCW / 2];
-        tc_wait_ld16(sr[c & 1]);
-        // the next columns are overwritten after chunk 2 c + 1 at the earliest
-        if (c + 1 < kTcTT / kCW) tm_ld16(tS + kCW * (c + 1), sr[(c + 1) & 1]);
-        soft_scores(sr[c & 1], ks + kCW * c, fac, r.M, t);
+        const uint32_t w = (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> (kCW * (c & 1));
+        tm_ld16(tS + kCW * c, x);
+        tc_wait_ld16(x);
+#pragma unroll
+        for (int i = 0; i < kCW; ++i) {
+            const bool sees = (w >> i) & 1;
+            const float sc = sees ? __uint_as_float(x[i]) * a * ks[kCW * c + i] : -INFINITY;
+            only = fmaxf(only, sc);
+            best = fmaxf(best, sees ? sc + lg2(vs[kCW * c + i]) : -INFINITY);
+        }
+    }
+    best = fmaxf(best, only - 100.f);                             // rows of zero values: keeps 2^(s - M) itself finite
+    float f = 1.f;
+    if (best > r.M + 8.f) {
+        if (r.M != -INFINITY) f = ex2(r.M - best);
+        r.M = best;
+        r.l *= f;
+    }
+    const float Mz = r.M == -INFINITY ? 0.f : r.M;
+#pragma unroll 1
+    for (int c = 0; c < kTcTT / kCW; ++c) {
+        const uint32_t w = (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> (kCW * (c & 1));
+        tm_ld16(tS + kCW * c, x);
+        tc_wait_ld16(x);
         uint32_t pk[kCW / 2];
-        const float add = soft_weights(t, vs + kCW * c, pk);
-        // also where r.M = -inf: add is infinite or NaN
-        if (__any_sync(0xffffffffu, !(add * vmax <= 8192.f && add <= 1e30f))) return c;
-        r.l += add;
+#pragma unroll
+        for (int i = 0; i < kCW; i += 2) {
+            float pw[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool sees = (w >> (i + j)) & 1;
+                const float e = sees ? ex2(__uint_as_float(x[i + j]) * a * ks[kCW * c + i + j] - Mz) : 0.f;
+                r.l += e;
+                pw[j] = sees ? e * vs[kCW * c + i + j] : 0.f;
+            }
+            const __half2 h = __floats2half2_rn(pw[0], pw[1]);
+            pk[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        }
         tm_st8(tS + kCW / 2 * c, pk);
     }
-    return kTcTT / kCW;
+    return f;
 }
 
 template <int IN, int D, int NT, int HV>
 __global__ void __launch_bounds__(kTcThreads, 1)
-attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                    const __grid_constant__ TreeParams p) {
+attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
     using S = TSmem<D, NT, HV>;
-    constexpr int ROWS = 128 * NT, RB = D / 2, RAW = S::RAW, E = D / 32;
+    constexpr int ROWS = 128 * NT, RB = D / 2;
+    constexpr bool KFOLD = HV == 1;                    // the scales of K go into the operand
     extern __shared__ uint8_t raw[];
     S &s = *reinterpret_cast<S *>(raw + ((1024u - (t_smem(raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < RAW; ++i) {
-            t_mbar_init(&s.raw_full[i], 1);
-            t_mbar_init(&s.raw_empty[i], kConvWarps);
-        }
         for (int i = 0; i < kSc; ++i) {
             t_mbar_init(&s.sc_full[i], 1);
-            t_mbar_init(&s.sc_empty[i], 4 * NT);
+            t_mbar_init(&s.sc_empty[i], 4 * NT + kTeamWarps);
         }
         for (int i = 0; i < kOps; ++i) {
-            t_mbar_init(&s.op_full[i], kConvWarps);
+            t_mbar_init(&s.op_full[i], kTeamWarps);
             t_mbar_init(&s.op_empty[i], 1);
         }
         t_mbar_init(&s.q_full, kSoftWarps);
@@ -405,46 +444,46 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
 
     if (warp == 0) {
-        // ---------------- producer ----------------
-        const int bt = min(kTcTT, 1 << p.log_page), pieces = kTcTT / bt;
-        uint32_t it = 0, sc = 0;                       // items and tiles so far
+        // ---------------- scales ----------------
+        uint32_t sc = 0;
         for (int64_t at = begin; at < end;) {
             const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
             const int T = w.t1 - w.t0;
             at += T;
-            for (int i = 0; i < 2 * T; ++i, ++it) {
-                int k;
-                bool is_v;
-                item_at<NT>(i, T, k, is_v);
-                const int t = (w.t0 + k) * kTcTT + lane * bt;
-                int64_t pg = -1;
-                if (lane < pieces && t < w.s.len) {
-                    pg = p.table[w.b * p.width + (t >> p.log_page)];
-                    if (pg >= p.pages) pg = -1;
+            // lane l: tokens 4 l .. 4 l + 3 of a tile, the next tile's loaded ahead
+            float4 nk, nv;
+            bool nthere;
+            auto load = [&](int k) {
+                const int64_t row = k < T ? tree_row(p, w, (w.t0 + k) * kTcTT + 4 * lane) : -1;
+                nthere = row >= 0;
+                nk = nv = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (nthere) {
+                    nk = *reinterpret_cast<const float4 *>(p.ks + row);
+                    nv = *reinterpret_cast<const float4 *>(p.vs + row);
                 }
-                const int st = it % RAW;
-                bool go = t_mbar_wait(&s.raw_empty[st], ((it / RAW) & 1) ^ 1, &s.abort_flag, p.err);
-                const uint32_t scs = (sc + k) % kSc;
-                if (!is_v) go &= t_mbar_wait(&s.sc_empty[scs], (((sc + k) / kSc) & 1) ^ 1, &s.abort_flag, p.err);
-                const uint32_t valid = __ballot_sync(0xffffffffu, pg >= 0 && go);
+            };
+            load(0);
+            for (int k = 0; k < T; ++k, ++sc) {
+                const uint32_t scs = sc % kSc;
+                const float4 ck = nk, cv = nv;
+                const bool there = nthere;
+                load(k + 1);
+                const uint32_t quads = __ballot_sync(0xffffffffu, there);
+                const bool masked = (w.t0 + k + 1) * kTcTT > w.s.ctx || quads != 0xffffffffu;
+                const int ek = KFOLD ? tile_exponent(ck) : 0, ev = tile_exponent(cv);
+                uint32_t chunks = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) chunks |= ((quads >> (4 * c)) & 1) << c;
+                warp_wait(&s.sc_empty[scs], ((sc / kSc) & 1) ^ 1, &s.abort_flag, p.err);
+                if (!KFOLD || masked) reinterpret_cast<float4 *>(s.ks[scs])[lane] = ck;
+                if (masked) reinterpret_cast<float4 *>(s.vs[scs])[lane] = cv;
                 if (lane == 0) {
-                    t_mbar_expect(&s.raw_full[st], __popc(valid) * bt * RB);
-                    if (!is_v) {
-                        s.valid[scs] = valid;
-                        t_mbar_expect(&s.sc_full[scs], __popc(valid) * bt * 8);
-                    }
+                    s.unit[scs] = masked ? make_float2(0.f, 0.f) : make_float2(pow2(ek), (float)ev);
+                    s.valid[scs] = chunks;
                 }
                 __syncwarp();
-                if ((valid >> lane) & 1) {
-                    const int64_t row = ((pg * p.kv_heads + w.h) << p.log_page) + (t & ((1 << p.log_page) - 1));
-                    t_tma_2d(s.rawt[st] + lane * bt * RB, is_v ? &tmv : &tmk, &s.raw_full[st], (int)row);
-                    if (!is_v) {
-                        t_bulk(&s.ks[scs][lane * bt], p.ks + row, bt * 4, &s.sc_full[scs]);
-                        t_bulk(&s.vs[scs][lane * bt], p.vs + row, bt * 4, &s.sc_full[scs]);
-                    }
-                }
+                if (lane == 0) t_mbar_arrive(&s.sc_full[scs]);
             }
-            sc += T;
         }
     } else if (warp == 1) {
         // ---------------- MMA ----------------
@@ -519,67 +558,85 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
             at += T;
             const int rows = min(ROWS, w.s.n * p.group - w.mt * ROWS);        // of the block
 
-            // ---- q~: each warp 32 (NT = 2) or 16 rows of the block's ----
-            {
-                constexpr int RW = ROWS / kSoftWarps, U = 8;         // U rows in flight
-                float sg[E];
-                lane_signs<E>(sg, lane, p.seed);
+            // ---- q~: four threads to a row, a quarter of its dims each; butterflies in
+            // registers but for two exchanges ----
 #pragma unroll 1
-                for (int i = 0; i < RW; i += U) {
-                    const int r0 = (warp - 4) * RW + i;
-                    float v[U][E], top[U], sum[U];
+            for (int pass = 0; pass < 2 * NT; ++pass) {
+                constexpr int HD = D / 4;
+                const int hf = threadIdx.x & 3, r = pass * 64 + ((threadIdx.x - 128) >> 2), rr = r & 127, gr = w.mt * ROWS + r;
+                float2 v[HD / 2];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int gr = w.mt * ROWS + r0 + u;
-                        const char *src = static_cast<const char *>(p.q) +
-                                          ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head) * 2;
+                for (int i = 0; i < HD / 2; ++i) v[i] = make_float2(0.f, 0.f);
+                if (r < rows) {
+                    const char *src = static_cast<const char *>(p.q) +
+                                      ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head + hf * HD) * 2;
 #pragma unroll
-                        for (int e = 0; e < E; ++e) v[u][e] = r0 + u < rows ? load_elem<IN>(src, lane * E + e) : 0.f;
+                    for (int i = 0; i < HD / 8; ++i) {
+                        float f[8];
+                        unpack16<IN>(reinterpret_cast<const uint4 *>(src)[i], f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[4 * i + e] = make_float2(f[2 * e], f[2 * e + 1]);
                     }
+                }
+                auto signs = [&] {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        warp_rotate<E>(v[u], sg, lane, signs_first, inv_sqrt_dim<D>());
-                        top[u] = 0.f;
-#pragma unroll
-                        for (int e = 0; e < E; ++e) top[u] = fmaxf(top[u], fabsf(v[u][e]));
+                    for (int i = 0; i < HD / 2; ++i) {
+                        const uint32_t m = s.sign_words[(hf * HD + 2 * i) >> 5] >> ((hf * HD + 2 * i) & 31);
+                        v[i].x = __uint_as_float(__float_as_uint(v[i].x) ^ (m << 31));
+                        v[i].y = __uint_as_float(__float_as_uint(v[i].y) ^ ((m >> 1) << 31));
                     }
+                };
+                if (signs_first) signs();
 #pragma unroll
-                    for (int o = 16; o; o >>= 1)
+                for (int i = 0; i < HD / 2; ++i) v[i] = make_float2(v[i].x + v[i].y, v[i].x - v[i].y);
 #pragma unroll
-                        for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+                for (int st = 1; st < HD / 2; st <<= 1)
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int r = r0 + u, rr = r & 127;
-                        int ex = (int)((__float_as_uint(top[u]) >> 23) & 255u) - 126;      // top < 2^ex
-                        ex = max(-100, min(ex, 104));
-                        top[u] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.score_scale;
-                        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                        sum[u] = 0.f;
+                    for (int i = 0; i < HD / 2; ++i)
+                        if (!(i & st)) {
+                            const float2 x = v[i], y = v[i + st];
+                            v[i] = __fadd2_rn(x, y);
+                            v[i + st] = __ffma2_rn(y, make_float2(-1.f, -1.f), x);
+                        }
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const int d = lane * E + e;
-                            const int pos = ((d & 3) << 1) + ((d >> 2) & 1);
-                            const uint32_t off = (uint32_t)((d >> 6) * S::PANEL + rr * 128 + ((((d & 63) >> 3) ^ (rr & 7)) << 4) + pos * 2);
-                            const float x = v[u][e] * down * (d & 1 ? 0.0625f : 1.f);
-                            const __half hi = __float2half_rn(x);
-                            float got = __half2float(hi);
-                            *reinterpret_cast<__half *>(s.q[NT == 2 ? r >> 7 : 0] + off) = hi;
-                            if constexpr (HV == 2) {
-                                const __half lo = __float2half_rn(x - got);
-                                got += __half2float(lo);
-                                *reinterpret_cast<__half *>(s.q[1] + off) = lo;
-                            }
-                            sum[u] += got * (d & 1 ? 16.f : 1.f);
+                for (int st = 1; st < 4; st <<= 1) {
+                    const float sg = hf & st ? -1.f : 1.f;
+#pragma unroll
+                    for (int i = 0; i < HD / 2; ++i) {
+                        const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v[i].x, st), __shfl_xor_sync(0xffffffffu, v[i].y, st));
+                        v[i] = __ffma2_rn(v[i], make_float2(sg, sg), o);
+                    }
+                }
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < HD / 2; ++i) top = max3(top, fabsf(v[i].x), fabsf(v[i].y));
+                if (!signs_first) signs();
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // top < 2^ex: q~ enters the MMA relative to that
+                const int ex = max(-100, min((int)((__float_as_uint(top) >> 23) & 255u) - 126, 120));
+                if (hf == 0) s.rfac[r] = pow2(ex) * inv_sqrt_dim<D>() * p.score_scale;
+                const float down = pow2(-ex);
+                uint8_t *const dst = s.q[NT == 2 ? r >> 7 : 0] + rr * 128;
+#pragma unroll
+                for (int i = 0; i < HD / 8; ++i) {
+                    uint32_t h[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {          // dims j and j + 4 of the group
+                        const float2 u0 = v[4 * i + (j >> 1)], u1 = v[4 * i + 2 + (j >> 1)];
+                        const float x = (j & 1 ? u0.y : u0.x) * down, y = (j & 1 ? u1.y : u1.x) * down;
+                        const __half2 hh = __floats2half2_rn(x, y);
+                        h[j] = *reinterpret_cast<const uint32_t *>(&hh);
+                        if constexpr (HV == 2) {
+                            const float2 got = __half22float2(hh);
+                            const __half2 ll = __floats2half2_rn(x - got.x, y - got.y);
+                            lo[j] = *reinterpret_cast<const uint32_t *>(&ll);
                         }
                     }
-#pragma unroll
-                    for (int o = 16; o; o >>= 1)
-#pragma unroll
-                        for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
-                    if (lane == 0) {
-#pragma unroll
-                        for (int u = 0; u < U; ++u) s.rfac[r0 + u] = make_float2(top[u] * 16777216.f, -8.f * sum[u] * top[u]);
-                    }
+                    const int d = hf * HD + 8 * i;
+                    const uint32_t off = (d >> 6) * S::PANEL + ((((d & 63) >> 3) ^ (rr & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(dst + off) = make_uint4(h[0], h[1], h[2], h[3]);
+                    if constexpr (HV == 2) *reinterpret_cast<uint4 *>(dst + S::TILE + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -587,11 +644,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
             if (lane == 0) t_mbar_arrive(&s.q_full);
             both_sync();
             const int brow = (NT == 2 ? team * 128 : 0) + row;               // row of the block
-            const float2 fac = s.rfac[brow];
+            const float fac = s.rfac[brow];
             const bool idle = (NT == 2 ? team * 128 : 0) + quarter * 32 >= rows;     // no row of this warp exists
             const int node = (w.mt * ROWS + brow) / p.group;
-            const uint32_t all = (uint32_t)((1ull << (kTcTT / min(kTcTT, 1 << p.log_page))) - 1);
-            SoftRow r{-INFINITY, 0.f, 1.f};
+            SoftRow r{-INFINITY, 0.f};
             bool first = true;
             for (int k = NT == 2 ? 0 : team; k < T; k += NT == 2 ? 1 : 2, ++uses) {
                 const uint32_t scs = (sc + k) % kSc;
@@ -601,23 +657,25 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
                 tc_fence_after();
                 if (ok && !idle) {
                     const int t0 = (w.t0 + k) * kTcTT;
-                    const uint32_t valid = s.valid[scs];
-                    const bool masked = t0 + kTcTT > w.s.ctx || valid != all;
-                    r.F = 1.f;
-                    const int fast = masked ? 0 : soft_tile(tS[team] + lanes, s.ks[scs], s.vs[scs], fac, r);
-#pragma unroll 1
-                    for (int c = fast; c < kTcTT / kCW; ++c) {
-                        const uint32_t vis = masked ? tree_visible(p, w, node, t0 + kCW * c, kCW * c, valid) : 0xffffu;
-                        soft_careful(tS[team] + lanes, c, s.ks[scs] + kCW * c, s.vs[scs] + kCW * c, fac, vis, r);
+                    const float2 unit = s.unit[scs];
+                    const bool masked = unit.x == 0.f;
+                    const float a = masked ? fac : fac * unit.x, ev = unit.y;
+                    float f;
+                    if (!masked) {
+                        f = soft_tile<!KFOLD>(tS[team] + lanes, s.ks[scs], a, ev, r);
+                    } else {
+                        const int wrow = w.mt * ROWS + brow - lane;
+                        f = soft_masked(p, w.s, tS[team] + lanes, s.ks[scs], s.vs[scs], a, node, wrow / p.group,
+                                        min((wrow + 31) / p.group, w.s.n - 1), t0, s.valid[scs], r);
                     }
-                    if (!first && __any_sync(0xffffffffu, r.F != 1.f)) {
+                    if (!first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t x[32];
                             tm_ld32(tO[team] + lanes + 32 * c, x);
                             tc_wait_ld32(x);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * r.F);
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
                             tm_st32(tO[team] + lanes + 32 * c, x);
                         }
                     }
@@ -640,7 +698,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
                 ++units;
             }
             tc_fence_after();
-            float M = r.M, l = r.l;
+            float l = r.l, M = r.M == -INFINITY && !(l == 0.f) ? 0.f : r.M;          // nothing but NaN seen: any reference
             l = fminf(l, 3.4028234e38f) + (l != l ? l : 0.f);                 // keeps NaN, bounds infinity
             float fa = 1.f, fb = 0.f;                                         // factors of the teams' accumulators
             if constexpr (NT == 1) {
@@ -774,55 +832,106 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
         }
     } else if (warp >= 4 + kSoftWarps) {
         // ---------------- converters ----------------
-        const int ct = threadIdx.x - 32 * (4 + kSoftWarps);                  // 0 .. 127
-        uint32_t it = 0;
+        const int ct = threadIdx.x & (32 * kTeamWarps - 1);                  // thread of the team
+        const uint32_t cteam = (warp - 4 - kSoftWarps) / kTeamWarps;
+        // 16 bytes of codes: 32 dims of one token -> four 16-byte pieces of the operand.  A
+        // warp loads 8 whole rows at a time; 8 lanes store 8 rows of one piece, so that no
+        // two share a bank.  Thread: chunk ch of rows r0, r0 + RSTEP, ...
+        constexpr int CH = RB / 16, N = kTcTT * CH / (32 * kTeamWarps), RSTEP = kTcTT / N;
+        const int r0 = (ct & 7) | ((ct / (8 * CH)) << 3), ch = (ct >> 3) % CH;
+        uint8_t *const dst0 = s.op[0] + (ch >> 1) * S::PANEL + r0 * 128;
+        uint32_t piece[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) piece[q] = (uint32_t)(((ch & 1) * 4 + q) ^ (r0 & 7)) << 4;
+        uint32_t base = 0, sc = 0;                       // items and tiles of earlier stretches
         for (int64_t at = begin; at < end;) {
             const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
             const int T = w.t1 - w.t0;
             at += T;
-            for (int i = 0; i < 2 * T; ++i, ++it) {
-                const int st = it % RAW, slot = it % kOps;
+            // a pipeline of three items: pages of the second next, codes and scales of the next
+            int32_t pg[N];
+            uint4 nx[N];
+            float nf[N];
+            auto pages = [&](int i) {
                 int k;
                 bool is_v;
                 item_at<NT>(i, T, k, is_v);
-                bool ok = t_mbar_wait(&s.raw_full[st], (it / RAW) & 1, &s.abort_flag, p.err);
-                ok = t_mbar_wait(&s.op_empty[slot], ((it / kOps) & 1) ^ 1, &s.abort_flag, p.err) && ok;
-                if (ok) {
-                    // 16 bytes of codes: 32 dims of one token -> four 16-byte pieces of the operand.
-                    // 8 lanes take 8 rows of one chunk: no bank conflicts on either side.
-                    constexpr int CH = RB / 16, N = kTcTT * CH / (32 * kConvWarps);
-                    uint4 x[N];
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        const int u = ct + n * 32 * kConvWarps;
-                        const int r = (u & 7) | ((u / (8 * CH)) << 3), ch = (u >> 3) % CH;
-                        const int sw = CH == 4 ? ch ^ ((r >> 1) & 3) : ch ^ ((r >> 2) & 1);
-                        x[n] = *reinterpret_cast<const uint4 *>(s.rawt[st] + r * RB + sw * 16);
+                for (int n = 0; n < N; ++n) {
+                    const int t = (w.t0 + k) * kTcTT + r0 + n * RSTEP;
+                    pg[n] = -1;
+                    if (i < 2 * T && t < w.s.len) pg[n] = p.table[w.b * p.width + (t >> p.log_page)];
+                }
+            };
+            auto load = [&](int i) {
+                int k;
+                bool is_v;
+                item_at<NT>(i, T, k, is_v);
+                const uint8_t *codes = (is_v ? p.vq : p.kq) + ch * 16;
+                const float *scales = is_v ? p.vs : p.ks;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const int t = (w.t0 + k) * kTcTT + r0 + n * RSTEP;
+                    nx[n] = make_uint4(0u, 0u, 0u, 0u);
+                    nf[n] = 0.f;
+                    if (pg[n] >= 0 && pg[n] < p.pages) {
+                        const int64_t row = (((int64_t)pg[n] * p.kv_heads + w.h) << p.log_page) + (t & ((1 << p.log_page) - 1));
+                        nx[n] = ld_once(codes + row * RB);
+                        if (is_v || KFOLD) nf[n] = scales[row];
                     }
+                }
+            };
+            int i = (int)((cteam + kConvTeams - base % kConvTeams) % kConvTeams);       // this team's next item
+            pages(i);
+            load(i);
+            pages(i + kConvTeams);
+            for (; i < 2 * T; i += kConvTeams) {
+                const uint32_t it = base + i, slot = it % kOps;
+                int k;
+                bool is_v;
+                item_at<NT>(i, T, k, is_v);
+                uint4 x[N];
+                float f[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    x[n] = nx[n];
+                    f[n] = nf[n];
+                }
+                load(i + kConvTeams);
+                pages(i + 2 * kConvTeams);
+                const uint32_t scs = (sc + k) % kSc;
+                bool ok = warp_wait(&s.sc_full[scs], ((sc + k) / kSc) & 1, &s.abort_flag, p.err);
+                ok = warp_wait(&s.op_empty[slot], ((it / kOps) & 1) ^ 1, &s.abort_flag, p.err) && ok;
+                if (ok) {
+                    const float2 unit = s.unit[scs];
+                    const bool fold = unit.x != 0.f && (is_v || KFOLD);
+                    const float down = is_v ? pow2(-(int)unit.y) : __uint_as_float((254u << 23) - __float_as_uint(unit.x));   // 1 / 2^ek
+                    uint8_t *const dst = dst0 + slot * S::TILE;
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        const int u = ct + n * 32 * kConvWarps;
-                        const int r = (u & 7) | ((u / (8 * CH)) << 3), ch = (u >> 3) % CH;
                         const uint32_t xw[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-                        uint8_t *dst = s.op[slot] + (ch >> 1) * S::PANEL + r * 128;
+                        const float fn = fold ? f[n] * down : 1.f;
+                        const __half fh = __float2half_rn(fn);
+                        const __half2 hi = __half2half2(fh), lo = __float2half2_rn(fn - __half2float(fh));
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            *reinterpret_cast<uint4 *>(dst + ((((ch & 1) * 4 + q) ^ (r & 7)) << 4)) =
-                                is_v ? v_operands(xw[q]) : k_operands(xw[q]);
+                            *reinterpret_cast<uint4 *>(dst + n * RSTEP * 128 + piece[q]) = operands(xw[q], hi, lo);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
                     t_mbar_arrive(&s.op_full[slot]);
-                    t_mbar_arrive(&s.raw_empty[st]);
+                    if (is_v) t_mbar_arrive(&s.sc_empty[scs]);
                 }
             }
+            base += 2 * T;
+            sc += T;
         }
     }
 
     __syncwarp();
-    // no copy and no MMA outlives the block, also when it gave up
+    // no MMA outlives the block, also when it gave up
     if (s.abort_flag) {
         const long long t0 = clock64();
         while (clock64() - t0 < 20000000ll) __nanosleep(1000);
@@ -836,14 +945,14 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_consta
 }
 
 template <int IN, int D, int NT, int HV>
-cudaError_t launch_tc(TreeParams &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
+cudaError_t launch_tc(TreeParams &p, cudaStream_t stream) {
     auto kern = attn_tree_tc_kernel<IN, D, NT, HV>;
     const size_t smem = sizeof(TSmem<D, NT, HV>) + 1024;
     static_assert(sizeof(TSmem<D, NT, HV>) + 1024 <= 232448, "shared memory of one block");
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem((const void *)kern, smem, allowed);
     if (e != cudaSuccess) return e;
-    kern<<<p.ctas, kTcThreads, smem, stream>>>(mk, mv, p);
+    kern<<<p.ctas, kTcThreads, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int bph = (int)(((int64_t)p.max_nodes * p.group + 128 * NT - 1) / (128 * NT));
@@ -876,14 +985,12 @@ cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream) {
     const int64_t bph = (rows + 128 * nt - 1) / (128 * nt);
     const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTcTT - 1) / kTcTT);
     p.ctas = (int)(max_tiles < sms ? max_tiles : sms);
-    CUtensorMap mk, mv;
-    if (!tree_maps(c, kTcTT, mk, mv)) return cudaErrorInvalidValue;
     const bool d128 = c.head_dim == 128;
     if (c.in_type == IN_F16)
-        return d128 ? launch_tc<IN_F16, 128, 1, 2>(p, mk, mv, stream) : launch_tc<IN_F16, 64, 1, 2>(p, mk, mv, stream);
+        return d128 ? launch_tc<IN_F16, 128, 1, 2>(p, stream) : launch_tc<IN_F16, 64, 1, 2>(p, stream);
     if (nt == 2)
-        return d128 ? launch_tc<IN_BF16, 128, 2, 1>(p, mk, mv, stream) : launch_tc<IN_BF16, 64, 2, 1>(p, mk, mv, stream);
-    return d128 ? launch_tc<IN_BF16, 128, 1, 1>(p, mk, mv, stream) : launch_tc<IN_BF16, 64, 1, 1>(p, mk, mv, stream);
+        return d128 ? launch_tc<IN_BF16, 128, 2, 1>(p, stream) : launch_tc<IN_BF16, 64, 2, 1>(p, stream);
+    return d128 ? launch_tc<IN_BF16, 128, 1, 1>(p, stream) : launch_tc<IN_BF16, 64, 1, 1>(p, stream);
 }
 
 }  // namespace rq

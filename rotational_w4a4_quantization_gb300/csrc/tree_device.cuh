@@ -17,6 +17,7 @@ namespace {
 struct TreeParams {
     const void *q;
     int64_t q_token, q_head;            // strides in elements
+    const uint8_t *kq, *vq;
     const float *ks, *vs;
     const int32_t *table, *contexts, *offsets;
     const uint8_t *mask;                // [rows][mask_stride], NULL: causal among the nodes
@@ -38,6 +39,8 @@ inline bool tree_params(const TreeCall &c, TreeParams &p) {
     p.q = c.q;
     p.q_token = c.q_token;
     p.q_head = c.q_head;
+    p.kq = c.cache.kq;
+    p.vq = c.cache.vq;
     p.ks = c.cache.ks;
     p.vs = c.cache.vs;
     p.table = c.table;

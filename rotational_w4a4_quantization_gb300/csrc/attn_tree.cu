@@ -10,18 +10,22 @@
 //  * A block of 4 warps streams tiles of 64 tokens through a TMA ring; each warp
 //    takes 16 of them.  A tile is codes of K and V (rows of D/2 bytes, swizzled by
 //    the TMA so that the reads below are free of bank conflicts) and their scales.
-//  * S = Q K^T: a lane reads the codes of a token straight into the B operand: the
-//    nibbles of a word, taken 4 bits apart, are pairs of fp16 (0x6400 | code + 8 is
-//    1024 + code + 8; one subtraction leaves the code, exactly).  The order of the
-//    dims is the same permutation on both sides and drops out.
+//  * S = Q K^T: a lane reads the codes of a token straight into the B operand: nibbles j
+//    and j + 4 of a word are a pair, and u = code + 8 in the low bits of an fp16 is the
+//    subnormal u 2^-24 (16 u 2^-24 for odd j; q~ holds a sixteenth there): one logic
+//    operation per pair and no arithmetic.  The row's factors take 2^24 and 8 sum q~ out
+//    again, s = (a S + b) ks.  The order of the dims is the same permutation on both
+//    sides and drops out.  fp32 queries subtract 8 from the codes instead: the offset
+//    costs 5 bits of the sum.
 //  * softmax on the fragments, base 2, with a lazy reference: it moves only when a
 //    score passes it by 8, so the accumulators are rarely rescaled.
 //  * O += (P vs) V: ldmatrix.trans pairs the codes of two tokens in a register, which
 //    is the B operand after the same nibble step.  P vs is rounded to fp16 (11 bits,
 //    below the rounding of 16-bit outputs), vs relative to a power of two that moves
 //    like the softmax's reference.
-//  * fp32 queries: q~ and P vs are split into two fp16 halves (22 bits) and the
-//    products run twice; codes are exact in either.
+//  * fp32 queries: q~ and P vs are split into two fp16 parts (22 bits) and the products
+//    run twice; codes are exact in either.  fp16 queries split q~ alone: their outputs
+//    resolve its rounding to 11 bits (4.6e-4 against 2.5e-4 of an output).
 #include "rq.h"
 #include "rq_internal.h"
 #include "tree_device.cuh"
@@ -32,18 +36,23 @@ namespace {
 constexpr int kRows = 16, kTT = 64, kStages = 4, kCWarps = 4;
 constexpr int kMThreads = 32 * (kCWarps + 1);
 
+// Blocks that share an SM: what the registers of the fragments allow.
+constexpr int blocks_per_sm(int in_type, int64_t head_dim) {
+    return head_dim == 256 ? (in_type == IN_BF16 ? 2 : 1) : (in_type == IN_BF16 ? 3 : 2);
+}
+
 template <int IN, int D>
 struct MSmem {
     static constexpr int RB = D / 2;
-    static constexpr int HALVES = IN == IN_F32 ? 2 : 1;
-    static constexpr int QS = D + 8;                 // row stride of q~ in halves
+    static constexpr int HQ = IN == IN_BF16 ? 1 : 2, HP = IN == IN_F32 ? 2 : 1;   // fp16 parts of q~, of the weights
     alignas(1024) uint8_t kq[kStages][kTT * RB];
     alignas(1024) uint8_t vq[kStages][kTT * RB];
     alignas(16) float ks[kStages][kTT];
     alignas(16) float vs[kStages][kTT];
-    alignas(16) __half q[HALVES][kRows * QS];
+    alignas(16) uint32_t q[HQ][D / 16][32][4];         // q~ as A fragments: k step, lane, register
     float acc[2][kRows][D + 4];                      // the warps' sums, joined two by two
-    float ref[kCWarps][kRows], sum[kCWarps][kRows], rscale[kRows];
+    float ref[kCWarps][kRows], sum[kCWarps][kRows];
+    float2 rfac[kRows];                              // a, b
     int vexp[kCWarps];
     int64_t prefix[kScan + 1];
     alignas(8) uint64_t full[kStages], empty[kStages];
@@ -57,11 +66,29 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// nibbles j and j + 4 of x (codes with the sign bit flipped) as two fp16 codes
-__device__ __forceinline__ uint32_t nibble_pair(uint32_t x, int j) {
-    const uint32_t t = ((x >> (4 * j)) & 0x000f000fu) | 0x64006400u;
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&t), __half2half2(__ushort_as_half(0x6408)));   // 1032
-    return *reinterpret_cast<const uint32_t *>(&h);
+// A word of 8 codes as four pairs (nibbles j and j + 4) of fp16 codes, exactly.  0x6400 | u
+// is 1024 + u, so nibbles 0 and 4 (u = code + 8 after the sign bit's flip) lose 1032;
+// nibbles 1 and 5, which stay four bits up, are 1024 + 16 u: times 1/16, less 72.
+__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&r)[4]) {
+    const __half2 m0 = __half2half2(__ushort_as_half(0xe408)), r16 = __half2half2(__ushort_as_half(0x2c00)),
+                  m1 = __half2half2(__ushort_as_half(0xd480));             // -1032, 1/16, -72
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        const uint32_t y = x >> (4 * j);
+        const uint32_t a = (y & 0x000f000fu) ^ 0x64086408u, b = (y & 0x00f000f0u) ^ 0x64806480u;
+        const __half2 ha = __hadd2(*reinterpret_cast<const __half2 *>(&a), m0);
+        const __half2 hb = __hfma2(*reinterpret_cast<const __half2 *>(&b), r16, m1);
+        r[j] = *reinterpret_cast<const uint32_t *>(&ha);
+        r[j + 1] = *reinterpret_cast<const uint32_t *>(&hb);
+    }
+}
+// The same as subnormals u 2^-24 and 16 u 2^-24.
+__device__ __forceinline__ void offset_pairs(uint32_t x, uint32_t (&r)[4]) {
+    const uint32_t y = x >> 8;
+    r[0] = (x ^ 0x00080008u) & 0x000f000fu;
+    r[1] = (x ^ 0x00800080u) & 0x00f000f0u;
+    r[2] = (y ^ 0x00080008u) & 0x000f000fu;
+    r[3] = (y ^ 0x00800080u) & 0x00f000f0u;
 }
 
 // byte address of 16-byte chunk `ch` of row `row` in a tile written by TMA
@@ -80,13 +107,13 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 __device__ __forceinline__ float2 unpack_h2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
 
 template <int IN, int D>
-__global__ void __launch_bounds__(kMThreads, IN == IN_F32 || D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(kMThreads, blocks_per_sm(IN, D))
 attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ TreeParams p) {
     using S = MSmem<IN, D>;
-    constexpr int RB = D / 2, WPT = D / 32, E = D / 32, HV = S::HALVES;
+    constexpr int RB = D / 2, WPT = D / 32, E = D / 32, HQ = S::HQ, HP = S::HP;
+    constexpr bool kOffset = IN != IN_F32;             // keys as u = code + 8 (see the top)
     constexpr int NQ = D / 32;                        // 16-byte chunks of a code row
-    constexpr bool kQRegs = D <= 128;                 // q~ fragments kept in registers
     extern __shared__ uint8_t raw[];
     S &s = *reinterpret_cast<S *>(raw + ((1024u - (t_smem(raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -185,37 +212,39 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             // 2^ex > top, within what a float's exponent holds
             int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 126;
-            ex = max(-100, min(ex, 120));
+            ex = max(-100, min(ex, 100));
             const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-            if (lane == 0) s.rscale[r] = up * p.score_scale;
+            float qsum = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int d = lane * E + e;
-                const int at_q = r * S::QS + (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1);   // 0 4 1 5 2 6 3 7
-                const float x = v[e] * down;
+                // lane column c of the fragments covers words of 8 dims: those of the 16-byte
+                // chunk(s) of a code row that its K operand comes from
+                const int d = lane * E + e, j = d & 3;
+                const int fc = D == 256 ? (d >> 5) & 3 : d / (D / 4), wd = D == 256 ? ((d >> 7) << 2) + ((d & 31) >> 3) : (d % (D / 4)) >> 3;
+                const int at_q = (((2 * wd + (j >> 1)) * 32 + (r & 7) * 4 + fc) * 4 + (j & 1) * 2 + (r >> 3)) * 2 + ((d >> 2) & 1);
+                const float x = v[e] * (kOffset && (d & 1) ? 0.0625f * down : down);
                 const __half hi = __float2half_rn(x);
-                s.q[0][at_q] = hi;
-                if constexpr (HV == 2) s.q[1][at_q] = __float2half_rn(x - __half2float(hi));
+                float got = __half2float(hi);
+                reinterpret_cast<__half *>(s.q[0])[at_q] = hi;
+                if constexpr (HQ == 2) {
+                    const __half lo = __float2half_rn(x - got);
+                    reinterpret_cast<__half *>(s.q[1])[at_q] = lo;
+                    got += __half2float(lo);
+                }
+                qsum += d & 1 ? 16.f * got : got;
+            }
+            if constexpr (kOffset) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) qsum += __shfl_xor_sync(0xffffffffu, qsum, o);
+            }
+            if (lane == 0) {
+                const float a = up * p.score_scale;
+                s.rfac[r] = kOffset ? make_float2(a * 16777216.f, -8.f * qsum * a) : make_float2(a, 0.f);
             }
         }
         cta_sync();
 
-        // fragments of q~: word wd of lane column c covers dims base .. base + 7
-        auto q_frag = [&](int half, int wd, uint32_t (&a)[2][4]) {
-            const int base = (D == 256 ? (wd < 4 ? c * 32 : (c + 4) * 32) + 8 * (wd & 3) : c * (D / 4) + 8 * wd);
-            const uint4 x = *reinterpret_cast<const uint4 *>(&s.q[half][g * S::QS + base]);
-            const uint4 y = *reinterpret_cast<const uint4 *>(&s.q[half][(g + 8) * S::QS + base]);
-            a[0][0] = x.x; a[0][2] = x.y; a[1][0] = x.z; a[1][2] = x.w;
-            a[0][1] = y.x; a[0][3] = y.y; a[1][1] = y.z; a[1][3] = y.w;
-        };
-        uint32_t qa[kQRegs ? HV : 1][kQRegs ? WPT : 1][2][4];
-        if constexpr (kQRegs) {
-#pragma unroll
-            for (int hv = 0; hv < HV; ++hv)
-#pragma unroll
-                for (int wd = 0; wd < WPT; ++wd) q_frag(hv, wd, qa[hv][wd]);
-        }
-        const float rs0 = s.rscale[g], rs1 = s.rscale[g + 8];
+        const float2 rs0 = s.rfac[g], rs1 = s.rfac[g + 8];
 
         float acc[NQ * 4][4];
 #pragma unroll
@@ -233,41 +262,42 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             if (ok && t_first < w.s.len) {
                 // ---- S = Q K^T ----
                 float sc[2][4];
+                uint32_t kw[2][WPT];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sc[t][k] = 0.f;
                     const int row = tk + t * 8 + g;
-                    uint32_t kw[WPT];
                     if constexpr (D == 32) {
-                        kw[0] = *reinterpret_cast<const uint32_t *>(s.kq[st] + row * RB + 4 * c);
+                        kw[t][0] = *reinterpret_cast<const uint32_t *>(s.kq[st] + row * RB + 4 * c);
                     } else if constexpr (D == 64) {
                         const uint2 x = *reinterpret_cast<const uint2 *>(s.kq[st] + tile_chunk<RB>(row, c >> 1) + 8 * (c & 1));
-                        kw[0] = x.x; kw[1] = x.y;
+                        kw[t][0] = x.x; kw[t][1] = x.y;
                     } else {
 #pragma unroll
                         for (int i = 0; i < WPT / 4; ++i) {
                             const uint4 x = *reinterpret_cast<const uint4 *>(s.kq[st] + tile_chunk<RB>(row, c + 4 * i));
-                            kw[4 * i] = x.x; kw[4 * i + 1] = x.y; kw[4 * i + 2] = x.z; kw[4 * i + 3] = x.w;
+                            kw[t][4 * i] = x.x; kw[t][4 * i + 1] = x.y; kw[t][4 * i + 2] = x.z; kw[t][4 * i + 3] = x.w;
                         }
                     }
+                }
 #pragma unroll
-                    for (int wd = 0; wd < WPT; ++wd) {
-                        const uint32_t x = kw[wd] ^ 0x88888888u;
-                        const uint32_t b[4] = {nibble_pair(x, 0), nibble_pair(x, 1), nibble_pair(x, 2), nibble_pair(x, 3)};
+                for (int wd = 0; wd < WPT; ++wd) {
+                    uint32_t b[2][4];
 #pragma unroll
-                        for (int hv = 0; hv < HV; ++hv) {
-                            if constexpr (kQRegs) {
-                                mma16816(sc[t], qa[hv][wd][0], b[0], b[1]);
-                                mma16816(sc[t], qa[hv][wd][1], b[2], b[3]);
-                            } else {
-                                uint32_t a[2][4];
-                                q_frag(hv, wd, a);
-                                mma16816(sc[t], a[0], b[0], b[1]);
-                                mma16816(sc[t], a[1], b[2], b[3]);
-                            }
-                        }
+                    for (int t = 0; t < 2; ++t) {
+                        if constexpr (kOffset) offset_pairs(kw[t][wd], b[t]);
+                        else code_pairs(kw[t][wd], b[t]);
                     }
+#pragma unroll
+                    for (int hv = 0; hv < HQ; ++hv)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * wd + i][lane]);
+                            const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+                            mma16816(sc[0], a, b[0][2 * i], b[0][2 * i + 1]);
+                            mma16816(sc[1], a, b[1][2 * i], b[1][2 * i + 1]);
+                        }
                 }
                 // ---- scales, mask ----
                 float kscale[2][2], vscale[2][2];
@@ -281,7 +311,10 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[t][k] *= kscale[t][k & 1] * (k < 2 ? rs0 : rs1);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = k < 2 ? rs0 : rs1;
+                        sc[t][k] = (kOffset ? fmaf(sc[t][k], f.x, f.y) : sc[t][k] * f.x) * kscale[t][k & 1];
+                    }
                 const int bt = min(kTT, 1 << p.log_page);
                 const uint32_t valid = s.valid[st];
                 if (t_first + 16 > w.s.ctx || valid != (uint32_t)((1ull << (kTT / bt)) - 1)) {
@@ -337,7 +370,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     }
                 }
                 // ---- weights ----
-                uint32_t pa[HV][4];
+                uint32_t pa[HP][4];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const float p0 = ex2(sc[t][0] - z0), p1 = ex2(sc[t][1] - z0);
@@ -353,7 +386,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     if (sc[t][3] == -INFINITY) w3 = 0.f;
                     pa[0][2 * t] = pack_h2(w0, w1);
                     pa[0][2 * t + 1] = pack_h2(w2, w3);
-                    if constexpr (HV == 2) {
+                    if constexpr (HP == 2) {
                         const float2 a = unpack_h2(pa[0][2 * t]), b = unpack_h2(pa[0][2 * t + 1]);
                         pa[1][2 * t] = pack_h2(w0 - a.x, w1 - a.y);
                         pa[1][2 * t + 1] = pack_h2(w2 - b.x, w3 - b.y);
@@ -361,14 +394,13 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 }
                 // ---- O += (P vs) V ----
                 auto pv = [&](int q, uint32_t x, uint32_t y) {
-                    x ^= 0x88888888u;
-                    y ^= 0x88888888u;
+                    uint32_t b0[4], b1[4];
+                    code_pairs(x, b0);
+                    code_pairs(y, b1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t b0 = nibble_pair(x, j), b1 = nibble_pair(y, j);
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int hv = 0; hv < HV; ++hv) mma16816(acc[4 * q + j], pa[hv], b0, b1);
-                    }
+                        for (int hv = 0; hv < HP; ++hv) mma16816(acc[4 * q + j], pa[hv], b0[j], b1[j]);
                 };
                 const uint32_t vbase = t_smem(s.vq[st]);
                 const int mrow = tk + ((lane >> 3) & 1) * 8 + (lane & 7);
@@ -506,7 +538,7 @@ cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, cons
 }  // namespace
 
 int64_t attn_tree_workspace(int64_t head_dim) {
-    const int64_t ctas = 2 * (int64_t)device_sm_count();
+    const int64_t ctas = 3 * (int64_t)device_sm_count();
     const int64_t small = 2 * ctas * kRows * (head_dim + 2) * (int64_t)sizeof(float);
     const int64_t wide = attn_tree_tc_workspace(head_dim);
     return small > wide ? small : wide;
@@ -519,7 +551,7 @@ cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
     if (!tree_params(c, p)) return cudaErrorUnknown;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorUnknown;
-    const int per_sm = c.in_type == IN_F32 || c.head_dim == 256 ? 1 : 2;
+    const int per_sm = blocks_per_sm(c.in_type, c.head_dim);
     const int64_t bph = (c.max_nodes * p.group + kRows - 1) / kRows;
     const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTT - 1) / kTT);
     p.ctas = (int)(max_tiles < per_sm * sms ? max_tiles : per_sm * sms);

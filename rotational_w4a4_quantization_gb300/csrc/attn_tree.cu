@@ -7,8 +7,8 @@
 // the nodes of a sequence together are the rows of one product, so the cache is read
 // once per 16 rows.
 //
-//  * A block of 4 warps streams tiles of 64 tokens through a TMA ring; each warp
-//    takes 16 of them.  A tile is codes of K and V (rows of D/2 bytes, swizzled by
+//  * A block of 4 warps streams tiles of 128 tokens through a TMA ring; each warp
+//    takes 32 of them (16 cost twice the waits, votes and query loads per token).  A tile is codes of K and V (rows of D/2 bytes, swizzled by
 //    the TMA so that the reads below are free of bank conflicts) and their scales.
 //  * S = Q K^T: a lane reads the codes of a token straight into the B operand: nibbles j
 //    and j + 4 of a word are a pair, and u = code + 8 in the low bits of an fp16 is the
@@ -33,12 +33,13 @@
 namespace rq {
 namespace {
 
-constexpr int kRows = 16, kTT = 64, kStages = 4, kCWarps = 4;
+constexpr int kRows = 16, kTT = 128, kStages = 3, kCWarps = 4;
+constexpr int kWT = kTT / kCWarps / 8;               // n8 tiles of tokens per warp and tile
 constexpr int kMThreads = 32 * (kCWarps + 1);
 
 // Blocks that share an SM: what the registers of the fragments allow.
 constexpr int blocks_per_sm(int in_type, int64_t head_dim) {
-    return head_dim == 256 ? (in_type == IN_BF16 ? 2 : 1) : (in_type == IN_BF16 ? 3 : 2);
+    return head_dim == 256 ? 1 : 2;
 }
 
 template <int IN, int D>
@@ -64,6 +65,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // A word of 8 codes as four pairs (nibbles j and j + 4) of fp16 codes, exactly.  0x6400 | u
@@ -191,30 +198,37 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 
         // ---- q~ of the block's rows: rotated in fp32, scaled by a power of two to below
         // 1 (its inverse goes into the row's score factor), rounded to fp16 once ----
-#pragma unroll 1
-        for (int i = 0; i < kRows / kCWarps; ++i) {
-            const int r = warp * (kRows / kCWarps) + i, gr = w.mt * kRows + r;
-            float v[E];
+        constexpr int RW = kRows / kCWarps;                  // rows warp, warp + 4, ... : all at once
+        float qv[RW][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = 0.f;
-            if (r < rows) {
-                const char *src = static_cast<const char *>(p.q) +
-                                  ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head) *
-                                      (IN == IN_F32 ? 4 : 2);
+        for (int i = 0; i < RW; ++i) {
+            const int r = i * kCWarps + warp, gr = w.mt * kRows + r;
+            const char *src = static_cast<const char *>(p.q) +
+                              ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head) *
+                                  (IN == IN_F32 ? 4 : 2);
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = load_elem<IN>(src, lane * E + e);
-                warp_rotate<E>(v, sg, lane, signs_first, inv_sqrt_dim<D>());
-            }
-            float top = 0.f;
+            for (int e = 0; e < E; ++e) qv[i][e] = r < rows ? load_elem<IN>(src, lane * E + e) : 0.f;
+        }
+        float top[RW], qsum[RW];
 #pragma unroll
-            for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
+        for (int i = 0; i < RW; ++i) {
+            warp_rotate<E>(qv[i], sg, lane, signs_first, inv_sqrt_dim<D>());
+            top[i] = 0.f;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int e = 0; e < E; ++e) top[i] = fmaxf(top[i], fabsf(qv[i][e]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < RW; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const int r = i * kCWarps + warp;
             // 2^ex > top, within what a float's exponent holds
-            int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 126;
-            ex = max(-100, min(ex, 100));
+            const int ex = max(-100, min((int)((__float_as_uint(top[i]) >> 23) & 255u) - 126, 100));
             const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-            float qsum = 0.f;
+            top[i] = up * p.score_scale;
+            qsum[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 // lane column c of the fragments covers words of 8 dims: those of the 16-byte
@@ -222,7 +236,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 const int d = lane * E + e, j = d & 3;
                 const int fc = D == 256 ? (d >> 5) & 3 : d / (D / 4), wd = D == 256 ? ((d >> 7) << 2) + ((d & 31) >> 3) : (d % (D / 4)) >> 3;
                 const int at_q = (((2 * wd + (j >> 1)) * 32 + (r & 7) * 4 + fc) * 4 + (j & 1) * 2 + (r >> 3)) * 2 + ((d >> 2) & 1);
-                const float x = v[e] * (kOffset && (d & 1) ? 0.0625f * down : down);
+                const float x = qv[i][e] * (kOffset && (d & 1) ? 0.0625f * down : down);
                 const __half hi = __float2half_rn(x);
                 float got = __half2float(hi);
                 reinterpret_cast<__half *>(s.q[0])[at_q] = hi;
@@ -231,16 +245,19 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     reinterpret_cast<__half *>(s.q[1])[at_q] = lo;
                     got += __half2float(lo);
                 }
-                qsum += d & 1 ? 16.f * got : got;
+                qsum[i] += d & 1 ? 16.f * got : got;
             }
-            if constexpr (kOffset) {
+        }
+        if constexpr (kOffset) {
 #pragma unroll
-                for (int o = 16; o; o >>= 1) qsum += __shfl_xor_sync(0xffffffffu, qsum, o);
-            }
-            if (lane == 0) {
-                const float a = up * p.score_scale;
-                s.rfac[r] = kOffset ? make_float2(a * 16777216.f, -8.f * qsum * a) : make_float2(a, 0.f);
-            }
+            for (int o = 16; o; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < RW; ++i) qsum[i] += __shfl_xor_sync(0xffffffffu, qsum[i], o);
+        }
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < RW; ++i)
+                s.rfac[i * kCWarps + warp] = kOffset ? make_float2(top[i] * 16777216.f, -8.f * qsum[i] * top[i]) : make_float2(top[i], 0.f);
         }
         cta_sync();
 
@@ -251,99 +268,101 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         for (int i = 0; i < NQ * 4; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f, l0 = 0.f, l1 = 0.f;   // z: finite reference
+        float z0 = 0.f, z1 = 0.f, l0 = 0.f, l1 = 0.f;                                     // references, sums
+        float lim0 = -INFINITY, lim1 = -INFINITY;                                         // a score beyond moves the reference
         int ve = -100;
         float vf = __uint_as_float((uint32_t)(127 + 100) << 23);                          // 2^-ve
 
+        const uint32_t all = (uint32_t)((1ull << (kTT / min(kTT, 1 << p.log_page))) - 1);
         for (int tile = w.t0; tile < w.t1; ++tile) {
             const bool ok = __all_sync(0xffffffffu, t_mbar_wait(&s.full[st], ph, &s.abort_flag, p.err));
-            const int tk = warp * 16;                                 // this warp's tokens of the tile
+            const int tk = warp * 8 * kWT;                            // this warp's tokens of the tile
             const int t_first = tile * kTT + tk;
             if (ok && t_first < w.s.len) {
                 // ---- S = Q K^T ----
-                float sc[2][4];
-                uint32_t kw[2][WPT];
+                float sc[kWT][4];
+                constexpr int KP = WPT < 4 ? WPT : 4;                 // words loaded at once
+                const uint8_t *krow = s.kq[st] + (tk + g) * RB;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int part = 0; part < WPT / KP; ++part) {
+                    uint32_t kw[kWT][KP];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[t][k] = 0.f;
-                    const int row = tk + t * 8 + g;
-                    if constexpr (D == 32) {
-                        kw[t][0] = *reinterpret_cast<const uint32_t *>(s.kq[st] + row * RB + 4 * c);
-                    } else if constexpr (D == 64) {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(s.kq[st] + tile_chunk<RB>(row, c >> 1) + 8 * (c & 1));
-                        kw[t][0] = x.x; kw[t][1] = x.y;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < WPT / 4; ++i) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(s.kq[st] + tile_chunk<RB>(row, c + 4 * i));
-                            kw[t][4 * i] = x.x; kw[t][4 * i + 1] = x.y; kw[t][4 * i + 2] = x.z; kw[t][4 * i + 3] = x.w;
+                    for (int t = 0; t < kWT; ++t) {
+                        // rows 8 apart have the same swizzle
+                        if constexpr (D == 32) {
+                            kw[t][0] = *reinterpret_cast<const uint32_t *>(krow + t * 8 * RB + 4 * c);
+                        } else if constexpr (D == 64) {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(krow + t * 8 * RB + tile_chunk<RB>(g, c >> 1) - g * RB + 8 * (c & 1));
+                            kw[t][0] = x.x; kw[t][1] = x.y;
+                        } else {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(krow + t * 8 * RB + tile_chunk<RB>(g, c + 4 * part) - g * RB);
+                            kw[t][0] = x.x; kw[t][1] = x.y; kw[t][2] = x.z; kw[t][3] = x.w;
                         }
                     }
-                }
 #pragma unroll
-                for (int wd = 0; wd < WPT; ++wd) {
-                    uint32_t b[2][4];
+                    for (int wd = 0; wd < KP; ++wd) {
+                        uint32_t b[kWT][4];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if constexpr (kOffset) offset_pairs(kw[t][wd], b[t]);
-                        else code_pairs(kw[t][wd], b[t]);
-                    }
-#pragma unroll
-                    for (int hv = 0; hv < HQ; ++hv)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * wd + i][lane]);
-                            const uint32_t a[4] = {x.x, x.y, x.z, x.w};
-                            mma16816(sc[0], a, b[0][2 * i], b[0][2 * i + 1]);
-                            mma16816(sc[1], a, b[1][2 * i], b[1][2 * i + 1]);
+                        for (int t = 0; t < kWT; ++t) {
+                            if constexpr (kOffset) offset_pairs(kw[t][wd], b[t]);
+                            else code_pairs(kw[t][wd], b[t]);
                         }
-                }
-                // ---- scales, mask ----
-                float kscale[2][2], vscale[2][2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float2 a = *reinterpret_cast<const float2 *>(&s.ks[st][tk + 8 * t + 2 * c]);
-                    const float2 b = *reinterpret_cast<const float2 *>(&s.vs[st][tk + 8 * t + 2 * c]);
-                    kscale[t][0] = a.x; kscale[t][1] = a.y;
-                    vscale[t][0] = b.x; vscale[t][1] = b.y;
-                }
+                        for (int hv = 0; hv < HQ; ++hv)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                            for (int i = 0; i < 2; ++i) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
+                                const uint32_t a[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = k < 2 ? rs0 : rs1;
-                        sc[t][k] = (kOffset ? fmaf(sc[t][k], f.x, f.y) : sc[t][k] * f.x) * kscale[t][k & 1];
+                                for (int t = 0; t < kWT; ++t) {
+                                    if (part == 0 && wd == 0 && hv == 0 && i == 0) mma16816_first(sc[t], a, b[t][0], b[t][1]);
+                                    else mma16816(sc[t], a, b[t][2 * i], b[t][2 * i + 1]);
+                                }
+                            }
                     }
-                const int bt = min(kTT, 1 << p.log_page);
+                }
+                // ---- scores against the references: s - z ----
+                float2 vscale[kWT];
+                const float *ks = s.ks[st] + tk + 2 * c, *vs = s.vs[st] + tk + 2 * c;
+#pragma unroll
+                for (int t = 0; t < kWT; ++t) {
+                    const float2 k = *reinterpret_cast<const float2 *>(ks + 8 * t);
+                    vscale[t] = *reinterpret_cast<const float2 *>(vs + 8 * t);
+                    sc[t][0] = fmaf(fmaf(sc[t][0], rs0.x, rs0.y), k.x, -z0);
+                    sc[t][1] = fmaf(fmaf(sc[t][1], rs0.x, rs0.y), k.y, -z0);
+                    sc[t][2] = fmaf(fmaf(sc[t][2], rs1.x, rs1.y), k.x, -z1);
+                    sc[t][3] = fmaf(fmaf(sc[t][3], rs1.x, rs1.y), k.y, -z1);
+                }
                 const uint32_t valid = s.valid[st];
-                if (t_first + 16 > w.s.ctx || valid != (uint32_t)((1ull << (kTT / bt)) - 1)) {
+                const bool masked = t_first + 8 * kWT > w.s.ctx || valid != all;
+                if (masked) {
+                    const int lp = min(p.log_page, 7);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
+                    for (int t = 0; t < kWT; ++t) {
                         bool any[2] = {false, false};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int tl = tk + 8 * t + 2 * c + (k & 1);
-                            const bool sees = ((valid >> (tl / bt)) & 1) &&
+                            const bool sees = ((valid >> (tl >> lp)) & 1) &&
                                               tree_sees<kRows>(p, w, g + (k < 2 ? 0 : 8), tile * kTT + tl);
                             any[k & 1] |= sees;
                             if (!sees) sc[t][k] = -INFINITY;
                         }
-                        // a value row that none of this lane's two query rows sees must not reach
-                        // them, whatever its scale holds
-                        if (!any[0]) vscale[t][0] = 0.f;
-                        if (!any[1]) vscale[t][1] = 0.f;
+                        // a value row that none of this lane's two query rows sees does not move
+                        // the unit of the values
+                        if (!any[0]) vscale[t].x = 0.f;
+                        if (!any[1]) vscale[t].y = 0.f;
                     }
                 }
                 // ---- lazy references ----
                 float up0 = -INFINITY, up1 = -INFINITY, vtop = 0.f;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < kWT; ++t) {
                     up0 = fmaxf(up0, fmaxf(sc[t][0], sc[t][1]));
                     up1 = fmaxf(up1, fmaxf(sc[t][2], sc[t][3]));
-                    vtop = fmaxf(vtop, fmaxf(vscale[t][0], vscale[t][1]));
+                    vtop = fmaxf(vtop, fmaxf(vscale[t].x, vscale[t].y));
                 }
-                if (__any_sync(0xffffffffu, up0 > m0 + 8.f || up1 > m1 + 8.f || vtop * vf > 64.f)) {
+                if (__any_sync(0xffffffffu, up0 > lim0 || up1 > lim1 || vtop * vf > 64.f)) {
 #pragma unroll
                     for (int o = 1; o < 4; o <<= 1) {
                         up0 = fmaxf(up0, __shfl_xor_sync(0xffffffffu, up0, o));
@@ -351,11 +370,19 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     }
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-                    const float n0 = fmaxf(m0, up0), n1 = fmaxf(m1, up1);
-                    const float zn0 = n0 == -INFINITY ? 0.f : n0, zn1 = n1 == -INFINITY ? 0.f : n1;
-                    float f0 = m0 == -INFINITY ? 1.f : ex2(m0 - zn0), f1 = m1 == -INFINITY ? 1.f : ex2(m1 - zn1);
-                    m0 = n0; m1 = n1; z0 = zn0; z1 = zn1;
+                    // z is 0 until something is seen (lim = -inf: the first score moves it)
+                    const float d0 = lim0 == 8.f ? fmaxf(up0, 0.f) : (up0 == -INFINITY ? 0.f : up0);
+                    const float d1 = lim1 == 8.f ? fmaxf(up1, 0.f) : (up1 == -INFINITY ? 0.f : up1);
+                    float f0 = lim0 == 8.f ? ex2(-d0) : 1.f, f1 = lim1 == 8.f ? ex2(-d1) : 1.f;
+                    if (up0 != -INFINITY) lim0 = 8.f;
+                    if (up1 != -INFINITY) lim1 = 8.f;
+                    z0 += d0; z1 += d1;
                     l0 *= f0; l1 *= f1;
+#pragma unroll
+                    for (int t = 0; t < kWT; ++t) {
+                        sc[t][0] -= d0; sc[t][1] -= d0;
+                        sc[t][2] -= d1; sc[t][3] -= d1;
+                    }
                     if (vtop * vf > 64.f) {
                         const int nv = max(-100, min((int)(__float_as_uint(vtop) >> 23) - 127, 100));
                         const float dv = ve - nv < -126 ? 0.f : __uint_as_float((uint32_t)(127 + ve - nv) << 23);
@@ -370,54 +397,65 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     }
                 }
                 // ---- weights ----
-                uint32_t pa[HP][4];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float p0 = ex2(sc[t][0] - z0), p1 = ex2(sc[t][1] - z0);
-                    const float p2 = ex2(sc[t][2] - z1), p3 = ex2(sc[t][3] - z1);
-                    l0 += p0 + p1;
-                    l1 += p2 + p3;
-                    const float v0 = vscale[t][0] * vf, v1 = vscale[t][1] * vf;
-                    float w0 = p0 * v0, w1 = p1 * v1, w2 = p2 * v0, w3 = p3 * v1;
-                    // a masked weight is zero, also where the value's scale is not finite
-                    if (sc[t][0] == -INFINITY) w0 = 0.f;
-                    if (sc[t][1] == -INFINITY) w1 = 0.f;
-                    if (sc[t][2] == -INFINITY) w2 = 0.f;
-                    if (sc[t][3] == -INFINITY) w3 = 0.f;
-                    pa[0][2 * t] = pack_h2(w0, w1);
-                    pa[0][2 * t + 1] = pack_h2(w2, w3);
-                    if constexpr (HP == 2) {
-                        const float2 a = unpack_h2(pa[0][2 * t]), b = unpack_h2(pa[0][2 * t + 1]);
-                        pa[1][2 * t] = pack_h2(w0 - a.x, w1 - a.y);
-                        pa[1][2 * t + 1] = pack_h2(w2 - b.x, w3 - b.y);
+                for (int t = 0; t < kWT; ++t) {
+                    const bool h0 = masked && sc[t][0] == -INFINITY, h1 = masked && sc[t][1] == -INFINITY;
+                    const bool h2 = masked && sc[t][2] == -INFINITY, h3 = masked && sc[t][3] == -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[t][k] = ex2(sc[t][k]);
+                    l0 += sc[t][0] + sc[t][1];
+                    l1 += sc[t][2] + sc[t][3];
+                    const float v0 = vscale[t].x * vf, v1 = vscale[t].y * vf;
+                    sc[t][0] *= v0; sc[t][1] *= v1;
+                    sc[t][2] *= v0; sc[t][3] *= v1;
+                    if (masked) {        // a masked weight is zero, also where the value's scale is not finite
+                        if (h0) sc[t][0] = 0.f;
+                        if (h1) sc[t][1] = 0.f;
+                        if (h2) sc[t][2] = 0.f;
+                        if (h3) sc[t][3] = 0.f;
                     }
                 }
-                // ---- O += (P vs) V ----
-                auto pv = [&](int q, uint32_t x, uint32_t y) {
-                    uint32_t b0[4], b1[4];
-                    code_pairs(x, b0);
-                    code_pairs(y, b1);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int hv = 0; hv < HP; ++hv) mma16816(acc[4 * q + j], pa[hv], b0[j], b1[j]);
-                };
+                // ---- O += (P vs) V, 16 tokens at a time ----
                 const uint32_t vbase = t_smem(s.vq[st]);
                 const int mrow = tk + ((lane >> 3) & 1) * 8 + (lane & 7);
-                if constexpr (NQ == 1) {
-                    uint32_t x, y;
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-                                 : "=r"(x), "=r"(y) : "r"(vbase + tile_chunk<RB>(mrow, 0)) : "memory");
-                    pv(0, x, y);
-                } else {
 #pragma unroll
-                    for (int q = 0; q < NQ; q += 2) {
-                        uint32_t x[4];
-                        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(vbase + tile_chunk<RB>(mrow, q + (lane >> 4))) : "memory");
-                        pv(q, x[0], x[1]);
-                        pv(q + 1, x[2], x[3]);
+                for (int h = 0; h < kWT / 2; ++h) {
+                    uint32_t pa[HP][4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const float *x = sc[2 * h + t];
+                        pa[0][2 * t] = pack_h2(x[0], x[1]);
+                        pa[0][2 * t + 1] = pack_h2(x[2], x[3]);
+                        if constexpr (HP == 2) {
+                            const float2 a = unpack_h2(pa[0][2 * t]), b = unpack_h2(pa[0][2 * t + 1]);
+                            pa[1][2 * t] = pack_h2(x[0] - a.x, x[1] - a.y);
+                            pa[1][2 * t + 1] = pack_h2(x[2] - b.x, x[3] - b.y);
+                        }
+                    }
+                    auto pv = [&](int q, uint32_t x, uint32_t y) {
+                        uint32_t b0[4], b1[4];
+                        code_pairs(x, b0);
+                        code_pairs(y, b1);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int hv = 0; hv < HP; ++hv) mma16816(acc[4 * q + j], pa[hv], b0[j], b1[j]);
+                    };
+                    if constexpr (NQ == 1) {
+                        uint32_t x, y;
+                        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+                                     : "=r"(x), "=r"(y) : "r"(vbase + tile_chunk<RB>(mrow + 16 * h, 0)) : "memory");
+                        pv(0, x, y);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < NQ; q += 2) {
+                            uint32_t x[4];
+                            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                         : "r"(vbase + tile_chunk<RB>(mrow + 16 * h, q + (lane >> 4))) : "memory");
+                            pv(q, x[0], x[1]);
+                            pv(q + 1, x[2], x[3]);
+                        }
                     }
                 }
             }
@@ -435,8 +473,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
-        if (m0 == -INFINITY && !(l0 == 0.f)) m0 = 0.f;      // nothing but NaN seen
-        if (m1 == -INFINITY && !(l1 == 0.f)) m1 = 0.f;
+        const float m0 = lim0 == 8.f || !(l0 == 0.f) ? z0 : -INFINITY, m1 = lim1 == 8.f || !(l1 == 0.f) ? z1 : -INFINITY;
         if (c == 0) {
             s.ref[warp][g] = m0;
             s.ref[warp][g + 8] = m1;
@@ -482,27 +519,32 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         // ---- rows out: finished, or as a partial ----
         float *part = p.part, *ml = p.part + (int64_t)2 * p.ctas * kRows * D;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (at - (w.t1 - w.t0) == begin ? 0 : 1);
-#pragma unroll 1
-        for (int i = 0; i < kRows / kCWarps; ++i) {
-            const int r = warp * (kRows / kCWarps) + i, gr = w.mt * kRows + r;
+        float vsum[RW];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const int r = i * kCWarps + warp;
+            joined(r, top[i], vsum[i]);
+            const float il = w.whole ? (vsum[i] == 0.f ? 0.f : 1.f / vsum[i]) : 1.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) qv[i][e] = (s.acc[0][r][lane * E + e] + s.acc[1][r][lane * E + e]) * il;
+        }
+        if (w.whole && !(p.flags & RQ_ATTN_ROTATED_OUT)) {
+#pragma unroll
+            for (int i = 0; i < RW; ++i) warp_rotate<E>(qv[i], sg, lane, !signs_first, inv_sqrt_dim<D>());
+        }
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const int r = i * kCWarps + warp, gr = w.mt * kRows + r;
             if (r >= rows) break;
-            float top, sum, v[E];
-            joined(r, top, sum);
+            if (w.whole) {
+                const int64_t o = ((w.s.row0 + gr / p.group) * p.kv_heads + w.h) * p.group + gr % p.group;
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = s.acc[0][r][lane * E + e] + s.acc[1][r][lane * E + e];
-            if (!w.whole) {
+                for (int e = 0; e < E; ++e) store_elem<IN>(p.out, o * D + lane * E + e, qv[i][e]);
+            } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) part[(slot * kRows + r) * D + lane * E + e] = v[e];
-                if (lane == 0) *reinterpret_cast<float2 *>(ml + (slot * kRows + r) * 2) = make_float2(top, sum);
-                continue;
+                for (int e = 0; e < E; ++e) part[(slot * kRows + r) * D + lane * E + e] = qv[i][e];
+                if (lane == 0) *reinterpret_cast<float2 *>(ml + (slot * kRows + r) * 2) = make_float2(top[i], vsum[i]);
             }
-            const float il = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= il;
-            if (!(p.flags & RQ_ATTN_ROTATED_OUT)) warp_rotate<E>(v, sg, lane, !signs_first, inv_sqrt_dim<D>());
-            const int64_t o = ((w.s.row0 + gr / p.group) * p.kv_heads + w.h) * p.group + gr % p.group;
-#pragma unroll
-            for (int e = 0; e < E; ++e) store_elem<IN>(p.out, o * D + lane * E + e, v[e]);
         }
         cta_sync();                                          // s.acc and s.q are free again
     }
@@ -538,7 +580,7 @@ cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, cons
 }  // namespace
 
 int64_t attn_tree_workspace(int64_t head_dim) {
-    const int64_t ctas = 3 * (int64_t)device_sm_count();
+    const int64_t ctas = 2 * (int64_t)device_sm_count();
     const int64_t small = 2 * ctas * kRows * (head_dim + 2) * (int64_t)sizeof(float);
     const int64_t wide = attn_tree_tc_workspace(head_dim);
     return small > wide ? small : wide;

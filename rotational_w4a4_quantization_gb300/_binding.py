@@ -388,37 +388,42 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _one_device(*tensors) -> int:
-    dev = tensors[0].get_device()
+def _one_device(dev: int, *tensors):
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t.get_device() != dev:
             raise ValueError("tensors must be on one device")
-    return dev
 
 
-def _expect_heads(t, name: str, dtype=None, tokens=None):
-    """A [tokens][heads][head_dim] tensor: any token and head strides, unit stride inside a head.  Returns its shape."""
-    shape = t.shape
-    if len(shape) != 3 or (t.stride(2) != 1 and shape[2] != 1):
+def _expect_heads(t, name: str):
+    """A [tokens][heads][head_dim] tensor: any token and head strides, unit stride inside a head.  Returns its shape and
+    strides."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] != 1):
         raise ValueError(f"{name} must be [tokens][heads][head_dim] with unit stride in the last dimension")
     if t.dtype not in _FLOATS:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    if dtype is not None and t.dtype != dtype:
+    return shape, stride
+
+
+def _expect_same(t, name: str, dtype, tokens: int):
+    """The same, of a given dtype and number of tokens."""
+    shape, stride = _expect_heads(t, name)
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if tokens is not None and shape[0] != tokens:
+    if shape[0] != tokens:
         raise ValueError(f"{name}: expected {tokens} tokens, got {shape[0]}")
-    return shape
+    return shape, stride
 
 
 def _expect_vector(t, name: str, dtype, n: int, what: str):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {what}")
 
 
 def _expect_turns(turns, head_dim: int) -> int:
-    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+    if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
         raise ValueError("turns must be a contiguous 1-D int64 tensor (rope_turns)")
     rot = 2 * turns.shape[0]
     if not 2 <= rot <= head_dim:
@@ -475,32 +480,36 @@ def rope(q, k, positions: torch.Tensor, turns: torch.Tensor, *, interleaved: boo
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k cannot both be None")
-    T, _, D = _expect_heads(ref, "q" if q is not None else "k")
-    dtype, dev = ref.dtype, ref.get_device()
-    flat, outs = [], []
+    dtype, dev, device = ref.dtype, ref.get_device(), ref.device
+    T, D = ref.shape[0], ref.shape[-1]
+    args, outs = [], []
     for i, x in enumerate((q, k)):
         if x is None:
-            flat += (None, 0, 0, 0, None, 0, 0)
+            args += (None, 0, 0, 0, None, 0, 0)
             outs.append(None)
             continue
         name = "qk"[i]
-        shape = _expect_heads(x, name, dtype, T)
+        shape, xs = _expect_same(x, name, dtype, T)
+        H = shape[1]
         if shape[2] != D:
             raise ValueError("q and k must have one head_dim")
-        o = None if out is None else out[i]
-        if o is None:
-            o = _empty(shape, dtype, x.device, stream)
-        elif _expect_heads(o, f"out ({name})", dtype, T) != shape:
-            raise ValueError(f"out ({name}): expected shape {tuple(shape)}, got {tuple(o.shape)}")
-        if x.get_device() != dev or o.get_device() != dev:
+        if out is None or out[i] is None:
+            o, ot, oh = _empty(shape, dtype, device, stream), H * D, D
+        else:
+            o = out[i]
+            oshape, os = _expect_same(o, f"out ({name})", dtype, T)
+            if oshape != shape:
+                raise ValueError(f"out ({name}): expected shape {tuple(shape)}, got {tuple(oshape)}")
+            ot, oh = os[0], os[1]
+            _one_device(dev, o)
+        if x.get_device() != dev:
             raise ValueError("tensors must be on one device")
-        xs, os = x.stride(), o.stride()
-        flat += (x.data_ptr(), shape[1], xs[0], xs[1], o.data_ptr(), os[0], os[1])
+        args += (x.data_ptr(), H, xs[0], xs[1], o.data_ptr(), ot, oh)
         outs.append(o)
     _expect_vector(positions, "positions", torch.int64, T, "int64 tensor with one entry per token")
     rot = _expect_turns(turns, D)
-    _one_device(positions, turns, ref)
-    _call(lib.rq_rope, "rq_rope", dev, stream, *flat, _DTYPES[dtype], T, D, rot, positions.data_ptr(), turns.data_ptr(),
+    _one_device(dev, positions, turns)
+    _call(lib.rq_rope, "rq_rope", dev, stream, *args, _DTYPES[dtype], T, D, rot, positions.data_ptr(), turns.data_ptr(),
           mscale, (RQ_ROPE_INTERLEAVED if interleaved else 0) | (RQ_ROPE_INVERSE if inverse else 0))
     return tuple(outs)
 
@@ -521,7 +530,7 @@ def _cache_parts(cache, head_dim=None):
     shape = kq.shape
     if len(shape) != 4 or (head_dim is not None and shape[3] * 2 != head_dim):
         raise ValueError(f"cache['kq']: expected [pages][heads][page_size][head_dim/2], got {tuple(shape)}")
-    if kq.dtype != torch.uint8 or vq.dtype != torch.uint8 or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+    if not (kq.dtype is vq.dtype is torch.uint8 and ks.dtype is vs.dtype is torch.float32):
         raise ValueError("cache: codes are uint8 and scales float32")
     if vq.shape != shape or ks.shape != shape[:3] or vs.shape != ks.shape:
         raise ValueError("cache: kq and vq, ks and vs must agree in shape")
@@ -531,7 +540,7 @@ def _cache_parts(cache, head_dim=None):
 
 
 def _expect_table(t):
-    if t.dim() != 2 or t.dtype != torch.int32 or not t.is_contiguous():
+    if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError("block_table must be a contiguous int32 tensor [seqs][width]")
     return t.shape
 
@@ -542,10 +551,12 @@ def kv_append(k, v, cache: dict, slots: torch.Tensor, seed: int, flags: int = RQ
     slots[t] = page * page_size + row (int64; outside the cache: skipped).  With positions and turns the keys take
     their rotary positions on the way (see :func:`rope`).  Returns the cache."""
     lib = _lib or load_library()
-    T, H, D = _expect_heads(k, "k")
-    dtype = k.dtype
-    if _expect_heads(v, "v", dtype, T) != k.shape:
-        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    kshape, kst = _expect_heads(k, "k")
+    T, H, D = kshape
+    dtype, dev = k.dtype, k.get_device()
+    vshape, vst = _expect_same(v, "v", dtype, T)
+    if vshape != kshape:
+        raise ValueError(f"v: expected shape {tuple(kshape)}, got {tuple(vshape)}")
     kq, ks, vq, vs, shape = _cache_parts(cache, D)
     if shape[1] != H:
         raise ValueError(f"cache holds {shape[1]} heads, k has {H}")
@@ -556,8 +567,8 @@ def kv_append(k, v, cache: dict, slots: torch.Tensor, seed: int, flags: int = RQ
     if turns is not None:
         _expect_vector(positions, "positions", torch.int64, T, "int64 tensor with one entry per token")
         rot, pp, tp = _expect_turns(turns, D), positions.data_ptr(), turns.data_ptr()
-    dev = _one_device(k, v, kq, ks, vq, vs, slots, positions, turns)
-    kst, vst = k.stride(), v.stride()
+        _one_device(dev, positions, turns)
+    _one_device(dev, v, kq, ks, vq, vs, slots)
     _call(lib.rq_kv_append, "rq_kv_append", dev, stream, k.data_ptr(), kst[0], kst[1], v.data_ptr(), vst[0], vst[1],
           _DTYPES[dtype], T, H, D, slots.data_ptr(), pp, tp, rot, mscale, seed,
           flags | RQ_ROPE_INTERLEAVED if interleaved else flags, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(),
@@ -576,21 +587,25 @@ def kv_read(cache: dict, block_table: torch.Tensor, starts, offsets: torch.Tenso
     pages, H, page, half = shape
     B, W = _expect_table(block_table)
     _expect_vector(offsets, "offsets", torch.int32, B + 1, "int32 tensor [seqs + 1]")
+    dev, sp = kq.get_device(), None
     if starts is not None:
         _expect_vector(starts, "starts", torch.int32, B, "int32 tensor [seqs]")
+        _one_device(dev, starts)
+        sp = starts.data_ptr()
     if dtype not in _FLOATS:
         raise ValueError("dtype must be float32, bfloat16 or float16")
     if out is None:
-        ko = _empty((total, H, 2 * half), dtype, kq.device, stream)
-        vo = _empty((total, H, 2 * half), dtype, kq.device, stream)
+        device = kq.device
+        ko = _empty((total, H, 2 * half), dtype, device, stream)
+        vo = _empty((total, H, 2 * half), dtype, device, stream)
     else:
         ko, vo = out
         _expect(ko, "out (k)", (total, H, 2 * half), dtype)
         _expect(vo, "out (v)", (total, H, 2 * half), dtype)
-    dev = _one_device(kq, ks, vq, vs, block_table, starts, offsets, ko, vo)
+        _one_device(dev, ko, vo)
+    _one_device(dev, ks, vq, vs, block_table, offsets)
     _call(lib.rq_kv_read, "rq_kv_read", dev, stream, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages,
-          H, page, 2 * half, block_table.data_ptr(), W, None if starts is None else starts.data_ptr(),
-          offsets.data_ptr(), B, total, seed, flags, ko.data_ptr(), vo.data_ptr(), _DTYPES[dtype])
+          H, page, 2 * half, block_table.data_ptr(), W, sp, offsets.data_ptr(), B, total, seed, flags, ko.data_ptr(), vo.data_ptr(), _DTYPES[dtype])
     return ko, vo
 
 
@@ -612,8 +627,9 @@ def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_l
     max_nodes bounds the nodes of a sequence (default: the mask's width, or the number of rows).  One node per sequence
     is a plain decode step.  Returns [rows][q_heads][head_dim] of q's dtype; rows that see nothing are 0."""
     lib = _lib or load_library()
-    N, Hq, D = _expect_heads(q, "q")
-    dtype = q.dtype
+    qshape, qs = _expect_heads(q, "q")
+    N, Hq, D = qshape
+    dtype, dev, device = q.dtype, q.get_device(), q.device
     kq, ks, vq, vs, shape = _cache_parts(cache, D)
     if Hq % shape[1]:
         raise ValueError(f"{Hq} query heads do not divide over {shape[1]} KV heads")
@@ -623,7 +639,7 @@ def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_l
     mask_ptr, mask_stride = None, 0
     if tree_mask is not None:
         ms = tree_mask.shape
-        if tree_mask.dtype != torch.bool or len(ms) != 2 or ms[0] != N or (tree_mask.stride(1) != 1 and ms[1] > 1):
+        if tree_mask.dtype is not torch.bool or len(ms) != 2 or ms[0] != N or (tree_mask.stride(1) != 1 and ms[1] > 1):
             raise ValueError("tree_mask must be bool [rows][width] with unit stride in the last dimension")
         mask_ptr = tree_mask.data_ptr()
         mask_stride = tree_mask.stride(0) if N > 1 else ms[1]     # the stride of a single row says nothing
@@ -631,27 +647,30 @@ def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_l
             max_nodes = ms[1]
         elif max_nodes > ms[1]:
             raise ValueError("tree_mask is narrower than max_nodes")
+        _one_device(dev, tree_mask)
     elif max_nodes is None:
         max_nodes = N
     if out is None:
-        out = _empty((N, Hq, D), dtype, q.device, stream)
+        out = _empty(qshape, dtype, device, stream)
     else:
         _expect(out, "out", (N, Hq, D), dtype)
-    dev = _one_device(q, kq, ks, vq, vs, block_table, context_lens, offsets, tree_mask, out, workspace)
+        _one_device(dev, out)
+    _one_device(dev, kq, ks, vq, vs, block_table, context_lens, offsets)
     if workspace is None:
         need = _workspace_bytes.get((dev, D))
         if need is None:
             with torch.cuda.device(dev):
                 need = _workspace_bytes[dev, D] = lib.rq_attn_tree_workspace(D)
-        workspace = _empty(need, torch.uint8, q.device, stream)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    qs = q.stride()
+        workspace = _empty(need, torch.uint8, device, stream)
+    else:
+        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        _one_device(dev, workspace)
+        need = workspace.numel()
     _call(lib.rq_attn_tree, "rq_attn_tree", dev, stream, q.data_ptr(), qs[0], qs[1], _DTYPES[dtype], N, Hq, D,
           kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2],
           block_table.data_ptr(), W, context_lens.data_ptr(), offsets.data_ptr(), B, max_nodes, mask_ptr, mask_stride,
-          seed, flags, D ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
-          workspace.numel())
+          seed, flags, D ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(), need)
     return out
 
 

@@ -73,23 +73,8 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// A word of 8 codes as four pairs (nibbles j and j + 4) of fp16 codes, exactly.  0x6400 | u
-// is 1024 + u, so nibbles 0 and 4 (u = code + 8 after the sign bit's flip) lose 1032;
-// nibbles 1 and 5, which stay four bits up, are 1024 + 16 u: times 1/16, less 72.
-__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&r)[4]) {
-    const __half2 m0 = __half2half2(__ushort_as_half(0xe408)), r16 = __half2half2(__ushort_as_half(0x2c00)),
-                  m1 = __half2half2(__ushort_as_half(0xd480));             // -1032, 1/16, -72
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-        const uint32_t y = x >> (4 * j);
-        const uint32_t a = (y & 0x000f000fu) ^ 0x64086408u, b = (y & 0x00f000f0u) ^ 0x64806480u;
-        const __half2 ha = __hadd2(*reinterpret_cast<const __half2 *>(&a), m0);
-        const __half2 hb = __hfma2(*reinterpret_cast<const __half2 *>(&b), r16, m1);
-        r[j] = *reinterpret_cast<const uint32_t *>(&ha);
-        r[j + 1] = *reinterpret_cast<const uint32_t *>(&hb);
-    }
-}
-// The same as subnormals u 2^-24 and 16 u 2^-24.
+// A word of 8 codes as code_pairs gives them, but as subnormals u 2^-24 and 16 u 2^-24,
+// u = code + 8.
 __device__ __forceinline__ void offset_pairs(uint32_t x, uint32_t (&r)[4]) {
     const uint32_t y = x >> 8;
     r[0] = (x ^ 0x00080008u) & 0x000f000fu;
@@ -133,6 +118,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         s.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    tree_join_may_begin();
     tree_scan<kRows, kTT>(p, s.prefix);               // ends with a block barrier
     const int64_t total = s.prefix[kScan];
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
@@ -560,11 +546,7 @@ cudaError_t launch_tree_d(TreeParams &p, const CUtensorMap &mk, const CUtensorMa
     kern<<<p.ctas, kMThreads, smem, stream>>>(mk, mv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int bph = (int)(((int64_t)p.max_nodes * p.group + kRows - 1) / kRows);
-    const int64_t units = (int64_t)p.seqs * p.kv_heads * bph;
-    if (units > 0x7fffffffll) return cudaErrorInvalidValue;
-    attn_tree_join_kernel<IN, D, kRows, kTT><<<dim3((unsigned)units, 1), 32 * kJoinWarps, 0, stream>>>(p, bph);
-    return cudaGetLastError();
+    return launch_tree_join<IN, D, kRows, kTT>(p, stream);
 }
 
 template <int IN>

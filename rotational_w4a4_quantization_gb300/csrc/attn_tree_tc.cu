@@ -435,6 +435,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     block_sign_words<D>(s.sign_words, p.seed);
+    tree_join_may_begin();
     tc_fence_before();
     tree_scan<ROWS, kTcTT>(p, s.prefix);               // ends with a block barrier
     tc_fence_after();
@@ -955,12 +956,7 @@ cudaError_t launch_tc(TreeParams &p, cudaStream_t stream) {
     kern<<<p.ctas, kTcThreads, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int bph = (int)(((int64_t)p.max_nodes * p.group + 128 * NT - 1) / (128 * NT));
-    const int64_t units = (int64_t)p.seqs * p.kv_heads * bph;
-    if (units > 0x7fffffffll) return cudaErrorInvalidValue;
-    attn_tree_join_kernel<IN, D, 128 * NT, kTcTT>
-        <<<dim3((unsigned)units, 128 * NT / kJoinWarps), 32 * kJoinWarps, 0, stream>>>(p, bph);
-    return cudaGetLastError();
+    return launch_tree_join<IN, D, 128 * NT, kTcTT>(p, stream);
 }
 
 }  // namespace

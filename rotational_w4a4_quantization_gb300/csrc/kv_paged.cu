@@ -158,21 +158,14 @@ struct ReadParams {
     void *out[2];
     const int32_t *table, *starts, *offsets;
     int64_t total, pages, width;
-    int heads, log_page, seqs, tb;
+    int heads, log_page, seqs, tb, log_tb;
     uint64_t seed;
     uint32_t flags;
 };
 
-template <int OUT, int D>
-__global__ void __launch_bounds__(kPThreads) kv_read_kernel(const __grid_constant__ ReadParams p) {
-    using L = RowLanes<D>;
-    constexpr int ES = OUT == IN_F32 ? 4 : 2;
-    constexpr int RPP = kPThreads / L::LPR;
-    __shared__ uint32_t sign_words[8];
-    __shared__ int64_t at_of[kMaxTok];       // cache row of head 0; -1: no such page (reads zeros); -2: not asked for
-    const int64_t n0 = (int64_t)blockIdx.x * p.tb;
-    const int nt = (int)min((int64_t)p.tb, p.total - n0);
-    block_sign_words<D>(sign_words, p.seed);
+// Cache rows of a block's output rows: the row of head 0; -1: no such page (reads
+// zeros); -2: not asked for.
+__device__ __forceinline__ void read_rows(const ReadParams &p, int64_t n0, int nt, int64_t *at_of) {
     if (threadIdx.x < nt) {
         const int64_t n = n0 + threadIdx.x;
         int lo = 0, hi = p.seqs;             // the last sequence whose first row is at or before n
@@ -194,6 +187,163 @@ __global__ void __launch_bounds__(kPThreads) kv_read_kernel(const __grid_constan
         }
         at_of[threadIdx.x] = at;
     }
+}
+
+// Rows of up to 128 elements, 16 to a warp, on mma.sync: the codes are exact in fp16 and
+// so are the sums of 16 of them in fp32, so a 16-point butterfly is a product with a
+// constant +-1 matrix.  A lane (g, c) of rows g and g + 8 holds the code words c, c + 4,
+// ... (8 codes each); index bits 0, 2 (the nibbles of a pair are 4 apart) and 3, 4 (c) are
+// inside the product, bit 1 and the bits above 4 are left to additions in registers,
+// where the results lie.  21 instructions a row; butterflies with shuffles take 41.
+template <int OUT, int D>
+__global__ void __launch_bounds__(kPThreads) kv_read_mma_kernel(const __grid_constant__ ReadParams p) {
+    constexpr int ES = OUT == IN_F32 ? 4 : 2, W = D / 32;            // code words per lane and row
+    __shared__ int64_t at_of[kMaxTok];
+    __shared__ uint32_t sign_words[4];
+    const int64_t n0 = (int64_t)blockIdx.x * p.tb;
+    const int nt = (int)min((int64_t)p.tb, p.total - n0);
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    block_sign_words<D>(sign_words, p.seed);
+    read_rows(p, n0, nt, at_of);
+    __syncthreads();
+    const bool rotated = (p.flags & RQ_KV_ROTATED_OUT) != 0;
+    const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;        // of R: R^T has them last
+    // sign bits of this lane's elements, a byte per word
+    uint32_t sgn = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) sgn |= ((sign_words[i] >> (8 * c)) & 0xffu) << (8 * i);
+    // B: column n = 8 j + 2 c + i is element bits (0: j, 2: i, 3 4: c); row k = 2 c + i + 8 j alike.
+    // This lane: column g of tile j, rows 2 c + {0, 1} and 8 more.
+    uint32_t bm[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int kj = 0; kj < 2; ++kj) {
+            const uint32_t base = __popc((g >> 1) & c) + (j & kj);
+            bm[j][kj] = (base & 1 ? 0xbc00u : 0x3c00u) | ((base + (g & 1)) & 1 ? 0xbc000000u : 0x3c000000u);
+        }
+    // rows in the order (head, K or V, token): neighbours in a page; tb is a power of two
+    const int rows = (2 * p.heads) << p.log_tb;
+    constexpr int RPB = 16 * (kPThreads / 32);
+    uint32_t cw[2][W];
+    float sc[2];
+    int64_t at0[2];
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = base + (threadIdx.x >> 5) * 16 + g + 8 * u;
+            const int hs = r >> p.log_tb, tk = r & ((1 << p.log_tb) - 1);
+            at0[u] = r < rows && tk < nt ? at_of[tk] : -2;
+            sc[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) cw[u][i] = 0;
+            if (at0[u] >= 0) {
+                const int64_t at = at0[u] + ((int64_t)(hs >> 1) << p.log_page);
+                sc[u] = p.scales[hs & 1][at];
+                const uint32_t *codes = reinterpret_cast<const uint32_t *>(p.codes[hs & 1] + at * (D / 2));
+#pragma unroll
+                for (int i = 0; i < W; ++i) cw[u][i] = codes[c + 4 * i];
+            }
+        }
+    };
+    fetch(0);
+    for (int base = 0; base < rows; base += RPB) {
+        float v[2 * W][2][4];                // [word, bit 1][bit 0][rows g: bit 2 = 0, 1; rows g + 8]
+        float scale[2] = {sc[0], sc[1]};
+        int64_t asked[2] = {at0[0], at0[1]};
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                code_pairs(cw[u][i], a[u]);  // pairs (e, e + 4), e = 0 .. 3
+                if (!rotated && !signs_first) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t b = sgn >> (8 * i + e);
+                        a[u][e] ^= ((b & 1u) << 15) | ((b & 16u) << 27);
+                    }
+                }
+            }
+#pragma unroll
+            for (int b1 = 0; b1 < 2; ++b1) {
+                if (rotated) {               // no butterflies: the codes as they are
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a[u][2 * b1 + j]));
+                            v[2 * i + b1][j][2 * u] = f.x;
+                            v[2 * i + b1][j][2 * u + 1] = f.y;
+                        }
+                    continue;
+                }
+                // k = 2 c + i: bit 2 = i, bit 0 = 0; k + 8: bit 0 = 1
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                                 : "=f"(v[2 * i + b1][j][0]), "=f"(v[2 * i + b1][j][1]), "=f"(v[2 * i + b1][j][2]), "=f"(v[2 * i + b1][j][3])
+                                 : "r"(a[0][2 * b1]), "r"(a[1][2 * b1]), "r"(a[0][2 * b1 + 1]), "r"(a[1][2 * b1 + 1]),
+                                   "r"(bm[j][0]), "r"(bm[j][1]), "f"(0.f));
+            }
+        }
+        if (base + RPB < rows) fetch(base + RPB);
+        if (!rotated) {
+#pragma unroll
+            for (int st = 1; st < 2 * W; st <<= 1)
+#pragma unroll
+                for (int i = 0; i < 2 * W; ++i)
+                    if (!(i & st)) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2) {
+                                const float2 x = make_float2(v[i][j][k], v[i][j][k + 1]), y = make_float2(v[i + st][j][k], v[i + st][j][k + 1]);
+                                const float2 s = __fadd2_rn(x, y), d = __ffma2_rn(y, make_float2(-1.f, -1.f), x);
+                                v[i][j][k] = s.x; v[i][j][k + 1] = s.y;
+                                v[i + st][j][k] = d.x; v[i + st][j][k + 1] = d.y;
+                            }
+                    }
+            scale[0] *= inv_sqrt_dim<D>();
+            scale[1] *= inv_sqrt_dim<D>();
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (asked[u] < -1) continue;
+            const int r = base + (threadIdx.x >> 5) * 16 + g + 8 * u;
+            const int hs = r >> p.log_tb, tk = r & ((1 << p.log_tb) - 1);
+            char *out = static_cast<char *>(p.out[hs & 1]) + ((n0 + tk) * p.heads + (hs >> 1)) * D * ES;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                pair_t x[4];                 // elements 2 q, 2 q + 1 of the word: bits 2 = q >> 1, 1 = q & 1
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float e0 = v[2 * i + (q & 1)][0][2 * u + (q >> 1)] * scale[u], e1 = v[2 * i + (q & 1)][1][2 * u + (q >> 1)] * scale[u];
+                    if (!rotated && signs_first) {
+                        const uint32_t b = sgn >> (8 * i + 2 * q);
+                        e0 = __uint_as_float(__float_as_uint(e0) ^ (b << 31));
+                        e1 = __uint_as_float(__float_as_uint(e1) ^ ((b >> 1) << 31));
+                    }
+                    x[q] = mk2(e0, e1);
+                }
+                store8<OUT>(out + (c + 4 * i) * 8 * ES, x);
+            }
+        }
+    }
+}
+
+// Rows of 256 elements, by butterflies with shuffles.
+template <int OUT, int D>
+__global__ void __launch_bounds__(kPThreads) kv_read_kernel(const __grid_constant__ ReadParams p) {
+    using L = RowLanes<D>;
+    constexpr int ES = OUT == IN_F32 ? 4 : 2;
+    constexpr int RPP = kPThreads / L::LPR;
+    __shared__ uint32_t sign_words[8];
+    __shared__ int64_t at_of[kMaxTok];
+    const int64_t n0 = (int64_t)blockIdx.x * p.tb;
+    const int nt = (int)min((int64_t)p.tb, p.total - n0);
+    block_sign_words<D>(sign_words, p.seed);
+    read_rows(p, n0, nt, at_of);
     __syncthreads();
     const int rl = threadIdx.x % L::LPR, r0 = threadIdx.x / L::LPR;
     pair_t sg[L::NP];
@@ -269,9 +419,9 @@ template <int OUT>
 cudaError_t launch_read_out(const ReadParams &p, int64_t d, cudaStream_t stream) {
     const unsigned blocks = (unsigned)((p.total + p.tb - 1) / p.tb);
     switch (d) {
-        case 32: kv_read_kernel<OUT, 32><<<blocks, kPThreads, 0, stream>>>(p); break;
-        case 64: kv_read_kernel<OUT, 64><<<blocks, kPThreads, 0, stream>>>(p); break;
-        case 128: kv_read_kernel<OUT, 128><<<blocks, kPThreads, 0, stream>>>(p); break;
+        case 32: kv_read_mma_kernel<OUT, 32><<<blocks, kPThreads, 0, stream>>>(p); break;
+        case 64: kv_read_mma_kernel<OUT, 64><<<blocks, kPThreads, 0, stream>>>(p); break;
+        case 128: kv_read_mma_kernel<OUT, 128><<<blocks, kPThreads, 0, stream>>>(p); break;
         default: kv_read_kernel<OUT, 256><<<blocks, kPThreads, 0, stream>>>(p); break;
     }
     return cudaGetLastError();
@@ -349,6 +499,7 @@ cudaError_t launch_kv_read(const PagedCache &c, int64_t head_dim, const int32_t 
     p.tb = kMaxTok;
     const int64_t want = 8 * (int64_t)device_sm_count();
     while (p.tb > 1 && total / p.tb < want) p.tb /= 2;
+    p.log_tb = log2_of(p.tb);
     if ((total + p.tb - 1) / p.tb > 0x7fffffffll) return cudaErrorInvalidValue;
     switch (out_type) {
         case IN_F32: return launch_read_out<IN_F32>(p, head_dim, stream);

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kRThreads) rope_kernel(const __grid_constant__
     const int ea = turn ? it * VE : 2 * p.half + (it - p.rot_items) * VE;
     const int eb = ea + p.half;
     const int rows = nt * heads;
-    constexpr int U = VEC ? 4 : 1;                        // rows in flight per thread
+    constexpr int U = VEC ? 2 : 1;                        // rows in flight per thread
     for (int rb = r0; rb < rows; rb += U * rpp) {
         const char *src[U];
         char *dst[U];

@@ -241,12 +241,17 @@ __device__ __forceinline__ void t_bulk(void *dst, const void *src, uint32_t byte
 // Joins the partials of the units that span CTAs: per row, in the order of the
 // CTAs (so results do not change from run to run), the largest reference, the
 // rescaled sums, then normalisation, R^T and the one rounding to the output type.
-// One warp per row.
+// A warp takes a row (two of 256-row units) and four partials at a time, so that their
+// loads overlap.
+// Launched so that it may begin while the kernel before it ends: it finds its units
+// first and waits only before it reads the partials.
 constexpr int kJoinWarps = 16;
+__device__ __forceinline__ void tree_join_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+constexpr int join_rows(int rows) { return rows >= 256 ? 2 : 1; }         // rows per warp
 template <int IN, int D, int ROWS, int TT>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const __grid_constant__ TreeParams p,
-                                                                         int blocks_per_head) {
-    constexpr int E = D / 32;
+                                                                         int blocks_per_head, int turns) {
+    constexpr int E = D / 32, RW = join_rows(ROWS);
     __shared__ int64_t prefix[kScan + 1];
     tree_scan<ROWS, TT>(p, prefix);
     const int64_t total = prefix[kScan];
@@ -255,8 +260,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
     const int h = hm / blocks_per_head, mt = hm - h * blocks_per_head;
     const TreeSeq s = tree_seq<ROWS, TT>(p, b);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.y * kJoinWarps + warp, gr = mt * ROWS + row;
-    if (mt >= s.mt || gr >= s.n * p.group) return;
+    const int rows = min(ROWS, s.n * p.group - mt * ROWS);
+    const int begin_row = (blockIdx.y * turns * kJoinWarps + warp) * RW;
+    if (mt >= s.mt || begin_row >= rows) return;
     const int per = (p.seqs + kScan - 1) / kScan;
     int64_t first = prefix[b / per];
     for (int i = b / per * per; i < b; ++i) {
@@ -267,57 +273,115 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
     // CTA of a tile: the last c with total c / ctas <= tile
     const int c0 = (int)(((first + 1) * p.ctas - 1) / total), c1 = (int)(((first + s.nt) * p.ctas - 1) / total);
     if (c0 == c1) return;                                   // finished in its CTA
+    float sg[E];
+    lane_signs<E>(sg, lane, p.seed);
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials are written
     const float *ml = p.part + (int64_t)2 * p.ctas * ROWS * D;
+    auto there = [&](int c) { return c <= c1 && tree_begin(total, p.ctas, c) != tree_begin(total, p.ctas, c + 1); };   // no empty stretch
     auto slot = [&](int c) { return (int64_t)(tree_begin(total, p.ctas, c) >= first ? 2 * c : 2 * c + 1); };
-    float top = -INFINITY;
+    for (int turn = 0; turn < turns; ++turn) {
+    const int row0 = begin_row + turn * kJoinWarps * RW;
+    if (row0 >= rows) break;
+    float top[RW], sum[RW], acc[RW][E];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        top[i] = -INFINITY;
+        sum[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+    }
     for (int c = c0 + lane; c <= c1; c += 32) {
-        if (tree_begin(total, p.ctas, c) == tree_begin(total, p.ctas, c + 1)) continue;   // an empty stretch
-        top = fmaxf(top, ml[(slot(c) * ROWS + row) * 2]);
+        if (!there(c)) continue;
+        const float2 *x = reinterpret_cast<const float2 *>(ml) + slot(c) * ROWS + row0;
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+            if (row0 + i < rows) top[i] = fmaxf(top[i], x[i].x);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float acc[E], sum = 0.f;
+    for (int o = 16; o; o >>= 1)
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int i = 0; i < RW; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
     for (int base = c0; base <= c1; base += 32) {
         const int c = base + lane;
-        float f = 0.f, l = 0.f;
-        int64_t sl = 0;
-        bool there = c <= c1 && tree_begin(total, p.ctas, c) != tree_begin(total, p.ctas, c + 1);
-        if (there) {
-            sl = slot(c);
-            const float2 x = *reinterpret_cast<const float2 *>(ml + (sl * ROWS + row) * 2);
-            there = x.x != -INFINITY;                      // an empty partial adds nothing
-            if (there) {
-                f = ex2(x.x - top);
-                l = x.y;
+        const bool on = there(c);
+        const int64_t sl = on ? slot(c) : 0;
+        float f[RW];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            f[i] = 0.f;
+            if (on && row0 + i < rows) {
+                const float2 x = reinterpret_cast<const float2 *>(ml)[sl * ROWS + row0 + i];
+                if (x.x != -INFINITY) {                     // an empty partial adds nothing
+                    f[i] = ex2(x.x - top[i]);
+                    sum[i] += x.y * f[i];
+                }
             }
         }
-        sum += l * f;
-        unsigned live = __ballot_sync(0xffffffffu, there);
-        while (live) {
-            const int k = __ffs(live) - 1;
-            live &= live - 1;
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const int64_t sk = __shfl_sync(0xffffffffu, sl, k);
-            const float *a = p.part + (sk * ROWS + row) * D + lane * E;
+        for (int k0 = 0; k0 < min(32, c1 - base + 1); k0 += 4) {
+            float x[4][RW][E], fk[4][RW];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += fk * a[e];
+            for (int k = 0; k < 4; ++k) {
+                const float *a = p.part + (__shfl_sync(0xffffffffu, sl, k0 + k) * ROWS + row0) * D + lane * E;
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    fk[k][i] = __shfl_sync(0xffffffffu, f[i], k0 + k);       // 0: nothing there to read
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[k][i][e] = fk[k][i] != 0.f ? a[i * D + e] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < RW; ++i)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[i][e] += fk[k][i] * x[k][i][e];
         }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float il = sum == 0.f ? 0.f : 1.f / sum;          // nothing visible: zeros
+    for (int o = 16; o; o >>= 1)
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= il;
-    if (!(p.flags & RQ_ATTN_ROTATED_OUT)) {
-        float sg[E];
-        lane_signs<E>(sg, lane, p.seed);
-        warp_rotate<E>(acc, sg, lane, !(p.flags & RQ_SIGNS_FIRST), inv_sqrt_dim<D>());
+        for (int i = 0; i < RW; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const float il = sum[i] == 0.f ? 0.f : 1.f / sum[i];    // nothing visible: zeros
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] *= il;
     }
-    const int64_t at = ((s.row0 + gr / p.group) * p.kv_heads + h) * p.group + gr % p.group;
+    if (!(p.flags & RQ_ATTN_ROTATED_OUT)) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) store_elem<IN>(p.out, at * D + lane * E + e, acc[e]);
+        for (int i = 0; i < RW; ++i) warp_rotate<E>(acc[i], sg, lane, !(p.flags & RQ_SIGNS_FIRST), inv_sqrt_dim<D>());
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int gr = mt * ROWS + row0 + i;
+        if (row0 + i >= rows) break;
+        const int64_t at = ((s.row0 + gr / p.group) * p.kv_heads + h) * p.group + gr % p.group;
+#pragma unroll
+        for (int e = 0; e < E; ++e) store_elem<IN>(p.out, at * D + lane * E + e, acc[i][e]);
+    }
+    }
+}
+
+template <int IN, int D, int ROWS, int TT>
+cudaError_t launch_tree_join(const TreeParams &p, cudaStream_t stream) {
+    const int bph = (int)(((int64_t)p.max_nodes * p.group + ROWS - 1) / ROWS);
+    const int64_t units = (int64_t)p.seqs * p.kv_heads * bph;
+    if (units > 0x7fffffffll) return cudaErrorInvalidValue;
+    // one turn per block while that leaves SMs idle; then blocks take several, so that
+    // each finds its unit once
+    constexpr int rows = kJoinWarps * join_rows(ROWS);
+    int turns = 1;
+    while (turns * rows < ROWS && units * (ROWS / (turns * rows)) > 2 * (int64_t)device_sm_count()) turns *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)units, (ROWS + turns * rows - 1) / (turns * rows));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tree_join_kernel<IN, D, ROWS, TT>, p, bph, turns);
 }
 
 }  // namespace

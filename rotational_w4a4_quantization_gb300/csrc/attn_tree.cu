@@ -569,8 +569,7 @@ int64_t attn_tree_workspace(int64_t head_dim) {
 }
 
 cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
-    if (attn_tree_tc_supported(c.in_type, c.head_dim, c.max_nodes * (c.q_heads / c.cache.heads)))
-        return launch_attn_tree_tc(c, stream);
+    if (attn_tree_tc_supported(c)) return launch_attn_tree_tc(c, stream);
     TreeParams p;
     if (!tree_params(c, p)) return cudaErrorUnknown;
     const int sms = device_sm_count();

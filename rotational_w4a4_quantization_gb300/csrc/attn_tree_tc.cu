@@ -61,10 +61,11 @@ struct TSmem {
     alignas(1024) uint8_t op[kOps][TILE];
     alignas(16) float ks[kSc][kTcTT];
     alignas(16) float vs[kSc][kTcTT];
-    float2 unit[kSc];                                       // a tile's 2^ek and ev; 0 and 0: masked, scales not folded in
+    float2 unit[kSc];                                       // a tile's 2^ek and ev; 0 and 0: scales not folded in
     float rfac[NT * 128];                                   // s = rfac S (times ks)
     float ref[2][NT == 1 ? 128 : 1], sum[2][NT == 1 ? 128 : 1];   // NT = 1: the teams' references and sums
     int64_t prefix[kScan + 1];
+    TreeWork work[2];                                       // each softmax team's stretch: kept here, not in registers
     alignas(8) uint64_t sc_full[kSc], sc_empty[kSc];
     uint64_t op_full[kOps], op_empty[kOps];
     uint64_t q_full, s_full[2], p_full[2], o_full[2];
@@ -192,6 +193,12 @@ __device__ __forceinline__ int tile_exponent(const float4 &x) {
                                                             max(__float_as_uint(x.z), __float_as_uint(x.w))));
     return top == 0 ? 0 : max(-100, min((int)((top >> 23) & 255u) - 126, 100));
 }
+// Each of four scales is 0 or within 2^12 of 2^e, and finite (checked where `asked`).
+__device__ __forceinline__ bool of_a_kind(const float4 &x, int e, bool asked) {
+    const float lo = __uint_as_float((uint32_t)(127 + max(e - 13, -120)) << 23), hi = __uint_as_float((uint32_t)(127 + e) << 23);
+    auto ok = [&](float v) { return v == 0.f || (v >= lo && v <= hi); };
+    return !asked || (ok(x.x) && ok(x.y) && ok(x.z) && ok(x.w));
+}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // |e| <= 126
 __device__ __forceinline__ uint4 ld_once(const void *p) {
     uint4 v;
@@ -238,9 +245,11 @@ struct SoftRow {
 // once for the tile and the second pass has neither votes nor branches (settling it per
 // chunk cost 200 cycles each); returns the factor that earlier tiles' sums need.
 //   s = a S (times ks where KS);  weight = 2^(s - M + ev)
-template <bool KS>
-__device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a, float ev, SoftRow &r) {
-    constexpr int C = kTcTT / kCW;
+// MASK: vis has a bit per token; the loops stay rolled, as few tiles come here.
+template <bool KS, bool MASK>
+__device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a, float ev, const uint32_t (&vis)[4], SoftRow &r) {
+    constexpr int C = kTcTT / kCW, UNROLL = MASK ? 1 : C / 2;
+    auto seen = [&](int c) { return (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> (kCW * (c & 1)); };
     uint32_t s0[kCW], s1[kCW];
     tm_ld16(tS, s0);
     float top0 = -INFINITY, top1 = -INFINITY;
@@ -255,11 +264,15 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a
                 v.z *= k.z;
                 v.w *= k.w;
             }
+            if constexpr (MASK) {
+                const uint32_t w = seen(c) >> i;
+                v = make_float4(w & 1 ? v.x : -INFINITY, w & 2 ? v.y : -INFINITY, w & 4 ? v.z : -INFINITY, w & 8 ? v.w : -INFINITY);
+            }
             top0 = max3(top0, v.x, v.y);
             top1 = max3(top1, v.z, v.w);
         }
     };
-#pragma unroll
+#pragma unroll(UNROLL)
     for (int c = 0; c < C; c += 2) {
         tc_wait_ld16(s0);
         tm_ld16(tS + kCW * (c + 1), s1);
@@ -292,6 +305,11 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a
                 t0 = __ffma2_rn(t0, a2, nm);
                 t1 = __ffma2_rn(t1, a2, nm);
             }
+            if constexpr (MASK) {
+                const uint32_t w = seen(c) >> (2 * i);
+                t0 = make_float2(w & 1 ? t0.x : -INFINITY, w & 2 ? t0.y : -INFINITY);
+                t1 = make_float2(w & 4 ? t1.x : -INFINITY, w & 8 ? t1.y : -INFINITY);
+            }
             const float2 p0 = make_float2(ex2(t0.x), ex2(t0.y)), p1 = make_float2(ex2(t1.x), ex2(t1.y));
             sum0 = __fadd2_rn(sum0, p0);
             sum1 = __fadd2_rn(sum1, p1);
@@ -302,7 +320,7 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a
         tm_st8(tS + kCW / 2 * c, pk);
     };
     // the columns of a chunk are overwritten by the weights of twice its number at the earliest
-#pragma unroll
+#pragma unroll(UNROLL)
     for (int c = 0; c < C; c += 2) {
         tc_wait_ld16(s0);
         tm_ld16(tS + kCW * (c + 1), s1);
@@ -316,20 +334,14 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a
     return f;
 }
 
-// The same for a tile with masks and exact codes: s = a S ks, weight = 2^(s - M) vs.  M
-// follows the largest s + log2 vs, the weight's exponent.  A masked weight is zero
-// whatever its scales hold.  Few tiles of a sequence come here, and their time is the
-// fetching of code that ran for none before: the loops stay rolled (unrolled, a masked
-// tile took 44,000 cycles, most of them instruction misses; now about 10,000).
+// The tokens of a tile that a row's node sees, a bit each: a warp reads a node's 32 mask
+// bytes together, and the rows of that node keep the ballot.
 //   node: this row's, node0, node1: the warp's first and last; valid: bit c says that
 //   tokens 16 c .. lie on a page of the cache.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
-__device__ __forceinline__ float soft_masked(const TreeParams &p, const TreeSeq &q, uint32_t tS, const float *ks, const float *vs,
-                                             float a, int node, int node0, int node1, int t0, uint32_t valid, SoftRow &r) {
-    // the tokens that this row's node sees, a bit each: a warp reads a node's 32 mask bytes
-    // together, and the rows of that node keep the ballot
+__device__ __forceinline__ void tree_visible(const TreeParams &p, const TreeSeq &q, int node, int node0, int node1, int t0,
+                                             uint32_t valid, uint32_t (&vis)[4]) {
     const int lane = threadIdx.x & 31;
-    uint32_t vis[4] = {0, 0, 0, 0};
 #pragma unroll 1
     for (int g = 0; g < 4; ++g) {
         const int t = t0 + 32 * g, j = t + lane - q.ctx;
@@ -341,7 +353,7 @@ __device__ __forceinline__ float soft_masked(const TreeParams &p, const TreeSeq 
         } else if (t < q.len) {
             const uint8_t *m = p.mask + q.row0 * p.mask_stride + j;
             const bool in = j >= 0 && j < q.n;
-#pragma unroll 4
+#pragma unroll 8
             for (int nd = node0; nd <= node1; ++nd) {
                 const uint32_t b = __ballot_sync(0xffffffffu, j < 0 || (in && m[nd * p.mask_stride] != 0));
                 if (nd == node) seen = b;
@@ -354,6 +366,15 @@ __device__ __forceinline__ float soft_masked(const TreeParams &p, const TreeSeq 
         vis[2] = vis[3];
         vis[3] = node < q.n ? seen : 0u;
     }
+}
+
+// A masked tile with exact codes, where some scale is not finite or the scales lie too
+// far apart to share a unit: s = a S ks, weight = 2^(s - M) vs.  M follows the largest
+// s + log2 vs, the weight's exponent.  A masked weight is zero whatever its scales hold.
+// Hardly a tile comes here, and its time is the fetching of code that ran for none
+// before: the loops stay rolled.
+__device__ __forceinline__ float soft_exact(uint32_t tS, const float *ks, const float *vs, float a, const uint32_t (&vis)[4],
+                                            SoftRow &r) {
     uint32_t x[kCW];
     float best = -INFINITY, only = -INFINITY;
 #pragma unroll 1
@@ -461,6 +482,11 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 if (nthere) {
                     nk = *reinterpret_cast<const float4 *>(p.ks + row);
                     nv = *reinterpret_cast<const float4 *>(p.vs + row);
+                    const int left = w.s.len - ((w.t0 + k) * kTcTT + 4 * lane);   // past the sequence: none
+                    if (left < 4) {
+                        nk = make_float4(nk.x, left > 1 ? nk.y : 0.f, left > 2 ? nk.z : 0.f, 0.f);
+                        nv = make_float4(nv.x, left > 1 ? nv.y : 0.f, left > 2 ? nv.z : 0.f, 0.f);
+                    }
                 }
             };
             load(0);
@@ -472,14 +498,16 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 const uint32_t quads = __ballot_sync(0xffffffffu, there);
                 const bool masked = (w.t0 + k + 1) * kTcTT > w.s.ctx || quads != 0xffffffffu;
                 const int ek = KFOLD ? tile_exponent(ck) : 0, ev = tile_exponent(cv);
+                // a tile that not every row sees whole folds its scales in if they are of a kind
+                const bool exact = masked && __any_sync(0xffffffffu, !(of_a_kind(ck, ek, KFOLD) && of_a_kind(cv, ev, true)));
                 uint32_t chunks = 0;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) chunks |= ((quads >> (4 * c)) & 1) << c;
                 warp_wait(&s.sc_empty[scs], ((sc / kSc) & 1) ^ 1, &s.abort_flag, p.err);
-                if (!KFOLD || masked) reinterpret_cast<float4 *>(s.ks[scs])[lane] = ck;
-                if (masked) reinterpret_cast<float4 *>(s.vs[scs])[lane] = cv;
+                if (!KFOLD || exact) reinterpret_cast<float4 *>(s.ks[scs])[lane] = ck;
+                if (exact) reinterpret_cast<float4 *>(s.vs[scs])[lane] = cv;
                 if (lane == 0) {
-                    s.unit[scs] = masked ? make_float2(0.f, 0.f) : make_float2(pow2(ek), (float)ev);
+                    s.unit[scs] = exact ? make_float2(0.f, 0.f) : make_float2(pow2(ek), (float)ev);
                     s.valid[scs] = chunks;
                 }
                 __syncwarp();
@@ -552,32 +580,35 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         auto both_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;
+        auto team_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + team) : "memory"); };
         uint32_t sc = 0, uses = 0, units = 0;          // tiles so far; S tiles of this team; finished stretches of this team
+        const TreeWork &w = s.work[team];
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
+            if (quarter == 0) {
+                const TreeWork x = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
+                if (lane == 0) s.work[team] = x;
+            }
+            team_sync();
             const int T = w.t1 - w.t0;
             at += T;
             const int rows = min(ROWS, w.s.n * p.group - w.mt * ROWS);        // of the block
 
             // ---- q~: four threads to a row, a quarter of its dims each; butterflies in
             // registers but for two exchanges ----
+            // 64 rows a pass; what lies in the tile beyond the last row's pass reaches no row that counts
 #pragma unroll 1
-            for (int pass = 0; pass < 2 * NT; ++pass) {
+            for (int pass = 0; pass * 64 < rows; ++pass) {
                 constexpr int HD = D / 4;
                 const int hf = threadIdx.x & 3, r = pass * 64 + ((threadIdx.x - 128) >> 2), rr = r & 127, gr = w.mt * ROWS + r;
+                const char *src = static_cast<const char *>(p.q) + ((w.s.row0 + gr / p.group) * p.q_token +
+                                  (w.h * p.group + gr % p.group) * p.q_head + hf * HD) * 2;
                 float2 v[HD / 2];
 #pragma unroll
-                for (int i = 0; i < HD / 2; ++i) v[i] = make_float2(0.f, 0.f);
-                if (r < rows) {
-                    const char *src = static_cast<const char *>(p.q) +
-                                      ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head + hf * HD) * 2;
+                for (int i = 0; i < HD / 8; ++i) {
+                    float f[8];
+                    unpack16<IN>(r < rows ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0u, 0u, 0u, 0u), f);
 #pragma unroll
-                    for (int i = 0; i < HD / 8; ++i) {
-                        float f[8];
-                        unpack16<IN>(reinterpret_cast<const uint4 *>(src)[i], f);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[4 * i + e] = make_float2(f[2 * e], f[2 * e + 1]);
-                    }
+                    for (int e = 0; e < 4; ++e) v[4 * i + e] = make_float2(f[2 * e], f[2 * e + 1]);
                 }
                 auto signs = [&] {
 #pragma unroll
@@ -659,15 +690,19 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 if (ok && !idle) {
                     const int t0 = (w.t0 + k) * kTcTT;
                     const float2 unit = s.unit[scs];
-                    const bool masked = unit.x == 0.f;
-                    const float a = masked ? fac : fac * unit.x, ev = unit.y;
+                    const uint32_t valid = s.valid[scs];
+                    const bool masked = t0 + kTcTT > w.s.ctx || valid != 0xffu;
+                    const float a = unit.x == 0.f ? fac : fac * unit.x, ev = unit.y;
                     float f;
                     if (!masked) {
-                        f = soft_tile<!KFOLD>(tS[team] + lanes, s.ks[scs], a, ev, r);
+                        const uint32_t none[4] = {0, 0, 0, 0};
+                        f = soft_tile<!KFOLD, false>(tS[team] + lanes, s.ks[scs], a, ev, none, r);
                     } else {
+                        uint32_t vis[4] = {0, 0, 0, 0};
                         const int wrow = w.mt * ROWS + brow - lane;
-                        f = soft_masked(p, w.s, tS[team] + lanes, s.ks[scs], s.vs[scs], a, node, wrow / p.group,
-                                        min((wrow + 31) / p.group, w.s.n - 1), t0, s.valid[scs], r);
+                        tree_visible(p, w.s, node, wrow / p.group, min((wrow + 31) / p.group, w.s.n - 1), t0, valid, vis);
+                        if (unit.x != 0.f) f = soft_tile<!KFOLD, true>(tS[team] + lanes, s.ks[scs], a, ev, vis, r);
+                        else f = soft_exact(tS[team] + lanes, s.ks[scs], s.vs[scs], a, vis, r);
                     }
                     if (!first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
@@ -830,6 +865,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             }
             tc_fence_before();
             if constexpr (NT == 1) both_sync();       // both accumulators are read: the next block may begin
+            else team_sync();                         // s.work may be written again
         }
     } else if (warp >= 4 + kSoftWarps) {
         // ---------------- converters ----------------
@@ -961,8 +997,14 @@ cudaError_t launch_tc(TreeParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-bool attn_tree_tc_supported(int in_type, int64_t head_dim, int64_t rows) {
-    return in_type != IN_F32 && (head_dim == 64 || head_dim == 128) && rows > 16;
+// Blocks of 128 rows pay a start of about 30 us per block of threads and then 2,600
+// cycles per 128 tokens; blocks of 16 rows start at once and pay 1,900 each.  Measured
+// (bf16, 8 KV heads x 128): 32 rows, 16 sequences of 4k: 82 us here, 68 us there; 48 rows:
+// 82 and 95; one sequence of 512, 128 rows: 31 and 23, as it has fewer tiles than SMs.
+bool attn_tree_tc_supported(const TreeCall &c) {
+    const int64_t rows = c.max_nodes * (c.q_heads / c.cache.heads);
+    const int64_t tiles = c.seqs * c.cache.heads * ((rows + 127) / 128) * ((c.width * c.cache.page_size + kTcTT - 1) / kTcTT);
+    return c.in_type != IN_F32 && (c.head_dim == 64 || c.head_dim == 128) && rows > 32 && tiles > device_sm_count();
 }
 
 int64_t attn_tree_tc_workspace(int64_t head_dim) {

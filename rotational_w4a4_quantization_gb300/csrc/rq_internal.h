@@ -142,8 +142,8 @@ struct TreeCall {
 int64_t attn_tree_workspace(int64_t head_dim);
 cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream);
 // Blocks of 128 or 256 rows on the tensor cores: 16-bit queries, head_dim 64 or 128,
-// more than 16 rows (nodes x query heads per KV head).
-bool attn_tree_tc_supported(int in_type, int64_t head_dim, int64_t rows);
+// enough rows (nodes x query heads per KV head) and tiles.
+bool attn_tree_tc_supported(const TreeCall &c);
 int64_t attn_tree_tc_workspace(int64_t head_dim);
 cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream);
 

@@ -27,16 +27,15 @@ __device__ __forceinline__ constexpr float inv_sqrt_dim() {
 
 // 8 consecutive elements (16 bytes, or 32 in fp32) at a 16-byte boundary, as 4 pairs.
 template <int IN>
-__device__ __forceinline__ void load8(const void *p, pair_t (&v)[4]) {
+__device__ __forceinline__ void unpack8(const uint4 *r, pair_t *v) {
     if constexpr (IN == IN_F32) {
-        const uint4 a = static_cast<const uint4 *>(p)[0], b = static_cast<const uint4 *>(p)[1];
+        const uint4 a = r[0], b = r[1];
         v[0] = ((pair_t)a.y << 32) | a.x;
         v[1] = ((pair_t)a.w << 32) | a.z;
         v[2] = ((pair_t)b.y << 32) | b.x;
         v[3] = ((pair_t)b.w << 32) | b.z;
     } else {
-        const uint4 a = *static_cast<const uint4 *>(p);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if constexpr (IN == IN_BF16) {
@@ -47,6 +46,13 @@ __device__ __forceinline__ void load8(const void *p, pair_t (&v)[4]) {
             }
         }
     }
+}
+template <int IN>
+__device__ __forceinline__ void load8(const void *p, pair_t (&v)[4]) {
+    uint4 r[IN == IN_F32 ? 2 : 1];
+#pragma unroll
+    for (int i = 0; i < (IN == IN_F32 ? 2 : 1); ++i) r[i] = static_cast<const uint4 *>(p)[i];
+    unpack8<IN>(r, v);
 }
 
 // 4 pairs rounded to the element type (once, to nearest even).

@@ -8,8 +8,9 @@
 // once per 16 rows.
 //
 //  * A block of 4 warps streams tiles of 128 tokens through a TMA ring; each warp
-//    takes 32 of them (16 cost twice the waits, votes and query loads per token).  A tile is codes of K and V (rows of D/2 bytes, swizzled by
-//    the TMA so that the reads below are free of bank conflicts) and their scales.
+//    takes 32 of them (16 cost twice the waits, votes and query loads per token).  A
+//    tile is codes of K and V (rows of D/2 bytes, swizzled by the TMA so that the reads
+//    below are free of bank conflicts) and their scales.
 //  * S = Q K^T: a lane reads the codes of a token straight into the B operand: nibbles j
 //    and j + 4 of a word are a pair, and u = code + 8 in the low bits of an fp16 is the
 //    subnormal u 2^-24 (16 u 2^-24 for odd j; q~ holds a sixteenth there): one logic
@@ -26,6 +27,13 @@
 //  * fp32 queries: q~ and P vs are split into two fp16 parts (22 bits) and the products
 //    run twice; codes are exact in either.  fp16 queries split q~ alone: their outputs
 //    resolve its rounding to 11 bits (4.6e-4 against 2.5e-4 of an output).
+//
+// Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
+// heads, one node: 130 us, 2.9 TB/s of cache, where 56 us is the reading alone; two
+// sequences of 256k, 4 query heads to a KV head: 167 us, 3.4 TB/s.  What bounds it is
+// instructions (about 380 per warp for 16 tokens: operands, softmax, fragments), so
+// memory waits; sequences shorter than that, one of 514 tokens, take the 15 us of their
+// latencies and 8 of the join, which overlap in part.
 #include "rq.h"
 #include "rq_internal.h"
 #include "tree_device.cuh"
@@ -130,7 +138,8 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         const int bt = min(kTT, 1 << p.log_page), pieces = kTT / bt;
         for (int64_t at = begin; at < end;) {
             const TreeWork w = tree_work<kRows, kTT>(p, s.prefix, at, end);
-            at += w.t1 - w.t0;
+            at += w.used;
+            if (w.t1 <= w.t0) continue;
             auto page_of = [&](int tile) -> int64_t {
                 const int t = tile * kTT + lane * bt;
                 if (lane >= pieces || t >= w.s.len) return -1;
@@ -179,7 +188,8 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 
     for (int64_t at = begin; at < end;) {
         const TreeWork w = tree_work<kRows, kTT>(p, s.prefix, at, end);
-        at += w.t1 - w.t0;
+        at += w.used;
+        if (w.t1 <= w.t0) continue;
         const int rows = min(kRows, w.s.n * p.group - w.mt * kRows);
 
         // ---- q~ of the block's rows: rotated in fp32, scaled by a power of two to below
@@ -504,7 +514,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         }
         // ---- rows out: finished, or as a partial ----
         float *part = p.part, *ml = p.part + (int64_t)2 * p.ctas * kRows * D;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (at - (w.t1 - w.t0) == begin ? 0 : 1);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (at - w.used == begin ? 0 : 1);
         float vsum[RW];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
@@ -578,6 +588,7 @@ cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
     const int64_t bph = (c.max_nodes * p.group + kRows - 1) / kRows;
     const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTT - 1) / kTT);
     p.ctas = (int)(max_tiles < per_sm * sms ? max_tiles : per_sm * sms);
+    p.lead = tree_lead(max_tiles, p.ctas);
     CUtensorMap mk, mv;
     if (!tree_maps(c, kTT, mk, mv)) return cudaErrorInvalidValue;
     switch (c.in_type) {

@@ -40,6 +40,15 @@
 // to keep P in range: it moves only when some P would pass 2^8 (the accumulator is then
 // rescaled in place, between the commit that delivers S and the arrival that delivers
 // P, when no MMA touches it).
+//
+// Measured (D = 128): 256 rows (bf16, 16 sequences of 32k, 8 KV heads): 404 us, 0.73
+// PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 4,600 cycles
+// of which the MMAs run 2,048.  The rest is the way from scores to weights and back, once
+// per team and tile (the softmax's 2,700 cycles of it are latency: the issue slots are a
+// third full).  Score buffers of 64 columns, so that a team's halves overlap, were slower
+// (423 us): Q K^T with N = 64 takes 48 cycles for 32's work, as it reads A for each.
+// 128 rows (fp16, 16 sequences of up to 4k): 88 us, where the bytes take 9: starts and
+// ends, 12,000 cycles to the first score and 18,000 from unit to unit.
 #include "rq.h"
 #include "rq_internal.h"
 #include "tree_device.cuh"
@@ -471,7 +480,8 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int64_t at = begin; at < end;) {
             const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
             const int T = w.t1 - w.t0;
-            at += T;
+            at += w.used;
+            if (T <= 0) continue;
             // lane l: tokens 4 l .. 4 l + 3 of a tile, the next tile's loaded ahead
             float4 nk, nv;
             bool nthere;
@@ -528,7 +538,8 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int64_t at = begin; at < end && ok; ++unit) {
             const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
             const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), J = NT * T;
-            at += T;
+            at += w.used;
+            if (T <= 0) continue;
             ok = warp_wait(&s.q_full, unit & 1, &s.abort_flag, p.err);
             auto qk = [&](int j) {
                 const int k = NT == 2 ? j >> 1 : j, t = j & 1;
@@ -590,7 +601,8 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             }
             team_sync();
             const int T = w.t1 - w.t0;
-            at += T;
+            at += w.used;
+            if (T <= 0) continue;
             const int rows = min(ROWS, w.s.n * p.group - w.mt * ROWS);        // of the block
 
             // ---- q~: four threads to a row, a quarter of its dims each; butterflies in
@@ -768,7 +780,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const int cfirst = NT == 2 ? 0 : team * C0;
             const int gr = w.mt * ROWS + brow;
             if (!w.whole) {
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (at - T == begin ? 0 : 1);
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (at - w.used == begin ? 0 : 1);
                 float *part = p.part + (slot * ROWS + brow) * D;
                 if (!idle) {
 #pragma unroll 1
@@ -884,7 +896,8 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int64_t at = begin; at < end;) {
             const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
             const int T = w.t1 - w.t0;
-            at += T;
+            at += w.used;
+            if (T <= 0) continue;
             // a pipeline of three items: pages of the second next, codes and scales of the next
             int32_t pg[N];
             uint4 nx[N];
@@ -1023,6 +1036,7 @@ cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream) {
     const int64_t bph = (rows + 128 * nt - 1) / (128 * nt);
     const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTcTT - 1) / kTcTT);
     p.ctas = (int)(max_tiles < sms ? max_tiles : sms);
+    p.lead = tree_lead(max_tiles, p.ctas);
     const bool d128 = c.head_dim == 128;
     if (c.in_type == IN_F16)
         return d128 ? launch_tc<IN_F16, 128, 1, 2>(p, stream) : launch_tc<IN_F16, 64, 1, 2>(p, stream);

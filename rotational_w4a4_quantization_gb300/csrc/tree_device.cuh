@@ -2,10 +2,10 @@
 // schedule of tiles over CTAs, and where partial results lie.  Internal linkage.
 //
 // A unit is (sequence, KV head, block of ROWS query rows); its tokens are cut into
-// tiles of TT.  All tiles of all units form one line, unit after unit, and CTA c of
-// G takes the stretch [c T / G, (c + 1) T / G): every CTA has the same number of
-// tiles whatever the lengths, long sequences spread over many CTAs, and a unit that
-// lies inside one stretch is finished there.  A unit that spans CTAs leaves one
+// tiles of TT.  All units form one line, each with its tiles and before them a lead
+// that stands for its fixed cost, and CTA c of G takes the stretch [c T / G,
+// (c + 1) T / G): CTAs end together whatever the lengths, long sequences spread over
+// many of them, and a unit that lies inside one stretch is finished there.  A unit that spans CTAs leaves one
 // partial per CTA: slot 2c for the unit the stretch begins in, 2c + 1 for the last.
 #pragma once
 
@@ -29,6 +29,7 @@ struct TreeParams {
     void *out;
     float *part;                        // [2 G][ROWS][D] fp32, then [2 G][ROWS][2] (reference, sum)
     int ctas;                           // G
+    int lead;                           // a unit's fixed cost, in tiles
     int *err;
 };
 
@@ -74,6 +75,14 @@ inline bool tree_maps(const TreeCall &c, int tile, CUtensorMap &mk, CUtensorMap 
     return make_tma_map_u8(&mk, c.cache.kq, rows, rb, rb, box, sw) && make_tma_map_u8(&mv, c.cache.vq, rows, rb, rb, box, sw);
 }
 
+// What a unit costs a CTA beside its tiles, in tiles: q~, the first tile's latency, the
+// masked tiles at its end and its output.  Measured: 0, 2, 4, 6 and 9 tiles give 97, 92,
+// 90, 88 and 88 us for 16 ragged sequences of up to 4k (128 rows, fp16), 136, 133, 131,
+// 130 and 131 us for 64 of up to 8k (8 rows, bf16).  Less where CTAs have few tiles each:
+// there the lead would leave some of them without any (one sequence of 512: 18.5 us
+// without, 20.5 with 6).
+inline int tree_lead(int64_t max_tiles, int ctas) { return (int)(max_tiles / ctas < 12 ? max_tiles / ctas / 2 : 6); }
+
 struct TreeSeq {
     int64_t row0;      // first query row
     int ctx, n, len;   // tokens before the tree, nodes, tokens in all
@@ -94,11 +103,15 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
     return s;
 }
 
-constexpr int kScan = 128;              // stretches of sequences whose tile counts are scanned
+constexpr int kScan = 128;              // stretches of sequences whose lengths are scanned
 
-// Exclusive prefix sums of the tile counts of kScan stretches of sequences, the
+// Exclusive prefix sums of the lengths in the line of kScan stretches of sequences, the
 // total in prefix[kScan].  Threads 0..kScan-1 of the block take part; the caller's
 // barrier follows.  Needs __syncthreads in between, so every thread calls it.
+// A unit's length in the line: its tiles, and before them its lead, what starting and
+// ending it costs a CTA.  With tiles alone CTAs that meet several short units end last.
+__device__ __forceinline__ int64_t unit_length(const TreeParams &p, const TreeSeq &s) { return s.nt ? s.nt + p.lead : 0; }
+
 template <int ROWS, int TT>
 __device__ __forceinline__ void tree_scan(const TreeParams &p, int64_t *prefix) {
     const int per = (p.seqs + kScan - 1) / kScan;
@@ -106,7 +119,7 @@ __device__ __forceinline__ void tree_scan(const TreeParams &p, int64_t *prefix) 
         int64_t sum = 0;
         for (int b = threadIdx.x * per; b < min(p.seqs, ((int)threadIdx.x + 1) * per); ++b) {
             const TreeSeq s = tree_seq<ROWS, TT>(p, b);
-            sum += (int64_t)p.kv_heads * s.mt * s.nt;
+            sum += (int64_t)p.kv_heads * s.mt * unit_length(p, s);
         }
         prefix[threadIdx.x] = sum;
     }
@@ -139,16 +152,17 @@ __device__ __forceinline__ void tree_scan(const TreeParams &p, int64_t *prefix) 
 struct TreeWork {
     TreeSeq s;
     int b, h, mt;          // sequence, KV head, row block
-    int t0, t1;            // the CTA's tiles of the unit
+    int t0, t1;            // the CTA's tiles of the unit; none where it ends within the unit's lead
+    int64_t used;          // of the line
     bool whole;            // the unit lies in this CTA alone
 };
 
 template <int ROWS, int TT>
-__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const int64_t *prefix, int64_t tile, int64_t end) {
+__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const int64_t *prefix, int64_t pos, int64_t end) {
     int lo = 0, hi = kScan;
-    while (hi - lo > 1) {                    // the last stretch that begins at or before the tile
+    while (hi - lo > 1) {                    // the last stretch that begins at or before pos
         const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= tile) lo = mid;
+        if (prefix[mid] <= pos) lo = mid;
         else hi = mid;
     }
     const int per = (p.seqs + kScan - 1) / kScan;
@@ -157,16 +171,17 @@ __device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const int64_t
     w.b = lo * per;
     while (true) {
         w.s = tree_seq<ROWS, TT>(p, w.b);
-        const int64_t tiles = (int64_t)p.kv_heads * w.s.mt * w.s.nt;
-        if (tile < at + tiles || w.b + 1 >= p.seqs) break;
-        at += tiles;
+        const int64_t length = (int64_t)p.kv_heads * w.s.mt * unit_length(p, w.s);
+        if (pos < at + length || w.b + 1 >= p.seqs) break;
+        at += length;
         ++w.b;
     }
-    const int64_t off = tile - at, u = off / w.s.nt;
-    w.t0 = (int)(off - u * w.s.nt);
+    const int64_t off = pos - at, length = unit_length(p, w.s), u = off / length, from = off - u * length;
+    w.used = min(length - from, end - pos);
+    w.t0 = (int)max((int64_t)0, from - p.lead);
+    w.t1 = (int)max((int64_t)0, from + w.used - p.lead);
     w.h = (int)(u / w.s.mt);
     w.mt = (int)(u - (int64_t)w.h * w.s.mt);
-    w.t1 = (int)min((int64_t)w.s.nt, w.t0 + (end - tile));
     w.whole = w.t0 == 0 && w.t1 == w.s.nt;
     return w;
 }
@@ -267,11 +282,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
     int64_t first = prefix[b / per];
     for (int i = b / per * per; i < b; ++i) {
         const TreeSeq x = tree_seq<ROWS, TT>(p, i);
-        first += (int64_t)p.kv_heads * x.mt * x.nt;
+        first += (int64_t)p.kv_heads * x.mt * unit_length(p, x);
     }
-    first += ((int64_t)h * s.mt + mt) * s.nt;
-    // CTA of a tile: the last c with total c / ctas <= tile
-    const int c0 = (int)(((first + 1) * p.ctas - 1) / total), c1 = (int)(((first + s.nt) * p.ctas - 1) / total);
+    first += ((int64_t)h * s.mt + mt) * unit_length(p, s);
+    const int64_t first_tile = first + p.lead, last = first + unit_length(p, s) - 1;
+    // CTA of a position: the last c with total c / ctas <= position
+    const int c0 = (int)(((first_tile + 1) * p.ctas - 1) / total), c1 = (int)(((last + 1) * p.ctas - 1) / total);
     if (c0 == c1) return;                                   // finished in its CTA
     float sg[E];
     lane_signs<E>(sg, lane, p.seed);

@@ -47,7 +47,7 @@
 // per team and tile (the softmax's 2,700 cycles of it are latency: the issue slots are a
 // third full).  Score buffers of 64 columns, so that a team's halves overlap, were slower
 // (423 us): Q K^T with N = 64 takes 48 cycles for 32's work, as it reads A for each.
-// 128 rows (fp16, 16 sequences of up to 4k): 88 us, where the bytes take 9: starts and
+// 64 rows (fp16, 16 sequences of up to 4k): 88 us, where the bytes take 9: starts and
 // ends, 12,000 cycles to the first score and 18,000 from unit to unit.
 #include "rq.h"
 #include "rq_internal.h"

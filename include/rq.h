@@ -404,7 +404,9 @@ rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, cons
  *   mask, the nodes j <= i.
  *     out = softmax(softmax_scale (q R) . k^) v^ R^T
  *   in fp32, with q~ and the weights rounded to fp16 on the way into the tensor cores
- *   (fp32 queries: split into two fp16 parts); a row that sees nothing is 0.  Tokens on
+ *   (fp32 queries: both, fp16 queries: q~ split into two fp16 parts), and with bf16
+ *   queries of more than 32 rows per KV head k^ and v^ as well; a row that sees nothing
+ *   is 0.  Tokens on
  *   a page number outside the cache, or past the table, are not seen.  What a cache row
  *   that a query does not see holds (NaN and infinite scales too) does not reach it.
  *

@@ -24,16 +24,18 @@
 // Tensor memory, 512 columns: S0 S1 (128 each; P overwrites the first half of its S)
 // and O0 O1 (D each).
 //
-// Scales.  In a tile that every row sees whole (all but the last ones of a sequence)
-// they are folded into the operands: k^ and v^ as fp16(code * scale), scales relative to
-// a power of two per tile, one rounding (the scale enters in two fp16 parts).  The
+// Scales.  With bf16 queries they are folded into the operands: k^ and v^ as fp16(code *
+// scale), scales relative to a power of two per tile, one rounding (the scale enters in
+// two fp16 parts).  The
 // softmax then reads nothing but its scores: broadcasting scales from shared memory
 // costs 4 cycles per 16 bytes and warp, and bound the kernel (8 warps x 64 loads per
 // tile; measured 2,150 cycles per tile for that softmax alone, against 2,048 of MMAs).
-// Tiles with masks keep exact codes and apply the scales to scores and weights, so that
-// what an unseen token holds (a NaN scale, say) reaches nobody.  fp16 queries, whose
-// outputs resolve an 11-bit rounding of q~ and k^, keep q~ in two fp16 parts (Q K^T runs
-// twice) and the scales of K out of the operand.
+// A tile that some row sees in part keeps exact codes if a scale of it is not finite or
+// they lie too far apart, and applies them to scores and weights, so that what an unseen
+// token holds (a NaN scale, say) reaches nobody.  fp16 queries, whose outputs resolve an
+// 11-bit rounding of q~, k^ and v^, keep q~ in two fp16 parts (Q K^T runs twice) and the
+// scales out of the operands; the weights with vs in them round once (16 sequences of up
+// to 4k: outputs 2.9e-4 off in 86 us; with the scales of V folded 3.3e-4 in 88).
 //
 // Weights: P = 2^(s - M + ev) (2^ev the tile's unit of vs) is what the MMA sees, rounded
 // to fp16; the sum l adds 2^(s - M) in fp32.  O / l does not depend on M, so M only has
@@ -47,7 +49,7 @@
 // per team and tile (the softmax's 2,700 cycles of it are latency: the issue slots are a
 // third full).  Score buffers of 64 columns, so that a team's halves overlap, were slower
 // (423 us): Q K^T with N = 64 takes 48 cycles for 32's work, as it reads A for each.
-// 64 rows (fp16, 16 sequences of up to 4k): 88 us, where the bytes take 9: starts and
+// 64 rows (fp16, 16 sequences of up to 4k): 86 us, where the bytes take 9: starts and
 // ends, 12,000 cycles to the first score and 18,000 from unit to unit.
 #include "rq.h"
 #include "rq_internal.h"
@@ -253,10 +255,11 @@ struct SoftRow {
 // the scores, the next kCW always on their way: the largest first, so that M is settled
 // once for the tile and the second pass has neither votes nor branches (settling it per
 // chunk cost 200 cycles each); returns the factor that earlier tiles' sums need.
-//   s = a S (times ks where KS);  weight = 2^(s - M + ev)
+//   s = a S;  weight = 2^(s - M + ev).  KS: the operands are exact codes, s = a S ks and
+//   the weights carry vs (relative to 2^ev).
 // MASK: vis has a bit per token; the loops stay rolled, as few tiles come here.
 template <bool KS, bool MASK>
-__device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a, float ev, const uint32_t (&vis)[4], SoftRow &r) {
+__device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, const float *vs, float a, float ev, const uint32_t (&vis)[4], SoftRow &r) {
     constexpr int C = kTcTT / kCW, UNROLL = MASK ? 1 : C / 2;
     auto seen = [&](int c) { return (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> (kCW * (c & 1)); };
     uint32_t s0[kCW], s1[kCW];
@@ -322,7 +325,13 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, float a
             const float2 p0 = make_float2(ex2(t0.x), ex2(t0.y)), p1 = make_float2(ex2(t1.x), ex2(t1.y));
             sum0 = __fadd2_rn(sum0, p0);
             sum1 = __fadd2_rn(sum1, p1);
-            const __half2 h0 = __floats2half2_rn(p0.x, p0.y), h1 = __floats2half2_rn(p1.x, p1.y);
+            float2 w0 = p0, w1 = p1;
+            if constexpr (KS) {
+                const float4 v = *reinterpret_cast<const float4 *>(vs + kCW * c + 2 * i);
+                w0 = __fmul2_rn(p0, make_float2(v.x, v.y));
+                w1 = __fmul2_rn(p1, make_float2(v.z, v.w));
+            }
+            const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
             pk[i] = *reinterpret_cast<const uint32_t *>(&h0);
             pk[i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
         }
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
     using S = TSmem<D, NT, HV>;
     constexpr int ROWS = 128 * NT, RB = D / 2;
-    constexpr bool KFOLD = HV == 1;                    // the scales of K go into the operand
+    constexpr bool FOLD = HV == 1;                     // the scales go into the operands
     extern __shared__ uint8_t raw[];
     S &s = *reinterpret_cast<S *>(raw + ((1024u - (t_smem(raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -507,15 +516,18 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 load(k + 1);
                 const uint32_t quads = __ballot_sync(0xffffffffu, there);
                 const bool masked = (w.t0 + k + 1) * kTcTT > w.s.ctx || quads != 0xffffffffu;
-                const int ek = KFOLD ? tile_exponent(ck) : 0, ev = tile_exponent(cv);
+                const int ek = FOLD ? tile_exponent(ck) : 0, ev = tile_exponent(cv);
                 // a tile that not every row sees whole folds its scales in if they are of a kind
-                const bool exact = masked && __any_sync(0xffffffffu, !(of_a_kind(ck, ek, KFOLD) && of_a_kind(cv, ev, true)));
+                const bool exact = masked && __any_sync(0xffffffffu, !(of_a_kind(ck, ek, FOLD) && of_a_kind(cv, ev, true)));
                 uint32_t chunks = 0;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) chunks |= ((quads >> (4 * c)) & 1) << c;
                 warp_wait(&s.sc_empty[scs], ((sc / kSc) & 1) ^ 1, &s.abort_flag, p.err);
-                if (!KFOLD || exact) reinterpret_cast<float4 *>(s.ks[scs])[lane] = ck;
-                if (exact) reinterpret_cast<float4 *>(s.vs[scs])[lane] = cv;
+                if (!FOLD || exact) {
+                    const float down = exact ? 1.f : pow2(-ev);
+                    reinterpret_cast<float4 *>(s.ks[scs])[lane] = ck;
+                    reinterpret_cast<float4 *>(s.vs[scs])[lane] = make_float4(cv.x * down, cv.y * down, cv.z * down, cv.w * down);
+                }
                 if (lane == 0) {
                     s.unit[scs] = exact ? make_float2(0.f, 0.f) : make_float2(pow2(ek), (float)ev);
                     s.valid[scs] = chunks;
@@ -708,12 +720,12 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     float f;
                     if (!masked) {
                         const uint32_t none[4] = {0, 0, 0, 0};
-                        f = soft_tile<!KFOLD, false>(tS[team] + lanes, s.ks[scs], a, ev, none, r);
+                        f = soft_tile<!FOLD, false>(tS[team] + lanes, s.ks[scs], s.vs[scs], a, ev, none, r);
                     } else {
                         uint32_t vis[4] = {0, 0, 0, 0};
                         const int wrow = w.mt * ROWS + brow - lane;
                         tree_visible(p, w.s, node, wrow / p.group, min((wrow + 31) / p.group, w.s.n - 1), t0, valid, vis);
-                        if (unit.x != 0.f) f = soft_tile<!KFOLD, true>(tS[team] + lanes, s.ks[scs], a, ev, vis, r);
+                        if (unit.x != 0.f) f = soft_tile<!FOLD, true>(tS[team] + lanes, s.ks[scs], s.vs[scs], a, ev, vis, r);
                         else f = soft_exact(tS[team] + lanes, s.ks[scs], s.vs[scs], a, vis, r);
                     }
                     if (!first && __any_sync(0xffffffffu, f != 1.f)) {
@@ -927,7 +939,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     if (pg[n] >= 0 && pg[n] < p.pages) {
                         const int64_t row = (((int64_t)pg[n] * p.kv_heads + w.h) << p.log_page) + (t & ((1 << p.log_page) - 1));
                         nx[n] = ld_once(codes + row * RB);
-                        if (is_v || KFOLD) nf[n] = scales[row];
+                        if (FOLD) nf[n] = scales[row];
                     }
                 }
             };
@@ -954,8 +966,8 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 ok = warp_wait(&s.op_empty[slot], ((it / kOps) & 1) ^ 1, &s.abort_flag, p.err) && ok;
                 if (ok) {
                     const float2 unit = s.unit[scs];
-                    const bool fold = unit.x != 0.f && (is_v || KFOLD);
-                    const float down = is_v ? pow2(-(int)unit.y) : __uint_as_float((254u << 23) - __float_as_uint(unit.x));   // 1 / 2^ek
+                    const bool fold = FOLD && unit.x != 0.f;
+                    const float down = !FOLD ? 1.f : is_v ? pow2(-(int)unit.y) : __uint_as_float((254u << 23) - __float_as_uint(unit.x));   // 1 / 2^ek
                     uint8_t *const dst = dst0 + slot * S::TILE;
 #pragma unroll
                     for (int n = 0; n < N; ++n) {

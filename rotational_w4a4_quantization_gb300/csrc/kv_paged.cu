@@ -12,7 +12,13 @@
 // the other).  A row is spread over 4 lanes (8 for D = 256), 32 elements each at
 // D = 128, interleaved in 8-element chunks so that every load and store covers whole
 // lines: 5 of the 7 butterfly stages run in registers as f32x2 operations, 2 as
-// shuffles, and no shared memory is passed through.
+// shuffles, and no shared memory is passed through.  Reading up to 128 elements a row
+// does without the shuffles (see there).
+//
+// Measured (32 heads x 128, bf16): writing 2048 tokens 17.9 us, 2.4 TB/s, where 6.3 us
+// is the moving alone: instructions and the shuffles' rate (one warp's per cycle and SM);
+// reading 8192 tokens 42 us, 4.0 TB/s, of which 134 of 170 MB are written.  Single
+// tokens of 16 sequences: 4.4 and 5.2 us, latencies.
 #include "rq.h"
 #include "rq_internal.h"
 #include "paged_device.cuh"

@@ -11,7 +11,7 @@
 // head rows, each thread always the same 16-byte piece (or pair of pieces) of a row.
 // Rows whose addresses or rot do not allow 16-byte pieces go element by element.
 //
-// Measured: 32,768 tokens of 32 + 8 heads x 128 (bf16) 227 us, 5.9 TB/s, 0.87 of a copy's
+// Measured: 65,536 tokens of 32 + 8 heads x 128 (bf16) 227 us, 5.9 TB/s, 0.87 of a copy's
 // rate; two rows in flight per thread, as one gives 232 us and four 249.  One token: 4 us,
 // its latencies; a call's host side takes 17.
 #include "rq.h"

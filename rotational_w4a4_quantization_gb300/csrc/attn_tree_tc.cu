@@ -43,7 +43,7 @@
 // rescaled in place, between the commit that delivers S and the arrival that delivers
 // P, when no MMA touches it).
 //
-// Measured (D = 128): 256 rows (bf16, 16 sequences of 32k, 8 KV heads): 404 us, 0.73
+// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 404 us, 0.73
 // PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 4,600 cycles
 // of which the MMAs run 2,048.  The rest is the way from scores to weights and back, once
 // per team and tile (the softmax's 2,700 cycles of it are latency: the issue slots are a

@@ -1,11 +1,11 @@
 // attn_tree.cu -- attention of trees of drafted tokens (or of single tokens) over
-// the paged rotated INT4 cache (sm_103a): blocks of 16 query rows on mma.sync.
+// the paged rotated INT4 cache (sm_103a): blocks of 8 or 16 query rows on mma.sync.
 //
 //   q~ = q R;  e_t = softmax_scale (q~ . k^_t) over the context and the visible
 //   nodes;  p = softmax(e);  out = (sum_t p_t v^_t) R^T
 // with k^_t = ks_t * codes, v^_t = vs_t * codes.  The G query heads of a KV head and
 // the nodes of a sequence together are the rows of one product, so the cache is read
-// once per 16 rows.
+// once per block of rows.
 //
 //  * A block of 4 warps streams tiles of 128 tokens through a TMA ring; each warp
 //    takes 32 of them (16 cost twice the waits, votes and query loads per token).  A
@@ -24,16 +24,21 @@
 //    is the B operand after the same nibble step.  P vs is rounded to fp16 (11 bits,
 //    below the rounding of 16-bit outputs), vs relative to a power of two that moves
 //    like the softmax's reference.
+//  * Up to 8 rows (single tokens of up to 8 query heads to a KV head): the products are
+//    turned, S^T = K q~^T and O^T = V^T P^T, with tokens and dims as the 16 of m16n8k16
+//    and the rows as its 8.  The same registers are the operands, P^T passes through
+//    movmatrix, and half of the products, of the softmax and of the accumulators is gone:
+//    three blocks fit an SM (128 registers) where two did (168).
 //  * fp32 queries: q~ and P vs are split into two fp16 parts (22 bits) and the products
 //    run twice; codes are exact in either.  fp16 queries split q~ alone: their outputs
 //    resolve its rounding to 11 bits (4.6e-4 against 2.5e-4 of an output).
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
-// heads, one node: 130 us, 2.9 TB/s of cache, where 56 us is the reading alone; two
-// sequences of 256k, 4 query heads to a KV head: 167 us, 3.4 TB/s.  What bounds it is
-// instructions (about 380 per warp for 16 tokens: operands, softmax, fragments), so
-// memory waits; sequences shorter than that, one of 514 tokens, take the 15 us of their
-// latencies and 8 of the join, which overlap in part.
+// heads, one node: 104 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
+// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 137
+// us, 4.2 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
+// memory waits.  One sequence of 514 tokens takes the 15 us of its latencies and 8 of the
+// join, which overlap in part.
 #include "rq.h"
 #include "rq_internal.h"
 #include "tree_device.cuh"
@@ -41,16 +46,16 @@
 namespace rq {
 namespace {
 
-constexpr int kRows = 16, kTT = 128, kStages = 3, kCWarps = 4;
+constexpr int kTT = 128, kStages = 3, kCWarps = 4;
 constexpr int kWT = kTT / kCWarps / 8;               // n8 tiles of tokens per warp and tile
 constexpr int kMThreads = 32 * (kCWarps + 1);
 
 // Blocks that share an SM: what the registers of the fragments allow.
-constexpr int blocks_per_sm(int in_type, int64_t head_dim) {
-    return head_dim == 256 ? 1 : 2;
+constexpr int blocks_per_sm(int rows, int64_t head_dim) {
+    return head_dim == 256 ? 1 : rows == 8 ? 3 : 2;
 }
 
-template <int IN, int D>
+template <int IN, int D, int ROWS>
 struct MSmem {
     static constexpr int RB = D / 2;
     static constexpr int HQ = IN == IN_BF16 ? 1 : 2, HP = IN == IN_F32 ? 2 : 1;   // fp16 parts of q~, of the weights
@@ -58,10 +63,10 @@ struct MSmem {
     alignas(1024) uint8_t vq[kStages][kTT * RB];
     alignas(16) float ks[kStages][kTT];
     alignas(16) float vs[kStages][kTT];
-    alignas(16) uint32_t q[HQ][D / 16][32][4];         // q~ as A fragments: k step, lane, register
-    float acc[2][kRows][D + 4];                      // the warps' sums, joined two by two
-    float ref[kCWarps][kRows], sum[kCWarps][kRows];
-    float2 rfac[kRows];                              // a, b
+    alignas(16) uint32_t q[HQ][D / 16][32][ROWS / 4];  // q~ as fragments: k step, lane, register
+    float acc[2][ROWS][D + 4];                       // the warps' sums, joined two by two
+    float ref[kCWarps][ROWS], sum[kCWarps][ROWS];
+    float2 rfac[ROWS];                               // a, b
     int vexp[kCWarps];
     int64_t prefix[kScan + 1];
     alignas(8) uint64_t full[kStages], empty[kStages];
@@ -104,16 +109,24 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// An 8 x 8 matrix of fp16 pairs, transposed across the warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ float2 unpack_h2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
 
-template <int IN, int D>
-__global__ void __launch_bounds__(kMThreads, blocks_per_sm(IN, D))
+template <int IN, int D, int ROWS>
+__global__ void __launch_bounds__(kMThreads, blocks_per_sm(ROWS, D))
 attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ TreeParams p) {
-    using S = MSmem<IN, D>;
+    using S = MSmem<IN, D, ROWS>;
     constexpr int RB = D / 2, WPT = D / 32, E = D / 32, HQ = S::HQ, HP = S::HP;
     constexpr bool kOffset = IN != IN_F32;             // keys as u = code + 8 (see the top)
     constexpr int NQ = D / 32;                        // 16-byte chunks of a code row
+    constexpr bool SIDE = ROWS == 8;                  // products of tokens x rows instead of rows x tokens
+    constexpr int kRowLo = SIDE ? 4 : 1, kRowHi = SIDE ? 32 : 4;   // lane bits that a row's scores are spread over
     extern __shared__ uint8_t raw[];
     S &s = *reinterpret_cast<S *>(raw + ((1024u - (t_smem(raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -127,7 +140,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tree_join_may_begin();
-    tree_scan<kRows, kTT>(p, s.prefix);               // ends with a block barrier
+    tree_scan<ROWS, kTT>(p, s.prefix);               // ends with a block barrier
     const int64_t total = s.prefix[kScan];
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
     int st = 0;
@@ -137,7 +150,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         // ---------------- producer: one lane per page piece of a tile ----------------
         const int bt = min(kTT, 1 << p.log_page), pieces = kTT / bt;
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<kRows, kTT>(p, s.prefix, at, end);
+            const TreeWork w = tree_work<ROWS, kTT>(p, s.prefix, at, end);
             at += w.used;
             if (w.t1 <= w.t0) continue;
             auto page_of = [&](int tile) -> int64_t {
@@ -187,18 +200,18 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;
 
     for (int64_t at = begin; at < end;) {
-        const TreeWork w = tree_work<kRows, kTT>(p, s.prefix, at, end);
+        const TreeWork w = tree_work<ROWS, kTT>(p, s.prefix, at, end);
         at += w.used;
         if (w.t1 <= w.t0) continue;
-        const int rows = min(kRows, w.s.n * p.group - w.mt * kRows);
+        const int rows = min(ROWS, w.s.n * p.group - w.mt * ROWS);
 
         // ---- q~ of the block's rows: rotated in fp32, scaled by a power of two to below
         // 1 (its inverse goes into the row's score factor), rounded to fp16 once ----
-        constexpr int RW = kRows / kCWarps;                  // rows warp, warp + 4, ... : all at once
+        constexpr int RW = ROWS / kCWarps;                  // rows warp, warp + 4, ... : all at once
         float qv[RW][E];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-            const int r = i * kCWarps + warp, gr = w.mt * kRows + r;
+            const int r = i * kCWarps + warp, gr = w.mt * ROWS + r;
             const char *src = static_cast<const char *>(p.q) +
                               ((w.s.row0 + gr / p.group) * p.q_token + (w.h * p.group + gr % p.group) * p.q_head) *
                                   (IN == IN_F32 ? 4 : 2);
@@ -231,7 +244,8 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 // chunk(s) of a code row that its K operand comes from
                 const int d = lane * E + e, j = d & 3;
                 const int fc = D == 256 ? (d >> 5) & 3 : d / (D / 4), wd = D == 256 ? ((d >> 7) << 2) + ((d & 31) >> 3) : (d % (D / 4)) >> 3;
-                const int at_q = (((2 * wd + (j >> 1)) * 32 + (r & 7) * 4 + fc) * 4 + (j & 1) * 2 + (r >> 3)) * 2 + ((d >> 2) & 1);
+                const int reg = SIDE ? j & 1 : (j & 1) * 2 + (r >> 3);
+                const int at_q = (((2 * wd + (j >> 1)) * 32 + (r & 7) * 4 + fc) * (ROWS / 4) + reg) * 2 + ((d >> 2) & 1);
                 const float x = qv[i][e] * (kOffset && (d & 1) ? 0.0625f * down : down);
                 const __half hi = __float2half_rn(x);
                 float got = __half2float(hi);
@@ -257,11 +271,14 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         }
         cta_sync();
 
-        const float2 rs0 = s.rfac[g], rs1 = s.rfac[g + 8];
+        // this lane's two rows of scores
+        const int row0 = SIDE ? 2 * c : g, row1 = SIDE ? 2 * c + 1 : g + 8;
+        const float2 rs0 = s.rfac[row0], rs1 = s.rfac[row1];
 
-        float acc[NQ * 4][4];
+        constexpr int NA = SIDE ? NQ * 2 : NQ * 4;
+        float acc[NA][4];
 #pragma unroll
-        for (int i = 0; i < NQ * 4; ++i)
+        for (int i = 0; i < NA; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
         float z0 = 0.f, z1 = 0.f, l0 = 0.f, l1 = 0.f;                                     // references, sums
@@ -276,7 +293,8 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             const int t_first = tile * kTT + tk;
             if (ok && t_first < w.s.len) {
                 // ---- S = Q K^T ----
-                float sc[kWT][4];
+                constexpr int NS = SIDE ? kWT / 2 : kWT;
+                float sc[NS][4];
                 constexpr int KP = WPT < 4 ? WPT : 4;                 // words loaded at once
                 const uint8_t *krow = s.kq[st] + (tk + g) * RB;
 #pragma unroll
@@ -307,41 +325,64 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         for (int hv = 0; hv < HQ; ++hv)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
-                                const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+                                const bool begins = part == 0 && wd == 0 && hv == 0 && i == 0;
+                                if constexpr (SIDE) {
+                                    const uint2 x = *reinterpret_cast<const uint2 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
 #pragma unroll
-                                for (int t = 0; t < kWT; ++t) {
-                                    if (part == 0 && wd == 0 && hv == 0 && i == 0) mma16816_first(sc[t], a, b[t][0], b[t][1]);
-                                    else mma16816(sc[t], a, b[t][2 * i], b[t][2 * i + 1]);
+                                    for (int t = 0; t < NS; ++t) {
+                                        const uint32_t a[4] = {b[2 * t][2 * i], b[2 * t + 1][2 * i], b[2 * t][2 * i + 1], b[2 * t + 1][2 * i + 1]};
+                                        if (begins) mma16816_first(sc[t], a, x.x, x.y);
+                                        else mma16816(sc[t], a, x.x, x.y);
+                                    }
+                                } else {
+                                    const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
+                                    const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                    for (int t = 0; t < kWT; ++t) {
+                                        if (begins) mma16816_first(sc[t], a, b[t][0], b[t][1]);
+                                        else mma16816(sc[t], a, b[t][2 * i], b[t][2 * i + 1]);
+                                    }
                                 }
                             }
                     }
                 }
                 // ---- scores against the references: s - z ----
-                float2 vscale[kWT];
-                const float *ks = s.ks[st] + tk + 2 * c, *vs = s.vs[st] + tk + 2 * c;
+                // sc[t][k]: row k < 2 of the lane's two where rows lead, k & 1 where tokens do;
+                // token tok(t, k) of the warp's
+                float2 vscale[NS];
+                const float *ks = s.ks[st] + tk + (SIDE ? g : 2 * c), *vs = s.vs[st] + tk + (SIDE ? g : 2 * c);
+                auto second = [](int k) { return SIDE ? (k & 1) != 0 : k >= 2; };          // of the two rows
+                auto later = [](int k) { return SIDE ? k >= 2 : (k & 1) != 0; };           // of the two tokens
+                auto tok = [&](int t, int k) { return SIDE ? 16 * t + 8 * (k >> 1) + g : 8 * t + 2 * c + (k & 1); };
 #pragma unroll
-                for (int t = 0; t < kWT; ++t) {
-                    const float2 k = *reinterpret_cast<const float2 *>(ks + 8 * t);
-                    vscale[t] = *reinterpret_cast<const float2 *>(vs + 8 * t);
-                    sc[t][0] = fmaf(fmaf(sc[t][0], rs0.x, rs0.y), k.x, -z0);
-                    sc[t][1] = fmaf(fmaf(sc[t][1], rs0.x, rs0.y), k.y, -z0);
-                    sc[t][2] = fmaf(fmaf(sc[t][2], rs1.x, rs1.y), k.x, -z1);
-                    sc[t][3] = fmaf(fmaf(sc[t][3], rs1.x, rs1.y), k.y, -z1);
+                for (int t = 0; t < NS; ++t) {
+                    float2 kk;
+                    if constexpr (SIDE) {
+                        kk = make_float2(ks[16 * t], ks[16 * t + 8]);
+                        vscale[t] = make_float2(vs[16 * t], vs[16 * t + 8]);
+                    } else {
+                        kk = *reinterpret_cast<const float2 *>(ks + 8 * t);
+                        vscale[t] = *reinterpret_cast<const float2 *>(vs + 8 * t);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 rs = second(k) ? rs1 : rs0;
+                        sc[t][k] = fmaf(fmaf(sc[t][k], rs.x, rs.y), later(k) ? kk.y : kk.x, second(k) ? -z1 : -z0);
+                    }
                 }
                 const uint32_t valid = s.valid[st];
                 const bool masked = t_first + 8 * kWT > w.s.ctx || valid != all;
                 if (masked) {
                     const int lp = min(p.log_page, 7);
 #pragma unroll
-                    for (int t = 0; t < kWT; ++t) {
+                    for (int t = 0; t < NS; ++t) {
                         bool any[2] = {false, false};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int tl = tk + 8 * t + 2 * c + (k & 1);
+                            const int tl = tk + tok(t, k);
                             const bool sees = ((valid >> (tl >> lp)) & 1) &&
-                                              tree_sees<kRows>(p, w, g + (k < 2 ? 0 : 8), tile * kTT + tl);
-                            any[k & 1] |= sees;
+                                              tree_sees<ROWS>(p, w, second(k) ? row1 : row0, tile * kTT + tl);
+                            any[later(k)] |= sees;
                             if (!sees) sc[t][k] = -INFINITY;
                         }
                         // a value row that none of this lane's two query rows sees does not move
@@ -353,14 +394,17 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 // ---- lazy references ----
                 float up0 = -INFINITY, up1 = -INFINITY, vtop = 0.f;
 #pragma unroll
-                for (int t = 0; t < kWT; ++t) {
-                    up0 = fmaxf(up0, fmaxf(sc[t][0], sc[t][1]));
-                    up1 = fmaxf(up1, fmaxf(sc[t][2], sc[t][3]));
+                for (int t = 0; t < NS; ++t) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float &up = second(k) ? up1 : up0;
+                        up = fmaxf(up, sc[t][k]);
+                    }
                     vtop = fmaxf(vtop, fmaxf(vscale[t].x, vscale[t].y));
                 }
                 if (__any_sync(0xffffffffu, up0 > lim0 || up1 > lim1 || vtop * vf > 64.f)) {
 #pragma unroll
-                    for (int o = 1; o < 4; o <<= 1) {
+                    for (int o = kRowLo; o < kRowHi; o <<= 1) {
                         up0 = fmaxf(up0, __shfl_xor_sync(0xffffffffu, up0, o));
                         up1 = fmaxf(up1, __shfl_xor_sync(0xffffffffu, up1, o));
                     }
@@ -375,10 +419,9 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     z0 += d0; z1 += d1;
                     l0 *= f0; l1 *= f1;
 #pragma unroll
-                    for (int t = 0; t < kWT; ++t) {
-                        sc[t][0] -= d0; sc[t][1] -= d0;
-                        sc[t][2] -= d1; sc[t][3] -= d1;
-                    }
+                    for (int t = 0; t < NS; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sc[t][k] -= second(k) ? d1 : d0;
                     if (vtop * vf > 64.f) {
                         const int nv = max(-100, min((int)(__float_as_uint(vtop) >> 23) - 127, 100));
                         const float dv = ve - nv < -126 ? 0.f : __uint_as_float((uint32_t)(127 + ve - nv) << 23);
@@ -387,28 +430,26 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         f0 *= dv; f1 *= dv;
                     }
 #pragma unroll
-                    for (int i = 0; i < NQ * 4; ++i) {
-                        acc[i][0] *= f0; acc[i][1] *= f0;
-                        acc[i][2] *= f1; acc[i][3] *= f1;
-                    }
+                    for (int i = 0; i < NA; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[i][k] *= second(k) ? f1 : f0;
                 }
                 // ---- weights ----
 #pragma unroll
-                for (int t = 0; t < kWT; ++t) {
-                    const bool h0 = masked && sc[t][0] == -INFINITY, h1 = masked && sc[t][1] == -INFINITY;
-                    const bool h2 = masked && sc[t][2] == -INFINITY, h3 = masked && sc[t][3] == -INFINITY;
+                for (int t = 0; t < NS; ++t) {
+                    bool hidden[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[t][k] = ex2(sc[t][k]);
-                    l0 += sc[t][0] + sc[t][1];
-                    l1 += sc[t][2] + sc[t][3];
+                    for (int k = 0; k < 4; ++k) {
+                        hidden[k] = masked && sc[t][k] == -INFINITY;
+                        sc[t][k] = ex2(sc[t][k]);
+                    }
+                    l0 += SIDE ? sc[t][0] + sc[t][2] : sc[t][0] + sc[t][1];
+                    l1 += SIDE ? sc[t][1] + sc[t][3] : sc[t][2] + sc[t][3];
                     const float v0 = vscale[t].x * vf, v1 = vscale[t].y * vf;
-                    sc[t][0] *= v0; sc[t][1] *= v1;
-                    sc[t][2] *= v0; sc[t][3] *= v1;
-                    if (masked) {        // a masked weight is zero, also where the value's scale is not finite
-                        if (h0) sc[t][0] = 0.f;
-                        if (h1) sc[t][1] = 0.f;
-                        if (h2) sc[t][2] = 0.f;
-                        if (h3) sc[t][3] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sc[t][k] *= later(k) ? v1 : v0;
+                        if (masked && hidden[k]) sc[t][k] = 0.f;   // also where the value's scale is not finite
                     }
                 }
                 // ---- O += (P vs) V, 16 tokens at a time ----
@@ -416,26 +457,49 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 const int mrow = tk + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
                 for (int h = 0; h < kWT / 2; ++h) {
-                    uint32_t pa[HP][4];
+                    uint32_t pa[HP][4];                             // SIDE: two registers of each
+                    if constexpr (SIDE) {
+                        // [token][row] -> [row][token]
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const float *x = sc[2 * h + t];
-                        pa[0][2 * t] = pack_h2(x[0], x[1]);
-                        pa[0][2 * t + 1] = pack_h2(x[2], x[3]);
-                        if constexpr (HP == 2) {
-                            const float2 a = unpack_h2(pa[0][2 * t]), b = unpack_h2(pa[0][2 * t + 1]);
-                            pa[1][2 * t] = pack_h2(x[0] - a.x, x[1] - a.y);
-                            pa[1][2 * t + 1] = pack_h2(x[2] - b.x, x[3] - b.y);
+                        for (int t = 0; t < 2; ++t) {
+                            const float *x = sc[h] + 2 * t;
+                            const uint32_t hi = pack_h2(x[0], x[1]);
+                            pa[0][t] = transposed(hi);
+                            if constexpr (HP == 2) {
+                                const float2 a = unpack_h2(hi);
+                                pa[1][t] = transposed(pack_h2(x[0] - a.x, x[1] - a.y));
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const float *x = sc[(2 * h + t) % NS];
+                            pa[0][2 * t] = pack_h2(x[0], x[1]);
+                            pa[0][2 * t + 1] = pack_h2(x[2], x[3]);
+                            if constexpr (HP == 2) {
+                                const float2 a = unpack_h2(pa[0][2 * t]), b = unpack_h2(pa[0][2 * t + 1]);
+                                pa[1][2 * t] = pack_h2(x[0] - a.x, x[1] - a.y);
+                                pa[1][2 * t + 1] = pack_h2(x[2] - b.x, x[3] - b.y);
+                            }
                         }
                     }
                     auto pv = [&](int q, uint32_t x, uint32_t y) {
                         uint32_t b0[4], b1[4];
                         code_pairs(x, b0);
                         code_pairs(y, b1);
+                        if constexpr (SIDE) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                            for (int j = 0; j < 4; j += 2) {
+                                const uint32_t a[4] = {b0[j], b0[j + 1], b1[j], b1[j + 1]};
 #pragma unroll
-                            for (int hv = 0; hv < HP; ++hv) mma16816(acc[4 * q + j], pa[hv], b0[j], b1[j]);
+                                for (int hv = 0; hv < HP; ++hv) mma16816(acc[2 * q + j / 2], a, pa[hv][0], pa[hv][1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int hv = 0; hv < HP; ++hv) mma16816(acc[(4 * q + j) % NA], pa[hv], b0[j], b1[j]);
+                        }
                     };
                     if constexpr (NQ == 1) {
                         uint32_t x, y;
@@ -465,16 +529,16 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 
         // ---- join the warps: references first, then the sums two by two ----
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
+        for (int o = kRowLo; o < kRowHi; o <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
         const float m0 = lim0 == 8.f || !(l0 == 0.f) ? z0 : -INFINITY, m1 = lim1 == 8.f || !(l1 == 0.f) ? z1 : -INFINITY;
-        if (c == 0) {
-            s.ref[warp][g] = m0;
-            s.ref[warp][g + 8] = m1;
-            s.sum[warp][g] = l0;
-            s.sum[warp][g + 8] = l1;
+        if (SIDE ? g == 0 : c == 0) {
+            s.ref[warp][row0] = m0;
+            s.ref[warp][row1] = m1;
+            s.sum[warp][row0] = l0;
+            s.sum[warp][row1] = l1;
         }
         cta_sync();
         auto joined = [&](int r, float &top, float &sum) {
@@ -487,11 +551,12 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 if (s.ref[i][r] != -INFINITY) sum += s.sum[i][r] * ex2(s.ref[i][r] - top);
         };
         float top0, top1, sum0, sum1;
-        joined(g, top0, sum0);
-        joined(g + 8, top1, sum1);
+        joined(row0, top0, sum0);
+        joined(row1, top1, sum1);
         const float vup = __uint_as_float((uint32_t)(127 + ve) << 23);
         const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - top0) * vup, f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top1) * vup;
-        // accumulator (chunk q, j) of lane column c: dims 32 q + 8 c + j and + 4 + j
+        // accumulators: dims 32 q + 8 c + j and + 4 + j of rows g, g + 8; SIDE: dim 32 q + 4 g + j
+        // of rows 2 c, 2 c + 1
 #pragma unroll
         for (int step = 0; step < 2; ++step) {
             if ((warp >> 1) == 1 - step) {                  // warps 2, 3 write, then 0, 1 add
@@ -499,21 +564,23 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 #pragma unroll
                 for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = g + (k < 2 ? 0 : 8);
-                        const float f = k < 2 ? f0 : f1;
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float *x = &dst[r][32 * q + 8 * c + 4 * (k & 1) + j];
-                            const float val = f == 0.f ? 0.f : acc[4 * q + j][k] * f;
-                            *x = step == 0 ? val : *x + val;
-                        }
-                    }
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int u = 0; u < (SIDE ? 1 : 2); ++u) {
+                                // row k of the lane's two; u: the second of its dims
+                                const float f = k ? f1 : f0;
+                                const float a = SIDE ? acc[(2 * q + j / 2) % NA][2 * (j & 1) + k] : acc[(4 * q + j) % NA][2 * k + u];
+                                float *x = &dst[k ? row1 : row0][32 * q + (SIDE ? 4 * g : 8 * c + 4 * u) + j];
+                                const float val = f == 0.f ? 0.f : a * f;
+                                *x = step == 0 ? val : *x + val;
+                            }
             }
             cta_sync();
         }
         // ---- rows out: finished, or as a partial ----
-        float *part = p.part, *ml = p.part + (int64_t)2 * p.ctas * kRows * D;
+        float *part = p.part, *ml = p.part + (int64_t)2 * p.ctas * ROWS * D;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (at - w.used == begin ? 0 : 1);
         float vsum[RW];
 #pragma unroll
@@ -530,7 +597,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         }
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-            const int r = i * kCWarps + warp, gr = w.mt * kRows + r;
+            const int r = i * kCWarps + warp, gr = w.mt * ROWS + r;
             if (r >= rows) break;
             if (w.whole) {
                 const int64_t o = ((w.s.row0 + gr / p.group) * p.kv_heads + w.h) * p.group + gr % p.group;
@@ -538,34 +605,34 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 for (int e = 0; e < E; ++e) store_elem<IN>(p.out, o * D + lane * E + e, qv[i][e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) part[(slot * kRows + r) * D + lane * E + e] = qv[i][e];
-                if (lane == 0) *reinterpret_cast<float2 *>(ml + (slot * kRows + r) * 2) = make_float2(top[i], vsum[i]);
+                for (int e = 0; e < E; ++e) part[(slot * ROWS + r) * D + lane * E + e] = qv[i][e];
+                if (lane == 0) *reinterpret_cast<float2 *>(ml + (slot * ROWS + r) * 2) = make_float2(top[i], vsum[i]);
             }
         }
         cta_sync();                                          // s.acc and s.q are free again
     }
 }
 
-template <int IN, int D>
+template <int IN, int D, int ROWS>
 cudaError_t launch_tree_d(TreeParams &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
-    auto kern = attn_tree_mma_kernel<IN, D>;
-    const size_t smem = sizeof(MSmem<IN, D>) + 1024;
+    auto kern = attn_tree_mma_kernel<IN, D, ROWS>;
+    const size_t smem = sizeof(MSmem<IN, D, ROWS>) + 1024;
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem((const void *)kern, smem, allowed);
     if (e != cudaSuccess) return e;
     kern<<<p.ctas, kMThreads, smem, stream>>>(mk, mv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_tree_join<IN, D, kRows, kTT>(p, stream);
+    return launch_tree_join<IN, D, ROWS, kTT>(p, stream);
 }
 
-template <int IN>
+template <int IN, int ROWS>
 cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
     switch (d) {
-        case 32: return launch_tree_d<IN, 32>(p, mk, mv, stream);
-        case 64: return launch_tree_d<IN, 64>(p, mk, mv, stream);
-        case 128: return launch_tree_d<IN, 128>(p, mk, mv, stream);
-        default: return launch_tree_d<IN, 256>(p, mk, mv, stream);
+        case 32: return launch_tree_d<IN, 32, ROWS>(p, mk, mv, stream);
+        case 64: return launch_tree_d<IN, 64, ROWS>(p, mk, mv, stream);
+        case 128: return launch_tree_d<IN, 128, ROWS>(p, mk, mv, stream);
+        default: return launch_tree_d<IN, 256, ROWS>(p, mk, mv, stream);
     }
 }
 
@@ -573,7 +640,7 @@ cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, cons
 
 int64_t attn_tree_workspace(int64_t head_dim) {
     const int64_t ctas = 2 * (int64_t)device_sm_count();
-    const int64_t small = 2 * ctas * kRows * (head_dim + 2) * (int64_t)sizeof(float);
+    const int64_t small = 2 * ctas * 16 * (head_dim + 2) * (int64_t)sizeof(float);
     const int64_t wide = attn_tree_tc_workspace(head_dim);
     return small > wide ? small : wide;
 }
@@ -584,17 +651,19 @@ cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
     if (!tree_params(c, p)) return cudaErrorUnknown;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorUnknown;
-    const int per_sm = blocks_per_sm(c.in_type, c.head_dim);
-    const int64_t bph = (c.max_nodes * p.group + kRows - 1) / kRows;
+    const int rows = c.max_nodes * p.group <= 8 ? 8 : 16;
+    const int per_sm = blocks_per_sm(rows, c.head_dim);
+    const int64_t bph = (c.max_nodes * p.group + rows - 1) / rows;
     const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTT - 1) / kTT);
     p.ctas = (int)(max_tiles < per_sm * sms ? max_tiles : per_sm * sms);
     p.lead = tree_lead(max_tiles, p.ctas);
     CUtensorMap mk, mv;
     if (!tree_maps(c, kTT, mk, mv)) return cudaErrorInvalidValue;
+    const bool side = rows == 8;
     switch (c.in_type) {
-        case IN_F32: return launch_tree_in<IN_F32>(p, c.head_dim, mk, mv, stream);
-        case IN_BF16: return launch_tree_in<IN_BF16>(p, c.head_dim, mk, mv, stream);
-        default: return launch_tree_in<IN_F16>(p, c.head_dim, mk, mv, stream);
+        case IN_F32: return side ? launch_tree_in<IN_F32, 8>(p, c.head_dim, mk, mv, stream) : launch_tree_in<IN_F32, 16>(p, c.head_dim, mk, mv, stream);
+        case IN_BF16: return side ? launch_tree_in<IN_BF16, 8>(p, c.head_dim, mk, mv, stream) : launch_tree_in<IN_BF16, 16>(p, c.head_dim, mk, mv, stream);
+        default: return side ? launch_tree_in<IN_F16, 8>(p, c.head_dim, mk, mv, stream) : launch_tree_in<IN_F16, 16>(p, c.head_dim, mk, mv, stream);
     }
 }
 

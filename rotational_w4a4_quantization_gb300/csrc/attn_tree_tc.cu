@@ -59,6 +59,7 @@ namespace rq {
 namespace {
 
 constexpr int kTcTT = 128;               // tokens per tile
+constexpr int kHT = kTcTT / 2;           // of which a softmax thread has half
 constexpr int kOps = 4;                  // operand slots
 constexpr int kSc = 4;                   // scale slots
 constexpr int kSoftWarps = 8, kConvTeams = 2, kTeamWarps = 4, kConvWarps = kConvTeams * kTeamWarps;
@@ -74,7 +75,7 @@ struct TSmem {
     alignas(16) float vs[kSc][kTcTT];
     float2 unit[kSc];                                       // a tile's 2^ek and ev; 0 and 0: scales not folded in
     float rfac[NT * 128];                                   // s = rfac S (times ks)
-    float ref[2][NT == 1 ? 128 : 1], sum[2][NT == 1 ? 128 : 1];   // NT = 1: the teams' references and sums
+    float best[2][2][128], sum[2][2][128];                  // what the two threads of a row tell each other: [buffer][team], [team][buffer]
     int64_t prefix[kScan + 1];
     TreeWork work[2];                                       // each softmax team's stretch: kept here, not in registers
     alignas(8) uint64_t sc_full[kSc], sc_empty[kSc];
@@ -258,10 +259,11 @@ struct SoftRow {
 //   s = a S;  weight = 2^(s - M + ev).  KS: the operands are exact codes, s = a S ks and
 //   the weights carry vs (relative to 2^ev).
 // MASK: vis has a bit per token; the loops stay rolled, as few tiles come here.
-template <bool KS, bool MASK>
-__device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, const float *vs, float a, float ev, const uint32_t (&vis)[4], SoftRow &r) {
-    constexpr int C = kTcTT / kCW, UNROLL = MASK ? 1 : C / 2;
-    auto seen = [&](int c) { return (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> (kCW * (c & 1)); };
+template <bool KS, bool MASK, class X>
+__device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, const float *vs, float a, float ev, uint32_t vis0, uint32_t vis1,
+                                           SoftRow &r, const X &both) {
+    constexpr int C = kHT / kCW, UNROLL = MASK ? 1 : C / 2;
+    auto seen = [&](int c) { return (c & 2 ? vis1 : vis0) >> (kCW * (c & 1)); };
     uint32_t s0[kCW], s1[kCW];
     tm_ld16(tS, s0);
     float top0 = -INFINITY, top1 = -INFINITY;
@@ -293,7 +295,7 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, const f
         tm_ld16(tS + kCW * ((c + 2) % C), s0);                    // at the end: the first again
         largest(s1, c + 1);
     }
-    const float best = fmaxf(top0, top1) * a + ev;                // a > 0
+    const float best = both(fmaxf(top0, top1) * a + ev);          // a > 0
     float f = 1.f;
     if (best > r.M + 8.f) {                                       // also the first time, where M = -inf
         if (r.M != -INFINITY) f = ex2(r.M - best);
@@ -352,16 +354,16 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, const f
     return f;
 }
 
-// The tokens of a tile that a row's node sees, a bit each: a warp reads a node's 32 mask
-// bytes together, and the rows of that node keep the ballot.
+// The tokens of half a tile that a row's node sees, a bit each: a warp reads a node's 32
+// mask bytes together, and the rows of that node keep the ballot.
 //   node: this row's, node0, node1: the warp's first and last; valid: bit c says that
 //   tokens 16 c .. lie on a page of the cache.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 __device__ __forceinline__ void tree_visible(const TreeParams &p, const TreeSeq &q, int node, int node0, int node1, int t0,
-                                             uint32_t valid, uint32_t (&vis)[4]) {
+                                             uint32_t valid, uint32_t &vis0, uint32_t &vis1) {
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kHT / 32; ++g) {
         const int t = t0 + 32 * g, j = t + lane - q.ctx;
         uint32_t seen = 0;
         if (!p.mask) {
@@ -379,10 +381,8 @@ __device__ __forceinline__ void tree_visible(const TreeParams &p, const TreeSeq 
         }
         const uint32_t v = valid >> (2 * g);
         seen &= below(q.len - t) & ((v & 1 ? 0xffffu : 0u) | (v & 2 ? 0xffff0000u : 0u));
-        vis[0] = vis[1];
-        vis[1] = vis[2];
-        vis[2] = vis[3];
-        vis[3] = node < q.n ? seen : 0u;
+        vis0 = vis1;
+        vis1 = node < q.n ? seen : 0u;
     }
 }
 
@@ -391,13 +391,14 @@ __device__ __forceinline__ void tree_visible(const TreeParams &p, const TreeSeq 
 // s + log2 vs, the weight's exponent.  A masked weight is zero whatever its scales hold.
 // Hardly a tile comes here, and its time is the fetching of code that ran for none
 // before: the loops stay rolled.
-__device__ __forceinline__ float soft_exact(uint32_t tS, const float *ks, const float *vs, float a, const uint32_t (&vis)[4],
-                                            SoftRow &r) {
+template <class X>
+__device__ __forceinline__ float soft_exact(uint32_t tS, const float *ks, const float *vs, float a, uint32_t vis0, uint32_t vis1,
+                                            SoftRow &r, const X &both) {
     uint32_t x[kCW];
     float best = -INFINITY, only = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < kTcTT / kCW; ++c) {
-        const uint32_t w = (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> (kCW * (c & 1));
+    for (int c = 0; c < kHT / kCW; ++c) {
+        const uint32_t w = (c & 2 ? vis1 : vis0) >> (kCW * (c & 1));
         tm_ld16(tS + kCW * c, x);
         tc_wait_ld16(x);
 #pragma unroll
@@ -408,7 +409,7 @@ __device__ __forceinline__ float soft_exact(uint32_t tS, const float *ks, const 
             best = fmaxf(best, sees ? sc + lg2(vs[kCW * c + i]) : -INFINITY);
         }
     }
-    best = fmaxf(best, only - 100.f);                             // rows of zero values: keeps 2^(s - M) itself finite
+    best = both(fmaxf(best, only - 100.f));                             // rows of zero values: keeps 2^(s - M) itself finite
     float f = 1.f;
     if (best > r.M + 8.f) {
         if (r.M != -INFINITY) f = ex2(r.M - best);
@@ -417,8 +418,8 @@ __device__ __forceinline__ float soft_exact(uint32_t tS, const float *ks, const 
     }
     const float Mz = r.M == -INFINITY ? 0.f : r.M;
 #pragma unroll 1
-    for (int c = 0; c < kTcTT / kCW; ++c) {
-        const uint32_t w = (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> (kCW * (c & 1));
+    for (int c = 0; c < kHT / kCW; ++c) {
+        const uint32_t w = (c & 2 ? vis1 : vis0) >> (kCW * (c & 1));
         tm_ld16(tS + kCW * c, x);
         tc_wait_ld16(x);
         uint32_t pk[kCW / 2];
@@ -453,7 +454,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSc; ++i) {
             t_mbar_init(&s.sc_full[i], 1);
-            t_mbar_init(&s.sc_empty[i], 4 * NT + kTeamWarps);
+            t_mbar_init(&s.sc_empty[i], kSoftWarps + kTeamWarps);
         }
         for (int i = 0; i < kOps; ++i) {
             t_mbar_init(&s.op_full[i], kTeamWarps);
@@ -462,7 +463,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         t_mbar_init(&s.q_full, kSoftWarps);
         for (int i = 0; i < 2; ++i) {
             t_mbar_init(&s.s_full[i], 1);
-            t_mbar_init(&s.p_full[i], 4);
+            t_mbar_init(&s.p_full[i], kSoftWarps);
             t_mbar_init(&s.o_full[i], 1);
         }
         s.abort_flag = 0;
@@ -479,7 +480,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
     tree_scan<ROWS, kTcTT>(p, s.prefix);               // ends with a block barrier
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
-    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + (uint32_t)D};
+    const uint32_t tO[2] = {tmem + 256, tmem + 256 + (uint32_t)D};
     const int64_t total = s.prefix[kScan];
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
 
@@ -588,7 +589,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 if (one) {
 #pragma unroll
                     for (int c = 0; c < kTcTT / 16; ++c)
-                        mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * c, b + c * (2048 >> 4), id_pv, j >= 2 || c > 0);
+                        mma_ts(tm + 256 + D * t, tm + 128 * t + (c < 4 ? 8 * c : 64 + 8 * (c - 4)), b + c * (2048 >> 4), id_pv, j >= 2 || c > 0);
                     if (NT == 1 || t == 1) tc_commit(&s.op_empty[slot]);
                     if (j + 2 >= J) tc_commit(&s.o_full[t]);
                 }
@@ -604,7 +605,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         auto both_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;
         auto team_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + team) : "memory"); };
-        uint32_t sc = 0, uses = 0, units = 0;          // tiles so far; S tiles of this team; finished stretches of this team
+        uint32_t sc = 0, uses = 0, units = 0;          // tiles so far; a bit per buffer: parity of its scores, of its finished sums
         const TreeWork &w = s.work[team];
         for (int64_t at = begin; at < end;) {
             if (quarter == 0) {
@@ -699,77 +700,107 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             __syncwarp();
             if (lane == 0) t_mbar_arrive(&s.q_full);
             both_sync();
-            const int brow = (NT == 2 ? team * 128 : 0) + row;               // row of the block
-            const float fac = s.rfac[brow];
-            const bool idle = (NT == 2 ? team * 128 : 0) + quarter * 32 >= rows;     // no row of this warp exists
-            const int node = (w.mt * ROWS + brow) / p.group;
-            SoftRow r{-INFINITY, 0.f};
-            bool first = true;
-            for (int k = NT == 2 ? 0 : team; k < T; k += NT == 2 ? 1 : 2, ++uses) {
-                const uint32_t scs = (sc + k) % kSc;
+            // Both threads of a row take every score buffer, half of its columns each: while
+            // the tensor core works for one buffer, all of them have the other.
+            float fac = s.rfac[row], fac2 = s.rfac[NT == 2 ? 128 + row : row];
+            SoftRow r{-INFINITY, 0.f}, r2{-INFINITY, 0.f};               // this buffer's, the other's
+            const int J = NT * T;
+            for (int j = 0; j < J; ++j) {
+                const int k = NT == 2 ? j >> 1 : j, t = j & 1, blk = NT == 2 ? 128 * t : 0;
+                const uint32_t scs = (sc + k) % kSc, tS = tmem + 128 * t + kHT * team + lanes;
                 bool ok = t_mbar_wait(&s.sc_full[scs], ((sc + k) / kSc) & 1, &s.abort_flag, p.err);
-                ok = t_mbar_wait(&s.s_full[team], uses & 1, &s.abort_flag, p.err) && ok;
+                ok = t_mbar_wait(&s.s_full[t], (uses >> t) & 1, &s.abort_flag, p.err) && ok;
                 ok = __all_sync(0xffffffffu, ok);
+                uses ^= 1u << t;
                 tc_fence_after();
-                if (ok && !idle) {
-                    const int t0 = (w.t0 + k) * kTcTT;
-                    const float2 unit = s.unit[scs];
-                    const uint32_t valid = s.valid[scs];
-                    const bool masked = t0 + kTcTT > w.s.ctx || valid != 0xffu;
-                    const float a = unit.x == 0.f ? fac : fac * unit.x, ev = unit.y;
-                    float f;
-                    if (!masked) {
-                        const uint32_t none[4] = {0, 0, 0, 0};
-                        f = soft_tile<!FOLD, false>(tS[team] + lanes, s.ks[scs], s.vs[scs], a, ev, none, r);
+                if (blk + quarter * 32 < rows) {                               // else no row of this warp exists
+                    // the larger of both threads' values; each step comes here once, also after a
+                    // wait that ran out, so that neither thread waits alone
+                    auto both = [&](float best) {
+                        s.best[t][team][row] = best;
+                        asm volatile("bar.sync %0, 64;" ::"r"(4 + quarter) : "memory");
+                        return fmaxf(best, s.best[t][team ^ 1][row]);
+                    };
+                    float f = 1.f;
+                    if (!ok) {
+                        both(-INFINITY);
                     } else {
-                        uint32_t vis[4] = {0, 0, 0, 0};
-                        const int wrow = w.mt * ROWS + brow - lane;
-                        tree_visible(p, w.s, node, wrow / p.group, min((wrow + 31) / p.group, w.s.n - 1), t0, valid, vis);
-                        if (unit.x != 0.f) f = soft_tile<!FOLD, true>(tS[team] + lanes, s.ks[scs], s.vs[scs], a, ev, vis, r);
-                        else f = soft_exact(tS[team] + lanes, s.ks[scs], s.vs[scs], a, vis, r);
-                    }
-                    if (!first && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t x[32];
-                            tm_ld32(tO[team] + lanes + 32 * c, x);
-                            tc_wait_ld32(x);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                            tm_st32(tO[team] + lanes + 32 * c, x);
+                        const int t0 = (w.t0 + k) * kTcTT + kHT * team;
+                        const float2 unit = s.unit[scs];
+                        const uint32_t valid = (s.valid[scs] >> (kHT / 16 * team)) & 15u;
+                        const float a = unit.x == 0.f ? fac : fac * unit.x, ev = unit.y;
+                        const float *ks = s.ks[scs] + kHT * team, *vs = s.vs[scs] + kHT * team;
+                        if (unit.x != 0.f && t0 + kHT <= w.s.ctx && valid == 15u) {
+                            f = soft_tile<!FOLD, false>(tS, ks, vs, a, ev, 0u, 0u, r, both);
+                        } else {
+                            uint32_t vis0 = 0, vis1 = 0;
+                            const int wrow = w.mt * ROWS + blk + quarter * 32;
+                            tree_visible(p, w.s, (wrow + lane) / p.group, wrow / p.group, min((wrow + 31) / p.group, w.s.n - 1), t0, valid, vis0, vis1);
+                            if (unit.x != 0.f) f = soft_tile<!FOLD, true>(tS, ks, vs, a, ev, vis0, vis1, r, both);
+                            else f = soft_exact(tS, ks, vs, a, vis0, vis1, r, both);
                         }
+                        if (j >= 2 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                            for (int c = team * (D / 64); c < (team + 1) * (D / 64); ++c) {
+                                uint32_t x[32];
+                                tm_ld32(tO[0] + D * t + lanes + 32 * c, x);
+                                tc_wait_ld32(x);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                                tm_st32(tO[0] + D * t + lanes + 32 * c, x);
+                            }
+                        }
+                        tc_wait_st();
                     }
-                    tc_wait_st();
                 }
-                first = false;
+                const SoftRow rt = r;
+                r = r2;
+                r2 = rt;
+                const float ft = fac;
+                fac = fac2;
+                fac2 = ft;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    t_mbar_arrive(&s.p_full[team]);
-                    t_mbar_arrive(&s.sc_empty[scs]);
+                    t_mbar_arrive(&s.p_full[t]);
+                    if (NT == 1 || t == 1) t_mbar_arrive(&s.sc_empty[scs]);
                 }
             }
             sc += T;
+            if (J & 1) {
+                const SoftRow rt = r;
+                r = r2;
+                r2 = rt;
+            }
 
             // ---- the block's sums are complete ----
-            bool done = true;
-            if (!first) {
-                done = __all_sync(0xffffffffu, t_mbar_wait(&s.o_full[team], units & 1, &s.abort_flag, p.err));
-                ++units;
-            }
+            const int brow = (NT == 2 ? team * 128 : 0) + row;               // row of the block
+            const bool idle = (NT == 2 ? team * 128 : 0) + quarter * 32 >= rows;     // no row of this warp exists
+            bool done = t_mbar_wait(&s.o_full[0], units & 1, &s.abort_flag, p.err);
+            if (J > 1) done = t_mbar_wait(&s.o_full[1], units >> 1, &s.abort_flag, p.err) && done;
+            units ^= J > 1 ? 3u : 1u;
+            done = __all_sync(0xffffffffu, done);
             tc_fence_after();
-            float l = r.l, M = r.M == -INFINITY && !(l == 0.f) ? 0.f : r.M;          // nothing but NaN seen: any reference
-            l = fminf(l, 3.4028234e38f) + (l != l ? l : 0.f);                 // keeps NaN, bounds infinity
-            float fa = 1.f, fb = 0.f;                                         // factors of the teams' accumulators
+            s.sum[team][0][row] = r.l;
+            s.sum[team][1][row] = r2.l;
+            both_sync();
+            // reference and sum of a buffer's rows, and what becomes of them where nothing but NaN was seen
+            auto settled = [&](int t, float M, float &l) {
+                l = s.sum[0][t][row] + s.sum[1][t][row];
+                M = M == -INFINITY && !(l == 0.f) ? 0.f : M;                   // any reference
+                l = fminf(l, 3.4028234e38f) + (l != l ? l : 0.f);              // keeps NaN, bounds infinity
+                return M;
+            };
+            float l, M, fa = 1.f, fb = 0.f;                                   // fa, fb: factors of the accumulators
             if constexpr (NT == 1) {
-                s.ref[team][row] = M;
-                s.sum[team][row] = l;
-                both_sync();
-                const float ma = s.ref[0][row], mb = s.ref[1][row];
+                float la, lb;
+                const float ma = settled(0, r.M, la), mb = settled(1, r2.M, lb);
                 M = fmaxf(ma, mb);
                 fa = ma == -INFINITY ? 0.f : ex2(ma - M);
                 fb = mb == -INFINITY ? 0.f : ex2(mb - M);
-                l = s.sum[0][row] * fa + s.sum[1][row] * fb;
+                l = la * fa + lb * fb;
+            } else {
+                M = settled(team, team ? r2.M : r.M, l);
             }
             const uint32_t oa = (NT == 2 ? tO[team] : tO[0]) + lanes, ob = tO[1] + lanes;
             const bool live = brow < rows && done;

@@ -709,6 +709,11 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 const int k = NT == 2 ? j >> 1 : j, t = j & 1, blk = NT == 2 ? 128 * t : 0;
                 const uint32_t scs = (sc + k) % kSc, tS = tmem + 128 * t + kHT * team + lanes;
                 bool ok = t_mbar_wait(&s.sc_full[scs], ((sc + k) / kSc) & 1, &s.abort_flag, p.err);
+                const int t0 = (w.t0 + k) * kTcTT + kHT * team;
+                const float2 unit = s.unit[scs];
+                const uint32_t valid = (s.valid[scs] >> (kHT / 16 * team)) & 15u;
+                const float a = unit.x == 0.f ? fac : fac * unit.x, ev = unit.y;
+                const bool plain = unit.x != 0.f && t0 + kHT <= w.s.ctx && valid == 15u;
                 ok = t_mbar_wait(&s.s_full[t], (uses >> t) & 1, &s.abort_flag, p.err) && ok;
                 ok = __all_sync(0xffffffffu, ok);
                 uses ^= 1u << t;
@@ -725,12 +730,8 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     if (!ok) {
                         both(-INFINITY);
                     } else {
-                        const int t0 = (w.t0 + k) * kTcTT + kHT * team;
-                        const float2 unit = s.unit[scs];
-                        const uint32_t valid = (s.valid[scs] >> (kHT / 16 * team)) & 15u;
-                        const float a = unit.x == 0.f ? fac : fac * unit.x, ev = unit.y;
                         const float *ks = s.ks[scs] + kHT * team, *vs = s.vs[scs] + kHT * team;
-                        if (unit.x != 0.f && t0 + kHT <= w.s.ctx && valid == 15u) {
+                        if (plain) {
                             f = soft_tile<!FOLD, false>(tS, ks, vs, a, ev, 0u, 0u, r, both);
                         } else {
                             uint32_t vis0 = 0, vis1 = 0;

@@ -5,29 +5,30 @@
 // (nodes x query heads of a KV head) fill the 128 lanes of a tcgen05 MMA:
 //   S = Q K^T   M128 N128 (tokens) K = D,  A = q~ in shared memory, fp16
 //   O += P V    M128 N = D  K128 (tokens), A = P in tensor memory, fp16
-// and a tile is 128 tokens.  Two softmax teams of 128 threads (one row each) work in
-// turn with the tensor core: while it runs P V and the next Q K^T for one team, the
-// other team turns its scores into weights.
-//   NT = 2: 256 rows, team w has rows 128 w ..; every tile is used by both.
-//   NT = 1: 128 rows; team w takes the tiles of parity w with an accumulator of its
-//           own, and the two are joined at the end.
+// and a tile is 128 tokens.  Two score buffers: while the tensor core runs P V and the
+// next Q K^T for one, 256 softmax threads, two to a row, turn the other's scores into
+// weights.
+//   NT = 2: 256 rows, buffer t has rows 128 t ..; every tile is used by both.
+//   NT = 1: 128 rows; the tiles take the buffers in turn, each buffer with an accumulator
+//           of its own, and the two are joined at the end.
 //
 // Roles (20 warps of which two idle, one block per SM):
 //   warp 0       scales of each tile: their units, and the scales themselves where they
 //                are not folded in
 //   warp 1       tensor memory, all MMAs (one lane)
-//   warps 4-11   softmax teams
+//   warps 4-11   softmax: warps 4-7 the first half of a tile's tokens, 8-11 the second;
+//                the two threads of a row agree on its reference
 //   warps 12-19  converters, two teams in turn: packed codes, loaded two operands ahead
 //                straight into registers, -> fp16 in the 128-byte-swizzled operand
 //                layout.  One layout serves both products: rows of 64 dims per token
 //                are K-major for Q K^T and MN-major for P V.
-// Tensor memory, 512 columns: S0 S1 (128 each; P overwrites the first half of its S)
-// and O0 O1 (D each).
+// Tensor memory, 512 columns: S0 S1 (128 each; the weights of each half overwrite the first
+// half of its scores) and O0 O1 (D each).
 //
 // Scales.  With bf16 queries they are folded into the operands: k^ and v^ as fp16(code *
 // scale), scales relative to a power of two per tile, one rounding (the scale enters in
-// two fp16 parts).  The
-// softmax then reads nothing but its scores: broadcasting scales from shared memory
+// two fp16 parts).  The softmax then reads nothing but its scores: broadcasting scales from
+// shared memory
 // costs 4 cycles per 16 bytes and warp, and bound the kernel (8 warps x 64 loads per
 // tile; measured 2,150 cycles per tile for that softmax alone, against 2,048 of MMAs).
 // A tile that some row sees in part keeps exact codes if a scale of it is not finite or
@@ -35,7 +36,7 @@
 // token holds (a NaN scale, say) reaches nobody.  fp16 queries, whose outputs resolve an
 // 11-bit rounding of q~, k^ and v^, keep q~ in two fp16 parts (Q K^T runs twice) and the
 // scales out of the operands; the weights with vs in them round once (16 sequences of up
-// to 4k: outputs 2.9e-4 off in 86 us; with the scales of V folded 3.3e-4 in 88).
+// to 4k: outputs 2.9e-4 off; with the scales of V folded 3.3e-4, and 2 us slower).
 //
 // Weights: P = 2^(s - M + ev) (2^ev the tile's unit of vs) is what the MMA sees, rounded
 // to fp16; the sum l adds 2^(s - M) in fp32.  O / l does not depend on M, so M only has
@@ -43,14 +44,16 @@
 // rescaled in place, between the commit that delivers S and the arrival that delivers
 // P, when no MMA touches it).
 //
-// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 404 us, 0.73
-// PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 4,600 cycles
-// of which the MMAs run 2,048.  The rest is the way from scores to weights and back, once
-// per team and tile (the softmax's 2,700 cycles of it are latency: the issue slots are a
-// third full).  Score buffers of 64 columns, so that a team's halves overlap, were slower
-// (423 us): Q K^T with N = 64 takes 48 cycles for 32's work, as it reads A for each.
-// 64 rows (fp16, 16 sequences of up to 4k): 86 us, where the bytes take 9: starts and
-// ends, 12,000 cycles to the first score and 18,000 from unit to unit.
+// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 422 us, 0.70
+// PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 5,000 cycles
+// of which the MMAs run 2,048.  The softmax bounds it: 1,800 cycles for half a tile, most
+// of it latency of tensor-memory loads, exponentials and the exchange between a row's
+// threads (issue slots are two fifths full), and 800 from one half to the next.  Slower
+// were: one pass over the scores with the old reference, weights kept back in registers
+// (431 us); scores kept in registers (457, spills); 32 columns a load (433); buffers of 64
+// columns (423, as Q K^T with N = 64 takes 48 cycles for 32's work).  64 rows (fp16, 16
+// sequences of up to 4k): 76 us, where the bytes take 9: starts and ends of units; with a
+// buffer per softmax team, 128 columns to a thread, 86 (and the 256 rows 404).
 #include "rq.h"
 #include "rq_internal.h"
 #include "tree_device.cuh"
@@ -77,10 +80,10 @@ struct TSmem {
     float rfac[NT * 128];                                   // s = rfac S (times ks)
     float best[2][2][128], sum[2][2][128];                  // what the two threads of a row tell each other: [buffer][team], [team][buffer]
     int64_t prefix[kScan + 1];
-    TreeWork work[2];                                       // each softmax team's stretch: kept here, not in registers
+    TreeWork work[2];                                       // each softmax team's copy of the stretch: kept here, not in registers
     alignas(8) uint64_t sc_full[kSc], sc_empty[kSc];
     uint64_t op_full[kOps], op_empty[kOps];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2];
+    uint64_t q_full, s_full[2], p_full[2], p_free[2], o_full[2];
     uint32_t valid[kSc];                                    // bit c: tokens 16 c .. lie on a page of the cache
     uint32_t sign_words[8];
     uint32_t tmem_base;
@@ -464,6 +467,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int i = 0; i < 2; ++i) {
             t_mbar_init(&s.s_full[i], 1);
             t_mbar_init(&s.p_full[i], kSoftWarps);
+            t_mbar_init(&s.p_free[i], 1);
             t_mbar_init(&s.o_full[i], 1);
         }
         s.abort_flag = 0;
@@ -542,7 +546,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         // The whole warp runs the loop, so that descriptors stay in uniform registers;
         // one lane issues (16 MMAs of 64 cycles each per tile leave no time for more).
         const bool one = elect_one();
-        uint32_t base = 0, unit = 0, pc[2] = {0, 0};         // items of earlier stretches; stretches; P tiles per team
+        uint32_t base = 0, unit = 0, pc[2] = {0, 0}, fc[2] = {0, 0};   // items of earlier stretches; stretches; weights per buffer, those given up
         constexpr uint32_t id_qk = idesc_f16(kTcTT, false), id_pv = idesc_f16(D, true);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t dq = op_desc(t_smem(s.q[0]), 16), dk = op_desc(t_smem(s.op[0]), 16);
@@ -591,15 +595,21 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     for (int c = 0; c < kTcTT / 16; ++c)
                         mma_ts(tm + 256 + D * t, tm + 128 * t + (c < 4 ? 8 * c : 64 + 8 * (c - 4)), b + c * (2048 >> 4), id_pv, j >= 2 || c > 0);
                     if (NT == 1 || t == 1) tc_commit(&s.op_empty[slot]);
-                    if (j + 2 >= J) tc_commit(&s.o_full[t]);
+                    tc_commit(j + 2 < J ? &s.p_free[t] : &s.o_full[t]);
                 }
                 __syncwarp();
-                if (j + 2 < J) qk(j + 2);
+                // products of different shapes need not run in the order of their issue: the
+                // weights are read before the next scores take their place
+                if (j + 2 < J) {
+                    ok = ok && warp_wait(&s.p_free[t], fc[t] & 1, &s.abort_flag, p.err);
+                    ++fc[t];
+                    qk(j + 2);
+                }
             }
             base += 2 * T;
         }
     } else if (warp >= 4 && warp < 4 + kSoftWarps) {
-        // ---------------- softmax teams ----------------
+        // ---------------- softmax: two teams, one per half of the tokens ----------------
         const int team = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;     // row of the 128
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         auto both_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
@@ -1054,10 +1064,11 @@ cudaError_t launch_tc(TreeParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-// Blocks of 128 rows pay a start of about 30 us per block of threads and then 2,600
-// cycles per 128 tokens; blocks of 16 rows start at once and pay 1,900 each.  Measured
-// (bf16, 8 KV heads x 128): 32 rows, 16 sequences of 4k: 82 us here, 68 us there; 48 rows:
-// 82 and 95; one sequence of 512, 128 rows: 31 and 23, as it has fewer tiles than SMs.
+// Blocks of 128 rows pay a long start and end per unit, blocks of 16 rows more per token and
+// row.  Measured (8 KV heads x 128, cold caches), here and there: 16 sequences of 4k, bf16,
+// 32 rows 82 and 70 us, 48 rows 86 and 94, 64 rows 88 and 117; 64 of 300, 32 rows 70 and 63,
+// 48 rows 74 and 85; fp16, 4 of 32k, 32 rows 123 and 115, 48 rows 123 and 160; bf16, 2 of
+// 512, 64 rows 27 and 25, as they have fewer tiles than SMs.
 bool attn_tree_tc_supported(const TreeCall &c) {
     const int64_t rows = c.max_nodes * (c.q_heads / c.cache.heads);
     const int64_t tiles = c.seqs * c.cache.heads * ((rows + 127) / 128) * ((c.width * c.cache.page_size + kTcTT - 1) / kTcTT);

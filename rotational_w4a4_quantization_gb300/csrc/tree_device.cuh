@@ -259,7 +259,9 @@ __device__ __forceinline__ void t_bulk(void *dst, const void *src, uint32_t byte
 // A warp takes a row (two of 256-row units) and four partials at a time, so that their
 // loads overlap.
 // Launched so that it may begin while the kernel before it ends: it finds its units
-// first and waits only before it reads the partials.
+// first and waits then.  Every thread waits, those without a unit to join too: the join
+// may not end before the kernel before it has, as what follows on the stream (or in a
+// captured graph) is ordered behind the join alone.
 constexpr int kJoinWarps = 16;
 __device__ __forceinline__ void tree_join_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 constexpr int join_rows(int rows) { return rows >= 256 ? 2 : 1; }         // rows per warp
@@ -277,21 +279,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = min(ROWS, s.n * p.group - mt * ROWS);
     const int begin_row = (blockIdx.y * turns * kJoinWarps + warp) * RW;
-    if (mt >= s.mt || begin_row >= rows) return;
-    const int per = (p.seqs + kScan - 1) / kScan;
-    int64_t first = prefix[b / per];
-    for (int i = b / per * per; i < b; ++i) {
-        const TreeSeq x = tree_seq<ROWS, TT>(p, i);
-        first += (int64_t)p.kv_heads * x.mt * unit_length(p, x);
+    int64_t first = 0;
+    int c0 = 0, c1 = 0;                                     // the unit's CTAs; one: finished there
+    if (mt < s.mt && begin_row < rows) {
+        const int per = (p.seqs + kScan - 1) / kScan;
+        first = prefix[b / per];
+        for (int i = b / per * per; i < b; ++i) {
+            const TreeSeq x = tree_seq<ROWS, TT>(p, i);
+            first += (int64_t)p.kv_heads * x.mt * unit_length(p, x);
+        }
+        first += ((int64_t)h * s.mt + mt) * unit_length(p, s);
+        const int64_t first_tile = first + p.lead, last = first + unit_length(p, s) - 1;
+        // CTA of a position: the last c with total c / ctas <= position
+        c0 = (int)(((first_tile + 1) * p.ctas - 1) / total);
+        c1 = (int)(((last + 1) * p.ctas - 1) / total);
     }
-    first += ((int64_t)h * s.mt + mt) * unit_length(p, s);
-    const int64_t first_tile = first + p.lead, last = first + unit_length(p, s) - 1;
-    // CTA of a position: the last c with total c / ctas <= position
-    const int c0 = (int)(((first_tile + 1) * p.ctas - 1) / total), c1 = (int)(((last + 1) * p.ctas - 1) / total);
-    if (c0 == c1) return;                                   // finished in its CTA
     float sg[E];
     lane_signs<E>(sg, lane, p.seed);
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials are written
+    if (c0 == c1) return;
     const float *ml = p.part + (int64_t)2 * p.ctas * ROWS * D;
     auto there = [&](int c) { return c <= c1 && tree_begin(total, p.ctas, c) != tree_begin(total, p.ctas, c + 1); };   // no empty stretch
     auto slot = [&](int c) { return (int64_t)(tree_begin(total, p.ctas, c) >= first ? 2 * c : 2 * c + 1); };

@@ -18,12 +18,15 @@
 //    again, s = (a S + b) ks.  The order of the dims is the same permutation on both
 //    sides and drops out.  fp32 queries subtract 8 from the codes instead: the offset
 //    costs 5 bits of the sum.
-//  * softmax on the fragments, base 2, with a lazy reference: it moves only when a
-//    score passes it by 8, so the accumulators are rarely rescaled.
-//  * O += (P vs) V: ldmatrix.trans pairs the codes of two tokens in a register, which
-//    is the B operand after the same nibble step.  P vs is rounded to fp16 (11 bits,
-//    below the rounding of 16-bit outputs), vs relative to a power of two that moves
-//    like the softmax's reference.
+//  * softmax on the fragments, base 2: a token's weight is w = 2^(s - z) vs, and a row's
+//    reference z follows the row's own largest w, over the tokens that it sees: neither a
+//    score whose values are nothing nor a value scale of no weight, or of another row's
+//    tokens, costs the others bits.  It moves only when a weight passes 2^8, so the
+//    accumulators are rarely rescaled; whether one may is seen from the largest score and
+//    the largest scale of a lane, and only then looked at token by token.
+//  * O += w V: ldmatrix.trans pairs the codes of two tokens in a register, which is the B
+//    operand after the same nibble step.  w is rounded to fp16 (11 bits, below the rounding
+//    of 16-bit outputs); the sum of 2^(s - z) stays in fp32.
 //  * Up to 8 rows (single tokens of up to 8 query heads to a KV head): the products are
 //    turned, S^T = K q~^T and O^T = V^T P^T, with tokens and dims as the 16 of m16n8k16
 //    and the rows as its 8.  The same registers are the operands, P^T passes through
@@ -49,6 +52,9 @@ namespace {
 constexpr int kTT = 128, kStages = 3, kCWarps = 4;
 constexpr int kWT = kTT / kCWarps / 8;               // n8 tiles of tokens per warp and tile
 constexpr int kMThreads = 32 * (kCWarps + 1);
+// log2 of a row's weights 2^(s - z) vs: where a move of the reference puts the largest, and
+// where the next move comes; and of the least value scale that counts for the reference.
+constexpr float kWeightTo = 0.f, kWeightMost = 8.f, kLeastValue = -60.f;
 
 // Blocks that share an SM: what the registers of the fragments allow.
 constexpr int blocks_per_sm(int rows, int64_t head_dim) {
@@ -67,7 +73,6 @@ struct MSmem {
     float acc[2][ROWS][D + 4];                       // the warps' sums, joined two by two
     float ref[kCWarps][ROWS], sum[kCWarps][ROWS];
     float2 rfac[ROWS];                               // a, b
-    int vexp[kCWarps];
     int64_t prefix[kScan + 1];
     alignas(8) uint64_t full[kStages], empty[kStages];
     uint32_t valid[kStages];
@@ -282,9 +287,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
         float z0 = 0.f, z1 = 0.f, l0 = 0.f, l1 = 0.f;                                     // references, sums
-        float lim0 = -INFINITY, lim1 = -INFINITY;                                         // a score beyond moves the reference
-        int ve = -100;
-        float vf = __uint_as_float((uint32_t)(127 + 100) << 23);                          // 2^-ve
+        float lim0 = -INFINITY, lim1 = -INFINITY;                                         // a weight beyond moves the reference
 
         const uint32_t all = (uint32_t)((1ull << (kTT / min(kTT, 1 << p.log_page))) - 1);
         for (int tile = w.t0; tile < w.t1; ++tile) {
@@ -376,22 +379,17 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     const int lp = min(p.log_page, 7);
 #pragma unroll
                     for (int t = 0; t < NS; ++t) {
-                        bool any[2] = {false, false};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int tl = tk + tok(t, k);
                             const bool sees = ((valid >> (tl >> lp)) & 1) &&
                                               tree_sees<ROWS>(p, w, second(k) ? row1 : row0, tile * kTT + tl);
-                            any[later(k)] |= sees;
                             if (!sees) sc[t][k] = -INFINITY;
                         }
-                        // a value row that none of this lane's two query rows sees does not move
-                        // the unit of the values
-                        if (!any[0]) vscale[t].x = 0.f;
-                        if (!any[1]) vscale[t].y = 0.f;
                     }
                 }
                 // ---- lazy references ----
+                // largest score and largest value scale of the lane together bound its weights
                 float up0 = -INFINITY, up1 = -INFINITY, vtop = 0.f;
 #pragma unroll
                 for (int t = 0; t < NS; ++t) {
@@ -402,33 +400,35 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     }
                     vtop = fmaxf(vtop, fmaxf(vscale[t].x, vscale[t].y));
                 }
-                if (__any_sync(0xffffffffu, up0 > lim0 || up1 > lim1 || vtop * vf > 64.f)) {
+                const float lv = fmaxf((float)((int)(__float_as_uint(vtop) >> 23) - 126), kLeastValue);
+                if (__any_sync(0xffffffffu, up0 + lv > lim0 || up1 + lv > lim1)) {
+                    // the rows' largest weights: a row's own, over the tokens that it sees
+                    float w0 = -INFINITY, w1 = -INFINITY;
 #pragma unroll
-                    for (int o = kRowLo; o < kRowHi; o <<= 1) {
-                        up0 = fmaxf(up0, __shfl_xor_sync(0xffffffffu, up0, o));
-                        up1 = fmaxf(up1, __shfl_xor_sync(0xffffffffu, up1, o));
+                    for (int t = 0; t < NS; ++t) {
+                        const float lx = fmaxf(lg2(vscale[t].x), kLeastValue), ly = fmaxf(lg2(vscale[t].y), kLeastValue);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float &w = second(k) ? w1 : w0;
+                            w = fmaxf(w, sc[t][k] + fminf(later(k) ? ly : lx, 128.f));
+                        }
                     }
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-                    // z is 0 until something is seen (lim = -inf: the first score moves it)
-                    const float d0 = lim0 == 8.f ? fmaxf(up0, 0.f) : (up0 == -INFINITY ? 0.f : up0);
-                    const float d1 = lim1 == 8.f ? fmaxf(up1, 0.f) : (up1 == -INFINITY ? 0.f : up1);
-                    float f0 = lim0 == 8.f ? ex2(-d0) : 1.f, f1 = lim1 == 8.f ? ex2(-d1) : 1.f;
-                    if (up0 != -INFINITY) lim0 = 8.f;
-                    if (up1 != -INFINITY) lim1 = 8.f;
+                    for (int o = kRowLo; o < kRowHi; o <<= 1) {
+                        w0 = fmaxf(w0, __shfl_xor_sync(0xffffffffu, w0, o));
+                        w1 = fmaxf(w1, __shfl_xor_sync(0xffffffffu, w1, o));
+                    }
+                    // z is 0 until something is seen (lim = -inf: the first weight moves it)
+                    const float d0 = w0 > lim0 ? w0 - kWeightTo : 0.f, d1 = w1 > lim1 ? w1 - kWeightTo : 0.f;
+                    const float f0 = lim0 == kWeightMost ? ex2(-d0) : 1.f, f1 = lim1 == kWeightMost ? ex2(-d1) : 1.f;
+                    if (w0 != -INFINITY) lim0 = kWeightMost;
+                    if (w1 != -INFINITY) lim1 = kWeightMost;
                     z0 += d0; z1 += d1;
                     l0 *= f0; l1 *= f1;
 #pragma unroll
                     for (int t = 0; t < NS; ++t)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) sc[t][k] -= second(k) ? d1 : d0;
-                    if (vtop * vf > 64.f) {
-                        const int nv = max(-100, min((int)(__float_as_uint(vtop) >> 23) - 127, 100));
-                        const float dv = ve - nv < -126 ? 0.f : __uint_as_float((uint32_t)(127 + ve - nv) << 23);
-                        ve = nv;
-                        vf = __uint_as_float((uint32_t)(127 - ve) << 23);
-                        f0 *= dv; f1 *= dv;
-                    }
 #pragma unroll
                     for (int i = 0; i < NA; ++i)
 #pragma unroll
@@ -445,10 +445,9 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     }
                     l0 += SIDE ? sc[t][0] + sc[t][2] : sc[t][0] + sc[t][1];
                     l1 += SIDE ? sc[t][1] + sc[t][3] : sc[t][2] + sc[t][3];
-                    const float v0 = vscale[t].x * vf, v1 = vscale[t].y * vf;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        sc[t][k] *= later(k) ? v1 : v0;
+                        sc[t][k] *= later(k) ? vscale[t].y : vscale[t].x;
                         if (masked && hidden[k]) sc[t][k] = 0.f;   // also where the value's scale is not finite
                     }
                 }
@@ -533,7 +532,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
-        const float m0 = lim0 == 8.f || !(l0 == 0.f) ? z0 : -INFINITY, m1 = lim1 == 8.f || !(l1 == 0.f) ? z1 : -INFINITY;
+        const float m0 = lim0 == kWeightMost || !(l0 == 0.f) ? z0 : -INFINITY, m1 = lim1 == kWeightMost || !(l1 == 0.f) ? z1 : -INFINITY;
         if (SIDE ? g == 0 : c == 0) {
             s.ref[warp][row0] = m0;
             s.ref[warp][row1] = m1;
@@ -553,8 +552,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         float top0, top1, sum0, sum1;
         joined(row0, top0, sum0);
         joined(row1, top1, sum1);
-        const float vup = __uint_as_float((uint32_t)(127 + ve) << 23);
-        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - top0) * vup, f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top1) * vup;
+        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - top0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top1);
         // accumulators: dims 32 q + 8 c + j and + 4 + j of rows g, g + 8; SIDE: dim 32 q + 4 g + j
         // of rows 2 c, 2 c + 1
 #pragma unroll

@@ -199,6 +199,12 @@ __device__ __forceinline__ bool tree_sees(const TreeParams &p, const TreeWork &w
     return p.mask ? p.mask[(w.s.row0 + i) * p.mask_stride + j] != 0 : j <= i;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t t_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 __device__ __forceinline__ void t_mbar_init(uint64_t *b, uint32_t count) {

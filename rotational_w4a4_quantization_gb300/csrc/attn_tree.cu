@@ -21,9 +21,11 @@
 //  * softmax on the fragments, base 2: a token's weight is w = 2^(s - z) vs, and a row's
 //    reference z follows the row's own largest w, over the tokens that it sees: neither a
 //    score whose values are nothing nor a value scale of no weight, or of another row's
-//    tokens, costs the others bits.  It moves only when a weight passes 2^8, so the
-//    accumulators are rarely rescaled; whether one may is seen from the largest score and
-//    the largest scale of a lane, and only then looked at token by token.
+//    tokens, costs the others bits.  It moves only when a weight passes 2^15, and then puts
+//    it at 2^9: fp16 keeps 11 bits of weights down to 2^-14, so of tokens at least 23 bits
+//    below the largest, and something down to 2^-25, and the accumulators are rarely
+//    rescaled.  Whether one may is seen from the largest score and the largest scale of a
+//    lane, and only then looked at token by token.
 //  * O += w V: ldmatrix.trans pairs the codes of two tokens in a register, which is the B
 //    operand after the same nibble step.  w is rounded to fp16 (11 bits, below the rounding
 //    of 16-bit outputs); the sum of 2^(s - z) stays in fp32.
@@ -32,9 +34,12 @@
 //    and the rows as its 8.  The same registers are the operands, P^T passes through
 //    movmatrix, and half of the products, of the softmax and of the accumulators is gone:
 //    three blocks fit an SM (128 registers) where two did (168).
-//  * fp32 queries: q~ and P vs are split into two fp16 parts (22 bits) and the products
-//    run twice; codes are exact in either.  fp16 queries split q~ alone: their outputs
-//    resolve its rounding to 11 bits (4.6e-4 against 2.5e-4 of an output).
+//  * fp32 queries: q~ and w are split into two fp16 parts and the products run twice; codes
+//    are exact in either.  The second part of w is kept 2^11 up, so that small weights have
+//    22 bits too.  What the tensor cores add to an accumulator is not rounded to nearest:
+//    a score 17 to 26 bits above the others', added up by 16 of them, had its weight 5e-6
+//    to 2e-5 off.  So each step of 16 starts from 0 and is added to the sums outside.  fp16 queries split q~ alone: their outputs resolve its rounding to 11
+//    bits (4.6e-4 against 2.5e-4 of an output).
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
 // heads, one node: 104 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
@@ -52,9 +57,6 @@ namespace {
 constexpr int kTT = 128, kStages = 3, kCWarps = 4;
 constexpr int kWT = kTT / kCWarps / 8;               // n8 tiles of tokens per warp and tile
 constexpr int kMThreads = 32 * (kCWarps + 1);
-// log2 of a row's weights 2^(s - z) vs: where a move of the reference puts the largest, and
-// where the next move comes; and of the least value scale that counts for the reference.
-constexpr float kWeightTo = 0.f, kWeightMost = 8.f, kLeastValue = -60.f;
 
 // Blocks that share an SM: what the registers of the fragments allow.
 constexpr int blocks_per_sm(int rows, int64_t head_dim) {
@@ -114,6 +116,13 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// The second part of fp32's weights is kept 2^11 larger, beside codes 2^-11 smaller (exact):
+// what is left of a small weight would be subnormal.
+constexpr float kLowUp = 2048.f;
+__device__ __forceinline__ uint32_t lowered(uint32_t x) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x1000)));   // 2^-11
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 // An 8 x 8 matrix of fp16 pairs, transposed across the warp.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
@@ -129,6 +138,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     using S = MSmem<IN, D, ROWS>;
     constexpr int RB = D / 2, WPT = D / 32, E = D / 32, HQ = S::HQ, HP = S::HP;
     constexpr bool kOffset = IN != IN_F32;             // keys as u = code + 8 (see the top)
+    constexpr bool kShort = IN == IN_F32;              // the tensor cores add two parts of one step, no more
     constexpr int NQ = D / 32;                        // 16-byte chunks of a code row
     constexpr bool SIDE = ROWS == 8;                  // products of tokens x rows instead of rows x tokens
     constexpr int kRowLo = SIDE ? 4 : 1, kRowHi = SIDE ? 32 : 4;   // lane bits that a row's scores are spread over
@@ -325,28 +335,37 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                             else code_pairs(kw[t][wd], b[t]);
                         }
 #pragma unroll
-                        for (int hv = 0; hv < HQ; ++hv)
+                        for (int i = 0; i < 2; ++i) {
+                            float own[kShort ? NS : 1][4];              // this step's sums (kShort)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const bool begins = part == 0 && wd == 0 && hv == 0 && i == 0;
+                            for (int hv = 0; hv < HQ; ++hv) {
+                                const bool begins = hv == 0 && (kShort || (part == 0 && wd == 0 && i == 0));
+                                auto add = [&](int t, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+                                    float(&to)[4] = kShort ? own[t % (kShort ? NS : 1)] : sc[t];
+                                    if (begins) mma16816_first(to, a, b0, b1);
+                                    else mma16816(to, a, b0, b1);
+                                };
                                 if constexpr (SIDE) {
                                     const uint2 x = *reinterpret_cast<const uint2 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
 #pragma unroll
                                     for (int t = 0; t < NS; ++t) {
                                         const uint32_t a[4] = {b[2 * t][2 * i], b[2 * t + 1][2 * i], b[2 * t][2 * i + 1], b[2 * t + 1][2 * i + 1]};
-                                        if (begins) mma16816_first(sc[t], a, x.x, x.y);
-                                        else mma16816(sc[t], a, x.x, x.y);
+                                        add(t, a, x.x, x.y);
                                     }
                                 } else {
                                     const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
                                     const uint32_t a[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                                    for (int t = 0; t < kWT; ++t) {
-                                        if (begins) mma16816_first(sc[t], a, b[t][0], b[t][1]);
-                                        else mma16816(sc[t], a, b[t][2 * i], b[t][2 * i + 1]);
-                                    }
+                                    for (int t = 0; t < kWT; ++t) add(t, a, b[t][2 * i], b[t][2 * i + 1]);
                                 }
                             }
+                            if constexpr (kShort) {
+#pragma unroll
+                                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) sc[t][k] = part == 0 && wd == 0 && i == 0 ? own[t][k] : sc[t][k] + own[t][k];
+                            }
+                        }
                     }
                 }
                 // ---- scores against the references: s - z ----
@@ -466,7 +485,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                             pa[0][t] = transposed(hi);
                             if constexpr (HP == 2) {
                                 const float2 a = unpack_h2(hi);
-                                pa[1][t] = transposed(pack_h2(x[0] - a.x, x[1] - a.y));
+                                pa[1][t] = transposed(pack_h2((x[0] - a.x) * kLowUp, (x[1] - a.y) * kLowUp));
                             }
                         }
                     } else {
@@ -477,8 +496,8 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                             pa[0][2 * t + 1] = pack_h2(x[2], x[3]);
                             if constexpr (HP == 2) {
                                 const float2 a = unpack_h2(pa[0][2 * t]), b = unpack_h2(pa[0][2 * t + 1]);
-                                pa[1][2 * t] = pack_h2(x[0] - a.x, x[1] - a.y);
-                                pa[1][2 * t + 1] = pack_h2(x[2] - b.x, x[3] - b.y);
+                                pa[1][2 * t] = pack_h2((x[0] - a.x) * kLowUp, (x[1] - a.y) * kLowUp);
+                                pa[1][2 * t + 1] = pack_h2((x[2] - b.x) * kLowUp, (x[3] - b.y) * kLowUp);
                             }
                         }
                     }
@@ -486,18 +505,39 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         uint32_t b0[4], b1[4];
                         code_pairs(x, b0);
                         code_pairs(y, b1);
-                        if constexpr (SIDE) {
+                        float own[kShort ? 4 : 1][4];
+                        auto add = [&](int hv, int j, float(&to)[4], const uint32_t (&a)[4], uint32_t x0, uint32_t x1) {
+                            if constexpr (kShort) {
+                                if (hv == 0) {
+                                    mma16816_first(own[j], a, x0, x1);
+                                } else {
+                                    mma16816(own[j], a, x0, x1);
 #pragma unroll
-                            for (int j = 0; j < 4; j += 2) {
-                                const uint32_t a[4] = {b0[j], b0[j + 1], b1[j], b1[j + 1]};
-#pragma unroll
-                                for (int hv = 0; hv < HP; ++hv) mma16816(acc[2 * q + j / 2], a, pa[hv][0], pa[hv][1]);
+                                    for (int k = 0; k < 4; ++k) to[k] += own[j][k];
+                                }
+                            } else {
+                                mma16816(to, a, x0, x1);
                             }
-                        } else {
+                        };
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                        for (int hv = 0; hv < HP; ++hv) {
+                            if (hv == 1) {
 #pragma unroll
-                                for (int hv = 0; hv < HP; ++hv) mma16816(acc[(4 * q + j) % NA], pa[hv], b0[j], b1[j]);
+                                for (int j = 0; j < 4; ++j) {
+                                    b0[j] = lowered(b0[j]);
+                                    b1[j] = lowered(b1[j]);
+                                }
+                            }
+                            if constexpr (SIDE) {
+#pragma unroll
+                                for (int j = 0; j < 4; j += 2) {
+                                    const uint32_t a[4] = {b0[j], b0[j + 1], b1[j], b1[j + 1]};
+                                    add(hv, j / 2, acc[2 * q + j / 2], a, pa[hv][0], pa[hv][1]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) add(hv, j, acc[(4 * q + j) % NA], pa[hv], b0[j], b1[j]);
+                            }
                         }
                     };
                     if constexpr (NQ == 1) {

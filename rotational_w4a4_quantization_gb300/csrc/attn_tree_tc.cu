@@ -40,9 +40,10 @@
 //
 // Weights: P = 2^(s - M + ev) (2^ev the tile's unit of vs) is what the MMA sees, rounded
 // to fp16; the sum l adds 2^(s - M) in fp32.  O / l does not depend on M, so M only has
-// to keep P in range: it moves only when some P would pass 2^8 (the accumulator is then
-// rescaled in place, between the commit that delivers S and the arrival that delivers
-// P, when no MMA touches it).
+// to keep P in range: it moves only when some P would pass 2^15, and then puts it at 2^9
+// (the accumulator is then rescaled in place, between the commit that delivers S and the
+// arrival that delivers P, when no MMA touches it).  fp16 keeps 11 bits down to 2^-14, so
+// of tokens at least 23 bits below the largest, and something down to 2^-25.
 //
 // Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 422 us, 0.70
 // PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 5,000 cycles
@@ -295,9 +296,9 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, const f
     }
     const float best = both(fmaxf(top0, top1) * a + ev);          // a > 0
     float f = 1.f;
-    if (best > r.M + 8.f) {                                       // also the first time, where M = -inf
-        if (r.M != -INFINITY) f = ex2(r.M - best);
-        r.M = best;
+    if (best > r.M + kWeightMost) {                               // also the first time, where M = -inf
+        if (r.M != -INFINITY) f = ex2(r.M - (best - kWeightTo));
+        r.M = best - kWeightTo;
         r.l *= f;
     }
     const float Mz = (r.M == -INFINITY ? 0.f : r.M) - ev;
@@ -407,11 +408,11 @@ __device__ __forceinline__ float soft_exact(uint32_t tS, const float *ks, const 
             best = fmaxf(best, sees ? sc + lg2(vs[kCW * c + i]) : -INFINITY);
         }
     }
-    best = both(fmaxf(best, only - 100.f));                             // rows of zero values: keeps 2^(s - M) itself finite
+    best = both(fmaxf(best, only + kLeastValue));                       // rows of zero values: keeps 2^(s - M) itself finite
     float f = 1.f;
-    if (best > r.M + 8.f) {
-        if (r.M != -INFINITY) f = ex2(r.M - best);
-        r.M = best;
+    if (best > r.M + kWeightMost) {
+        if (r.M != -INFINITY) f = ex2(r.M - (best - kWeightTo));
+        r.M = best - kWeightTo;
         r.l *= f;
     }
     const float Mz = r.M == -INFINITY ? 0.f : r.M;

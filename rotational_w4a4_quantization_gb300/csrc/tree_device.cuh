@@ -83,6 +83,12 @@ inline bool tree_maps(const TreeCall &c, int tile, CUtensorMap &mk, CUtensorMap 
 // without, 20.5 with 6).
 inline int tree_lead(int64_t max_tiles, int ctas) { return (int)(max_tiles / ctas < 12 ? max_tiles / ctas / 2 : 6); }
 
+// log2 of a row's weights relative to its reference: where a move of the reference puts the
+// largest, and past what the next move comes.  The products take weights as fp16, which
+// holds 11 bits from 2^-14 to 2^16.  And log2 of the least value scale that the reference
+// follows, so that the sum of the weights without their scales stays in range.
+constexpr float kWeightTo = 9.f, kWeightMost = 15.f, kLeastValue = -60.f;
+
 struct TreeSeq {
     int64_t row0;      // first query row
     int ctx, n, len;   // tokens before the tree, nodes, tokens in all

@@ -15,8 +15,8 @@ import rotational_w4a4_quantization_gb300 as rq
 from test_gpu_paged import DEV, DTYPES, SEED, _built, _status, dev_cache, gen, paged, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
-# query heads to a KV head, nodes: blocks of 8 and 16 rows
-ROWS = [(1, 5), (4, 4)]
+# query heads to a KV head, nodes: blocks of 8 and 16 rows, of 128, and (bf16) of 256
+ROWS = [(1, 5), (4, 4), (4, 12), (4, 40)]
 
 
 def pack(codes):
@@ -74,6 +74,26 @@ def put(cache, table, page, at, name, codes=None, scale=None):
 
 @pytest.mark.parametrize("G,n", ROWS)
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bits,value", [(10, 1e-3), (14, 1e-3), (17, 0.0), (24, 0.0), (26, 0.0)])
+@pytest.mark.parametrize("first", [True, False])
+def test_one_token_holds_the_weight(G, n, dtype, bits, value, first):
+    """A token whose value row is small or nothing, `bits` bits of weight above each of 32k others, whose values have a
+    common part."""
+    N, H, D, page = 32768, 1, 128, 64
+    q, cache, table, along, step = aligned(N, H, G, n, D, dtype, 400 + bits)
+    g = gen(401)
+    cache["ks"] = (0.3 + 0.2 * torch.rand(cache["ks"].shape, generator=g)) * (5.0 / step)     # scores within a few of 0
+    pages = cache["kq"].shape[0]
+    cache["vq"] = pack(3 + torch.randint(-3, 4, (pages, H, page, D), generator=g))
+    cache["vs"] = 0.2 + 0.2 * torch.rand(cache["vs"].shape, generator=g)
+    at = torch.tensor([0 if first else N - 200])
+    put(cache, table, page, at, "k", along, bits * math.log(2) / step)
+    put(cache, table, page, at, "v", None, value)
+    check(q, cache, table, [N], [n], None)
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("every", [16, 1000])
 def test_large_values_of_no_weight(G, n, dtype, D, every):
@@ -90,7 +110,7 @@ def test_large_values_of_no_weight(G, n, dtype, D, every):
     check(q, cache, table, [N], [n], None)
 
 
-@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("G,n", ROWS[:2])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("bits", [6, 13, 20, 30])
 def test_value_scales_apart(G, n, dtype, bits):
@@ -106,7 +126,7 @@ def test_value_scales_apart(G, n, dtype, bits):
     check(q, cache, table, [N], [n], None)
 
 
-@pytest.mark.parametrize("G,n", [(1, 7), (1, 13), (4, 3)])
+@pytest.mark.parametrize("G,n", [(1, 7), (1, 13), (4, 3), (4, 12), (4, 40)])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("scale", [float("inf"), 3e38, 2.0**20, float("nan")])
 def test_a_place_that_only_some_rows_see(G, n, dtype, scale):

@@ -31,9 +31,10 @@
 // shared memory
 // costs 4 cycles per 16 bytes and warp, and bound the kernel (8 warps x 64 loads per
 // tile; measured 2,150 cycles per tile for that softmax alone, against 2,048 of MMAs).
-// A tile that some row sees in part keeps exact codes if a scale of it is not finite or
-// they lie too far apart, and applies them to scores and weights, so that what an unseen
-// token holds (a NaN scale, say) reaches nobody.  fp16 queries, whose outputs resolve an
+// A tile keeps exact codes if a scale of it is not finite or they lie too far apart (values
+// by more than 2^8, keys 2^12), and applies them to scores and weights, so that a large
+// scale costs the others no bits and what an unseen token holds (a NaN scale, say) reaches
+// nobody.  fp16 queries, whose outputs resolve an
 // 11-bit rounding of q~, k^ and v^, keep q~ in two fp16 parts (Q K^T runs twice) and the
 // scales out of the operands; the weights with vs in them round once (16 sequences of up
 // to 4k: outputs 2.9e-4 off; with the scales of V folded 3.3e-4, and 2 us slower).
@@ -209,12 +210,16 @@ __device__ __forceinline__ int tile_exponent(const float4 &x) {
                                                             max(__float_as_uint(x.z), __float_as_uint(x.w))));
     return top == 0 ? 0 : max(-100, min((int)((top >> 23) & 255u) - 126, 100));
 }
-// Each of four scales is 0 or within 2^12 of 2^e, and finite (checked where `asked`).
-__device__ __forceinline__ bool of_a_kind(const float4 &x, int e, bool asked) {
-    const float lo = __uint_as_float((uint32_t)(127 + max(e - 13, -120)) << 23), hi = __uint_as_float((uint32_t)(127 + e) << 23);
+// Each of four scales is 0 or within 2^(bits + 1) of 2^e, and finite.
+__device__ __forceinline__ bool of_a_kind(const float4 &x, int e, int bits) {
+    const float lo = __uint_as_float((uint32_t)(127 + max(e - 1 - bits, -120)) << 23), hi = __uint_as_float((uint32_t)(127 + e) << 23);
     auto ok = [&](float v) { return v == 0.f || (v >= lo && v <= hi); };
-    return !asked || (ok(x.x) && ok(x.y) && ok(x.z) && ok(x.w));
+    return ok(x.x) && ok(x.y) && ok(x.z) && ok(x.w);
 }
+// How far apart a tile's scales may lie to share a unit: the products of keys keep 11 bits in
+// fp16; values may cost the weights' range that much, as a row's reference takes a tile's
+// largest score and largest value scale for one token's.
+constexpr int kKeyBits = 12, kValueBits = 8;
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // |e| <= 126
 __device__ __forceinline__ uint4 ld_once(const void *p) {
     uint4 v;
@@ -385,8 +390,8 @@ __device__ __forceinline__ void tree_visible(const TreeParams &p, const TreeSeq 
     }
 }
 
-// A masked tile with exact codes, where some scale is not finite or the scales lie too
-// far apart to share a unit: s = a S ks, weight = 2^(s - M) vs.  M follows the largest
+// A tile with exact codes, where some scale is not finite or the scales lie too far apart
+// to share a unit: s = a S ks, weight = 2^(s - M) vs.  M follows the largest
 // s + log2 vs, the weight's exponent.  A masked weight is zero whatever its scales hold.
 // Hardly a tile comes here, and its time is the fetching of code that ran for none
 // before: the loops stay rolled.
@@ -516,10 +521,9 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 const bool there = nthere;
                 load(k + 1);
                 const uint32_t quads = __ballot_sync(0xffffffffu, there);
-                const bool masked = (w.t0 + k + 1) * kTcTT > w.s.ctx || quads != 0xffffffffu;
                 const int ek = FOLD ? tile_exponent(ck) : 0, ev = tile_exponent(cv);
-                // a tile that not every row sees whole folds its scales in if they are of a kind
-                const bool exact = masked && __any_sync(0xffffffffu, !(of_a_kind(ck, ek, FOLD) && of_a_kind(cv, ev, true)));
+                // scales that are not of a kind stay out of the operands and the tile's unit
+                const bool exact = __any_sync(0xffffffffu, !((!FOLD || of_a_kind(ck, ek, kKeyBits)) && of_a_kind(cv, ev, kValueBits)));
                 uint32_t chunks = 0;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) chunks |= ((quads >> (4 * c)) & 1) << c;

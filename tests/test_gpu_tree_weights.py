@@ -15,6 +15,7 @@ import rotational_w4a4_quantization_gb300 as rq
 from test_gpu_paged import DEV, DTYPES, SEED, _built, _status, dev_cache, gen, paged, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+HALVES = [torch.bfloat16, torch.float16]
 # query heads to a KV head, nodes: blocks of 8 and 16 rows, of 128, and (bf16) of 256
 ROWS = [(1, 5), (4, 4), (4, 12), (4, 40)]
 
@@ -110,7 +111,7 @@ def test_large_values_of_no_weight(G, n, dtype, D, every):
     check(q, cache, table, [N], [n], None)
 
 
-@pytest.mark.parametrize("G,n", ROWS[:2])
+@pytest.mark.parametrize("G,n", ROWS)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("bits", [6, 13, 20, 30])
 def test_value_scales_apart(G, n, dtype, bits):
@@ -124,6 +125,23 @@ def test_value_scales_apart(G, n, dtype, bits):
         ((1.5 * down - 1).abs() * math.log(2) / step)[:, None])
     put(cache, table, page, at, "v", None, (0.3 * torch.exp2(-down))[:, None])
     check(q, cache, table, [N], [n], None)
+
+
+@pytest.mark.parametrize("G,n", [(4, 12), (4, 40)])
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("bits", [13, 20, 27])
+def test_key_scales_apart(G, n, dtype, bits):
+    """One key per tile with a scale 2^bits above the others', far below them in score: the others' scores decide."""
+    N, H, D, page = 16384, 2, 128, 64
+    q, cache, table, along, step = aligned(N, H, G, n, D, dtype, 430)
+    g = gen(431)
+    small = 20.0 / step
+    cache["ks"] = (0.3 + 0.2 * torch.rand(cache["ks"].shape, generator=g)) * small
+    at = torch.arange(5, N, 100)
+    put(cache, table, page, at, "k", -along, small * 2.0**bits)
+    seen = {name: t.clone() for name, t in cache.items()}
+    put(seen, table, page, at, "k", -along, 40.0 / step)              # e^-40 of the others' weight as well
+    check(q, cache, table, [N], [n], None, seen=seen)
 
 
 @pytest.mark.parametrize("G,n", [(1, 7), (1, 13), (4, 3), (4, 12), (4, 40)])

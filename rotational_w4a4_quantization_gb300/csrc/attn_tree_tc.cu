@@ -203,12 +203,12 @@ __device__ __forceinline__ uint4 operands(uint32_t x, __half2 hi, __half2 lo) {
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
-// The exponent e with 2^e above the largest of a tile's 128 scales (0 where all are 0):
-// one warp, four scales a lane.  Scales are not negative, so their bits order them.
-__device__ __forceinline__ int tile_exponent(const float4 &x) {
+// The exponent e >= least with 2^e above the largest of a tile's 128 scales (`none` where all
+// are 0): one warp, four scales a lane.  Scales are not negative, so their bits order them.
+__device__ __forceinline__ int tile_exponent(const float4 &x, int least, int none) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(__float_as_uint(x.x), __float_as_uint(x.y)),
                                                             max(__float_as_uint(x.z), __float_as_uint(x.w))));
-    return top == 0 ? 0 : max(-100, min((int)((top >> 23) & 255u) - 126, 100));
+    return top == 0 ? none : max(least, min((int)((top >> 23) & 255u) - 126, 100));
 }
 // Each of four scales is 0 or within 2^(bits + 1) of 2^e, and finite.
 __device__ __forceinline__ bool of_a_kind(const float4 &x, int e, int bits) {
@@ -521,7 +521,8 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 const bool there = nthere;
                 load(k + 1);
                 const uint32_t quads = __ballot_sync(0xffffffffu, there);
-                const int ek = FOLD ? tile_exponent(ck) : 0, ev = tile_exponent(cv);
+                // a tile of zero values moves no row's reference: its unit is the least
+                const int ek = FOLD ? tile_exponent(ck, -100, 0) : 0, ev = tile_exponent(cv, (int)kLeastValue, (int)kLeastValue);
                 // scales that are not of a kind stay out of the operands and the tile's unit
                 const bool exact = __any_sync(0xffffffffu, !((!FOLD || of_a_kind(ck, ek, kKeyBits)) && of_a_kind(cv, ev, kValueBits)));
                 uint32_t chunks = 0;

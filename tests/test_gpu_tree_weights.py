@@ -144,6 +144,20 @@ def test_key_scales_apart(G, n, dtype, bits):
     check(q, cache, table, [N], [n], None, seen=seen)
 
 
+@pytest.mark.parametrize("G,n,dtype", [(4, 12, torch.bfloat16), (4, 40, torch.bfloat16), (4, 12, torch.float16), (1, 5, torch.bfloat16)])
+@pytest.mark.parametrize("zero", [(0, 128), (128, 256), (256, 640)])
+def test_tiles_of_zero_values(G, n, dtype, zero):
+    """Whole tiles of zero value rows before and between tiles of small values."""
+    B, H, D, page = 16, 2, 128, 64
+    contexts, counts = [700 + 5 * b for b in range(B)], [n] * B
+    cache, table = paged([c + n for c in contexts], H, page, D, 440)
+    cache["vs"] *= 1e-9 if dtype == torch.bfloat16 else 2e-3
+    at = torch.arange(*zero)
+    for b in range(B):
+        cache["vs"][table[b].long()[at // page], :, at % page] = 0.0
+    check(randn(B * n, H * G, D, seed=441, dtype=dtype), cache, table, contexts, counts, None)
+
+
 @pytest.mark.parametrize("G,n", [(1, 7), (1, 13), (4, 3), (4, 12), (4, 40)])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("scale", [float("inf"), 3e38, 2.0**20, float("nan")])

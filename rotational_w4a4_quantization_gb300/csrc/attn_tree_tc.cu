@@ -299,7 +299,7 @@ __device__ __forceinline__ float soft_tile(uint32_t tS, const float *ks, const f
         tm_ld16(tS + kCW * ((c + 2) % C), s0);                    // at the end: the first again
         largest(s1, c + 1);
     }
-    const float best = both(fmaxf(top0, top1) * a + ev);          // a > 0
+    const float best = both(fmaxf(top0, top1) * a + ev);          // a >= 0
     float f = 1.f;
     if (best > r.M + kWeightMost) {                               // also the first time, where M = -inf
         if (r.M != -INFINITY) f = ex2(r.M - (best - kWeightTo));
@@ -683,8 +683,9 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // top < 2^ex: q~ enters the MMA relative to that
                 const int ex = max(-100, min((int)((__float_as_uint(top) >> 23) & 255u) - 126, 120));
-                if (hf == 0) s.rfac[r] = pow2(ex) * inv_sqrt_dim<D>() * p.score_scale;
-                const float down = pow2(-ex);
+                // the scale's sign goes into q~: the softmax takes the largest score for the largest product
+                if (hf == 0) s.rfac[r] = pow2(ex) * inv_sqrt_dim<D>() * fabsf(p.score_scale);
+                const float down = copysignf(pow2(-ex), p.score_scale);
                 uint8_t *const dst = s.q[NT == 2 ? r >> 7 : 0] + rr * 128;
 #pragma unroll
                 for (int i = 0; i < HD / 8; ++i) {

@@ -182,3 +182,15 @@ def test_a_place_that_only_some_rows_see(G, n, dtype, scale):
     rows = ~sees.to(DEV)
     got = check(randn(B * n, H * G, D, seed=452, dtype=dtype), cache, table, contexts, counts, None, mask, rows, seen)
     assert torch.isfinite(got[rows]).all()
+
+
+@pytest.mark.parametrize("G,n", [(1, 5), (4, 4), (4, 12), (4, 40)])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scale", [-0.3, -1e-3])
+def test_negative_scale(G, n, dtype, scale):
+    """The softmax of negative multiples of the scores; contexts that end inside a tile, a mask."""
+    B, H, D, page = 80, 1, 128, 32
+    g = gen(460)
+    contexts, counts = torch.randint(1, 150, (B,), generator=g).tolist(), [n] * B
+    cache, table = paged([c + n for c in contexts], H, page, D, 461)
+    check(randn(B * n, H * G, D, seed=462, dtype=dtype), cache, table, contexts, counts, scale, ref.tree_mask(counts, g))

@@ -75,7 +75,7 @@ struct MSmem {
     float acc[2][ROWS][D + 4];                       // the warps' sums, joined two by two
     float ref[kCWarps][ROWS], sum[kCWarps][ROWS];
     float2 rfac[ROWS];                               // a, b
-    int64_t prefix[kScan + 1];
+    TreeLine line;
     alignas(8) uint64_t full[kStages], empty[kStages];
     uint32_t valid[kStages];
     volatile int abort_flag;
@@ -155,8 +155,8 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tree_join_may_begin();
-    tree_scan<ROWS, kTT>(p, s.prefix);               // ends with a block barrier
-    const int64_t total = s.prefix[kScan];
+    tree_scan<ROWS, kTT>(p, s.line);               // ends with a block barrier
+    const int64_t total = s.line.prefix[kScan];
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
     int st = 0;
     uint32_t ph = 0;
@@ -164,9 +164,11 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     if (warp == kCWarps) {
         // ---------------- producer: one lane per page piece of a tile ----------------
         const int bt = min(kTT, 1 << p.log_page), pieces = kTT / bt;
+        TreeJoin join{};
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<ROWS, kTT>(p, s.prefix, at, end);
+            const TreeWork w = tree_work<ROWS, kTT>(p, s.line, at, end);
             at += w.used;
+            tree_note<ROWS>(p, s.line, w, begin, join);
             if (w.t1 <= w.t0) continue;
             auto page_of = [&](int tile) -> int64_t {
                 const int t = tile * kTT + lane * bt;
@@ -199,6 +201,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 }
             }
         }
+        if (lane == 0) reinterpret_cast<TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x] = join;
         // no copy outlives the block, also when it gave up
         if (s.abort_flag) {
             const long long t0 = clock64();
@@ -215,7 +218,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;
 
     for (int64_t at = begin; at < end;) {
-        const TreeWork w = tree_work<ROWS, kTT>(p, s.prefix, at, end);
+        const TreeWork w = tree_work<ROWS, kTT>(p, s.line, at, end);
         at += w.used;
         if (w.t1 <= w.t0) continue;
         const int rows = min(ROWS, w.s.n * p.group - w.mt * ROWS);
@@ -661,7 +664,7 @@ cudaError_t launch_tree_d(TreeParams &p, const CUtensorMap &mk, const CUtensorMa
     kern<<<p.ctas, kMThreads, smem, stream>>>(mk, mv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_tree_join<IN, D, ROWS, kTT>(p, stream);
+    return launch_tree_join<IN, D, ROWS>(p, stream);
 }
 
 template <int IN, int ROWS>
@@ -678,7 +681,7 @@ cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, cons
 
 int64_t attn_tree_workspace(int64_t head_dim) {
     const int64_t ctas = 2 * (int64_t)device_sm_count();
-    const int64_t small = 2 * ctas * 16 * (head_dim + 2) * (int64_t)sizeof(float);
+    const int64_t small = tree_join_at((int)ctas, 16, (int)head_dim) * (int64_t)sizeof(float) + 2 * ctas * (int64_t)sizeof(TreeJoin);
     const int64_t wide = attn_tree_tc_workspace(head_dim);
     return small > wide ? small : wide;
 }
@@ -689,12 +692,10 @@ cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
     if (!tree_params(c, p)) return cudaErrorUnknown;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorUnknown;
-    const int rows = c.max_nodes * p.group <= 8 ? 8 : 16;
+    const int rows = tree_rows(c) <= 8 ? 8 : 16;
     const int per_sm = blocks_per_sm(rows, c.head_dim);
-    const int64_t bph = (c.max_nodes * p.group + rows - 1) / rows;
-    const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTT - 1) / kTT);
+    const int64_t max_tiles = tree_tiles(c, rows, kTT);
     p.ctas = (int)(max_tiles < per_sm * sms ? max_tiles : per_sm * sms);
-    p.lead = tree_lead(max_tiles, p.ctas);
     CUtensorMap mk, mv;
     if (!tree_maps(c, kTT, mk, mv)) return cudaErrorInvalidValue;
     const bool side = rows == 8;

@@ -81,7 +81,7 @@ struct TSmem {
     float2 unit[kSc];                                       // a tile's 2^ek and ev; 0 and 0: scales not folded in
     float rfac[NT * 128];                                   // s = rfac S (times ks)
     float best[2][2][128], sum[2][2][128];                  // what the two threads of a row tell each other: [buffer][team], [team][buffer]
-    int64_t prefix[kScan + 1];
+    TreeLine line;
     TreeWork work[2];                                       // each softmax team's copy of the stretch: kept here, not in registers
     alignas(8) uint64_t sc_full[kSc], sc_empty[kSc];
     uint64_t op_full[kOps], op_empty[kOps];
@@ -482,20 +482,22 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
     block_sign_words<D>(s.sign_words, p.seed);
     tree_join_may_begin();
     tc_fence_before();
-    tree_scan<ROWS, kTcTT>(p, s.prefix);               // ends with a block barrier
+    tree_scan<ROWS, kTcTT>(p, s.line);               // ends with a block barrier
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
     const uint32_t tO[2] = {tmem + 256, tmem + 256 + (uint32_t)D};
-    const int64_t total = s.prefix[kScan];
+    const int64_t total = s.line.prefix[kScan];
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
 
     if (warp == 0) {
         // ---------------- scales ----------------
         uint32_t sc = 0;
+        TreeJoin join{};
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
+            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, end);
             const int T = w.t1 - w.t0;
             at += w.used;
+            tree_note<ROWS>(p, s.line, w, begin, join);
             if (T <= 0) continue;
             // lane l: tokens 4 l .. 4 l + 3 of a tile, the next tile's loaded ahead
             float4 nk, nv;
@@ -542,6 +544,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 if (lane == 0) t_mbar_arrive(&s.sc_full[scs]);
             }
         }
+        if (lane == 0) reinterpret_cast<TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x] = join;
     } else if (warp == 1) {
         // ---------------- MMA ----------------
         // The whole warp runs the loop, so that descriptors stay in uniform registers;
@@ -554,7 +557,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         const uint64_t dv = op_desc(t_smem(s.op[0]), S::PANEL);
         bool ok = true;
         for (int64_t at = begin; at < end && ok; ++unit) {
-            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
+            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, end);
             const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), J = NT * T;
             at += w.used;
             if (T <= 0) continue;
@@ -620,7 +623,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         const TreeWork &w = s.work[team];
         for (int64_t at = begin; at < end;) {
             if (quarter == 0) {
-                const TreeWork x = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
+                const TreeWork x = tree_work<ROWS, kTcTT>(p, s.line, at, end);
                 if (lane == 0) s.work[team] = x;
             }
             team_sync();
@@ -950,7 +953,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int q = 0; q < 4; ++q) piece[q] = (uint32_t)(((ch & 1) * 4 + q) ^ (r0 & 7)) << 4;
         uint32_t base = 0, sc = 0;                       // items and tiles of earlier stretches
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.prefix, at, end);
+            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, end);
             const int T = w.t1 - w.t0;
             at += w.used;
             if (T <= 0) continue;
@@ -1061,7 +1064,7 @@ cudaError_t launch_tc(TreeParams &p, cudaStream_t stream) {
     kern<<<p.ctas, kTcThreads, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_tree_join<IN, D, 128 * NT, kTcTT>(p, stream);
+    return launch_tree_join<IN, D, 128 * NT>(p, stream);
 }
 
 }  // namespace
@@ -1072,13 +1075,13 @@ cudaError_t launch_tc(TreeParams &p, cudaStream_t stream) {
 // 48 rows 74 and 85; fp16, 4 of 32k, 32 rows 123 and 115, 48 rows 123 and 160; bf16, 2 of
 // 512, 64 rows 27 and 25, as they have fewer tiles than SMs.
 bool attn_tree_tc_supported(const TreeCall &c) {
-    const int64_t rows = c.max_nodes * (c.q_heads / c.cache.heads);
-    const int64_t tiles = c.seqs * c.cache.heads * ((rows + 127) / 128) * ((c.width * c.cache.page_size + kTcTT - 1) / kTcTT);
+    const int64_t rows = tree_rows(c), tiles = tree_tiles(c, 128, kTcTT);
     return c.in_type != IN_F32 && (c.head_dim == 64 || c.head_dim == 128) && rows > 32 && tiles > device_sm_count();
 }
 
 int64_t attn_tree_tc_workspace(int64_t head_dim) {
-    return 2 * (int64_t)device_sm_count() * 256 * (head_dim + 2) * (int64_t)sizeof(float);
+    const int sms = device_sm_count();
+    return tree_join_at(sms, 256, (int)head_dim) * (int64_t)sizeof(float) + sms * (int64_t)sizeof(TreeJoin);
 }
 
 cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream) {
@@ -1086,14 +1089,11 @@ cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream) {
     if (!tree_params(c, p)) return cudaErrorUnknown;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorUnknown;
-    const int64_t rows = c.max_nodes * p.group;
     // two row blocks share each converted tile; fp16 queries keep the second's shared
     // memory for the low parts of q~
-    const int nt = rows > 128 && c.in_type == IN_BF16 ? 2 : 1;
-    const int64_t bph = (rows + 128 * nt - 1) / (128 * nt);
-    const int64_t max_tiles = c.seqs * c.cache.heads * bph * ((c.width * c.cache.page_size + kTcTT - 1) / kTcTT);
+    const int nt = tree_rows(c) > 128 && c.in_type == IN_BF16 ? 2 : 1;
+    const int64_t max_tiles = tree_tiles(c, 128 * nt, kTcTT);
     p.ctas = (int)(max_tiles < sms ? max_tiles : sms);
-    p.lead = tree_lead(max_tiles, p.ctas);
     const bool d128 = c.head_dim == 128;
     if (c.in_type == IN_F16)
         return d128 ? launch_tc<IN_F16, 128, 1, 2>(p, stream) : launch_tc<IN_F16, 64, 1, 2>(p, stream);

@@ -27,16 +27,23 @@ struct TreeParams {
     uint32_t flags;
     float score_scale;                  // softmax_scale * log2(e)
     void *out;
-    float *part;                        // [2 G][ROWS][D] fp32, then [2 G][ROWS][2] (reference, sum)
+    float *part;                        // [2 G][ROWS][D] fp32, then [2 G][ROWS][2] (reference, sum), then [G] TreeJoin
+    int64_t rows_each;                  // query rows per KV head and sequence, on average
     int ctas;                           // G
-    int lead;                           // a unit's fixed cost, in tiles
     int *err;
 };
 
+// Query rows per KV head and sequence on average: what the choice of a kernel goes by.  The
+// bound max_nodes may be far above it (it is the number of rows where a caller has none).
+inline int64_t tree_rows(const TreeCall &c) {
+    const int64_t nodes = (c.rows + c.seqs - 1) / c.seqs;
+    return (nodes < c.max_nodes ? nodes : c.max_nodes) * (c.q_heads / c.cache.heads);
+}
 // Host side: the parameters that do not depend on the kernel, and TMA maps whose boxes
 // are whole pages, or a tile's worth of a larger page.
 inline bool tree_params(const TreeCall &c, TreeParams &p) {
     p = TreeParams{};
+    p.rows_each = tree_rows(c);
     p.q = c.q;
     p.q_token = c.q_token;
     p.q_head = c.q_head;
@@ -75,13 +82,13 @@ inline bool tree_maps(const TreeCall &c, int tile, CUtensorMap &mk, CUtensorMap 
     return make_tma_map_u8(&mk, c.cache.kq, rows, rb, rb, box, sw) && make_tma_map_u8(&mv, c.cache.vq, rows, rb, rb, box, sw);
 }
 
-// What a unit costs a CTA beside its tiles, in tiles: q~, the first tile's latency, the
-// masked tiles at its end and its output.  Measured: 0, 2, 4, 6 and 9 tiles give 97, 92,
-// 90, 88 and 88 us for 16 ragged sequences of up to 4k (128 rows, fp16), 136, 133, 131,
-// 130 and 131 us for 64 of up to 8k (8 rows, bf16).  Less where CTAs have few tiles each:
-// there the lead would leave some of them without any (one sequence of 512: 18.5 us
-// without, 20.5 with 6).
-inline int tree_lead(int64_t max_tiles, int ctas) { return (int)(max_tiles / ctas < 12 ? max_tiles / ctas / 2 : 6); }
+// At most so many tiles in all, with blocks of `block` rows: as far as the table reaches.
+inline int64_t tree_tiles(const TreeCall &c, int64_t block, int64_t tile) {
+    const int64_t group = c.q_heads / c.cache.heads, each = c.seqs * ((c.max_nodes * group + block - 1) / block),
+                  all = c.seqs + c.rows * group / block;
+    const double tiles = (double)(c.cache.heads * (each < all ? each : all)) * (double)((c.width * c.cache.page_size + tile - 1) / tile);
+    return tiles < 1e9 ? (int64_t)tiles : 1000000000;
+}
 
 // log2 of a row's weights relative to its reference: where a move of the reference puts the
 // largest, and past what the next move comes.  The products take weights as fp16, which
@@ -111,32 +118,54 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
 
 constexpr int kScan = 128;              // stretches of sequences whose lengths are scanned
 
-// Exclusive prefix sums of the lengths in the line of kScan stretches of sequences, the
-// total in prefix[kScan].  Threads 0..kScan-1 of the block take part; the caller's
-// barrier follows.  Needs __syncthreads in between, so every thread calls it.
-// A unit's length in the line: its tiles, and before them its lead, what starting and
-// ending it costs a CTA.  With tiles alone CTAs that meet several short units end last.
-__device__ __forceinline__ int64_t unit_length(const TreeParams &p, const TreeSeq &s) { return s.nt ? s.nt + p.lead : 0; }
+// The line of units: where each of kScan stretches of sequences begins and, at the end, its
+// length; and the units' lead.
+struct TreeLine {
+    int64_t prefix[kScan + 1];
+    int64_t units[kScan];
+    int lead;
+};
 
+// What a unit costs a CTA beside its tiles, in tiles: q~, the first tile's latency, the
+// masked tiles at its end and its output.  With tiles alone CTAs that meet several short
+// units end last.  Measured: 0, 2, 4, 6 and 9 tiles give 97, 92, 90, 88 and 88 us for 16
+// ragged sequences of up to 4k (128 rows, fp16), 136, 133, 131, 130 and 131 us for 64 of up
+// to 8k (8 rows, bf16).  Less where CTAs have few tiles each: there the lead would leave
+// some of them without any (one sequence of 512: 18.5 us without, 20.5 with 6).
+__device__ __forceinline__ int tree_lead(int64_t tiles, int ctas) { return (int)(tiles / ctas < 12 ? tiles / ctas / 2 : 6); }
+
+// A unit's length in the line: its tiles, and before them its lead.
+__device__ __forceinline__ int64_t unit_length(int lead, const TreeSeq &s) { return s.nt ? s.nt + lead : 0; }
+
+// Fills the line.  Every thread of the block calls it; ends with a block barrier.
 template <int ROWS, int TT>
-__device__ __forceinline__ void tree_scan(const TreeParams &p, int64_t *prefix) {
+__device__ __forceinline__ void tree_scan(const TreeParams &p, TreeLine &line) {
     const int per = (p.seqs + kScan - 1) / kScan;
     if (threadIdx.x < kScan) {
-        int64_t sum = 0;
+        int64_t tiles = 0, units = 0;
         for (int b = threadIdx.x * per; b < min(p.seqs, ((int)threadIdx.x + 1) * per); ++b) {
             const TreeSeq s = tree_seq<ROWS, TT>(p, b);
-            sum += (int64_t)p.kv_heads * s.mt * unit_length(p, s);
+            tiles += (int64_t)p.kv_heads * s.mt * s.nt;
+            units += s.nt ? (int64_t)p.kv_heads * s.mt : 0;
         }
-        prefix[threadIdx.x] = sum;
+        line.prefix[threadIdx.x] = tiles;
+        line.units[threadIdx.x] = units;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        int64_t v[kScan / 32], run = 0;
+        int64_t v[kScan / 32], u[kScan / 32], tiles = 0, units = 0;
 #pragma unroll
         for (int i = 0; i < kScan / 32; ++i) {
-            v[i] = prefix[threadIdx.x * (kScan / 32) + i];
-            run += v[i];
+            v[i] = line.prefix[threadIdx.x * (kScan / 32) + i];
+            u[i] = line.units[threadIdx.x * (kScan / 32) + i];
+            tiles += v[i];
+            units += u[i];
         }
+        int64_t all = tiles;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        const int lead = tree_lead(all, p.ctas);
+        const int64_t run = tiles + lead * units;
         int64_t incl = run;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -146,10 +175,11 @@ __device__ __forceinline__ void tree_scan(const TreeParams &p, int64_t *prefix) 
         int64_t at = incl - run;
 #pragma unroll
         for (int i = 0; i < kScan / 32; ++i) {
-            prefix[threadIdx.x * (kScan / 32) + i] = at;
-            at += v[i];
+            line.prefix[threadIdx.x * (kScan / 32) + i] = at;
+            at += v[i] + lead * u[i];
         }
-        if (threadIdx.x == 31) prefix[kScan] = at;
+        if (threadIdx.x == 31) line.prefix[kScan] = at;
+        if (threadIdx.x == 0) line.lead = lead;
     }
     __syncthreads();
 }
@@ -159,33 +189,34 @@ struct TreeWork {
     TreeSeq s;
     int b, h, mt;          // sequence, KV head, row block
     int t0, t1;            // the CTA's tiles of the unit; none where it ends within the unit's lead
-    int64_t used;          // of the line
+    int64_t first, used;   // where the unit begins in the line; the stretch's length
     bool whole;            // the unit lies in this CTA alone
 };
 
 template <int ROWS, int TT>
-__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const int64_t *prefix, int64_t pos, int64_t end) {
+__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const TreeLine &line, int64_t pos, int64_t end) {
     int lo = 0, hi = kScan;
     while (hi - lo > 1) {                    // the last stretch that begins at or before pos
         const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= pos) lo = mid;
+        if (line.prefix[mid] <= pos) lo = mid;
         else hi = mid;
     }
     const int per = (p.seqs + kScan - 1) / kScan;
-    int64_t at = prefix[lo];
+    int64_t at = line.prefix[lo];
     TreeWork w;
     w.b = lo * per;
     while (true) {
         w.s = tree_seq<ROWS, TT>(p, w.b);
-        const int64_t length = (int64_t)p.kv_heads * w.s.mt * unit_length(p, w.s);
+        const int64_t length = (int64_t)p.kv_heads * w.s.mt * unit_length(line.lead, w.s);
         if (pos < at + length || w.b + 1 >= p.seqs) break;
         at += length;
         ++w.b;
     }
-    const int64_t off = pos - at, length = unit_length(p, w.s), u = off / length, from = off - u * length;
+    const int64_t off = pos - at, length = unit_length(line.lead, w.s), u = off / length, from = off - u * length;
+    w.first = pos - from;
     w.used = min(length - from, end - pos);
-    w.t0 = (int)max((int64_t)0, from - p.lead);
-    w.t1 = (int)max((int64_t)0, from + w.used - p.lead);
+    w.t0 = (int)max((int64_t)0, from - line.lead);
+    w.t1 = (int)max((int64_t)0, from + w.used - line.lead);
     w.h = (int)(u / w.s.mt);
     w.mt = (int)(u - (int64_t)w.h * w.s.mt);
     w.whole = w.t0 == 0 && w.t1 == w.s.nt;
@@ -193,6 +224,28 @@ __device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const int64_t
 }
 
 __device__ __forceinline__ int64_t tree_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
+
+// What the join has to know of a unit that spans CTAs; the CTA with its first tile leaves it,
+// the others (and that one for none) one without rows.  The join has neither scan nor search,
+// and as many blocks as CTAs, however many units there are.
+struct alignas(16) TreeJoin {
+    int row0, rows, h, mt; // the unit's first query row, its rows, KV head, row block
+    int c1, slot0;         // its last CTA; the slot of the first CTA's partial
+    int64_t total;         // the line's length
+};
+// floats before the TreeJoin of CTA 0
+__host__ __device__ inline int64_t tree_join_at(int ctas, int rows, int dim) { return (int64_t)2 * ctas * rows * (dim + 2); }
+
+// After each of a CTA's stretches (`join` begins as {}): notes a unit that goes on past it.
+template <int ROWS>
+__device__ __forceinline__ void tree_note(const TreeParams &p, const TreeLine &line, const TreeWork &w, int64_t begin, TreeJoin &join) {
+    if (w.t0 != 0 || w.t1 == 0 || w.whole) return;
+    const int64_t total = line.prefix[kScan], last = w.first + unit_length(line.lead, w.s) - 1;
+    // CTA of a position: the last c with total c / ctas <= position
+    const int c1 = (int)(((last + 1) * p.ctas - 1) / total);
+    join = TreeJoin{(int)w.s.row0, min(ROWS, w.s.n * p.group - w.mt * ROWS), w.h, w.mt, c1,
+                    2 * (int)blockIdx.x + (begin >= w.first ? 0 : 1), total};
+}
 
 // May query row `r` of the row block see token `t` of the sequence?  Rows past the
 // sequence's last see nothing.
@@ -268,51 +321,30 @@ __device__ __forceinline__ void t_bulk(void *dst, const void *src, uint32_t byte
 // Joins the partials of the units that span CTAs: per row, in the order of the
 // CTAs (so results do not change from run to run), the largest reference, the
 // rescaled sums, then normalisation, R^T and the one rounding to the output type.
-// A warp takes a row (two of 256-row units) and four partials at a time, so that their
-// loads overlap.
-// Launched so that it may begin while the kernel before it ends: it finds its units
-// first and waits then.  Every thread waits, those without a unit to join too: the join
-// may not end before the kernel before it has, as what follows on the stream (or in a
-// captured graph) is ordered behind the join alone.
-constexpr int kJoinWarps = 16;
+// Block c takes the unit whose first tile CTA c has, if that spans CTAs.  A warp takes a row
+// (two of 256-row units) and four partials at a time, so that their loads overlap.
+// Launched so that it may begin while the kernel before it ends.  Every thread waits for
+// that, those without a unit to join too: the join may not end before the kernel before it
+// has, as what follows on the stream (or in a captured graph) is ordered behind the join
+// alone.
 __device__ __forceinline__ void tree_join_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 constexpr int join_rows(int rows) { return rows >= 256 ? 2 : 1; }         // rows per warp
-template <int IN, int D, int ROWS, int TT>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const __grid_constant__ TreeParams p,
-                                                                         int blocks_per_head, int turns) {
-    constexpr int E = D / 32, RW = join_rows(ROWS);
-    __shared__ int64_t prefix[kScan + 1];
-    tree_scan<ROWS, TT>(p, prefix);
-    const int64_t total = prefix[kScan];
-    const int per_seq = p.kv_heads * blocks_per_head;
-    const int b = blockIdx.x / per_seq, hm = blockIdx.x - b * per_seq;
-    const int h = hm / blocks_per_head, mt = hm - h * blocks_per_head;
-    const TreeSeq s = tree_seq<ROWS, TT>(p, b);
+constexpr int join_warps(int rows) { return rows < 16 ? rows : 16; }
+template <int IN, int D, int ROWS>
+__global__ void __launch_bounds__(32 * join_warps(ROWS)) attn_tree_join_kernel(const __grid_constant__ TreeParams p, int turns) {
+    constexpr int E = D / 32, RW = join_rows(ROWS), kJoinWarps = join_warps(ROWS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = min(ROWS, s.n * p.group - mt * ROWS);
     const int begin_row = (blockIdx.y * turns * kJoinWarps + warp) * RW;
-    int64_t first = 0;
-    int c0 = 0, c1 = 0;                                     // the unit's CTAs; one: finished there
-    if (mt < s.mt && begin_row < rows) {
-        const int per = (p.seqs + kScan - 1) / kScan;
-        first = prefix[b / per];
-        for (int i = b / per * per; i < b; ++i) {
-            const TreeSeq x = tree_seq<ROWS, TT>(p, i);
-            first += (int64_t)p.kv_heads * x.mt * unit_length(p, x);
-        }
-        first += ((int64_t)h * s.mt + mt) * unit_length(p, s);
-        const int64_t first_tile = first + p.lead, last = first + unit_length(p, s) - 1;
-        // CTA of a position: the last c with total c / ctas <= position
-        c0 = (int)(((first_tile + 1) * p.ctas - 1) / total);
-        c1 = (int)(((last + 1) * p.ctas - 1) / total);
-    }
     float sg[E];
     lane_signs<E>(sg, lane, p.seed);
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials are written
-    if (c0 == c1) return;
+    const TreeJoin u = reinterpret_cast<const TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x];
+    const int rows = u.rows, c0 = blockIdx.x, c1 = u.c1;
+    if (begin_row >= rows) return;
+    const int64_t total = u.total;
     const float *ml = p.part + (int64_t)2 * p.ctas * ROWS * D;
     auto there = [&](int c) { return c <= c1 && tree_begin(total, p.ctas, c) != tree_begin(total, p.ctas, c + 1); };   // no empty stretch
-    auto slot = [&](int c) { return (int64_t)(tree_begin(total, p.ctas, c) >= first ? 2 * c : 2 * c + 1); };
+    auto slot = [&](int c) { return (int64_t)(c == c0 ? u.slot0 : 2 * c); };
     for (int turn = 0; turn < turns; ++turn) {
     const int row0 = begin_row + turn * kJoinWarps * RW;
     if (row0 >= rows) break;
@@ -387,35 +419,34 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
     }
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        const int gr = mt * ROWS + row0 + i;
+        const int gr = u.mt * ROWS + row0 + i;
         if (row0 + i >= rows) break;
-        const int64_t at = ((s.row0 + gr / p.group) * p.kv_heads + h) * p.group + gr % p.group;
+        const int64_t at = (((int64_t)u.row0 + gr / p.group) * p.kv_heads + u.h) * p.group + gr % p.group;
 #pragma unroll
         for (int e = 0; e < E; ++e) store_elem<IN>(p.out, at * D + lane * E + e, acc[i][e]);
     }
     }
 }
 
-template <int IN, int D, int ROWS, int TT>
+template <int IN, int D, int ROWS>
 cudaError_t launch_tree_join(const TreeParams &p, cudaStream_t stream) {
-    const int bph = (int)(((int64_t)p.max_nodes * p.group + ROWS - 1) / ROWS);
-    const int64_t units = (int64_t)p.seqs * p.kv_heads * bph;
-    if (units > 0x7fffffffll) return cudaErrorInvalidValue;
-    // one turn per block while that leaves SMs idle; then blocks take several, so that
-    // each finds its unit once
-    constexpr int rows = kJoinWarps * join_rows(ROWS);
+    if (p.ctas == 1) return cudaSuccess;                    // every unit lies in it
+    // one turn per block while an SM holds them all (the registers of two, or three), counting
+    // the rows that there are on average; then blocks take several
+    constexpr int rows = join_warps(ROWS) * join_rows(ROWS), per_sm = ROWS >= 256 ? 2 : 3;
+    const int64_t filled = p.rows_each < ROWS ? p.rows_each : ROWS;
     int turns = 1;
-    while (turns * rows < ROWS && units * (ROWS / (turns * rows)) > 2 * (int64_t)device_sm_count()) turns *= 2;
+    while (turns * rows < filled && (p.ctas - 1) * ((filled + turns * rows - 1) / (turns * rows)) > per_sm * device_sm_count()) turns *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)units, (ROWS + turns * rows - 1) / (turns * rows));
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.gridDim = dim3((unsigned)(p.ctas - 1), (ROWS + turns * rows - 1) / (turns * rows));
+    cfg.blockDim = dim3(32 * join_warps(ROWS));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tree_join_kernel<IN, D, ROWS, TT>, p, bph, turns);
+    return cudaLaunchKernelEx(&cfg, attn_tree_join_kernel<IN, D, ROWS>, p, turns);
 }
 
 }  // namespace

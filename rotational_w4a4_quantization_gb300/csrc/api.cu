@@ -305,8 +305,8 @@ rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_str
     if (rq_status st = check_cache(c, head_dim)) return st;
     if (q_heads % kv_heads != 0 || (tree_mask && mask_stride < max_nodes)) return RQ_ERR_INVALID_ARG;
     // the row index of a page is a TMA coordinate, a row of the tree an int
-    if (pages * kv_heads * page_size > 0x7fffffffll || seqs > 0x7fffffffll || max_nodes * q_heads > 0x3fffffffll ||
-        table_width * page_size > 0x7fffff00ll)
+    if (pages * kv_heads * page_size > 0x7fffffffll || seqs > 0x7fffffffll || max_nodes > 0x3fffffffll / q_heads ||
+        table_width > 0x7fffff00ll / page_size)
         return RQ_ERR_UNSUPPORTED;
     if (rows == 0 || seqs == 0 || max_nodes == 0) return RQ_OK;
     if (table_width < 1 || !q || !block_table || !context_lens || !offsets || !out) return RQ_ERR_INVALID_ARG;

@@ -362,8 +362,9 @@ def w4a8_gemm(a_q: torch.Tensor, a_scales, w_q: torch.Tensor, w_scales, *, out_d
 
 # Small calls cost what their checks cost, so these entry points ask for a tensor's
 # properties once, compare device numbers, and take the raw stream handle.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# A torch that lacks the short forms of these has the public ones.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 
 

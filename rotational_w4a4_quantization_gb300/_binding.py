@@ -7,6 +7,7 @@ library's kernels; a non-OK status raises :class:`RQError`.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -476,7 +477,13 @@ def rope(q, k, positions: torch.Tensor, turns: torch.Tensor, *, interleaved: boo
     """Rotary positions on q and k ([tokens][heads][head_dim], strided views welcome; either may be None): the first
     2 * len(turns) elements of each head turn by positions[token] * turns, the others pass.  Returns (q', k'), new
     contiguous tensors or the pair given as `out` (which may be (q, k): in place).  ``inverse=True`` is the transposed
-    turn, the gradient of the forward one.  turns and mscale come from :func:`rope_turns`."""
+    turn, the gradient of the forward one, which backward() takes where q or k asks for a gradient (not with `out`).
+    turns and mscale come from :func:`rope_turns`."""
+    if torch.is_grad_enabled() and any(x is not None and x.requires_grad for x in (q, k)):
+        if out is not None:
+            raise ValueError("out cannot take part where gradients are asked for")
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            return _Rope.apply(q, k, positions, turns, interleaved, inverse, mscale)
     lib = _lib or load_library()
     ref = q if q is not None else k
     if ref is None:
@@ -513,6 +520,27 @@ def rope(q, k, positions: torch.Tensor, turns: torch.Tensor, *, interleaved: boo
     _call(lib.rq_rope, "rq_rope", dev, stream, *args, _DTYPES[dtype], T, D, rot, positions.data_ptr(), turns.data_ptr(),
           mscale, (RQ_ROPE_INTERLEAVED if interleaved else 0) | (RQ_ROPE_INVERSE if inverse else 0))
     return tuple(outs)
+
+
+class _Rope(torch.autograd.Function):
+    """rope of what asks for a gradient: backward is the transposed turn of the gradients that arrive."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, turns, interleaved, inverse, mscale):
+        ctx.save_for_backward(positions, turns)
+        ctx.turn = dict(interleaved=interleaved, inverse=not inverse, mscale=mscale)
+        ctx.set_materialize_grads(False)
+        out = rope(q, k, positions, turns, interleaved=interleaved, inverse=inverse, mscale=mscale)
+        ctx.mark_non_differentiable(*(o for x, o in zip((q, k), out) if x is not None and not x.requires_grad))
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk):
+        gq, gk = (g.contiguous() if g is not None and ctx.needs_input_grad[i] else None for i, g in enumerate((gq, gk)))
+        if gq is not None or gk is not None:
+            gq, gk = rope(gq, gk, *ctx.saved_tensors, **ctx.turn)
+        return gq, gk, None, None, None, None, None
 
 
 def kv_cache(pages: int, heads: int, head_dim: int, page_size: int = 64, device="cuda") -> dict:

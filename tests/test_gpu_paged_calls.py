@@ -6,10 +6,73 @@ import numpy as np
 import pytest
 import torch
 
+import paged_ref as ref
 import rotational_w4a4_quantization_gb300 as rq
 from test_gpu_paged import DEV, DTYPES, SEED, _built, _status, check_tree, dev_cache, gen, paged, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("who", ["qk", "q", "k"])
+def test_rope_carries_gradients(interleaved, dtype, who):
+    """backward() through rope: the transposed turn of what comes back, for q, k or both; also where the gradient that
+    arrives is a broadcast value, and where it passes a slice of a projection's rows."""
+    T, H, K, D, rot = 9, 4, 2, 64, 48
+    turns, m = rq.rope_turns(rot, scaling="parts", factor=4.0)
+    pos = torch.randint(0, 9000, (T,), generator=gen(630)).to(DEV)
+    rows = randn(T, (H + K) * D, seed=631, dtype=dtype).to(DEV)
+    rows.requires_grad_()
+    parts = {"q": rows[:, :H * D].view(T, H, D), "k": rows[:, H * D:].view(T, K, D)}
+    q, k = (parts[n] if n in who else parts[n].detach() for n in "qk")
+    q2, k2 = rq.rope(q, k, pos, turns, interleaved=interleaved, mscale=m)
+    assert q2.requires_grad == ("q" in who) and k2.requires_grad == ("k" in who)
+    gq, gk = (randn(T, n, D, seed=632 + n, dtype=dtype).to(DEV) for n in (H, K))
+    loss = 0.0
+    if "q" in who:
+        loss = loss + (q2 * gq).sum()
+    if "k" in who:
+        loss = loss + (k2 * gk).sum() + k2[..., rot:].sum() * 0
+    loss.backward()
+    back = rq.rope(gq, gk, pos, turns, interleaved=interleaved, inverse=True, mscale=m)
+    want = torch.zeros_like(rows)
+    if "q" in who:
+        want[:, :H * D] = back[0].view(T, -1)
+    if "k" in who:
+        want[:, H * D:] = back[1].view(T, -1)
+    assert torch.equal(rows.grad, want)
+    rows.grad = None
+    y = rq.rope(rows[:, :H * D].view(T, H, D), None, pos, turns, interleaved=interleaved, mscale=m)[0]
+    y.sum().backward()                                           # the gradient of a sum has strides of 0
+    one = rq.rope(torch.ones(T, H, D, dtype=dtype, device=DEV), None, pos, turns, interleaved=interleaved, inverse=True, mscale=m)[0]
+    assert torch.equal(rows.grad[:, :H * D], one.view(T, -1)) and (rows.grad[:, H * D:] == 0).all()
+
+
+def test_rope_gradient_by_differences():
+    """And against differences of the formula in 64 bits."""
+    T, H, D = 3, 2, 32
+    turns, _ = rq.rope_turns(D, device="cpu")
+    pos = torch.tensor([0, 5, 131071])
+    x = randn(T, H, D, seed=640).to(DEV).requires_grad_()
+    g = randn(T, H, D, seed=641).to(DEV)
+    y, _ = rq.rope(x, None, pos.to(DEV), turns.to(DEV))
+    y.backward(g)
+    x64, g64 = x.detach().cpu().double(), g.cpu().double()
+    for t, h, d in [(0, 0, 0), (1, 1, 7), (2, 0, 31), (2, 1, 16)]:
+        e = torch.zeros(T, H, D, dtype=torch.float64)
+        e[t, h, d] = 1.0                                         # the turn is linear
+        diff = ((ref.turn(x64 + e, pos, turns, False) - ref.turn(x64 - e, pos, turns, False)) * g64).sum() / 2
+        assert abs(float(diff) - float(x.grad[t, h, d])) < 2e-6 * float(g.abs().max())
+
+
+def test_rope_refuses_out_where_gradients_are_asked_for():
+    turns, _ = rq.rope_turns(32)
+    x, pos = torch.zeros(2, 1, 32, device=DEV, requires_grad=True), torch.zeros(2, dtype=torch.int64, device=DEV)
+    with pytest.raises(ValueError, match="gradients"):
+        rq.rope(x, None, pos, turns, out=(torch.empty(2, 1, 32, device=DEV), None))
+    with torch.no_grad():
+        assert not rq.rope(x, None, pos, turns, out=(torch.empty(2, 1, 32, device=DEV), None))[0].requires_grad
 
 
 def test_rotary_coefficients():

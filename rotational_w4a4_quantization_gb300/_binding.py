@@ -400,13 +400,14 @@ def _one_device(dev: int, *tensors):
 
 def _expect_heads(t, name: str):
     """A [tokens][heads][head_dim] tensor: any token and head strides, unit stride inside a head.  Returns its shape and
-    strides."""
+    token and head strides; the stride of a dimension of size one, which nothing uses, is that of contiguous rows."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or (stride[2] != 1 and shape[2] != 1):
         raise ValueError(f"{name} must be [tokens][heads][head_dim] with unit stride in the last dimension")
     if t.dtype not in _FLOATS:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    return shape, stride
+    H, D = shape[1], shape[2]
+    return shape, (stride[0] if shape[0] != 1 else H * D, stride[1] if H != 1 else D)
 
 
 def _expect_same(t, name: str, dtype, tokens: int):

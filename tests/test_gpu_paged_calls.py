@@ -13,6 +13,28 @@ from test_gpu_paged import DEV, DTYPES, SEED, _built, _status, check_tree, dev_c
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_strides_of_dimensions_of_size_one(dtype):
+    """One token whose row is an odd slice, one head at an odd stride: strides that nothing uses are not asked of."""
+    D, page = 64, 16
+    rows = randn(3, 3 * D + 5, seed=620, dtype=dtype).to(DEV)
+    odd = lambda x: x.as_strided(x.shape, [s if n > 1 else s + 5 for n, s in zip(x.shape[:2], x.stride()[:2])] + [1])
+    k1, v1 = (rows[0, i * D:(i + 1) * D].view(1, 1, D) for i in (0, 1))
+    cache, plain = rq.kv_cache(2, 1, D, page), rq.kv_cache(2, 1, D, page)
+    slot = torch.tensor([5], device=DEV)
+    rq.kv_append(odd(k1), odd(v1), cache, slot, SEED)
+    rq.kv_append(k1.contiguous(), v1.contiguous(), plain, slot, SEED)
+    assert all(torch.equal(cache[x], plain[x]) for x in cache)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    got = rq.attn_tree(odd(k1), cache, table, i32(6), i32(0, 1), SEED)
+    assert torch.equal(got, rq.attn_tree(k1.contiguous(), cache, table, i32(6), i32(0, 1), SEED))
+    turns, _ = rq.rope_turns(D)
+    pos = torch.tensor([77], device=DEV)
+    for a, b in zip(rq.rope(odd(k1), odd(v1), pos, turns), rq.rope(k1.contiguous(), v1.contiguous(), pos, turns)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("who", ["qk", "q", "k"])

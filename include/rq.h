@@ -413,7 +413,8 @@ rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, cons
  *   q        [rows][q_heads][head_dim] of dtype, strides in elements (16-byte
  *            multiples); q head h reads KV head h / (q_heads / kv_heads).
  *   out      [rows][q_heads][head_dim] contiguous, of dtype.
- *   tree_mask [rows][mask_stride] bytes, mask_stride >= max_nodes, or NULL.
+ *   tree_mask [rows][mask_stride] bytes, mask_stride >= max_nodes (0: one row of max_nodes bytes
+ *            for every node), or NULL.
  *   workspace, workspace_bytes: scratch of the call, at least
  *            rq_attn_tree_workspace(head_dim) bytes; nothing is kept in it between calls.
  *   flags    RQ_SIGNS_FIRST (as given to rq_kv_append), RQ_ATTN_ROTATED_OUT.

@@ -303,7 +303,7 @@ rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_str
     const rq::PagedCache c{const_cast<uint8_t *>(kq), const_cast<float *>(ks), const_cast<uint8_t *>(vq),
                            const_cast<float *>(vs), pages, kv_heads, page_size};
     if (rq_status st = check_cache(c, head_dim)) return st;
-    if (q_heads % kv_heads != 0 || (tree_mask && mask_stride < max_nodes)) return RQ_ERR_INVALID_ARG;
+    if (q_heads % kv_heads != 0 || (tree_mask && mask_stride != 0 && mask_stride < max_nodes)) return RQ_ERR_INVALID_ARG;
     // the row index of a page is a TMA coordinate, a row of the tree an int
     if (pages * kv_heads * page_size > 0x7fffffffll || seqs > 0x7fffffffll || max_nodes > 0x3fffffffll / q_heads ||
         table_width > 0x7fffff00ll / page_size)

@@ -14,6 +14,22 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("G,n", [(4, 3), (4, 12)])
+def test_one_mask_row_for_all_nodes(dtype, G, n):
+    B, H, D = 50, 2, 64
+    contexts, counts = [150 + b for b in range(B)], [n] * B
+    cache, table = paged([c + n for c in contexts], H, 32, D, 610)
+    one = torch.zeros(1, n, dtype=torch.bool)
+    one[0, ::2] = True
+    q = randn(B * n, H * G, D, seed=611, dtype=dtype)
+    want = check_tree(q, cache, table, contexts, counts, mask=one.repeat(B * n, 1))
+    offsets = torch.arange(0, B * n + 1, n, dtype=torch.int32, device=DEV)
+    got = rq.attn_tree(q.to(DEV), dev_cache(cache), table.to(DEV), torch.tensor(contexts, dtype=torch.int32, device=DEV),
+                       offsets, SEED, 1, tree_mask=one.to(DEV).expand(B * n, n))
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_strides_of_dimensions_of_size_one(dtype):
     """One token whose row is an odd slice, one head at an odd stride: strides that nothing uses are not asked of."""
     D, page = 64, 16

@@ -680,10 +680,14 @@ cudaError_t launch_tree_in(TreeParams &p, int64_t d, const CUtensorMap &mk, cons
 }  // namespace
 
 int64_t attn_tree_workspace(int64_t head_dim) {
-    const int64_t ctas = 2 * (int64_t)device_sm_count();
-    const int64_t small = tree_join_at((int)ctas, 16, (int)head_dim) * (int64_t)sizeof(float) + 2 * ctas * (int64_t)sizeof(TreeJoin);
-    const int64_t wide = attn_tree_tc_workspace(head_dim);
-    return small > wide ? small : wide;
+    const int sms = device_sm_count();
+    int64_t most = attn_tree_tc_workspace(head_dim);
+    for (int rows = 8; rows <= 16; rows *= 2) {
+        const int ctas = blocks_per_sm(rows, head_dim) * sms;
+        const int64_t bytes = tree_join_at(ctas, rows, (int)head_dim) * (int64_t)sizeof(float) + ctas * (int64_t)sizeof(TreeJoin);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {

@@ -1080,6 +1080,7 @@ bool attn_tree_tc_supported(const TreeCall &c) {
 }
 
 int64_t attn_tree_tc_workspace(int64_t head_dim) {
+    if (head_dim != 64 && head_dim != 128) return 0;
     const int sms = device_sm_count();
     return tree_join_at(sms, 256, (int)head_dim) * (int64_t)sizeof(float) + sms * (int64_t)sizeof(TreeJoin);
 }

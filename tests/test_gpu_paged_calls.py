@@ -13,6 +13,15 @@ from test_gpu_paged import DEV, DTYPES, SEED, _built, _status, check_tree, dev_c
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_workspace_is_that_of_the_kernels_that_run(D):
+    """Heads of 32 and 256 elements have no blocks of 128 rows: two partials of 16 rows a block, three blocks to an SM."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    few = 2 * 3 * sms * 16 * (D + 2) * 4 + 64 * 4 * sms
+    many = 2 * sms * 256 * (D + 2) * 4 + 64 * sms
+    assert 0 < rq.attn_tree_workspace(D) <= (few if D in (32, 256) else max(few, many))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("G,n", [(4, 3), (4, 12)])
 def test_one_mask_row_for_all_nodes(dtype, G, n):

@@ -109,7 +109,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
     s.row0 = o0;
     s.n = o0 < 0 ? 0 : (int)max((int64_t)0, min(o1 - o0, (int64_t)p.max_nodes));
     const int64_t cap = p.width << p.log_page;
-    s.ctx = max(0, p.contexts[b]);
+    s.ctx = (int)min((int64_t)max(0, p.contexts[b]), cap);         // what lies past the table is not seen
     s.len = (int)min((int64_t)s.ctx + s.n, cap);
     s.mt = (s.n * p.group + ROWS - 1) / ROWS;
     s.nt = s.mt ? (s.len + TT - 1) / TT : 0;

@@ -22,6 +22,16 @@ def test_workspace_is_that_of_the_kernels_that_run(D):
     assert 0 < rq.attn_tree_workspace(D) <= (few if D in (32, 256) else max(few, many))
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_contexts_far_past_the_table(n):
+    """What lies past the table is not seen, also where the number of tokens is int32's last."""
+    H, D, page = 2, 64, 16
+    cache, table = paged([200] * 60, H, page, D, 600)
+    q = randn(60 * n, 4 * H, D, seed=601, dtype=torch.bfloat16)
+    a, b = (check_tree(q, cache, table, [c] * 60, [n] * 60) for c in (table.shape[1] * page, 2**31 - 1))
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("G,n", [(4, 3), (4, 12)])
 def test_one_mask_row_for_all_nodes(dtype, G, n):

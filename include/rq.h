@@ -368,7 +368,8 @@ rq_status rq_rope(const void *q, int64_t q_heads, int64_t q_token_stride, int64_
  *   are skipped.  No two tokens may name one slot.  With turns, the keys first take
  *   their rotary positions as in rq_rope, without leaving fp32 (rot_dim a multiple of
  *   16, or of 8 with RQ_ROPE_INTERLEAVED).  A row that holds a NaN or an infinity gets
- *   scale NaN.
+ *   scale NaN, and so does one whose turn or sums of head_dim elements (before they are
+ *   divided by sqrt(head_dim)) pass fp32's range.
  *   flags    RQ_SIGNS_FIRST, RQ_ROPE_INTERLEAVED.
  */
 rq_status rq_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,

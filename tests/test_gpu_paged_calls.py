@@ -154,3 +154,17 @@ def test_rotary_coefficients():
     for have, want, other in ((got[:, :D // 2], cos, sin), (got[:, D // 2:], sin, cos)):
         err = np.abs(have - want)
         assert (err <= 2.4e-8 * np.abs(other) + ulp(want) + 1e-15).all(), float((err - 2.4e-8 * np.abs(other) - ulp(want)).max())
+
+
+def test_append_rows_near_the_end_of_fp32():
+    """A finite row whose sums pass fp32's range before they are divided by sqrt(D) has scale NaN, as one that holds an
+    infinity; a row whose sums stay inside is kept."""
+    H, D, page = 1, 64, 16
+    k = torch.full((4, H, D), 1e38)
+    k[1] = 3e38 / D / 2
+    k[2] = torch.where(torch.arange(D) % 2 == 0, 3e38, -3e38)
+    cache = rq.kv_cache(1, H, D, page)
+    rq.kv_append(k.to(DEV), k.to(DEV), cache, torch.arange(4, device=DEV), SEED, 1)
+    for n in "kv":
+        s = cache[n + "s"][0, 0, :4].cpu()
+        assert torch.isnan(s[[0, 2, 3]]).all() and torch.isfinite(s[1])

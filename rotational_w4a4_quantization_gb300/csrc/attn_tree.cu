@@ -38,7 +38,8 @@
 //    are exact in either.  The second part of w is kept 2^11 up, so that small weights have
 //    22 bits too.  What the tensor cores add to an accumulator is not rounded to nearest:
 //    a score 17 to 26 bits above the others', added up by 16 of them, had its weight 5e-6
-//    to 2e-5 off.  So each step of 16 starts from 0 and is added to the sums outside.  fp16 queries split q~ alone: their outputs resolve its rounding to 11
+//    to 2e-5 off.  So each step of 16 starts from 0 and is added to the sums outside, and
+//    the scale, with the rotation's 1/sqrt(D), has two fp32 parts.  fp16 queries split q~ alone: their outputs resolve its rounding to 11
 //    bits (4.6e-4 against 2.5e-4 of an output).
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
@@ -74,7 +75,7 @@ struct MSmem {
     alignas(16) uint32_t q[HQ][D / 16][32][ROWS / 4];  // q~ as fragments: k step, lane, register
     float acc[2][ROWS][D + 4];                       // the warps' sums, joined two by two
     float ref[kCWarps][ROWS], sum[kCWarps][ROWS];
-    float2 rfac[ROWS];                               // a, b
+    float2 rfac[ROWS];                               // a, b; fp32: a in two parts
     TreeLine line;
     alignas(8) uint64_t full[kStages], empty[kStages];
     uint32_t valid[kStages];
@@ -239,7 +240,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         float top[RW], qsum[RW];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-            warp_rotate<E>(qv[i], sg, lane, signs_first, inv_sqrt_dim<D>());
+            warp_rotate<E>(qv[i], sg, lane, signs_first, kOffset ? inv_sqrt_dim<D>() : 1.f);
             top[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) top[i] = fmaxf(top[i], fabsf(qv[i][e]));
@@ -254,7 +255,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             // 2^ex > top, within what a float's exponent holds
             const int ex = max(-100, min((int)((__float_as_uint(top[i]) >> 23) & 255u) - 126, 100));
             const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-            top[i] = up * p.score_scale;
+            top[i] = kOffset ? up * p.score_scale : up;
             qsum[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -285,7 +286,8 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         if (lane == 0) {
 #pragma unroll
             for (int i = 0; i < RW; ++i)
-                s.rfac[i * kCWarps + warp] = kOffset ? make_float2(top[i] * 16777216.f, -8.f * qsum[i] * top[i]) : make_float2(top[i], 0.f);
+                s.rfac[i * kCWarps + warp] = kOffset ? make_float2(top[i] * 16777216.f, -8.f * qsum[i] * top[i])
+                                                               : make_float2(top[i] * p.full_scale.x, top[i] * p.full_scale.y);
         }
         cta_sync();
 
@@ -341,8 +343,10 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         for (int i = 0; i < 2; ++i) {
                             float own[kShort ? NS : 1][4];              // this step's sums (kShort)
 #pragma unroll
-                            for (int hv = 0; hv < HQ; ++hv) {
-                                const bool begins = hv == 0 && (kShort || (part == 0 && wd == 0 && i == 0));
+                            for (int at_hv = 0; at_hv < HQ; ++at_hv) {
+                                // kShort: the small part first, so that one addition meets the large one
+                                const int hv = kShort ? HQ - 1 - at_hv : at_hv;
+                                const bool begins = at_hv == 0 && (kShort || (part == 0 && wd == 0 && i == 0));
                                 auto add = [&](int t, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
                                     float(&to)[4] = kShort ? own[t % (kShort ? NS : 1)] : sc[t];
                                     if (begins) mma16816_first(to, a, b0, b1);
@@ -392,7 +396,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 rs = second(k) ? rs1 : rs0;
-                        sc[t][k] = fmaf(fmaf(sc[t][k], rs.x, rs.y), later(k) ? kk.y : kk.x, second(k) ? -z1 : -z0);
+                        sc[t][k] = fmaf(fmaf(sc[t][k], rs.x, kOffset ? rs.y : sc[t][k] * rs.y), later(k) ? kk.y : kk.x, second(k) ? -z1 : -z0);
                     }
                 }
                 const uint32_t valid = s.valid[st];

@@ -11,6 +11,8 @@
 
 #include "paged_device.cuh"
 
+#include <cmath>
+
 namespace rq {
 namespace {
 
@@ -26,6 +28,7 @@ struct TreeParams {
     uint64_t seed;
     uint32_t flags;
     float score_scale;                  // softmax_scale * log2(e)
+    float2 full_scale;                  // that by 1/sqrt(D), in two parts
     void *out;
     float *part;                        // [2 G][ROWS][D] fp32, then [2 G][ROWS][2] (reference, sum), then [G] TreeJoin
     int64_t rows_each;                  // query rows per KV head and sequence, on average
@@ -67,6 +70,9 @@ inline bool tree_params(const TreeCall &c, TreeParams &p) {
     p.seed = c.seed;
     p.flags = c.flags;
     p.score_scale = (float)((double)c.softmax_scale * 1.4426950408889634);
+    const double full = (double)c.softmax_scale * 1.4426950408889634 / sqrt((double)c.head_dim);
+    p.full_scale.x = (float)full;
+    p.full_scale.y = (float)(full - (double)p.full_scale.x);
     p.out = c.out;
     p.part = static_cast<float *>(c.workspace);
     p.err = error_word_device_ptr();

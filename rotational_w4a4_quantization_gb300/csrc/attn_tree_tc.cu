@@ -210,15 +210,16 @@ __device__ __forceinline__ int tile_exponent(const float4 &x, int least, int non
                                                             max(__float_as_uint(x.z), __float_as_uint(x.w))));
     return top == 0 ? none : max(least, min((int)((top >> 23) & 255u) - 126, 100));
 }
-// Each of four scales is 0 or within 2^(bits + 1) of 2^e, and finite.
-__device__ __forceinline__ bool of_a_kind(const float4 &x, int e, int bits) {
+// The first n of four scales are within 2^(bits + 1) of 2^e, and finite, or 0 where that may be.
+__device__ __forceinline__ bool of_a_kind(const float4 &x, int n, int e, int bits, bool zeros) {
     const float lo = __uint_as_float((uint32_t)(127 + max(e - 1 - bits, -120)) << 23), hi = __uint_as_float((uint32_t)(127 + e) << 23);
-    auto ok = [&](float v) { return v == 0.f || (v >= lo && v <= hi); };
-    return ok(x.x) && ok(x.y) && ok(x.z) && ok(x.w);
+    auto ok = [&](float v, int i) { return i >= n || (v >= lo && v <= hi) || (zeros && v == 0.f); };
+    return ok(x.x, 0) && ok(x.y, 1) && ok(x.z, 2) && ok(x.w, 3);
 }
 // How far apart a tile's scales may lie to share a unit: the products of keys keep 11 bits in
 // fp16; values may cost the weights' range that much, as a row's reference takes a tile's
-// largest score and largest value scale for one token's.
+// largest score and largest value scale for one token's.  So a value row of zeros is not of
+// a kind with others either: it may be the one with the score.
 constexpr int kKeyBits = 12, kValueBits = 8;
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // |e| <= 126
 __device__ __forceinline__ uint4 ld_once(const void *p) {
@@ -501,15 +502,16 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             if (T <= 0) continue;
             // lane l: tokens 4 l .. 4 l + 3 of a tile, the next tile's loaded ahead
             float4 nk, nv;
-            bool nthere;
+            int nthere;
             auto load = [&](int k) {
                 const int64_t row = k < T ? tree_row(p, w, (w.t0 + k) * kTcTT + 4 * lane) : -1;
-                nthere = row >= 0;
+                nthere = 0;
                 nk = nv = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (nthere) {
+                if (row >= 0) {
                     nk = *reinterpret_cast<const float4 *>(p.ks + row);
                     nv = *reinterpret_cast<const float4 *>(p.vs + row);
                     const int left = w.s.len - ((w.t0 + k) * kTcTT + 4 * lane);   // past the sequence: none
+                    nthere = min(left, 4);
                     if (left < 4) {
                         nk = make_float4(nk.x, left > 1 ? nk.y : 0.f, left > 2 ? nk.z : 0.f, 0.f);
                         nv = make_float4(nv.x, left > 1 ? nv.y : 0.f, left > 2 ? nv.z : 0.f, 0.f);
@@ -520,13 +522,15 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             for (int k = 0; k < T; ++k, ++sc) {
                 const uint32_t scs = sc % kSc;
                 const float4 ck = nk, cv = nv;
-                const bool there = nthere;
+                const int there = nthere;
                 load(k + 1);
-                const uint32_t quads = __ballot_sync(0xffffffffu, there);
+                const uint32_t quads = __ballot_sync(0xffffffffu, there > 0);
                 // a tile of zero values moves no row's reference: its unit is the least
                 const int ek = FOLD ? tile_exponent(ck, -100, 0) : 0, ev = tile_exponent(cv, (int)kLeastValue, (int)kLeastValue);
                 // scales that are not of a kind stay out of the operands and the tile's unit
-                const bool exact = __any_sync(0xffffffffu, !((!FOLD || of_a_kind(ck, ek, kKeyBits)) && of_a_kind(cv, ev, kValueBits)));
+                const bool nothing = __all_sync(0xffffffffu, cv.x == 0.f && cv.y == 0.f && cv.z == 0.f && cv.w == 0.f);
+                const bool exact = __any_sync(0xffffffffu, !((!FOLD || of_a_kind(ck, there, ek, kKeyBits, true)) &&
+                                                             of_a_kind(cv, there, ev, kValueBits, nothing)));
                 uint32_t chunks = 0;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) chunks |= ((quads >> (4 * c)) & 1) << c;

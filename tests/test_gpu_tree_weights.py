@@ -75,7 +75,7 @@ def put(cache, table, page, at, name, codes=None, scale=None):
 
 @pytest.mark.parametrize("G,n", ROWS)
 @pytest.mark.parametrize("dtype,bits,value", [(d, *w) for d in DTYPES for w in ((10, 1e-3), (14, 1e-3), (17, 0.0), (24, 0.0), (26, 0.0))]
-                         + [(torch.float32, 45, 0.0)])
+                         + [(d, 45, 0.0) for d in DTYPES])
 @pytest.mark.parametrize("first", [True, False])
 def test_one_token_holds_the_weight(G, n, dtype, bits, value, first):
     """A token whose value row is small or nothing, `bits` bits of weight above each of 32k others, whose values have a

@@ -1075,9 +1075,10 @@ cudaError_t launch_tc(TreeParams &p, cudaStream_t stream) {
 
 // Blocks of 128 rows pay a long start and end per unit, blocks of 16 rows more per token and
 // row.  Measured (8 KV heads x 128, cold caches), here and there: 16 sequences of 4k, bf16,
-// 32 rows 82 and 70 us, 48 rows 86 and 94, 64 rows 88 and 117; 64 of 300, 32 rows 70 and 63,
-// 48 rows 74 and 85; fp16, 4 of 32k, 32 rows 123 and 115, 48 rows 123 and 160; bf16, 2 of
-// 512, 64 rows 27 and 25, as they have fewer tiles than SMs.
+// 32 rows 81 and 71 us, 48 rows 81 and 94, 64 rows 84 and 116; 64 of 300, 32 rows 66 and 63,
+// 48 rows 68 and 84; fp16, 4 of 32k, 32 rows 120 and 115, 48 rows 122 and 161.  Where there
+// are fewer tiles than SMs either does (2 of 512, 64 rows: 23 and 24).  The rows are those
+// that there are on average, the tiles as many as the table can name.
 bool attn_tree_tc_supported(const TreeCall &c) {
     const int64_t rows = tree_rows(c), tiles = tree_tiles(c, 128, kTcTT);
     return c.in_type != IN_F32 && (c.head_dim == 64 || c.head_dim == 128) && rows > 32 && tiles > device_sm_count();

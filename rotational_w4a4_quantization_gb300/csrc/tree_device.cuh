@@ -134,11 +134,12 @@ struct TreeLine {
 
 // What a unit costs a CTA beside its tiles, in tiles: q~, the first tile's latency, the
 // masked tiles at its end and its output.  With tiles alone CTAs that meet several short
-// units end last.  Measured: 0, 2, 4, 6 and 9 tiles give 97, 92, 90, 88 and 88 us for 16
-// ragged sequences of up to 4k (128 rows, fp16), 136, 133, 131, 130 and 131 us for 64 of up
-// to 8k (8 rows, bf16).  Less where CTAs have few tiles each: there the lead would leave
-// some of them without any (one sequence of 512: 18.5 us without, 20.5 with 6).
-__device__ __forceinline__ int tree_lead(int64_t tiles, int ctas) { return (int)(tiles / ctas < 12 ? tiles / ctas / 2 : 6); }
+// units end last.  Measured: 0, 2, 4, 6 and 9 tiles give 87, 80, 77, 79 and 78 us for 16
+// ragged sequences of up to 4k (128 rows, fp16), 105, 104, 103, 105 and 106 us for 64 of up
+// to 8k (8 rows, bf16); 2 of 256k take 138 or 139 with any.  Less where CTAs have few tiles
+// each: there the lead would leave some of them without any (one sequence of 512: 16 us
+// without, 18 with 9).
+__device__ __forceinline__ int tree_lead(int64_t tiles, int ctas) { return (int)(tiles / ctas < 8 ? tiles / ctas / 2 : 4); }
 
 // A unit's length in the line: its tiles, and before them its lead.
 __device__ __forceinline__ int64_t unit_length(int lead, const TreeSeq &s) { return s.nt ? s.nt + lead : 0; }

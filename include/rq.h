@@ -402,14 +402,22 @@ rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, cons
  *   offsets[b] nodes (<= max_nodes; more are ignored), whose keys and values are in the
  *   cache at the next n places.  Node i sees every token of the context and the nodes j
  *   with tree_mask[offsets[b] + i][j] != 0 (itself only if the mask says so); without a
- *   mask, the nodes j <= i.
- *     out = softmax(softmax_scale (q R) . k^) v^ R^T
- *   in fp32, with q~ and the weights rounded to fp16 on the way into the tensor cores
- *   (fp32 queries: both, fp16 queries: q~ split into two fp16 parts), and with bf16
- *   queries of more than 32 rows per KV head k^ and v^ as well; a row that sees nothing
- *   is 0.  Tokens on
- *   a page number outside the cache, or past the table, are not seen.  What a cache row
- *   that a query does not see holds (NaN and infinite scales too) does not reach it.
+ *   mask, the nodes j <= i.  max_nodes and table_width are bounds: the time goes by the
+ *   rows and tokens that there are.
+ *     out = softmax(softmax_scale (q R) . k^) v^ R^T,   any finite softmax_scale
+ *   with the softmax's sums in fp32.  q~ and a token's weight times its value scale are
+ *   rounded to fp16 on the way into the tensor cores, each by 2^-12 of itself at most (fp32
+ *   queries: both, fp16 queries: q~ in two fp16 parts); with bf16 queries of more than 32
+ *   rows per KV head the keys and values times their scales are, too.  Weights 2^-23 of a
+ *   row's largest keep those bits, those below 2^-34 of it may vanish; on the blocks for
+ *   more than 32 rows up to 2^8 of that room may go to value scales that differ within 128
+ *   tokens.  Sums of more than 2^16 tokens in one thread block lose up to 1e-4 (2^18: 6e-4
+ *   with fp16, 1.6e-3 with bf16 queries) to the tensor cores' additions, which are not
+ *   rounded to nearest; fp32 queries add outside them.
+ *   A row that sees nothing is 0.  Tokens on a page number outside the cache, or past the
+ *   table, are not seen.  What a cache row that a query does not see holds (NaN and
+ *   infinite scales too) does not reach it.  Rows of q that belong to no sequence, or lie
+ *   past max_nodes of theirs, leave their rows of out as they are.
  *
  *   q        [rows][q_heads][head_dim] of dtype, strides in elements (16-byte
  *            multiples); q head h reads KV head h / (q_heads / kv_heads).

@@ -579,7 +579,7 @@ def kv_append(k, v, cache: dict, slots: torch.Tensor, seed: int, flags: int = RQ
               turns=None, interleaved: bool = False, mscale: float = 1.0, stream=None) -> dict:
     """Quantise k and v ([tokens][heads][head_dim], strided views welcome) into the paged cache: row t goes to slot
     slots[t] = page * page_size + row (int64; outside the cache: skipped).  With positions and turns the keys take
-    their rotary positions on the way (see :func:`rope`).  Returns the cache."""
+    their rotary positions on the way (see :func:`rope`).  Returns the cache, which carries no gradient."""
     lib = _lib or load_library()
     kshape, kst = _expect_heads(k, "k")
     T, H, D = kshape
@@ -655,7 +655,8 @@ def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_l
     cache at places context_lens[b], context_lens[b] + 1, ...  A node sees the context and the nodes that its row of
     tree_mask (bool [rows][width], width >= the largest tree) names; without a mask, itself and those before it.
     max_nodes bounds the nodes of a sequence (default: the mask's width, or the number of rows).  One node per sequence
-    is a plain decode step.  Returns [rows][q_heads][head_dim] of q's dtype; rows that see nothing are 0."""
+    is a plain decode step.  Returns [rows][q_heads][head_dim] of q's dtype; rows that see nothing are 0, rows of no
+    sequence are not written.  The result carries no gradient."""
     lib = _lib or load_library()
     qshape, qs = _expect_heads(q, "q")
     N, Hq, D = qshape

@@ -39,14 +39,15 @@
 //    22 bits too.  What the tensor cores add to an accumulator is not rounded to nearest:
 //    a score 17 to 26 bits above the others', added up by 16 of them, had its weight 5e-6
 //    to 2e-5 off.  So each step of 16 starts from 0 and is added to the sums outside, and
-//    the scale, with the rotation's 1/sqrt(D), has two fp32 parts.  fp16 queries split q~ alone: their outputs resolve its rounding to 11
-//    bits (4.6e-4 against 2.5e-4 of an output).
+//    the scale, with the rotation's 1/sqrt(D), has two fp32 parts.  fp16 queries split q~
+//    alone: their outputs resolve its rounding to 11 bits (4.6e-4 against 2.5e-4 of an
+//    output).
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
-// heads, one node: 104 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
-// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 137
-// us, 4.2 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
-// memory waits.  One sequence of 514 tokens takes the 15 us of its latencies and 8 of the
+// heads, one node: 103 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
+// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 138
+// us, 4.1 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
+// memory waits.  One sequence of 514 tokens takes the 15 us of its latencies and 7 of the
 // join, which overlap in part.
 #include "rq.h"
 #include "rq_internal.h"

@@ -28,16 +28,16 @@
 // Scales.  With bf16 queries they are folded into the operands: k^ and v^ as fp16(code *
 // scale), scales relative to a power of two per tile, one rounding (the scale enters in
 // two fp16 parts).  The softmax then reads nothing but its scores: broadcasting scales from
-// shared memory
-// costs 4 cycles per 16 bytes and warp, and bound the kernel (8 warps x 64 loads per
-// tile; measured 2,150 cycles per tile for that softmax alone, against 2,048 of MMAs).
+// shared memory costs 4 cycles per 16 bytes and warp, and bound the kernel (8 warps x 64
+// loads per tile; measured 2,150 cycles per tile for that softmax alone, against 2,048 of
+// MMAs).
 // A tile keeps exact codes if a scale of it is not finite or they lie too far apart (values
 // by more than 2^8, keys 2^12), and applies them to scores and weights, so that a large
 // scale costs the others no bits and what an unseen token holds (a NaN scale, say) reaches
-// nobody.  fp16 queries, whose outputs resolve an
-// 11-bit rounding of q~, k^ and v^, keep q~ in two fp16 parts (Q K^T runs twice) and the
-// scales out of the operands; the weights with vs in them round once (16 sequences of up
-// to 4k: outputs 2.9e-4 off; with the scales of V folded 3.3e-4, and 2 us slower).
+// nobody.  fp16 queries, whose outputs resolve an 11-bit rounding of q~, k^ and v^, keep q~
+// in two fp16 parts (Q K^T runs twice) and the scales out of the operands; the weights with
+// vs in them round once (16 sequences of up to 4k: outputs 3.0e-4 off; with the scales of V
+// folded 3.3e-4, and 2 us slower).
 //
 // Weights: P = 2^(s - M + ev) (2^ev the tile's unit of vs) is what the MMA sees, rounded
 // to fp16; the sum l adds 2^(s - M) in fp32.  O / l does not depend on M, so M only has
@@ -46,16 +46,17 @@
 // arrival that delivers P, when no MMA touches it).  fp16 keeps 11 bits down to 2^-14, so
 // of tokens at least 23 bits below the largest, and something down to 2^-25.
 //
-// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 422 us, 0.70
+// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 424 us, 0.69
 // PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 5,000 cycles
 // of which the MMAs run 2,048.  The softmax bounds it: 1,800 cycles for half a tile, most
 // of it latency of tensor-memory loads, exponentials and the exchange between a row's
 // threads (issue slots are two fifths full), and 800 from one half to the next.  Slower
-// were: one pass over the scores with the old reference, weights kept back in registers
-// (431 us); scores kept in registers (457, spills); 32 columns a load (433); buffers of 64
-// columns (423, as Q K^T with N = 64 takes 48 cycles for 32's work).  64 rows (fp16, 16
-// sequences of up to 4k): 76 us, where the bytes take 9: starts and ends of units; with a
-// buffer per softmax team, 128 columns to a thread, 86 (and the 256 rows 404).
+// were, with one limit of 96 registers for all warps: one pass over the scores with the old
+// reference, weights kept back in registers (431 us); scores kept in registers (457,
+// spills); 32 columns a load (433); buffers of 64 columns (423, as Q K^T with N = 64 takes
+// 48 cycles for 32's work).  64 rows (fp16, 16 sequences of up to 4k): 78 us, where the
+// bytes take 9: starts and ends of units; with a buffer per softmax team, 128 columns to a
+// thread, 86 (and the 256 rows 404).
 #include "rq.h"
 #include "rq_internal.h"
 #include "tree_device.cuh"

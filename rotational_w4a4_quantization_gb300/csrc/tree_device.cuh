@@ -5,8 +5,9 @@
 // tiles of TT.  All units form one line, each with its tiles and before them a lead
 // that stands for its fixed cost, and CTA c of G takes the stretch [c T / G,
 // (c + 1) T / G): CTAs end together whatever the lengths, long sequences spread over
-// many of them, and a unit that lies inside one stretch is finished there.  A unit that spans CTAs leaves one
-// partial per CTA: slot 2c for the unit the stretch begins in, 2c + 1 for the last.
+// many of them, and a unit that lies inside one stretch is finished there.  A unit that
+// spans CTAs leaves one partial per CTA: slot 2c for the unit the stretch begins in, 2c + 1
+// for the last.
 #pragma once
 
 #include "paged_device.cuh"

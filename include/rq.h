@@ -411,9 +411,9 @@ rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, cons
  *   rows per KV head the keys and values times their scales are, too.  Weights 2^-23 of a
  *   row's largest keep those bits, those below 2^-34 of it may vanish; on the blocks for
  *   more than 32 rows up to 2^8 of that room may go to value scales that differ within 128
- *   tokens.  Sums of more than 2^16 tokens in one thread block lose up to 1e-4 (2^18: 6e-4
- *   with fp16, 1.6e-3 with bf16 queries) to the tensor cores' additions, which are not
- *   rounded to nearest; fp32 queries add outside them.
+ *   tokens.  The tensor cores, whose additions are not rounded to nearest, add up 2^15
+ *   tokens at most, where values of a common sign lose less than 1e-4; fp32 queries add
+ *   outside them.
  *   A row that sees nothing is 0.  Tokens on a page number outside the cache, or past the
  *   table, are not seen.  What a cache row that a query does not see holds (NaN and
  *   infinite scales too) does not reach it.  Rows of q that belong to no sequence, or lie

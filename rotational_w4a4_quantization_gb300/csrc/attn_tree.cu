@@ -168,9 +168,9 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         const int bt = min(kTT, 1 << p.log_page), pieces = kTT / bt;
         TreeJoin join{};
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<ROWS, kTT>(p, s.line, at, end);
+            const TreeWork w = tree_work<ROWS, kTT>(p, s.line, at, begin, end);
             at += w.used;
-            tree_note<ROWS>(p, s.line, w, begin, join);
+            tree_note<ROWS>(p, s.line, w, begin, end, join);
             if (w.t1 <= w.t0) continue;
             auto page_of = [&](int tile) -> int64_t {
                 const int t = tile * kTT + lane * bt;
@@ -220,7 +220,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     const bool signs_first = (p.flags & RQ_SIGNS_FIRST) != 0;
 
     for (int64_t at = begin; at < end;) {
-        const TreeWork w = tree_work<ROWS, kTT>(p, s.line, at, end);
+        const TreeWork w = tree_work<ROWS, kTT>(p, s.line, at, begin, end);
         at += w.used;
         if (w.t1 <= w.t0) continue;
         const int rows = min(ROWS, w.s.n * p.group - w.mt * ROWS);
@@ -627,15 +627,27 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         }
         // ---- rows out: finished, or as a partial ----
         float *part = p.part, *ml = p.part + (int64_t)2 * p.ctas * ROWS * D;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (at - w.used == begin ? 0 : 1);
+        const int64_t slot = tree_slot(w, begin);
         float vsum[RW];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
             const int r = i * kCWarps + warp;
             joined(r, top[i], vsum[i]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) qv[i][e] = s.acc[0][r][lane * E + e] + s.acc[1][r][lane * E + e];
+            if (!w.begins) {                                // the pieces before this one
+                const float2 x = *reinterpret_cast<const float2 *>(ml + (slot * ROWS + r) * 2);
+                if (r < rows && x.x != -INFINITY) {
+                    const float t = fmaxf(top[i], x.x), f = ex2(x.x - t), g0 = top[i] == -INFINITY ? 0.f : ex2(top[i] - t);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) qv[i][e] = (g0 == 0.f ? 0.f : qv[i][e] * g0) + part[(slot * ROWS + r) * D + lane * E + e] * f;
+                    vsum[i] = (g0 == 0.f ? 0.f : vsum[i] * g0) + x.y * f;
+                    top[i] = t;
+                }
+            }
             const float il = w.whole ? (vsum[i] == 0.f ? 0.f : 1.f / vsum[i]) : 1.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) qv[i][e] = (s.acc[0][r][lane * E + e] + s.acc[1][r][lane * E + e]) * il;
+            for (int e = 0; e < E; ++e) qv[i][e] *= il;
         }
         if (w.whole && !(p.flags & RQ_ATTN_ROTATED_OUT)) {
 #pragma unroll

@@ -496,10 +496,10 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         uint32_t sc = 0;
         TreeJoin join{};
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, end);
+            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, begin, end);
             const int T = w.t1 - w.t0;
             at += w.used;
-            tree_note<ROWS>(p, s.line, w, begin, join);
+            tree_note<ROWS>(p, s.line, w, begin, end, join);
             if (T <= 0) continue;
             // lane l: tokens 4 l .. 4 l + 3 of a tile, the next tile's loaded ahead
             float4 nk, nv;
@@ -562,7 +562,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         const uint64_t dv = op_desc(t_smem(s.op[0]), S::PANEL);
         bool ok = true;
         for (int64_t at = begin; at < end && ok; ++unit) {
-            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, end);
+            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, begin, end);
             const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), J = NT * T;
             at += w.used;
             if (T <= 0) continue;
@@ -628,7 +628,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         const TreeWork &w = s.work[team];
         for (int64_t at = begin; at < end;) {
             if (quarter == 0) {
-                const TreeWork x = tree_work<ROWS, kTcTT>(p, s.line, at, end);
+                const TreeWork x = tree_work<ROWS, kTcTT>(p, s.line, at, begin, end);
                 if (lane == 0) s.work[team] = x;
             }
             team_sync();
@@ -825,6 +825,25 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             }
             const uint32_t oa = (NT == 2 ? tO[team] : tO[0]) + lanes, ob = tO[1] + lanes;
             const bool live = brow < rows && done;
+            // the pieces before this one: fo times what lies in the slot
+            const int64_t at_row = (int64_t)tree_slot(w, begin) * ROWS + brow;
+            float *const part = p.part + at_row * D;
+            float2 *const ml = reinterpret_cast<float2 *>(p.part + (int64_t)2 * p.ctas * ROWS * D) + at_row;
+            float fo = 0.f;
+            if (!w.begins && live) {
+                const float2 x = *ml;
+                if (x.x != -INFINITY) {
+                    const float t = fmaxf(M, x.x), f = M == -INFINITY ? 0.f : ex2(M - t);
+                    fo = ex2(x.x - t);
+                    fa *= f;
+                    fb *= f;
+                    l = (f == 0.f ? 0.f : l * f) + x.y * fo;
+                    M = t;
+                }
+            }
+            if constexpr (NT == 1) {
+                if (!w.begins) both_sync();           // both threads of a row have read its sum
+            }
             // 32 accumulator columns, joined, in the order of the dims
             auto load32 = [&](int c, float (&v)[32]) {
                 uint32_t x[32];
@@ -839,13 +858,21 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     for (int i = 0; i < 32; ++i)
                         if (fb != 0.f) v[(i & ~7) + perm8(i & 7)] += __uint_as_float(x[i]) * fb;
                 }
+                if (fo != 0.f) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(part + 32 * c + i);
+                        v[i] += y.x * fo;
+                        v[i + 1] += y.y * fo;
+                        v[i + 2] += y.z * fo;
+                        v[i + 3] += y.w * fo;
+                    }
+                }
             };
             constexpr int C0 = 1, STEP = NT == 2 ? 1 : 2;                     // NT = 1: the teams share the columns
             const int cfirst = NT == 2 ? 0 : team * C0;
             const int gr = w.mt * ROWS + brow;
             if (!w.whole) {
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (at - w.used == begin ? 0 : 1);
-                float *part = p.part + (slot * ROWS + brow) * D;
                 if (!idle) {
 #pragma unroll 1
                     for (int c = cfirst; c < D / 32; c += STEP) {
@@ -858,8 +885,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         }
                     }
                 }
-                if (live && (NT == 2 || team == 0))
-                    *reinterpret_cast<float2 *>(p.part + (int64_t)2 * p.ctas * ROWS * D + (slot * ROWS + brow) * 2) = make_float2(M, l);
+                if (live && (NT == 2 || team == 0)) *ml = make_float2(M, l);
             } else {
                 const float il = l == 0.f ? 0.f : 1.f / l;
                 const bool turn = !(p.flags & RQ_ATTN_ROTATED_OUT);
@@ -958,7 +984,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int q = 0; q < 4; ++q) piece[q] = (uint32_t)(((ch & 1) * 4 + q) ^ (r0 & 7)) << 4;
         uint32_t base = 0, sc = 0;                       // items and tiles of earlier stretches
         for (int64_t at = begin; at < end;) {
-            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, end);
+            const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, begin, end);
             const int T = w.t1 - w.t0;
             at += w.used;
             if (T <= 0) continue;

@@ -192,17 +192,25 @@ __device__ __forceinline__ void tree_scan(const TreeParams &p, TreeLine &line) {
     __syncthreads();
 }
 
-// One stretch of a unit, as one CTA works on it.
+// Tiles that one accumulator adds up.  The tensor cores do not round their additions to
+// nearest: sums of a common sign lose about 2^-24 of themselves with each, 256 tiles of 8
+// additions 6e-5, as the sum grows meanwhile.  2048 tiles in one sum were 2e-4 (few rows) to
+// 1.5e-3 (256 rows) off; fp16 is 2e-5 off now.
+constexpr int kPieceTiles = 256;
+
+// A piece of a CTA's stretch of a unit: all of it, or so many tiles.  What the pieces before
+// have summed waits where the stretch's partial goes.
 struct TreeWork {
     TreeSeq s;
     int b, h, mt;          // sequence, KV head, row block
-    int t0, t1;            // the CTA's tiles of the unit; none where it ends within the unit's lead
-    int64_t first, used;   // where the unit begins in the line; the stretch's length
-    bool whole;            // the unit lies in this CTA alone
+    int t0, t1;            // the piece's tiles; none where the stretch ends within the unit's lead
+    int64_t first, used;   // where the unit begins in the line; the piece's length
+    bool begins;           // the stretch's first piece
+    bool whole;            // the unit lies in this CTA alone, and this is its last piece
 };
 
 template <int ROWS, int TT>
-__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const TreeLine &line, int64_t pos, int64_t end) {
+__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const TreeLine &line, int64_t pos, int64_t begin, int64_t end) {
     int lo = 0, hi = kScan;
     while (hi - lo > 1) {                    // the last stretch that begins at or before pos
         const int mid = (lo + hi) >> 1;
@@ -222,12 +230,13 @@ __device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const TreeLin
     }
     const int64_t off = pos - at, length = unit_length(line.lead, w.s), u = off / length, from = off - u * length;
     w.first = pos - from;
-    w.used = min(length - from, end - pos);
+    w.begins = from == 0 || pos == begin;
     w.t0 = (int)max((int64_t)0, from - line.lead);
+    w.used = min(min(length - from, end - pos), w.t0 + kPieceTiles + line.lead - from);
     w.t1 = (int)max((int64_t)0, from + w.used - line.lead);
     w.h = (int)(u / w.s.mt);
     w.mt = (int)(u - (int64_t)w.h * w.s.mt);
-    w.whole = w.t0 == 0 && w.t1 == w.s.nt;
+    w.whole = begin - w.first <= line.lead && w.t1 == w.s.nt;
     return w;
 }
 
@@ -244,15 +253,18 @@ struct alignas(16) TreeJoin {
 // floats before the TreeJoin of CTA 0
 __host__ __device__ inline int64_t tree_join_at(int ctas, int rows, int dim) { return (int64_t)2 * ctas * rows * (dim + 2); }
 
-// After each of a CTA's stretches (`join` begins as {}): notes a unit that goes on past it.
+// The slot of a stretch's partial.
+__device__ __forceinline__ int tree_slot(const TreeWork &w, int64_t begin) { return 2 * (int)blockIdx.x + (begin >= w.first ? 0 : 1); }
+
+// After each of a CTA's pieces (`join` begins as {}): notes a unit that goes on past the CTA.
 template <int ROWS>
-__device__ __forceinline__ void tree_note(const TreeParams &p, const TreeLine &line, const TreeWork &w, int64_t begin, TreeJoin &join) {
-    if (w.t0 != 0 || w.t1 == 0 || w.whole) return;
+__device__ __forceinline__ void tree_note(const TreeParams &p, const TreeLine &line, const TreeWork &w, int64_t begin, int64_t end, TreeJoin &join) {
     const int64_t total = line.prefix[kScan], last = w.first + unit_length(line.lead, w.s) - 1;
+    if (w.t0 != 0 || w.t1 == 0 || last < end) return;
     // CTA of a position: the last c with total c / ctas <= position
     const int c1 = (int)(((last + 1) * p.ctas - 1) / total);
     join = TreeJoin{(int)w.s.row0, min(ROWS, w.s.n * p.group - w.mt * ROWS), w.h, w.mt, c1,
-                    2 * (int)blockIdx.x + (begin >= w.first ? 0 : 1), total};
+                    tree_slot(w, begin), total};
 }
 
 // May query row `r` of the row block see token `t` of the sequence?  Rows past the

@@ -480,7 +480,7 @@ def rope(q, k, positions: torch.Tensor, turns: torch.Tensor, *, interleaved: boo
     contiguous tensors or the pair given as `out` (which may be (q, k): in place).  ``inverse=True`` is the transposed
     turn, the gradient of the forward one, which backward() takes where q or k asks for a gradient (not with `out`).
     turns and mscale come from :func:`rope_turns`."""
-    if torch.is_grad_enabled() and any(x is not None and x.requires_grad for x in (q, k)):
+    if (q is not None and q.requires_grad or k is not None and k.requires_grad) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot take part where gradients are asked for")
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):

@@ -44,7 +44,7 @@
 //    output).
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
-// heads, one node: 103 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
+// heads, one node: 102 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
 // blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 138
 // us, 4.1 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
 // memory waits.  One sequence of 514 tokens takes the 15 us of its latencies and 7 of the

@@ -45,9 +45,9 @@
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
 // heads, one node: 102 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
-// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 138
-// us, 4.1 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
-// memory waits.  One sequence of 514 tokens takes the 15 us of its latencies and 7 of the
+// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 137
+// us, 4.2 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
+// memory waits.  One sequence of 514 tokens takes the 16 us of its latencies and 7 of the
 // join, which overlap in part.
 #include "rq.h"
 #include "rq_internal.h"
@@ -170,7 +170,6 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         for (int64_t at = begin; at < end;) {
             const TreeWork w = tree_work<ROWS, kTT>(p, s.line, at, begin, end);
             at += w.used;
-            tree_note<ROWS>(p, s.line, w, begin, end, join);
             if (w.t1 <= w.t0) continue;
             auto page_of = [&](int tile) -> int64_t {
                 const int t = tile * kTT + lane * bt;
@@ -202,6 +201,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     ph ^= 1;
                 }
             }
+            tree_note<ROWS>(p, s.line, w, begin, end, join);
         }
         if (lane == 0) reinterpret_cast<TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x] = join;
         // no copy outlives the block, also when it gave up

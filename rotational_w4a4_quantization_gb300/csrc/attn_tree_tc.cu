@@ -47,7 +47,7 @@
 // arrival that delivers P, when no MMA touches it).  fp16 keeps 11 bits down to 2^-14, so
 // of tokens at least 23 bits below the largest, and something down to 2^-25.
 //
-// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 417 us, 0.71
+// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 422 us, 0.70
 // PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 5,000 cycles
 // of which the MMAs run 2,048.  The softmax bounds it: 1,800 cycles for half a tile, most
 // of it latency of tensor-memory loads, exponentials and the exchange between a row's
@@ -500,7 +500,6 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const TreeWork w = tree_work<ROWS, kTcTT>(p, s.line, at, begin, end);
             const int T = w.t1 - w.t0;
             at += w.used;
-            tree_note<ROWS>(p, s.line, w, begin, end, join);
             if (T <= 0) continue;
             // lane l: tokens 4 l .. 4 l + 3 of a tile, the next tile's loaded ahead
             float4 nk, nv;
@@ -549,6 +548,7 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 __syncwarp();
                 if (lane == 0) t_mbar_arrive(&s.sc_full[scs]);
             }
+            tree_note<ROWS>(p, s.line, w, begin, end, join);
         }
         if (lane == 0) reinterpret_cast<TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x] = join;
     } else if (warp == 1) {

@@ -256,7 +256,8 @@ __host__ __device__ inline int64_t tree_join_at(int ctas, int rows, int dim) { r
 // The slot of a stretch's partial.
 __device__ __forceinline__ int tree_slot(const TreeWork &w, int64_t begin) { return 2 * (int)blockIdx.x + (begin >= w.first ? 0 : 1); }
 
-// After each of a CTA's pieces (`join` begins as {}): notes a unit that goes on past the CTA.
+// After each of a CTA's pieces (`join` begins as {}), when its loads are on their way: notes a
+// unit that goes on past the CTA.
 template <int ROWS>
 __device__ __forceinline__ void tree_note(const TreeParams &p, const TreeLine &line, const TreeWork &w, int64_t begin, int64_t end, TreeJoin &join) {
     const int64_t total = line.prefix[kScan], last = w.first + unit_length(line.lead, w.s) - 1;

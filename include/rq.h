@@ -405,15 +405,15 @@ rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, cons
  *   mask, the nodes j <= i.  max_nodes and table_width are bounds: the time goes by the
  *   rows and tokens that there are.
  *     out = softmax(softmax_scale (q R) . k^) v^ R^T,   any finite softmax_scale
- *   with the softmax's sums in fp32.  q~ and a token's weight times its value scale are
- *   rounded to fp16 on the way into the tensor cores, each by 2^-12 of itself at most (fp32
- *   queries: both, fp16 queries: q~ in two fp16 parts); with bf16 queries of more than 32
- *   rows per KV head the keys and values times their scales are, too.  Weights 2^-23 of a
- *   row's largest keep those bits, those below 2^-34 of it may vanish; on the blocks for
- *   more than 32 rows up to 2^8 of that room may go to value scales that differ within 128
- *   tokens.  The tensor cores, whose additions are not rounded to nearest, add up 2^15
- *   tokens at most, where values of a common sign lose less than 1e-4; fp32 queries add
- *   outside them.
+ *   with the softmax's sums in fp32.  q~ (relative to its row's largest element) and a
+ *   token's weight times its value scale are rounded to fp16 on the way into the tensor
+ *   cores, to 11 bits (fp32 queries: both, fp16 queries: q~ in two fp16 parts); with bf16
+ *   queries of more than 32 rows per KV head the keys and values times their scales are,
+ *   too.  Weights keep those bits down to 2^-23 of the row's largest, and below 2^-34 of it
+ *   may vanish (a value scale below 2^-60 counts as 2^-60 there); in blocks for more than 32
+ *   rows up to 2^8 of that may go to value scales that differ within 128 tokens.  The tensor
+ *   cores, whose additions are not rounded to nearest, add up 2^15 tokens at most, where
+ *   values of a common sign lose less than 1e-4; fp32 queries add outside them.
  *   A row that sees nothing is 0.  Tokens on a page number outside the cache, or past the
  *   table, are not seen.  What a cache row that a query does not see holds (NaN and
  *   infinite scales too) does not reach it.  Rows of q that belong to no sequence, or lie
@@ -427,7 +427,8 @@ rq_status rq_kv_read(const uint8_t *kq, const float *ks, const uint8_t *vq, cons
  *   workspace, workspace_bytes: scratch of the call, at least
  *            rq_attn_tree_workspace(head_dim) bytes; nothing is kept in it between calls.
  *   flags    RQ_SIGNS_FIRST (as given to rq_kv_append), RQ_ATTN_ROTATED_OUT.
- *   RQ_ERR_UNSUPPORTED: pages * kv_heads * page_size or table_width * page_size past 2^31.
+ *   RQ_ERR_UNSUPPORTED: pages * kv_heads * page_size or table_width * page_size past 2^31,
+ *            max_nodes * q_heads past 2^30.
  */
 int64_t rq_attn_tree_workspace(int64_t head_dim);
 rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_stride, rq_dtype dtype, int64_t rows,

@@ -55,7 +55,7 @@
 // were, with one limit of 96 registers for all warps: one pass over the scores with the old
 // reference, weights kept back in registers (431 us); scores kept in registers (457,
 // spills); 32 columns a load (433); buffers of 64 columns (423, as Q K^T with N = 64 takes
-// 48 cycles for 32's work).  64 rows (fp16, 16 sequences of up to 4k): 78 us, where the
+// 48 cycles for 32's work).  64 rows (fp16, 16 sequences of up to 4k): 75 us, where the
 // bytes take 9: starts and ends of units; with a buffer per softmax team, 128 columns to a
 // thread, 86 (and the 256 rows 404).
 #include "rq.h"

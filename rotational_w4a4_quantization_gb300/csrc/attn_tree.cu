@@ -38,8 +38,10 @@
 //    are exact in either.  The second part of w is kept 2^11 up, so that small weights have
 //    22 bits too.  What the tensor cores add to an accumulator is not rounded to nearest:
 //    a score 17 to 26 bits above the others', added up by 16 of them, had its weight 5e-6
-//    to 2e-5 off.  So each step of 16 starts from 0 and is added to the sums outside, and
-//    the scale, with the rotation's 1/sqrt(D), has two fp32 parts.  fp16 queries split q~
+//    to 2e-5 off.  So each word of scores and each 16 tokens of outputs start from 0 and
+//    are added to the sums outside, and the scale, with the rotation's 1/sqrt(D), has two
+//    fp32 parts.  That and the second part's range cost 10 to 15% (18 sequences of 12k, 88
+//    rows: 206 us for 179).  fp16 queries split q~
 //    alone: their outputs resolve its rounding to 11 bits (4.6e-4 against 2.5e-4 of an
 //    output).
 //
@@ -125,6 +127,14 @@ __device__ __forceinline__ uint32_t lowered(uint32_t x) {
     const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x1000)));   // 2^-11
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ void add4(float (&to)[4], const float (&x)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+        const float2 y = __fadd2_rn(make_float2(to[k], to[k + 1]), make_float2(x[k], x[k + 1]));
+        to[k] = y.x;
+        to[k + 1] = y.y;
+    }
+}
 // An 8 x 8 matrix of fp16 pairs, transposed across the warp.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
@@ -140,7 +150,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     using S = MSmem<IN, D, ROWS>;
     constexpr int RB = D / 2, WPT = D / 32, E = D / 32, HQ = S::HQ, HP = S::HP;
     constexpr bool kOffset = IN != IN_F32;             // keys as u = code + 8 (see the top)
-    constexpr bool kShort = IN == IN_F32;              // the tensor cores add two parts of one step, no more
+    constexpr bool kShort = IN == IN_F32;              // the tensor cores add up few products, the rest is added outside
     constexpr int NQ = D / 32;                        // 16-byte chunks of a code row
     constexpr bool SIDE = ROWS == 8;                  // products of tokens x rows instead of rows x tokens
     constexpr int kRowLo = SIDE ? 4 : 1, kRowHi = SIDE ? 32 : 4;   // lane bits that a row's scores are spread over
@@ -340,38 +350,40 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                             if constexpr (kOffset) offset_pairs(kw[t][wd], b[t]);
                             else code_pairs(kw[t][wd], b[t]);
                         }
+                        float own[kShort ? NS : 1][4];                  // this word's sums (kShort)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float own[kShort ? NS : 1][4];              // this step's sums (kShort)
+                        for (int step = 0; step < 2 * HQ; ++step) {
+                            // kShort: the small part first, so that fewer additions meet the large one
+                            const int hv = kShort ? HQ - 1 - step / 2 : step / 2, i = step & 1;
+                            const bool begins = step == 0 && (kShort || (part == 0 && wd == 0));
+                            auto add = [&](int t, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+                                float(&to)[4] = kShort ? own[t % (kShort ? NS : 1)] : sc[t];
+                                if (begins) mma16816_first(to, a, b0, b1);
+                                else mma16816(to, a, b0, b1);
+                            };
+                            if constexpr (SIDE) {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
 #pragma unroll
-                            for (int at_hv = 0; at_hv < HQ; ++at_hv) {
-                                // kShort: the small part first, so that one addition meets the large one
-                                const int hv = kShort ? HQ - 1 - at_hv : at_hv;
-                                const bool begins = at_hv == 0 && (kShort || (part == 0 && wd == 0 && i == 0));
-                                auto add = [&](int t, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-                                    float(&to)[4] = kShort ? own[t % (kShort ? NS : 1)] : sc[t];
-                                    if (begins) mma16816_first(to, a, b0, b1);
-                                    else mma16816(to, a, b0, b1);
-                                };
-                                if constexpr (SIDE) {
-                                    const uint2 x = *reinterpret_cast<const uint2 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
-#pragma unroll
-                                    for (int t = 0; t < NS; ++t) {
-                                        const uint32_t a[4] = {b[2 * t][2 * i], b[2 * t + 1][2 * i], b[2 * t][2 * i + 1], b[2 * t + 1][2 * i + 1]};
-                                        add(t, a, x.x, x.y);
-                                    }
-                                } else {
-                                    const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
-                                    const uint32_t a[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                    for (int t = 0; t < kWT; ++t) add(t, a, b[t][2 * i], b[t][2 * i + 1]);
+                                for (int t = 0; t < NS; ++t) {
+                                    const uint32_t a[4] = {b[2 * t][2 * i], b[2 * t + 1][2 * i], b[2 * t][2 * i + 1], b[2 * t + 1][2 * i + 1]};
+                                    add(t, a, x.x, x.y);
                                 }
+                            } else {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(s.q[hv][2 * (part * KP + wd) + i][lane]);
+                                const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int t = 0; t < kWT; ++t) add(t, a, b[t][2 * i], b[t][2 * i + 1]);
                             }
-                            if constexpr (kShort) {
+                        }
+                        if constexpr (kShort) {
 #pragma unroll
-                                for (int t = 0; t < NS; ++t)
+                            for (int t = 0; t < NS; ++t) {
+                                if (part == 0 && wd == 0) {
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) sc[t][k] = part == 0 && wd == 0 && i == 0 ? own[t][k] : sc[t][k] + own[t][k];
+                                    for (int k = 0; k < 4; ++k) sc[t][k] = own[t][k];
+                                } else {
+                                    add4(sc[t], own[t]);
+                                }
                             }
                         }
                     }
@@ -520,8 +532,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                                     mma16816_first(own[j], a, x0, x1);
                                 } else {
                                     mma16816(own[j], a, x0, x1);
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) to[k] += own[j][k];
+                                    add4(to, own[j]);
                                 }
                             } else {
                                 mma16816(to, a, x0, x1);

@@ -41,13 +41,13 @@
 //    to 2e-5 off.  So each word of scores and each 16 tokens of outputs start from 0 and
 //    are added to the sums outside, and the scale, with the rotation's 1/sqrt(D), has two
 //    fp32 parts.  That and the second part's range cost 10 to 15% (18 sequences of 12k, 88
-//    rows: 206 us for 179).  fp16 queries split q~
+//    rows: 201 us for 179).  fp16 queries split q~
 //    alone: their outputs resolve its rounding to 11 bits (4.6e-4 against 2.5e-4 of an
 //    output).
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
-// heads, one node: 102 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
-// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 137
+// heads, one node: 103 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
+// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 135
 // us, 4.2 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
 // memory waits.  One sequence of 514 tokens takes the 16 us of its latencies and 7 of the
 // join, which overlap in part.
@@ -211,9 +211,9 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     ph ^= 1;
                 }
             }
-            tree_note<ROWS>(p, s.line, w, begin, end, join);
+            tree_note<ROWS, D>(p, s.line, w, begin, end, join);
         }
-        if (lane == 0) reinterpret_cast<TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x] = join;
+        tree_noted<ROWS, D>(p, join);
         // no copy outlives the block, also when it gave up
         if (s.abort_flag) {
             const long long t0 = clock64();
@@ -525,38 +525,31 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         uint32_t b0[4], b1[4];
                         code_pairs(x, b0);
                         code_pairs(y, b1);
-                        float own[kShort ? 4 : 1][4];
-                        auto add = [&](int hv, int j, float(&to)[4], const uint32_t (&a)[4], uint32_t x0, uint32_t x1) {
+                        // a product of 16 tokens; kShort: both parts from 0, then added to the sums
+                        auto product = [&](float(&to)[4], auto part) {
                             if constexpr (kShort) {
-                                if (hv == 0) {
-                                    mma16816_first(own[j], a, x0, x1);
-                                } else {
-                                    mma16816(own[j], a, x0, x1);
-                                    add4(to, own[j]);
-                                }
+                                float own[4];
+                                part(0, [&](const uint32_t (&a)[4], uint32_t x0, uint32_t x1) { mma16816_first(own, a, x0, x1); });
+                                part(1, [&](const uint32_t (&a)[4], uint32_t x0, uint32_t x1) { mma16816(own, a, x0, x1); });
+                                add4(to, own);
                             } else {
-                                mma16816(to, a, x0, x1);
+                                part(0, [&](const uint32_t (&a)[4], uint32_t x0, uint32_t x1) { mma16816(to, a, x0, x1); });
                             }
                         };
+                        if constexpr (SIDE) {
 #pragma unroll
-                        for (int hv = 0; hv < HP; ++hv) {
-                            if (hv == 1) {
+                            for (int j = 0; j < 4; j += 2)
+                                product(acc[2 * q + j / 2], [&](int hv, auto run) {
+                                    const uint32_t a[4] = {hv ? lowered(b0[j]) : b0[j], hv ? lowered(b0[j + 1]) : b0[j + 1],
+                                                           hv ? lowered(b1[j]) : b1[j], hv ? lowered(b1[j + 1]) : b1[j + 1]};
+                                    run(a, pa[hv % HP][0], pa[hv % HP][1]);
+                                });
+                        } else {
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    b0[j] = lowered(b0[j]);
-                                    b1[j] = lowered(b1[j]);
-                                }
-                            }
-                            if constexpr (SIDE) {
-#pragma unroll
-                                for (int j = 0; j < 4; j += 2) {
-                                    const uint32_t a[4] = {b0[j], b0[j + 1], b1[j], b1[j + 1]};
-                                    add(hv, j / 2, acc[2 * q + j / 2], a, pa[hv][0], pa[hv][1]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) add(hv, j, acc[(4 * q + j) % NA], pa[hv], b0[j], b1[j]);
-                            }
+                            for (int j = 0; j < 4; ++j)
+                                product(acc[(4 * q + j) % NA], [&](int hv, auto run) {
+                                    run(pa[hv % HP], hv ? lowered(b0[j]) : b0[j], hv ? lowered(b1[j]) : b1[j]);
+                                });
                         }
                     };
                     if constexpr (NQ == 1) {
@@ -646,16 +639,27 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             joined(r, top[i], vsum[i]);
 #pragma unroll
             for (int e = 0; e < E; ++e) qv[i][e] = s.acc[0][r][lane * E + e] + s.acc[1][r][lane * E + e];
-            if (!w.begins) {                                // the pieces before this one
+        }
+        if (!w.begins) {                                    // the pieces before this one
+            // 16 rows: rolled, as short calls take their time fetching code
+#pragma unroll(SIDE ? RW : 1)
+            for (int i = 0; i < RW; ++i) {
+                const int r = i * kCWarps + warp;
                 const float2 x = *reinterpret_cast<const float2 *>(ml + (slot * ROWS + r) * 2);
-                if (r < rows && x.x != -INFINITY) {
-                    const float t = fmaxf(top[i], x.x), f = ex2(x.x - t), g0 = top[i] == -INFINITY ? 0.f : ex2(top[i] - t);
+                if (r >= rows || x.x == -INFINITY) continue;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) qv[i][e] = (g0 == 0.f ? 0.f : qv[i][e] * g0) + part[(slot * ROWS + r) * D + lane * E + e] * f;
-                    vsum[i] = (g0 == 0.f ? 0.f : vsum[i] * g0) + x.y * f;
-                    top[i] = t;
-                }
+                for (int k = 0; k < RW; ++k)
+                    if (k == i) {
+                        const float t = fmaxf(top[k], x.x), f = ex2(x.x - t), g0 = top[k] == -INFINITY ? 0.f : ex2(top[k] - t);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) qv[k][e] = (g0 == 0.f ? 0.f : qv[k][e] * g0) + part[(slot * ROWS + r) * D + lane * E + e] * f;
+                        vsum[k] = (g0 == 0.f ? 0.f : vsum[k] * g0) + x.y * f;
+                        top[k] = t;
+                    }
             }
+        }
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
             const float il = w.whole ? (vsum[i] == 0.f ? 0.f : 1.f / vsum[i]) : 1.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) qv[i][e] *= il;
@@ -726,8 +730,7 @@ cudaError_t launch_attn_tree(const TreeCall &c, cudaStream_t stream) {
     if (sms <= 0) return cudaErrorUnknown;
     const int rows = tree_rows(c) <= 8 ? 8 : 16;
     const int per_sm = blocks_per_sm(rows, c.head_dim);
-    const int64_t max_tiles = tree_tiles(c, rows, kTT);
-    p.ctas = (int)(max_tiles < per_sm * sms ? max_tiles : per_sm * sms);
+    tree_ctas(c, p, rows, kTT, per_sm * sms);
     CUtensorMap mk, mv;
     if (!tree_maps(c, kTT, mk, mv)) return cudaErrorInvalidValue;
     const bool side = rows == 8;

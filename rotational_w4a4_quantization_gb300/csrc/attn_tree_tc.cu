@@ -47,7 +47,7 @@
 // arrival that delivers P, when no MMA touches it).  fp16 keeps 11 bits down to 2^-14, so
 // of tokens at least 23 bits below the largest, and something down to 2^-25.
 //
-// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 422 us, 0.70
+// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 426 us, 0.69
 // PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 5,000 cycles
 // of which the MMAs run 2,048.  The softmax bounds it: 1,800 cycles for half a tile, most
 // of it latency of tensor-memory loads, exponentials and the exchange between a row's
@@ -55,7 +55,7 @@
 // were, with one limit of 96 registers for all warps: one pass over the scores with the old
 // reference, weights kept back in registers (431 us); scores kept in registers (457,
 // spills); 32 columns a load (433); buffers of 64 columns (423, as Q K^T with N = 64 takes
-// 48 cycles for 32's work).  64 rows (fp16, 16 sequences of up to 4k): 75 us, where the
+// 48 cycles for 32's work).  64 rows (fp16, 16 sequences of up to 4k): 72 us, where the
 // bytes take 9: starts and ends of units; with a buffer per softmax team, 128 columns to a
 // thread, 86 (and the 256 rows 404).
 #include "rq.h"
@@ -548,9 +548,9 @@ attn_tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 __syncwarp();
                 if (lane == 0) t_mbar_arrive(&s.sc_full[scs]);
             }
-            tree_note<ROWS>(p, s.line, w, begin, end, join);
+            tree_note<ROWS, D>(p, s.line, w, begin, end, join);
         }
-        if (lane == 0) reinterpret_cast<TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x] = join;
+        tree_noted<ROWS, D>(p, join);
     } else if (warp == 1) {
         // ---------------- MMA ----------------
         // The whole warp runs the loop, so that descriptors stay in uniform registers;
@@ -1126,8 +1126,7 @@ cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream) {
     // two row blocks share each converted tile; fp16 queries keep the second's shared
     // memory for the low parts of q~
     const int nt = tree_rows(c) > 128 && c.in_type == IN_BF16 ? 2 : 1;
-    const int64_t max_tiles = tree_tiles(c, 128 * nt, kTcTT);
-    p.ctas = (int)(max_tiles < sms ? max_tiles : sms);
+    tree_ctas(c, p, 128 * nt, kTcTT, sms);
     const bool d128 = c.head_dim == 128;
     if (c.in_type == IN_F16)
         return d128 ? launch_tc<IN_F16, 128, 1, 2>(p, stream) : launch_tc<IN_F16, 64, 1, 2>(p, stream);

@@ -33,6 +33,7 @@ struct TreeParams {
     void *out;
     float *part;                        // [2 G][ROWS][D] fp32, then [2 G][ROWS][2] (reference, sum), then [G] TreeJoin
     int64_t rows_each;                  // query rows per KV head and sequence, on average
+    int per_head;                       // blocks of rows per KV head and sequence that the join has blocks for; 0: see TreeJoin
     int ctas;                           // G
     int *err;
 };
@@ -102,6 +103,13 @@ inline int64_t tree_tiles(const TreeCall &c, int64_t block, int64_t tile) {
 // holds 11 bits from 2^-14 to 2^16.  And log2 of the least value scale that the reference
 // follows, so that the sum of the weights without their scales stays in range.
 constexpr float kWeightTo = 9.f, kWeightMost = 15.f, kLeastValue = -60.f;
+
+// The CTAs of a call, and whether the join goes by units: where there can be fewer of them.
+inline void tree_ctas(const TreeCall &c, TreeParams &p, int64_t block, int64_t tile, int most) {
+    const int64_t tiles = tree_tiles(c, block, tile), each = (c.max_nodes * p.group + block - 1) / block;
+    p.ctas = (int)(tiles < most ? tiles : most);
+    p.per_head = (double)c.seqs * p.kv_heads * each < p.ctas ? (int)each : 0;
+}
 
 struct TreeSeq {
     int64_t row0;      // first query row
@@ -244,28 +252,41 @@ __device__ __forceinline__ int64_t tree_begin(int64_t total, int ctas, int c) { 
 
 // What the join has to know of a unit that spans CTAs; the CTA with its first tile leaves it,
 // the others (and that one for none) one without rows.  The join has neither scan nor search,
-// and as many blocks as CTAs, however many units there are.
+// and as many blocks as CTAs, however many units there are; or, where there can be fewer
+// units than CTAs, as many as units (p.per_head > 0), each with a place of its own.
 struct alignas(16) TreeJoin {
     int row0, rows, h, mt; // the unit's first query row, its rows, KV head, row block
-    int c1, slot0;         // its last CTA; the slot of the first CTA's partial
+    int c1, slot0;         // its last CTA; the slot of the first CTA's partial, 2 c0 or one more
     int64_t total;         // the line's length
 };
 // floats before the TreeJoin of CTA 0
 __host__ __device__ inline int64_t tree_join_at(int ctas, int rows, int dim) { return (int64_t)2 * ctas * rows * (dim + 2); }
+
+template <int ROWS, int D>
+__device__ __forceinline__ TreeJoin *tree_joins(const TreeParams &p) { return reinterpret_cast<TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D)); }
 
 // The slot of a stretch's partial.
 __device__ __forceinline__ int tree_slot(const TreeWork &w, int64_t begin) { return 2 * (int)blockIdx.x + (begin >= w.first ? 0 : 1); }
 
 // After each of a CTA's pieces (`join` begins as {}), when its loads are on their way: notes a
 // unit that goes on past the CTA.
-template <int ROWS>
+template <int ROWS, int D>
 __device__ __forceinline__ void tree_note(const TreeParams &p, const TreeLine &line, const TreeWork &w, int64_t begin, int64_t end, TreeJoin &join) {
+    if (w.t0 != 0 || w.t1 == 0) return;
     const int64_t total = line.prefix[kScan], last = w.first + unit_length(line.lead, w.s) - 1;
-    if (w.t0 != 0 || w.t1 == 0 || last < end) return;
-    // CTA of a position: the last c with total c / ctas <= position
-    const int c1 = (int)(((last + 1) * p.ctas - 1) / total);
-    join = TreeJoin{(int)w.s.row0, min(ROWS, w.s.n * p.group - w.mt * ROWS), w.h, w.mt, c1,
-                    tree_slot(w, begin), total};
+    if (last >= end) {
+        // CTA of a position: the last c with total c / ctas <= position
+        const int c1 = (int)(((last + 1) * p.ctas - 1) / total);
+        join = TreeJoin{(int)w.s.row0, min(ROWS, w.s.n * p.group - w.mt * ROWS), w.h, w.mt, c1,
+                        tree_slot(w, begin), total};
+    }
+    if (p.per_head && (threadIdx.x & 31) == 0)              // that of a unit that ends here is {}
+        tree_joins<ROWS, D>(p)[((int64_t)w.b * p.kv_heads + w.h) * p.per_head + w.mt] = join;
+}
+// At the end of the CTA.
+template <int ROWS, int D>
+__device__ __forceinline__ void tree_noted(const TreeParams &p, const TreeJoin &join) {
+    if (!p.per_head && (threadIdx.x & 31) == 0) tree_joins<ROWS, D>(p)[blockIdx.x] = join;
 }
 
 // May query row `r` of the row block see token `t` of the sequence?  Rows past the
@@ -342,8 +363,9 @@ __device__ __forceinline__ void t_bulk(void *dst, const void *src, uint32_t byte
 // Joins the partials of the units that span CTAs: per row, in the order of the
 // CTAs (so results do not change from run to run), the largest reference, the
 // rescaled sums, then normalisation, R^T and the one rounding to the output type.
-// Block c takes the unit whose first tile CTA c has, if that spans CTAs.  A warp takes a row
-// (two of 256-row units) and four partials at a time, so that their loads overlap.
+// Block c takes the unit whose first tile CTA c has (or unit c), if that spans CTAs.  A warp
+// takes a row (two of 256-row units) and four partials at a time, so that their loads
+// overlap.
 // Launched so that it may begin while the kernel before it ends.  Every thread waits for
 // that, those without a unit to join too: the join may not end before the kernel before it
 // has, as what follows on the stream (or in a captured graph) is ordered behind the join
@@ -351,16 +373,23 @@ __device__ __forceinline__ void t_bulk(void *dst, const void *src, uint32_t byte
 __device__ __forceinline__ void tree_join_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 constexpr int join_rows(int rows) { return rows >= 256 ? 2 : 1; }         // rows per warp
 constexpr int join_warps(int rows) { return rows < 16 ? rows : 16; }
+constexpr int kJoinPerSm = 2;          // blocks: three leave registers for fewer loads at once (16 sequences of up to 4k: 76 us for 72)
 template <int IN, int D, int ROWS>
-__global__ void __launch_bounds__(32 * join_warps(ROWS)) attn_tree_join_kernel(const __grid_constant__ TreeParams p, int turns) {
+__global__ void __launch_bounds__(32 * join_warps(ROWS), kJoinPerSm) attn_tree_join_kernel(const __grid_constant__ TreeParams p, int turns) {
     constexpr int E = D / 32, RW = join_rows(ROWS), kJoinWarps = join_warps(ROWS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int begin_row = (blockIdx.y * turns * kJoinWarps + warp) * RW;
+    bool there_is = true;                                   // unit c, if blocks have units: its notes are old where it is not
+    if (p.per_head) {
+        const int b = blockIdx.x / (p.kv_heads * p.per_head);
+        there_is = (int)(blockIdx.x % p.per_head) < tree_seq<ROWS, 128>(p, b).mt;
+    }
     float sg[E];
     lane_signs<E>(sg, lane, p.seed);
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials are written
-    const TreeJoin u = reinterpret_cast<const TreeJoin *>(p.part + tree_join_at(p.ctas, ROWS, D))[blockIdx.x];
-    const int rows = u.rows, c0 = blockIdx.x, c1 = u.c1;
+    TreeJoin u{};
+    if (there_is) u = tree_joins<ROWS, D>(p)[blockIdx.x];
+    const int rows = u.rows, c0 = u.slot0 >> 1, c1 = u.c1;
     if (begin_row >= rows) return;
     const int64_t total = u.total;
     const float *ml = p.part + (int64_t)2 * p.ctas * ROWS * D;
@@ -452,14 +481,15 @@ __global__ void __launch_bounds__(32 * join_warps(ROWS)) attn_tree_join_kernel(c
 template <int IN, int D, int ROWS>
 cudaError_t launch_tree_join(const TreeParams &p, cudaStream_t stream) {
     if (p.ctas == 1) return cudaSuccess;                    // every unit lies in it
-    // one turn per block while an SM holds them all (the registers of two, or three), counting
-    // the rows that there are on average; then blocks take several
-    constexpr int rows = join_warps(ROWS) * join_rows(ROWS), per_sm = ROWS >= 256 ? 2 : 3;
+    const int blocks = p.per_head ? p.seqs * p.kv_heads * p.per_head : p.ctas - 1;
+    // one turn per block while the SMs hold them all, counting the rows that there are on
+    // average; then blocks take several
+    constexpr int rows = join_warps(ROWS) * join_rows(ROWS);
     const int64_t filled = p.rows_each < ROWS ? p.rows_each : ROWS;
     int turns = 1;
-    while (turns * rows < filled && (p.ctas - 1) * ((filled + turns * rows - 1) / (turns * rows)) > per_sm * device_sm_count()) turns *= 2;
+    while (turns * rows < filled && blocks * ((filled + turns * rows - 1) / (turns * rows)) > kJoinPerSm * device_sm_count()) turns *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.ctas - 1), (ROWS + turns * rows - 1) / (turns * rows));
+    cfg.gridDim = dim3((unsigned)blocks, (ROWS + turns * rows - 1) / (turns * rows));
     cfg.blockDim = dim3(32 * join_warps(ROWS));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -22,8 +22,12 @@
  *                       are written (with their rotary positions), read back dense;
  *   rq_attn_tree        attention of trees of drafted tokens (or of one token per
  *                       sequence) over the paged cache, grouped-query heads;
+ *   rq_kv_plan          block tables and slots of that cache from request lengths;
+ *   rq_attn_prefix      the same attention where groups of sequences share a prefix,
+ *                       which is read once for all of them;
  *   rq_w4a8_gemm        the W4A8 variant of the linear layer (INT8 activations),
- *                       with per-channel or per-group weight scales.
+ *                       with per-channel or per-group weight scales;
+ *   rq_w4a16_gemm       products of a few unquantised rows with the 4-bit weights.
  *
  * Sources (page title, then section / equation):
  *   [ROT] "Rotational Quantization: How Orthogonal Transforms and Hadamard
@@ -437,6 +441,81 @@ rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_str
                        int64_t table_width, const int32_t *context_lens, const int32_t *offsets, int64_t seqs,
                        int64_t max_nodes, const uint8_t *tree_mask, int64_t mask_stride, uint64_t seed, uint32_t flags,
                        float softmax_scale, void *out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rq_kv_plan -- block tables and slots of a step from the requests' lengths, on the GPU.
+ *
+ *   Request b has c = context_lens[b] tokens in the cache and gets n = new_lens[b] more
+ *   (negative lengths count as 0).  Its row of block_table keeps the entries of the pages
+ *   that hold the c tokens; the pages that the n tokens need beside them come from
+ *   free_pages, request by request from entry *head on; the entries behind are set to -1.
+ *   Token j of the n is row offsets[b] + j of the step:
+ *     slots[row]     = its page * page_size + its row there, as rq_kv_append takes it
+ *     positions[row] = c + j + base[b]    (base: tokens of a shared prefix before the row's
+ *                                          own, see rq_attn_prefix)
+ *   Rows from offsets[seqs] to total get slot -1 (no token) and position 0, tokens past total
+ *   get none.  A page that free_pages does not have, or that lies past the table's width, is
+ *   -1 and so are its tokens' slots; *head_out is *head and the pages asked for within the
+ *   width: past free_count where they did not suffice.
+ *
+ *   context_lens, new_lens [seqs] int32; base [seqs] int32 or NULL; seqs <= 65536.
+ *   block_table [seqs][table_width] int32, in and out.
+ *   free_pages [free_count] int32 page numbers; head [1] int32, or NULL: 0.
+ *   page_size a power of two, 16 to 256.
+ *   offsets [seqs + 1] int32, slots and positions [total] int64, head_out [1] int32: out.  The sum
+ *   of new_lens has to fit 31 bits.  Nothing written may overlap anything else (head_out
+ *   is not head).  The kept entries of a request are its pages, and no other request's.
+ */
+rq_status rq_kv_plan(const int32_t *context_lens, const int32_t *new_lens, const int32_t *base, int64_t seqs,
+                     int32_t *block_table, int64_t table_width, const int32_t *free_pages, int64_t free_count,
+                     const int32_t *head, int64_t page_size, int64_t total, int32_t *offsets, int64_t *slots,
+                     int64_t *positions, int32_t *head_out, void *stream);
+
+/*
+ * rq_attn_prefix -- rq_attn_tree for groups of sequences that share a prefix.
+ *
+ *   Sequences groups[g] to groups[g + 1] - 1 have the prefix_lens[g] tokens of prefix_table's
+ *   row g before their own.  Their nodes see all of them, then what rq_attn_tree lets them
+ *   see: block_table and context_lens speak of a sequence's own tokens alone, which
+ *   begin on a page of their own.  The result is that of rq_attn_tree on tables that name the prefix's
+ *   pages for each sequence, where the prefix is a whole number of pages, up to rounding;
+ *   the prefix is read once for all rows of its group.  Sequences of no group have no prefix.
+ *   Roundings as in rq_attn_tree; what the two parts add up is joined in fp32.
+ *
+ *   prefix_table [n_groups][prefix_width] int32, prefix_lens [n_groups] int32,
+ *   groups [n_groups + 1] int32, not decreasing, within 0 .. seqs.
+ *   workspace: at least rq_attn_prefix_workspace(rows, q_heads, head_dim) bytes.
+ *   Everything else as in rq_attn_tree; n_groups = 0 is rq_attn_tree.
+ *   RQ_ERR_UNSUPPORTED: as there, and rows * q_heads past 2^30.
+ */
+int64_t rq_attn_prefix_workspace(int64_t rows, int64_t q_heads, int64_t head_dim);
+rq_status rq_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_stride, rq_dtype dtype, int64_t rows,
+                         int64_t q_heads, int64_t head_dim, const uint8_t *kq, const float *ks, const uint8_t *vq,
+                         const float *vs, int64_t pages, int64_t kv_heads, int64_t page_size,
+                         const int32_t *block_table, int64_t table_width, const int32_t *context_lens,
+                         const int32_t *offsets, int64_t seqs, const int32_t *prefix_table, int64_t prefix_width,
+                         const int32_t *prefix_lens, const int32_t *groups, int64_t n_groups, int64_t max_nodes,
+                         const uint8_t *tree_mask, int64_t mask_stride, uint64_t seed, uint32_t flags,
+                         float softmax_scale, void *out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rq_w4a16_gemm -- products of a few rows with 4-bit weights, activations not quantised.
+ *
+ *   y[m][c] = sum_g w_scales[c][g] sum_{k in g} x[m][k] w_q[c][k]
+ *   The products are exact and the sums fp32; one rounding, to y_dtype.  The rows are those
+ *   that the fold of w_q asks for: rotated ones (a rotated residual stream, rq_attn_tree with
+ *   RQ_ATTN_ROTATED_OUT, or rq_fwht_quant's y) for weights from rq_fwht_quant.
+ *
+ *   x         [M][ld_x] of x_dtype (RQ_F32, RQ_BF16, RQ_F16), ld_x >= K, or 0: one row for all; rows at 16-byte
+ *             boundaries.  A row that holds a NaN or an infinity has NaN or infinities in y.
+ *   w_q       [N][K/2] packed INT4 codes, one output channel per row.
+ *   w_scales  [N] fp32 (group == K) or [N][K/128] fp32 (group == 128).
+ *   M <= 64 rows (RQ_ERR_UNSUPPORTED above: that is work for rq_w4a8_gemm and
+ *   rq_w4a4_gemm); N any; K a multiple of 128.
+ *   y         [M][N] of y_dtype (RQ_F32, RQ_BF16, RQ_F16).
+ */
+rq_status rq_w4a16_gemm(const void *x, rq_dtype x_dtype, int64_t M, int64_t K, int64_t ld_x, const uint8_t *w_q,
+                        const float *w_scales, int64_t N, int64_t group, void *y, rq_dtype y_dtype, void *stream);
 
 /*
  * rq_w4a8_gemm -- the W4A8 linear layer with per-channel or per-group weight scales.

@@ -27,6 +27,12 @@ Entry points (same names as the C ABI):
   back dense;
 * :func:`attn_tree` -- attention of trees of drafted tokens, or of one token per
   sequence, over the paged cache, grouped-query heads;
+* :func:`kv_plan` -- block tables and slots of that cache from the requests'
+  lengths;
+* :func:`attn_prefix` -- the same attention where groups of sequences share a
+  prefix, which is read once for all of them;
+* :func:`w4a16_gemm` -- products of a few unquantised rows with the 4-bit
+  weights, per-channel or per-group weight scales;
 * :func:`sync_status` -- drain a stream and read (and clear) the device error
   word that bounded waits raise; :func:`selftest_wait_timeout` makes one such
   wait run out on purpose, to exercise that path;
@@ -46,12 +52,15 @@ from ._binding import (  # noqa: F401
     RQ_SIGNS_FIRST,
     RQError,
     attn_decode,
+    attn_prefix,
+    attn_prefix_workspace,
     attn_tree,
     attn_tree_workspace,
     fwht_quant,
     fwht_quant_gemm,
     kv_append,
     kv_cache,
+    kv_plan,
     kv_read,
     kv_rotate_quant,
     library_path,
@@ -61,12 +70,13 @@ from ._binding import (  # noqa: F401
     rope_turns,
     selftest_wait_timeout,
     sync_status,
+    w4a16_gemm,
     w4a4_gemm,
     w4a8_gemm,
 )
 
 __all__ = ["RQ_A_E4M3", "RQ_ATTN_ROTATED_OUT", "RQ_E4M3_CODES", "RQ_GROUP_SCALES", "RQ_INT4_BYTES", "RQ_INT8_CODES",
            "RQ_KV_ROTATED_OUT", "RQ_ROPE_INTERLEAVED", "RQ_ROPE_INVERSE", "RQ_SIGNS_FIRST", "RQError",
-           "attn_decode", "attn_tree", "attn_tree_workspace", "fwht_quant", "fwht_quant_gemm", "kv_append",
-           "kv_cache", "kv_read", "kv_rotate_quant", "library_path", "load_library", "probe_f8_mma", "rope",
-           "rope_turns", "selftest_wait_timeout", "sync_status", "w4a4_gemm", "w4a8_gemm"]
+           "attn_decode", "attn_prefix", "attn_prefix_workspace", "attn_tree", "attn_tree_workspace", "fwht_quant",
+           "fwht_quant_gemm", "kv_append", "kv_cache", "kv_plan", "kv_read", "kv_rotate_quant",
+           "library_path", "load_library", "probe_f8_mma", "rope", "rope_turns", "selftest_wait_timeout", "sync_status", "w4a16_gemm", "w4a4_gemm", "w4a8_gemm"]

@@ -81,6 +81,15 @@ def load_library() -> ctypes.CDLL:
     lib.rq_attn_tree.restype = i32
     lib.rq_attn_tree.argtypes = [P, i64, i64, i32, i64, i64, i64, P, P, P, P, i64, i64, i64, P, i64, P, P, i64, i64,
                                  P, i64, u64, u32, f32, P, P, i64, P]
+    lib.rq_kv_plan.restype = i32
+    lib.rq_kv_plan.argtypes = [P, P, P, i64, P, i64, P, i64, P, i64, i64, P, P, P, P, P]
+    lib.rq_attn_prefix_workspace.restype = i64
+    lib.rq_attn_prefix_workspace.argtypes = [i64, i64, i64]
+    lib.rq_attn_prefix.restype = i32
+    lib.rq_attn_prefix.argtypes = [P, i64, i64, i32, i64, i64, i64, P, P, P, P, i64, i64, i64, P, i64, P, P, i64,
+                                   P, i64, P, P, i64, i64, P, i64, u64, u32, f32, P, P, i64, P]
+    lib.rq_w4a16_gemm.restype = i32
+    lib.rq_w4a16_gemm.argtypes = [P, i32, i64, i64, i64, P, P, i64, i64, P, i32, P]
     lib.rq_sync_status.restype = i32
     lib.rq_sync_status.argtypes = [P]
     lib.rq_selftest_wait_timeout.restype = i32
@@ -569,10 +578,57 @@ def _cache_parts(cache, head_dim=None):
     return kq, ks, vq, vs, shape
 
 
-def _expect_table(t):
+def _expect_table(t, name: str = "block_table"):
     if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_contiguous():
-        raise ValueError("block_table must be a contiguous int32 tensor [seqs][width]")
+        raise ValueError(f"{name} must be a contiguous int32 tensor [seqs][width]")
     return t.shape
+
+
+def kv_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+            total: int, page_size: int, *, head=None, base=None, out=None, stream=None):
+    """Block tables and slots of a step from the requests' lengths, on the GPU.  Request b has context_lens[b] tokens in
+    the cache and gets new_lens[b] more (int32 [seqs]).  Its row of block_table (int32 [seqs][width], changed in place)
+    keeps the entries of the pages that hold the former; the pages that the latter need beside them come from
+    free_pages (int32, in its order from entry head[0], int32 [1], on; None: 0); entries behind are set to -1.
+
+    Returns (offsets, slots, positions, head'), or fills the four given as `out`: offsets int32 [seqs + 1], the first
+    row of each request's new tokens among the step's `total` rows; slots int64 [total] for :func:`kv_append`; positions
+    int64 [total], the token's place plus base[b] (int32 [seqs], the tokens of a shared prefix; None: 0); head' int32
+    [1], the free list's entry for the next step.  Rows behind the last token get slot -1 and position 0.  Where
+    free_pages or the table's width does not suffice, entries and slots are -1, and head' passes len(free_pages)
+    in the first case."""
+    lib = _lib or load_library()
+    B, W = _expect_table(block_table)
+    _expect_vector(context_lens, "context_lens", torch.int32, B, "int32 tensor [seqs]")
+    _expect_vector(new_lens, "new_lens", torch.int32, B, "int32 tensor [seqs]")
+    if free_pages.dtype is not torch.int32 or free_pages.dim() != 1 or not free_pages.is_contiguous():
+        raise ValueError("free_pages must be a contiguous 1-D int32 tensor")
+    dev, device = block_table.get_device(), block_table.device
+    _one_device(dev, context_lens, new_lens, free_pages)
+    hp = bp = None
+    if head is not None:
+        _expect_vector(head, "head", torch.int32, 1, "int32 tensor [1]")
+        _one_device(dev, head)
+        hp = head.data_ptr()
+    if base is not None:
+        _expect_vector(base, "base", torch.int32, B, "int32 tensor [seqs]")
+        _one_device(dev, base)
+        bp = base.data_ptr()
+    if total < 0:
+        raise ValueError("total must not be negative")
+    if out is None:
+        out = (_empty(B + 1, torch.int32, device, stream), _empty(total, torch.int64, device, stream),
+               _empty(total, torch.int64, device, stream), _empty(1, torch.int32, device, stream))
+    else:
+        for t, name, n, dt in zip(out, ("offsets", "slots", "positions", "head"), (B + 1, total, total, 1),
+                                  (torch.int32, torch.int64, torch.int64, torch.int32), strict=True):
+            _expect(t, f"out ({name})", (n,), dt)
+        _one_device(dev, *out)
+    offsets, slots, positions, after = out
+    _call(lib.rq_kv_plan, "rq_kv_plan", dev, stream, context_lens.data_ptr(), new_lens.data_ptr(), bp, B,
+          block_table.data_ptr(), W, free_pages.data_ptr(), free_pages.shape[0], hp, page_size, total,
+          offsets.data_ptr(), slots.data_ptr(), positions.data_ptr(), after.data_ptr())
+    return offsets, slots, positions, after
 
 
 def kv_append(k, v, cache: dict, slots: torch.Tensor, seed: int, flags: int = RQ_SIGNS_FIRST, *, positions=None,
@@ -647,16 +703,9 @@ def attn_tree_workspace(head_dim: int) -> int:
     return int(load_library().rq_attn_tree_workspace(head_dim))
 
 
-def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_lens: torch.Tensor,
-              offsets: torch.Tensor, seed: int, flags: int = RQ_SIGNS_FIRST, *, tree_mask=None, max_nodes=None,
-              softmax_scale=None, out=None, workspace=None, stream=None):
-    """Attention of trees of drafted tokens over the paged cache.  Rows offsets[b] .. offsets[b + 1] - 1 of q
-    ([rows][q_heads][head_dim], strided views welcome) are the nodes of sequence b, whose keys and values lie in the
-    cache at places context_lens[b], context_lens[b] + 1, ...  A node sees the context and the nodes that its row of
-    tree_mask (bool [rows][width], width >= the largest tree) names; without a mask, itself and those before it.
-    max_nodes bounds the nodes of a sequence (default: the mask's width, or the number of rows).  One node per sequence
-    is a plain decode step.  Returns [rows][q_heads][head_dim] of q's dtype; rows that see nothing are 0, rows of no
-    sequence are not written.  The result carries no gradient."""
+def _attn_paged(entry, q, cache, block_table, context_lens, offsets, seed, flags, tree_mask, max_nodes, softmax_scale,
+                out, workspace, stream, prefix):
+    """The calls of attn_tree (prefix None) and attn_prefix (prefix: its table, lengths and groups)."""
     lib = _lib or load_library()
     qshape, qs = _expect_heads(q, "q")
     N, Hq, D = qshape
@@ -687,21 +736,99 @@ def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_l
         _expect(out, "out", (N, Hq, D), dtype)
         _one_device(dev, out)
     _one_device(dev, kq, ks, vq, vs, block_table, context_lens, offsets)
+    extra = ()
+    if prefix is not None:
+        table, lens, groups = prefix
+        G, PW = _expect_table(table, "prefix_table")
+        _expect_vector(lens, "prefix_lens", torch.int32, G, "int32 tensor [groups]")
+        _expect_vector(groups, "groups", torch.int32, G + 1, "int32 tensor [groups + 1]")
+        _one_device(dev, table, lens, groups)
+        extra = (table.data_ptr(), PW, lens.data_ptr(), groups.data_ptr(), G)
     if workspace is None:
         need = _workspace_bytes.get((dev, D))
         if need is None:
             with torch.cuda.device(dev):
                 need = _workspace_bytes[dev, D] = lib.rq_attn_tree_workspace(D)
+        if prefix is not None:
+            need += N * Hq * (D + 2) * 4
         workspace = _empty(need, torch.uint8, device, stream)
     else:
         if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor")
         _one_device(dev, workspace)
         need = workspace.numel()
-    _call(lib.rq_attn_tree, "rq_attn_tree", dev, stream, q.data_ptr(), qs[0], qs[1], _DTYPES[dtype], N, Hq, D,
+    _call(getattr(lib, entry), entry, dev, stream, q.data_ptr(), qs[0], qs[1], _DTYPES[dtype], N, Hq, D,
           kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2],
-          block_table.data_ptr(), W, context_lens.data_ptr(), offsets.data_ptr(), B, max_nodes, mask_ptr, mask_stride,
-          seed, flags, D ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(), need)
+          block_table.data_ptr(), W, context_lens.data_ptr(), offsets.data_ptr(), B, *extra, max_nodes, mask_ptr,
+          mask_stride, seed, flags, D ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(),
+          workspace.data_ptr(), need)
+    return out
+
+
+def attn_tree(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_lens: torch.Tensor,
+              offsets: torch.Tensor, seed: int, flags: int = RQ_SIGNS_FIRST, *, tree_mask=None, max_nodes=None,
+              softmax_scale=None, out=None, workspace=None, stream=None):
+    """Attention of trees of drafted tokens over the paged cache.  Rows offsets[b] .. offsets[b + 1] - 1 of q
+    ([rows][q_heads][head_dim], strided views welcome) are the nodes of sequence b, whose keys and values lie in the
+    cache at places context_lens[b], context_lens[b] + 1, ...  A node sees the context and the nodes that its row of
+    tree_mask (bool [rows][width], width >= the largest tree) names; without a mask, itself and those before it.
+    max_nodes bounds the nodes of a sequence (default: the mask's width, or the number of rows).  One node per sequence
+    is a plain decode step.  Returns [rows][q_heads][head_dim] of q's dtype; rows that see nothing are 0, rows of no
+    sequence are not written.  The result carries no gradient."""
+    return _attn_paged("rq_attn_tree", q, cache, block_table, context_lens, offsets, seed, flags, tree_mask, max_nodes,
+                       softmax_scale, out, workspace, stream, None)
+
+
+def attn_prefix_workspace(rows: int, q_heads: int, head_dim: int) -> int:
+    """Bytes of scratch that :func:`attn_prefix` needs on the current device for queries [rows][q_heads][head_dim]."""
+    return int(load_library().rq_attn_prefix_workspace(rows, q_heads, head_dim))
+
+
+def attn_prefix(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context_lens: torch.Tensor,
+                offsets: torch.Tensor, prefix_table: torch.Tensor, prefix_lens: torch.Tensor, groups: torch.Tensor,
+                seed: int, flags: int = RQ_SIGNS_FIRST, *, tree_mask=None, max_nodes=None, softmax_scale=None, out=None,
+                workspace=None, stream=None):
+    """:func:`attn_tree` for groups of sequences that share a prefix, which is read once for all of them.  Sequences
+    groups[g] .. groups[g + 1] - 1 (groups int32 [n_groups + 1]) have the prefix_lens[g] tokens (int32 [n_groups]) on the
+    pages of prefix_table's row g (int32 [n_groups][width]) before their own, and every node sees them.  block_table and
+    context_lens name a sequence's own tokens, on pages of its own; so do the places of its nodes.  Rotary
+    positions count the prefix (:func:`kv_plan`'s base).  Sequences of no group have no prefix.  The other arguments and
+    the result are those of :func:`attn_tree`."""
+    return _attn_paged("rq_attn_prefix", q, cache, block_table, context_lens, offsets, seed, flags, tree_mask, max_nodes,
+                       softmax_scale, out, workspace, stream, (prefix_table, prefix_lens, groups))
+
+
+def w4a16_gemm(x: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor, *, out_dtype=None, out=None, stream=None):
+    """x (M x K, M <= 64; bf16, fp16 or fp32, unit stride in the last dimension) by w_q (N x K/2 packed INT4): y (M x N)
+    of out_dtype (default: x's), activations not quantised.  w_scales of shape (N,) are per channel, (N, K/128) per group
+    of 128 (:func:`fwht_quant` with RQ_GROUP_SCALES on the rows of W^T).  The rows are in the basis of the weights'
+    fold: rotated ones for weights from :func:`fwht_quant`.  The result carries no gradient."""
+    lib = _lib or load_library()
+    xs, ws = x.shape, w_q.shape
+    if len(xs) != 2 or (x.stride(1) != 1 and xs[1] != 1):
+        raise ValueError("x must be 2-D with unit stride in the last dimension")
+    M, K = xs
+    dtype, dev = x.dtype, x.get_device()
+    if dtype not in _FLOATS:
+        raise ValueError("x must be float32, bfloat16 or float16")
+    if len(ws) != 2 or ws[1] * 2 != K or w_q.dtype is not torch.uint8 or not w_q.is_contiguous():
+        raise ValueError("w_q must be contiguous uint8 (N x K/2)")
+    N = ws[0]
+    grouped = w_scales.dim() == 2
+    if (w_scales.shape != ((N, K // 128) if grouped else (N,)) or w_scales.dtype is not torch.float32
+            or not w_scales.is_contiguous()):
+        raise ValueError(f"w_scales must be contiguous float32 of shape ({N},) or ({N}, {K // 128})")
+    if out is None:
+        out_dtype = dtype if out_dtype is None else out_dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be float32, bfloat16 or float16")
+        out = _empty((M, N), out_dtype, x.device, stream)
+    else:
+        _expect(out, "out", (M, N), _FLOATS)
+    _one_device(dev, w_q, w_scales, out)
+    _call(lib.rq_w4a16_gemm, "rq_w4a16_gemm", dev, stream, x.data_ptr(), _DTYPES[dtype], M, K,
+          x.stride(0) if M > 1 else K, w_q.data_ptr(), w_scales.data_ptr(), N, 128 if grouped else K, out.data_ptr(),
+          _DTYPES[out.dtype])
     return out
 
 

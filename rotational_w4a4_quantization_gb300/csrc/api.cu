@@ -80,6 +80,32 @@ rq_status check_cache(const rq::PagedCache &c, int64_t head_dim) {
         return RQ_ERR_MISALIGNED;
     return RQ_OK;
 }
+
+// What rq_attn_tree asks of a call; `work`: there is something to do.
+rq_status check_tree(const rq::TreeCall &c, rq_dtype dtype, int64_t workspace_bytes, int64_t need_bytes, bool &work) {
+    work = false;
+    if (c.rows < 0 || c.q_heads <= 0 || c.seqs < 0 || c.max_nodes < 0 || c.width < 0) return RQ_ERR_INVALID_ARG;
+    if (c.flags & ~uint32_t(RQ_SIGNS_FIRST | RQ_ATTN_ROTATED_OUT)) return RQ_ERR_INVALID_ARG;
+    if (!rq::is_rot_input(dtype)) return RQ_ERR_UNSUPPORTED;
+    if (rq_status st = check_cache(c.cache, c.head_dim)) return st;
+    const int64_t kv_heads = c.cache.heads, page_size = c.cache.page_size;
+    if (c.q_heads % kv_heads != 0 || (c.mask && c.mask_stride != 0 && c.mask_stride < c.max_nodes)) return RQ_ERR_INVALID_ARG;
+    // the row index of a page is a TMA coordinate, a row of the tree an int
+    if (c.cache.pages * kv_heads * page_size > 0x7fffffffll || c.seqs > 0x7fffffffll ||
+        c.max_nodes > 0x3fffffffll / c.q_heads || c.width > 0x7fffff00ll / page_size)
+        return RQ_ERR_UNSUPPORTED;
+    if (c.rows == 0 || c.seqs == 0 || c.max_nodes == 0) return RQ_OK;
+    if (c.width < 1 || !c.q || !c.table || !c.contexts || !c.offsets || !c.out) return RQ_ERR_INVALID_ARG;
+    if (!c.workspace || workspace_bytes < need_bytes) return RQ_ERR_INVALID_ARG;
+    const int64_t es = rq::elem_size(dtype);
+    if (!rq::aligned16(c.q) || !rq::aligned16(c.out) || !rq::aligned16(c.workspace) || c.q_token * es % 16 ||
+        c.q_head * es % 16)
+        return RQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(c.table) | reinterpret_cast<uintptr_t>(c.contexts) | reinterpret_cast<uintptr_t>(c.offsets)) & 3u)
+        return RQ_ERR_MISALIGNED;
+    work = true;
+    return RQ_OK;
+}
 }  // namespace
 
 extern "C" {
@@ -297,30 +323,88 @@ rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_str
                        int64_t table_width, const int32_t *context_lens, const int32_t *offsets, int64_t seqs,
                        int64_t max_nodes, const uint8_t *tree_mask, int64_t mask_stride, uint64_t seed, uint32_t flags,
                        float softmax_scale, void *out, void *workspace, int64_t workspace_bytes, void *stream) {
-    if (rows < 0 || q_heads <= 0 || seqs < 0 || max_nodes < 0 || table_width < 0) return RQ_ERR_INVALID_ARG;
-    if (flags & ~uint32_t(RQ_SIGNS_FIRST | RQ_ATTN_ROTATED_OUT)) return RQ_ERR_INVALID_ARG;
-    if (!rq::is_rot_input(dtype)) return RQ_ERR_UNSUPPORTED;
     const rq::PagedCache c{const_cast<uint8_t *>(kq), const_cast<float *>(ks), const_cast<uint8_t *>(vq),
                            const_cast<float *>(vs), pages, kv_heads, page_size};
-    if (rq_status st = check_cache(c, head_dim)) return st;
-    if (q_heads % kv_heads != 0 || (tree_mask && mask_stride != 0 && mask_stride < max_nodes)) return RQ_ERR_INVALID_ARG;
-    // the row index of a page is a TMA coordinate, a row of the tree an int
-    if (pages * kv_heads * page_size > 0x7fffffffll || seqs > 0x7fffffffll || max_nodes > 0x3fffffffll / q_heads ||
-        table_width > 0x7fffff00ll / page_size)
-        return RQ_ERR_UNSUPPORTED;
-    if (rows == 0 || seqs == 0 || max_nodes == 0) return RQ_OK;
-    if (table_width < 1 || !q || !block_table || !context_lens || !offsets || !out) return RQ_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < rq::attn_tree_workspace(head_dim)) return RQ_ERR_INVALID_ARG;
-    const int64_t es = rq::elem_size(dtype);
-    if (!rq::aligned16(q) || !rq::aligned16(out) || !rq::aligned16(workspace) || q_token_stride * es % 16 ||
-        q_head_stride * es % 16)
-        return RQ_ERR_MISALIGNED;
-    if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens) | reinterpret_cast<uintptr_t>(offsets)) & 3u)
-        return RQ_ERR_MISALIGNED;
     const rq::TreeCall call{q, (int)dtype, rows, q_heads, head_dim, q_token_stride, q_head_stride, c, block_table,
                             table_width, context_lens, offsets, seqs, max_nodes, tree_mask, mask_stride, seed, flags,
                             softmax_scale, out, workspace};
+    bool work;
+    if (rq_status st = check_tree(call, dtype, workspace_bytes, rq_attn_tree_workspace(head_dim), work)) return st;
+    if (!work) return RQ_OK;
     cudaError_t e = rq::launch_attn_tree(call, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+rq_status rq_kv_plan(const int32_t *context_lens, const int32_t *new_lens, const int32_t *base, int64_t seqs,
+                     int32_t *block_table, int64_t table_width, const int32_t *free_pages, int64_t free_count,
+                     const int32_t *head, int64_t page_size, int64_t total, int32_t *offsets, int64_t *slots,
+                     int64_t *positions, int32_t *head_out, void *stream) {
+    if (seqs < 0 || table_width < 0 || free_count < 0 || page_size <= 0 || total < 0) return RQ_ERR_INVALID_ARG;
+    if (!rq::pow2(page_size) || page_size < 16 || page_size > 256 || seqs > 65536 || total > 0x7fffffffll ||
+        table_width > 0x7fffff00ll / page_size)
+        return RQ_ERR_UNSUPPORTED;
+    if (!offsets || !head_out || (total && (!slots || !positions)) || (seqs && (!context_lens || !new_lens)) ||
+        (seqs && table_width && !block_table) || (free_count && !free_pages) || head_out == head)
+        return RQ_ERR_INVALID_ARG;
+    const void *words[] = {context_lens, new_lens, base, block_table, free_pages, head, offsets, head_out};
+    for (const void *p : words)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return RQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(positions)) & 7u) return RQ_ERR_MISALIGNED;
+    const rq::PlanCall call{context_lens, new_lens, base, seqs, block_table, table_width, free_pages, free_count,
+                            head, page_size, total, offsets, slots, positions, head_out};
+    cudaError_t e = rq::launch_kv_plan(call, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+int64_t rq_attn_prefix_workspace(int64_t rows, int64_t q_heads, int64_t head_dim) {
+    if (rows < 0 || q_heads < 0 || (q_heads && rows > 0x3fffffffll / q_heads) || !rq::attn_decode_supported(head_dim)) return 0;
+    return rq::attn_prefix_workspace(rows, q_heads, head_dim);
+}
+
+rq_status rq_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_stride, rq_dtype dtype, int64_t rows,
+                         int64_t q_heads, int64_t head_dim, const uint8_t *kq, const float *ks, const uint8_t *vq,
+                         const float *vs, int64_t pages, int64_t kv_heads, int64_t page_size,
+                         const int32_t *block_table, int64_t table_width, const int32_t *context_lens,
+                         const int32_t *offsets, int64_t seqs, const int32_t *prefix_table, int64_t prefix_width,
+                         const int32_t *prefix_lens, const int32_t *groups, int64_t n_groups, int64_t max_nodes,
+                         const uint8_t *tree_mask, int64_t mask_stride, uint64_t seed, uint32_t flags,
+                         float softmax_scale, void *out, void *workspace, int64_t workspace_bytes, void *stream) {
+    const rq::PagedCache c{const_cast<uint8_t *>(kq), const_cast<float *>(ks), const_cast<uint8_t *>(vq),
+                           const_cast<float *>(vs), pages, kv_heads, page_size};
+    const rq::TreeCall call{q, (int)dtype, rows, q_heads, head_dim, q_token_stride, q_head_stride, c, block_table,
+                            table_width, context_lens, offsets, seqs, max_nodes, tree_mask, mask_stride, seed, flags,
+                            softmax_scale, out, workspace};
+    if (n_groups < 0 || prefix_width < 0) return RQ_ERR_INVALID_ARG;
+    bool work;
+    if (rq_status st = check_tree(call, dtype, workspace_bytes, rq_attn_prefix_workspace(rows, q_heads, head_dim), work)) return st;
+    if (rows > 0x3fffffffll / q_heads || n_groups > 0x7fffffffll || prefix_width > 0x7fffff00ll / page_size)
+        return RQ_ERR_UNSUPPORTED;
+    if (!work) return RQ_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (n_groups == 0) {
+        e = rq::launch_attn_tree(call, s);
+    } else {
+        if (prefix_width < 1 || !prefix_table || !prefix_lens || !groups) return RQ_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(prefix_table) | reinterpret_cast<uintptr_t>(prefix_lens) | reinterpret_cast<uintptr_t>(groups)) & 3u)
+            return RQ_ERR_MISALIGNED;
+        e = rq::launch_attn_prefix(call, {prefix_table, prefix_width, prefix_lens, groups, n_groups}, s);
+    }
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+rq_status rq_w4a16_gemm(const void *x, rq_dtype x_dtype, int64_t M, int64_t K, int64_t ld_x, const uint8_t *w_q,
+                        const float *w_scales, int64_t N, int64_t group, void *y, rq_dtype y_dtype, void *stream) {
+    if (M < 0 || N < 0 || K <= 0 || group <= 0 || (ld_x < K && ld_x != 0)) return RQ_ERR_INVALID_ARG;
+    if (!rq::is_rot_input(x_dtype) || !rq::is_rot_input(y_dtype)) return RQ_ERR_UNSUPPORTED;
+    if (K % 128 != 0 || (group != 128 && group != K) || M > 64 || N > 0x7fffffffll) return RQ_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return RQ_OK;
+    if (!x || !w_q || !w_scales || !y) return RQ_ERR_INVALID_ARG;
+    if (!rq::aligned16(x) || !rq::aligned16(w_q) || !rq::aligned16(y) || ld_x * rq::elem_size(x_dtype) % 16 != 0 ||
+        (reinterpret_cast<uintptr_t>(w_scales) & 3u))
+        return RQ_ERR_MISALIGNED;
+    const rq::W16Call call{x, (int)x_dtype, M, K, ld_x, w_q, w_scales, N, group, y, (int)y_dtype};
+    cudaError_t e = rq::launch_w4a16_gemm(call, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }
 

@@ -1,0 +1,44 @@
+// attn_prefix.cu -- attention of sequences that share a prefix, over the paged rotated INT4
+// cache (sm_103a).
+//
+//   out = softmax([e_prefix, e_own]) [v^_prefix; v^_own] R^T
+// with the scores of attn_tree_mma.cuh.  The softmax over both is that of either with its
+// reference z and sum l, joined:  z = max(z1, z2), l = l1 2^(z1 - z) + l2 2^(z2 - z), and O
+// alike.  So the prefix is read once for all rows of its group: a first pass takes the groups
+// for sequences, with the rows of all their sequences as nodes that see every token, and
+// leaves O, z and l of each row in fp32; the second goes over each sequence's own tokens and
+// begins each row from there.  Both are the kernels of tree attention, which choose their
+// blocks by the rows of the pass.
+#include "attn_tree_mma.cuh"
+
+namespace rq {
+namespace {
+
+cudaError_t launch_tree_pass(const TreePass &pass, cudaStream_t stream) {
+    if (attn_tree_tc_supported(pass.call)) return launch_tree_pass_tc(pass, stream);
+    TreePassParams p;
+    if (!tree_params(pass, p)) return cudaErrorUnknown;
+    return launch_tree_mma(pass.call, p, stream);
+}
+
+}  // namespace
+
+// The kernels' scratch (a multiple of 16 bytes), then the state.
+int64_t attn_prefix_workspace(int64_t rows, int64_t q_heads, int64_t head_dim) {
+    return attn_tree_workspace(head_dim) + rows * q_heads * (head_dim + 2) * (int64_t)sizeof(float);
+}
+
+cudaError_t launch_attn_prefix(const TreeCall &c, const PrefixCall &prefix, cudaStream_t stream) {
+    float *const state = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + attn_tree_workspace(c.head_dim));
+    TreePass first{c, prefix.groups, c.seqs, state}, second{c, nullptr, 0, state};
+    first.call.table = prefix.table;
+    first.call.width = prefix.width;
+    first.call.contexts = prefix.lens;
+    first.call.seqs = prefix.n_groups;
+    first.call.max_nodes = c.rows;
+    first.call.mask = nullptr;
+    const cudaError_t e = launch_tree_pass(first, stream);
+    return e == cudaSuccess ? launch_tree_pass(second, stream) : e;
+}
+
+}  // namespace rq

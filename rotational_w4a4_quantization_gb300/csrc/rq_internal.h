@@ -147,6 +147,25 @@ bool attn_tree_tc_supported(const TreeCall &c);
 int64_t attn_tree_tc_workspace(int64_t head_dim);
 cudaError_t launch_attn_tree_tc(const TreeCall &c, cudaStream_t stream);
 
+// The same with a prefix for each group of sequences, in two passes over one state: a row
+// (query row, head) has its running softmax there, O [rows][q_heads][D] and behind them
+// (reference, sum) [rows][q_heads].
+struct PrefixCall {
+    const int32_t *table;           // [groups][width]
+    int64_t width;
+    const int32_t *lens, *groups;   // [n_groups], [n_groups + 1]: first sequences
+    int64_t n_groups;
+};
+struct TreePass {
+    TreeCall call;                  // of the prefixes: groups are its sequences, all rows of one its nodes
+    const int32_t *groups;          // NULL: the pass over the sequences' own tokens
+    int64_t group_seqs;             // sequences that the groups may name
+    float *state;
+};
+int64_t attn_prefix_workspace(int64_t rows, int64_t q_heads, int64_t head_dim);
+cudaError_t launch_attn_prefix(const TreeCall &c, const PrefixCall &prefix, cudaStream_t stream);
+cudaError_t launch_tree_pass_tc(const TreePass &pass, cudaStream_t stream);
+
 // W4A8 product: INT8 activations, INT4 weights, per-channel (group == K) or
 // per-group (group == 128) weight scales.  Per-channel scales with more than 64
 // tokens run on the tensor cores (launch_w4a8_gemm_tc), the rest on mma.sync.
@@ -165,6 +184,36 @@ cudaError_t launch_w4a4_group_tc(const uint8_t *aq_e4m3, const float *sa2, const
                                  int64_t M, int64_t N, int64_t K, void *y, int y_mode, cudaStream_t stream);
 cudaError_t launch_w4a8_gemm(const int8_t *aq, const float *sa, const uint8_t *wq, const float *sw, int64_t M,
                              int64_t N, int64_t K, int64_t group, void *y, int y_mode, cudaStream_t stream);
+
+// W4A16 product: rows of fp32, bf16 or fp16, weights with per-channel (group == K) or
+// per-group (group == 128) scales.
+struct W16Call {
+    const void *x;
+    int in_type;
+    int64_t M, K, ldx;
+    const uint8_t *w;
+    const float *scales;
+    int64_t N, group;
+    void *y;
+    int out_type;               // as in_type
+};
+cudaError_t launch_w4a16_gemm(const W16Call &c, cudaStream_t stream);
+
+// Block tables and slots of a step from the requests' lengths.
+struct PlanCall {
+    const int32_t *contexts, *news, *base;      // base NULL: 0
+    int64_t seqs;
+    int32_t *table;
+    int64_t width;
+    const int32_t *free_pages;
+    int64_t free_count;
+    const int32_t *head;                        // NULL: 0
+    int64_t page_size, total;
+    int32_t *offsets;
+    int64_t *slots, *positions;
+    int32_t *head_out;
+};
+cudaError_t launch_kv_plan(const PlanCall &c, cudaStream_t stream);
 
 // One thread waits on a barrier that nothing arrives on, with the rotation
 // kernels' bounded wait and the given limit: raises the error word on expiry.

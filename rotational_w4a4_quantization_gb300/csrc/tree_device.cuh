@@ -36,6 +36,18 @@ struct TreeParams {
     int per_head;                       // blocks of rows per KV head and sequence that the join has blocks for; 0: see TreeJoin
     int ctas;                           // G
     int *err;
+    static constexpr bool kPass = false;
+};
+
+// One of two passes over a state (see TreePass): a unit that is finished leaves its rows there
+// (out), or a unit's first tile begins with what they hold (in).
+struct TreePassParams : TreeParams {
+    const int32_t *groups;              // out: [seqs + 1] first sequences of the groups that are its sequences
+    int group_seqs;
+    float *state;
+    float2 *state_ml;
+    bool out_pass;
+    static constexpr bool kPass = true;
 };
 
 // Query rows per KV head and sequence on average: what the choice of a kernel goes by.  The
@@ -80,6 +92,16 @@ inline bool tree_params(const TreeCall &c, TreeParams &p) {
     p.err = error_word_device_ptr();
     return p.err != nullptr;
 }
+inline bool tree_params(const TreePass &t, TreePassParams &p) {
+    p = TreePassParams{};
+    if (!tree_params(t.call, static_cast<TreeParams &>(p))) return false;
+    p.groups = t.groups;
+    p.group_seqs = (int)t.group_seqs;
+    p.state = t.state;
+    p.state_ml = reinterpret_cast<float2 *>(t.state + t.call.rows * t.call.q_heads * t.call.head_dim);
+    p.out_pass = t.groups != nullptr;
+    return true;
+}
 inline bool tree_maps(const TreeCall &c, int tile, CUtensorMap &mk, CUtensorMap &mv) {
     const int64_t rows = c.cache.pages * c.cache.heads * c.cache.page_size;
     const int rb = (int)(c.head_dim / 2), box = (int)(c.cache.page_size < tile ? c.cache.page_size : tile);
@@ -117,18 +139,56 @@ struct TreeSeq {
     int mt, nt;        // row blocks, tiles
 };
 
-template <int ROWS, int TT>
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
+// Is this the pass over the groups' prefixes?
+template <class P>
+__device__ __forceinline__ bool out_pass(const P &p) {
+    if constexpr (P::kPass) return p.out_pass;
+    else return false;
+}
+
+template <int ROWS, int TT, class P>
+__device__ __forceinline__ TreeSeq tree_seq(const P &p, int b) {
     TreeSeq s;
-    const int64_t o0 = p.offsets[b], o1 = min((int64_t)p.offsets[b + 1], p.rows);
+    int b0 = b, b1 = b + 1;
+    if constexpr (P::kPass) {
+        if (p.out_pass) {                                          // the rows of a group's sequences
+            b0 = max(0, min(p.groups[b], p.group_seqs));
+            b1 = max(0, min(p.groups[b + 1], p.group_seqs));
+        }
+    }
+    const int64_t o0 = p.offsets[b0], o1 = min((int64_t)p.offsets[b1], p.rows);
     s.row0 = o0;
     s.n = o0 < 0 ? 0 : (int)max((int64_t)0, min(o1 - o0, (int64_t)p.max_nodes));
     const int64_t cap = p.width << p.log_page;
     s.ctx = (int)min((int64_t)max(0, p.contexts[b]), cap);         // what lies past the table is not seen
-    s.len = (int)min((int64_t)s.ctx + s.n, cap);
-    s.mt = (s.n * p.group + ROWS - 1) / ROWS;
+    s.len = out_pass(p) ? s.ctx : (int)min((int64_t)s.ctx + s.n, cap);
+    s.mt = s.len ? (s.n * p.group + ROWS - 1) / ROWS : 0;          // no unit without a tile: the join goes by mt
     s.nt = s.mt ? (s.len + TT - 1) / TT : 0;
     return s;
+}
+
+// The state's place of row `r` of a row block.
+template <int ROWS>
+__device__ __forceinline__ int64_t tree_state(const TreeParams &p, int64_t row0, int mt, int h, int r) {
+    const int gr = mt * ROWS + r;
+    return ((row0 + gr / p.group) * p.kv_heads + h) * p.group + gr % p.group;
+}
+
+// Rows whose group has no prefix, or that belong to none, begin from nothing: what the pass over
+// the prefixes leaves for them.  By all threads of its kernel.
+template <int ROWS, int TT>
+__device__ __forceinline__ void tree_clear(const TreePassParams &p) {
+    const int64_t heads = (int64_t)p.kv_heads * p.group;
+    auto clear = [&](int64_t r0, int64_t r1) {
+        for (int64_t i = r0 * heads + threadIdx.x; i < r1 * heads; i += blockDim.x) p.state_ml[i] = make_float2(-INFINITY, 0.f);
+    };
+    auto row = [&](int g) { return max((int64_t)0, min((int64_t)p.offsets[max(0, min(p.groups[g], p.group_seqs))], p.rows)); };
+    if (blockIdx.x == 0) {
+        clear(0, row(0));
+        clear(row(p.seqs), p.rows);
+    }
+    for (int g = blockIdx.x; g < p.seqs; g += gridDim.x)
+        if (tree_seq<ROWS, TT>(p, g).nt == 0) clear(row(g), row(g + 1));
 }
 
 constexpr int kScan = 128;              // stretches of sequences whose lengths are scanned
@@ -154,8 +214,8 @@ __device__ __forceinline__ int tree_lead(int64_t tiles, int ctas) { return (int)
 __device__ __forceinline__ int64_t unit_length(int lead, const TreeSeq &s) { return s.nt ? s.nt + lead : 0; }
 
 // Fills the line.  Every thread of the block calls it; ends with a block barrier.
-template <int ROWS, int TT>
-__device__ __forceinline__ void tree_scan(const TreeParams &p, TreeLine &line) {
+template <int ROWS, int TT, class P>
+__device__ __forceinline__ void tree_scan(const P &p, TreeLine &line) {
     const int per = (p.seqs + kScan - 1) / kScan;
     if (threadIdx.x < kScan) {
         int64_t tiles = 0, units = 0;
@@ -217,8 +277,8 @@ struct TreeWork {
     bool whole;            // the unit lies in this CTA alone, and this is its last piece
 };
 
-template <int ROWS, int TT>
-__device__ __forceinline__ TreeWork tree_work(const TreeParams &p, const TreeLine &line, int64_t pos, int64_t begin, int64_t end) {
+template <int ROWS, int TT, class P>
+__device__ __forceinline__ TreeWork tree_work(const P &p, const TreeLine &line, int64_t pos, int64_t begin, int64_t end) {
     int lo = 0, hi = kScan;
     while (hi - lo > 1) {                    // the last stretch that begins at or before pos
         const int mid = (lo + hi) >> 1;
@@ -374,8 +434,8 @@ __device__ __forceinline__ void tree_join_may_begin() { asm volatile("griddepcon
 constexpr int join_rows(int rows) { return rows >= 256 ? 2 : 1; }         // rows per warp
 constexpr int join_warps(int rows) { return rows < 16 ? rows : 16; }
 constexpr int kJoinPerSm = 2;          // blocks: three leave registers for fewer loads at once (16 sequences of up to 4k: 76 us for 72)
-template <int IN, int D, int ROWS>
-__global__ void __launch_bounds__(32 * join_warps(ROWS), kJoinPerSm) attn_tree_join_kernel(const __grid_constant__ TreeParams p, int turns) {
+template <int IN, int D, int ROWS, class P>
+__global__ void __launch_bounds__(32 * join_warps(ROWS), kJoinPerSm) attn_tree_join_kernel(const __grid_constant__ P p, int turns) {
     constexpr int E = D / 32, RW = join_rows(ROWS), kJoinWarps = join_warps(ROWS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int begin_row = (blockIdx.y * turns * kJoinWarps + warp) * RW;
@@ -457,6 +517,19 @@ __global__ void __launch_bounds__(32 * join_warps(ROWS), kJoinPerSm) attn_tree_j
     for (int o = 16; o; o >>= 1)
 #pragma unroll
         for (int i = 0; i < RW; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+    if constexpr (P::kPass) {
+        if (p.out_pass) {
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                if (row0 + i >= rows) break;
+                const int64_t at = tree_state<ROWS>(p, u.row0, u.mt, u.h, row0 + i);
+#pragma unroll
+                for (int e = 0; e < E; ++e) p.state[at * D + lane * E + e] = acc[i][e];
+                if (lane == 0) p.state_ml[at] = make_float2(top[i], sum[i]);
+            }
+            continue;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
         const float il = sum[i] == 0.f ? 0.f : 1.f / sum[i];    // nothing visible: zeros
@@ -478,8 +551,8 @@ __global__ void __launch_bounds__(32 * join_warps(ROWS), kJoinPerSm) attn_tree_j
     }
 }
 
-template <int IN, int D, int ROWS>
-cudaError_t launch_tree_join(const TreeParams &p, cudaStream_t stream) {
+template <int IN, int D, int ROWS, class P>
+cudaError_t launch_tree_join(const P &p, cudaStream_t stream) {
     if (p.ctas == 1) return cudaSuccess;                    // every unit lies in it
     const int blocks = p.per_head ? p.seqs * p.kv_heads * p.per_head : p.ctas - 1;
     // one turn per block while the SMs hold them all, counting the rows that there are on
@@ -497,7 +570,7 @@ cudaError_t launch_tree_join(const TreeParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tree_join_kernel<IN, D, ROWS>, p, turns);
+    return cudaLaunchKernelEx(&cfg, attn_tree_join_kernel<IN, D, ROWS, P>, p, turns);
 }
 
 }  // namespace

@@ -21,7 +21,7 @@ import argparse
 
 import torch
 
-from . import attn_tree, kv_append, kv_cache, kv_read, rope, rope_turns, sync_status
+from . import attn_tree, kv_append, kv_cache, kv_plan, kv_read, rope, rope_turns, sync_status
 
 SEED = 0x5EED
 
@@ -45,7 +45,7 @@ class TreeStep:
         self.seqs, self.context, self.nodes, self.page = seqs, context, nodes, page
         width = (context + nodes + page - 1) // page
         self.cache = kv_cache(seqs * width, kv_heads, dim, page, device)
-        self.table = torch.randperm(seqs * width, generator=g).to(torch.int32).view(seqs, width).to(device)
+        free = torch.randperm(seqs * width, generator=g).to(torch.int32).to(device)
         self.turns, self.mscale = rope_turns(dim, device=device)
         mask, depth = zip(*(drafted_tree(nodes, g) for _ in range(seqs)))
         self.mask = torch.cat(mask).to(device)
@@ -55,10 +55,13 @@ class TreeStep:
         rand = lambda rows, h: torch.randn(rows, h, dim, generator=g).to(dtype).to(device)
         self.q = rand(seqs * nodes, heads)
         self.k, self.v = rand(seqs * nodes, kv_heads), rand(seqs * nodes, kv_heads)
-        place = torch.arange(context, device=device).repeat(seqs, 1)
-        kv_append(rand(seqs * context, kv_heads), rand(seqs * context, kv_heads), self.cache, self.slots(place), SEED,
-                  positions=place.flatten(), turns=self.turns, mscale=self.mscale)
-        self.node_slots = self.slots(context + torch.arange(nodes, device=device).repeat(seqs, 1))
+        # pages for the prompts, then for the nodes behind them
+        self.table = torch.full((seqs, width), -1, dtype=torch.int32, device=device)
+        _, slots, place, head = kv_plan(torch.zeros_like(self.contexts), self.contexts, self.table, free, seqs * context, page)
+        kv_append(rand(seqs * context, kv_heads), rand(seqs * context, kv_heads), self.cache, slots, SEED,
+                  positions=place, turns=self.turns, mscale=self.mscale)
+        _, self.node_slots, _, _ = kv_plan(self.contexts, torch.full_like(self.contexts, nodes), self.table, free,
+                                           seqs * nodes, page, head=head)
         self.positions = (context + self.depth).flatten()
         self.out = torch.empty_like(self.q)
 

@@ -511,7 +511,7 @@ rq_status rq_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_s
  *   w_q       [N][K/2] packed INT4 codes, one output channel per row.
  *   w_scales  [N] fp32 (group == K) or [N][K/128] fp32 (group == 128).
  *   M <= 64 rows (RQ_ERR_UNSUPPORTED above: that is work for rq_w4a8_gemm and
- *   rq_w4a4_gemm); N any; K a multiple of 128.
+ *   rq_w4a4_gemm); N any; K a multiple of 128, <= 262144.
  *   y         [M][N] of y_dtype (RQ_F32, RQ_BF16, RQ_F16).
  */
 rq_status rq_w4a16_gemm(const void *x, rq_dtype x_dtype, int64_t M, int64_t K, int64_t ld_x, const uint8_t *w_q,

@@ -397,7 +397,7 @@ rq_status rq_w4a16_gemm(const void *x, rq_dtype x_dtype, int64_t M, int64_t K, i
                         const float *w_scales, int64_t N, int64_t group, void *y, rq_dtype y_dtype, void *stream) {
     if (M < 0 || N < 0 || K <= 0 || group <= 0 || (ld_x < K && ld_x != 0)) return RQ_ERR_INVALID_ARG;
     if (!rq::is_rot_input(x_dtype) || !rq::is_rot_input(y_dtype)) return RQ_ERR_UNSUPPORTED;
-    if (K % 128 != 0 || (group != 128 && group != K) || M > 64 || N > 0x7fffffffll) return RQ_ERR_UNSUPPORTED;
+    if (K % 128 != 0 || (group != 128 && group != K) || M > 64 || N > 0x7fffff00ll || K > 262144) return RQ_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return RQ_OK;
     if (!x || !w_q || !w_scales || !y) return RQ_ERR_INVALID_ARG;
     if (!rq::aligned16(x) || !rq::aligned16(w_q) || !rq::aligned16(y) || ld_x * rq::elem_size(x_dtype) % 16 != 0 ||

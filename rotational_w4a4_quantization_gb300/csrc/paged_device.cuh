@@ -175,6 +175,13 @@ __device__ __forceinline__ void block_sign_words(uint32_t *sign_words, uint64_t 
     }
 }
 
+// (x & mask) ^ flip in one instruction: two constants written out take two.
+__device__ __forceinline__ uint32_t masked_flip(uint32_t x, uint32_t mask, uint32_t flip) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(x), "r"(mask), "r"(flip));
+    return y;
+}
+
 // A word of 8 codes as four pairs (nibbles j and j + 4) of fp16 codes, exactly.  0x6400 | u
 // is 1024 + u, so nibbles 0 and 4 (u = code + 8 after the sign bit's flip) lose 1032;
 // nibbles 1 and 5, which stay four bits up, are 1024 + 16 u: times 1/16, less 72.
@@ -184,7 +191,7 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&r)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
         const uint32_t y = x >> (4 * j);
-        const uint32_t a = (y & 0x000f000fu) ^ 0x64086408u, b = (y & 0x00f000f0u) ^ 0x64806480u;
+        const uint32_t a = masked_flip(y, 0x000f000fu, 0x64086408u), b = masked_flip(y, 0x00f000f0u, 0x64806480u);
         const __half2 ha = __hadd2(*reinterpret_cast<const __half2 *>(&a), m0);
         const __half2 hb = __hfma2(*reinterpret_cast<const __half2 *>(&b), r16, m1);
         r[j] = *reinterpret_cast<const uint32_t *>(&ha);

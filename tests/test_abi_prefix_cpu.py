@@ -112,6 +112,7 @@ def w4a16(lib, x=A16, dt=1, M=4, K=256, ld=256, w=A16, s=A16, N=7, group=128, y=
     (dict(K=192), 2),
     (dict(group=64), 2),
     (dict(M=65), 2),
+    (dict(K=262272, ld=262272), 2),
     (dict(N=1 << 31), 2),
     (dict(x=NULL), 1),
     (dict(w=NULL), 1),

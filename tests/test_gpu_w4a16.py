@@ -39,7 +39,9 @@ def check(x, codes, scales, out_dtype=None, **kw):
 @pytest.mark.parametrize("grouped", [False, True])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 128), (1, 16, 128), (1, 17, 256), (2, 100, 384), (3, 4101, 1024), (5, 15, 2048),
                                    (7, 33, 14336), (8, 1000, 4096), (9, 200, 1152), (16, 129, 4096), (17, 64, 512),
-                                   (31, 50, 1408), (33, 70, 256), (61, 1030, 4096), (64, 256, 8192), (1, 2048, 28672)])
+                                   (31, 50, 1408), (33, 70, 256), (61, 1030, 4096), (64, 256, 8192), (1, 2048, 28672),
+                                   (2, 5000, 16384), (8, 30, 65536), (13, 3000, 8192), (16, 5001, 8192), (24, 700, 28672),
+                                   (3, 20, 262144), (6, 40000, 128), (29, 9000, 1024)])
 def test_shapes(dtype, grouped, M, N, K):
     codes, scales = layer(N, K, grouped, M + N)
     check(randn(M, K, seed=K + M, dtype=dtype).to(DEV), codes, scales)
@@ -98,6 +100,22 @@ def test_magnitudes(dtype, M):
     assert (got[:, 3] == 0).all() and (got[1] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M", [2, 20])
+def test_ends_of_the_range(dtype, M):
+    """Rows near the ends of fp32's range, in one step and in another: what fits the output is right."""
+    K, N = 512, 40
+    codes, scales = layer(N, K, True, 19)
+    scales = torch.full_like(scales, 2.0**-20)
+    x = randn(M, K, seed=20)
+    x /= x.abs().amax()
+    x[:, :128] *= 3e38
+    x[:, 128:256] *= 1e-30
+    x[1] *= 1e-25
+    check(x.to(dtype).to(DEV), codes, scales, torch.float32)
+    check((x[:, 128:256] * 1e-8).to(dtype).to(DEV), codes[:, :64].contiguous(), torch.ones(N, 1, device=DEV), torch.float32)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("M", [3, 30])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
@@ -138,6 +156,20 @@ def test_strides_outputs_streams_and_repeats(M):
     assert torch.equal(y, want)
     assert rq.w4a16_gemm(x[:0], codes, scales).shape == (0, N)
     assert rq.w4a16_gemm(x, codes[:0], scales[:0]).shape == (M, 0)
+
+
+def test_weights_past_32_bits():
+    """Codes, and results, at byte offsets that pass 2^32."""
+    N, K = 140000, 65536
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.ones(N, device=DEV)
+    g = gen(21)
+    for n in (0, 1, 65536, 131071, 131072, 139999):
+        codes[n] = torch.randint(0, 256, (K // 2,), generator=g, dtype=torch.uint8).to(DEV)
+    at = torch.tensor([0, 1, 2, 65536, 131071, 131072, 139998, 139999], device=DEV)
+    x = torch.randint(-3, 4, (2, K), generator=g).to(torch.bfloat16).to(DEV)
+    got = rq.w4a16_gemm(x, codes, scales, out_dtype=torch.float32)
+    assert torch.equal(got[:, at].double(), x.double() @ ref.weights(codes[at], scales[at]).T)
 
 
 def test_nothing_is_written_beside_the_output():

@@ -17,7 +17,7 @@
 //  * an item's sums of 128 products begin from 0 in the tensor core (whose additions are not
 //    rounded to nearest) and are scaled and added in fp32 outside.
 //  * rows that do not fit shared memory, or take long to get there, split K over a cluster of
-//    CTAs, whose sums meet in distributed shared memory; more than 32 rows take the weights
+//    CTAs, whose sums meet in distributed shared memory; more than 16 rows take the weights
 //    again, from L2.
 #include "rq.h"
 #include "rq_internal.h"
@@ -364,7 +364,7 @@ int w16_clusters(int log_ks) {
 
 // How a call is split: the one with the least to do for the fullest CTA, in steps of its 16
 // warps (about 0.35 us): half a step for an item's own cost and one for a block's, the rows'
-// way into shared memory (48 KB a step), four steps for a cluster's meeting.  false: the
+// way into shared memory (16 KB a step), four steps for a cluster's meeting.  false: the
 // rows fit no cluster's shared memory.
 template <int IN, int MT>
 bool w16_split(W16Params &p, size_t &bytes) {
@@ -379,7 +379,7 @@ bool w16_split(W16Params &p, size_t &bytes) {
             const int64_t cw = kGWarps >> log_kw, blocks = (p.N + 16 * cw - 1) / (16 * cw);
             const int each = (steps + (1 << log_kw) - 1) >> log_kw, per = each < kItem ? each : kItem;
             const double cost = (double)((blocks + clusters - 1) / clusters) * ((each + per - 1) / per * (per + 0.5) + 1.0) +
-                                (double)rows / 49152 + (log_ks ? 4.0 : 0.0);
+                                (double)rows / 16384 + (log_ks ? 4.0 : 0.0);
             if (cost >= least) continue;
             least = cost;
             p.log_ks = log_ks;
@@ -428,8 +428,7 @@ cudaError_t launch_w16_m(W16Params p, cudaStream_t stream) {
 
 template <int IN>
 cudaError_t launch_w16(const W16Params &p, cudaStream_t stream) {
-    if (p.M <= 8) return launch_w16_m<IN, 1>(p, stream);
-    return p.M <= 16 ? launch_w16_m<IN, 2>(p, stream) : launch_w16_m<IN, 4>(p, stream);
+    return p.M <= 8 ? launch_w16_m<IN, 1>(p, stream) : launch_w16_m<IN, 2>(p, stream);
 }
 
 }  // namespace

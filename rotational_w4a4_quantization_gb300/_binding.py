@@ -434,6 +434,11 @@ def _expect_vector(t, name: str, dtype, n: int, what: str):
         raise ValueError(f"{name} must be a contiguous {what}")
 
 
+def _is_vector(t, dtype, n: int, dev: int) -> bool:
+    """The same with its device, for the calls that ask all of their tensors first and for the reason only then."""
+    return t.dtype is dtype and t.get_device() == dev and t.shape == (n,) and t.is_contiguous()
+
+
 def _expect_turns(turns, head_dim: int) -> int:
     if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
         raise ValueError("turns must be a contiguous 1-D int64 tensor (rope_turns)")
@@ -584,6 +589,20 @@ def _expect_table(t, name: str = "block_table"):
     return t.shape
 
 
+def _refuse_plan(context_lens, new_lens, free_pages, head, base, B, dev, total):
+    """kv_plan's checks one by one: raises for the one that failed."""
+    _expect_vector(context_lens, "context_lens", torch.int32, B, "int32 tensor [seqs]")
+    _expect_vector(new_lens, "new_lens", torch.int32, B, "int32 tensor [seqs]")
+    if free_pages.dtype is not torch.int32 or free_pages.dim() != 1 or not free_pages.is_contiguous():
+        raise ValueError("free_pages must be a contiguous 1-D int32 tensor")
+    if head is not None:
+        _expect_vector(head, "head", torch.int32, 1, "int32 tensor [1]")
+    if base is not None:
+        _expect_vector(base, "base", torch.int32, B, "int32 tensor [seqs]")
+    _one_device(dev, context_lens, new_lens, free_pages, *(t for t in (head, base) if t is not None))
+    raise ValueError("total must not be negative")
+
+
 def kv_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
             total: int, page_size: int, *, head=None, base=None, out=None, stream=None):
     """Block tables and slots of a step from the requests' lengths, on the GPU.  Request b has context_lens[b] tokens in
@@ -599,34 +618,24 @@ def kv_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: tor
     in the first case."""
     lib = _lib or load_library()
     B, W = _expect_table(block_table)
-    _expect_vector(context_lens, "context_lens", torch.int32, B, "int32 tensor [seqs]")
-    _expect_vector(new_lens, "new_lens", torch.int32, B, "int32 tensor [seqs]")
-    if free_pages.dtype is not torch.int32 or free_pages.dim() != 1 or not free_pages.is_contiguous():
-        raise ValueError("free_pages must be a contiguous 1-D int32 tensor")
-    dev, device = block_table.get_device(), block_table.device
-    _one_device(dev, context_lens, new_lens, free_pages)
-    hp = bp = None
-    if head is not None:
-        _expect_vector(head, "head", torch.int32, 1, "int32 tensor [1]")
-        _one_device(dev, head)
-        hp = head.data_ptr()
-    if base is not None:
-        _expect_vector(base, "base", torch.int32, B, "int32 tensor [seqs]")
-        _one_device(dev, base)
-        bp = base.data_ptr()
-    if total < 0:
-        raise ValueError("total must not be negative")
+    i32, dev = torch.int32, block_table.get_device()
+    if not (dev >= 0 and _is_vector(context_lens, i32, B, dev) and _is_vector(new_lens, i32, B, dev)
+            and free_pages.dtype is i32 and free_pages.dim() == 1 and free_pages.is_contiguous() and free_pages.get_device() == dev
+            and (head is None or _is_vector(head, i32, 1, dev)) and (base is None or _is_vector(base, i32, B, dev)) and total >= 0):
+        _refuse_plan(context_lens, new_lens, free_pages, head, base, B, dev, total)
     if out is None:
-        out = (_empty(B + 1, torch.int32, device, stream), _empty(total, torch.int64, device, stream),
-               _empty(total, torch.int64, device, stream), _empty(1, torch.int32, device, stream))
+        device = block_table.device
+        out = (_empty((B + 1,), i32, device, stream), _empty((total,), torch.int64, device, stream),
+               _empty((total,), torch.int64, device, stream), _empty((1,), i32, device, stream))
     else:
         for t, name, n, dt in zip(out, ("offsets", "slots", "positions", "head"), (B + 1, total, total, 1),
-                                  (torch.int32, torch.int64, torch.int64, torch.int32), strict=True):
+                                  (i32, torch.int64, torch.int64, i32), strict=True):
             _expect(t, f"out ({name})", (n,), dt)
         _one_device(dev, *out)
     offsets, slots, positions, after = out
-    _call(lib.rq_kv_plan, "rq_kv_plan", dev, stream, context_lens.data_ptr(), new_lens.data_ptr(), bp, B,
-          block_table.data_ptr(), W, free_pages.data_ptr(), free_pages.shape[0], hp, page_size, total,
+    _call(lib.rq_kv_plan, "rq_kv_plan", dev, stream, context_lens.data_ptr(), new_lens.data_ptr(),
+          None if base is None else base.data_ptr(), B, block_table.data_ptr(), W, free_pages.data_ptr(),
+          free_pages.shape[0], None if head is None else head.data_ptr(), page_size, total,
           offsets.data_ptr(), slots.data_ptr(), positions.data_ptr(), after.data_ptr())
     return offsets, slots, positions, after
 
@@ -750,7 +759,7 @@ def _attn_paged(entry, q, cache, block_table, context_lens, offsets, seed, flags
             with torch.cuda.device(dev):
                 need = _workspace_bytes[dev, D] = lib.rq_attn_tree_workspace(D)
         if prefix is not None:
-            need += N * Hq * (D + 2) * 4
+            need = 2 * need + N * Hq * (D + 2) * 4
         workspace = _empty(need, torch.uint8, device, stream)
     else:
         if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():

@@ -8,7 +8,8 @@
 // for sequences, with the rows of all their sequences as nodes that see every token, and
 // leaves O, z and l of each row in fp32; the second goes over each sequence's own tokens and
 // begins each row from there.  Both are the kernels of tree attention, which choose their
-// blocks by the rows of the pass.
+// blocks by the rows of the pass.  The second needs the first's rows only where it finishes its
+// own, so it begins beside the first's end, with scratch of its own.
 #include "attn_tree_mma.cuh"
 
 namespace rq {
@@ -23,13 +24,15 @@ cudaError_t launch_tree_pass(const TreePass &pass, cudaStream_t stream) {
 
 }  // namespace
 
-// The kernels' scratch (a multiple of 16 bytes), then the state.
+// Each pass's scratch (a multiple of 16 bytes), then the state.
 int64_t attn_prefix_workspace(int64_t rows, int64_t q_heads, int64_t head_dim) {
-    return attn_tree_workspace(head_dim) + rows * q_heads * (head_dim + 2) * (int64_t)sizeof(float);
+    return 2 * attn_tree_workspace(head_dim) + rows * q_heads * (head_dim + 2) * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_attn_prefix(const TreeCall &c, const PrefixCall &prefix, cudaStream_t stream) {
-    float *const state = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + attn_tree_workspace(c.head_dim));
+    char *const scratch = static_cast<char *>(c.workspace);
+    const int64_t each = attn_tree_workspace(c.head_dim);
+    float *const state = reinterpret_cast<float *>(scratch + 2 * each);
     TreePass first{c, prefix.groups, c.seqs, state}, second{c, nullptr, 0, state};
     first.call.table = prefix.table;
     first.call.width = prefix.width;
@@ -37,6 +40,7 @@ cudaError_t launch_attn_prefix(const TreeCall &c, const PrefixCall &prefix, cuda
     first.call.seqs = prefix.n_groups;
     first.call.max_nodes = c.rows;
     first.call.mask = nullptr;
+    second.call.workspace = scratch + each;
     const cudaError_t e = launch_tree_pass(first, stream);
     return e == cudaSuccess ? launch_tree_pass(second, stream) : e;
 }

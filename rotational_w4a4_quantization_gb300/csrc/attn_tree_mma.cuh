@@ -103,10 +103,10 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
 // u = code + 8.
 __device__ __forceinline__ void offset_pairs(uint32_t x, uint32_t (&r)[4]) {
     const uint32_t y = x >> 8;
-    r[0] = (x ^ 0x00080008u) & 0x000f000fu;
-    r[1] = (x ^ 0x00800080u) & 0x00f000f0u;
-    r[2] = (y ^ 0x00080008u) & 0x000f000fu;
-    r[3] = (y ^ 0x00800080u) & 0x00f000f0u;
+    r[0] = masked_flip(x, 0x000f000fu, 0x00080008u);
+    r[1] = masked_flip(x, 0x00f000f0u, 0x00800080u);
+    r[2] = masked_flip(y, 0x000f000fu, 0x00080008u);
+    r[3] = masked_flip(y, 0x00f000f0u, 0x00800080u);
 }
 
 // byte address of 16-byte chunk `ch` of row `row` in a tile written by TMA
@@ -219,6 +219,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             tree_note<ROWS, D>(p, s.line, w, begin, end, join);
         }
         tree_noted<ROWS, D>(p, join);
+        if constexpr (P::kPass) pass_wait();
         // no copy outlives the block, also when it gave up
         if (s.abort_flag) {
             const long long t0 = clock64();
@@ -646,6 +647,9 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             for (int e = 0; e < E; ++e) qv[i][e] = s.acc[0][r][lane * E + e] + s.acc[1][r][lane * E + e];
         }
         const bool resumes = P::kPass && !out_pass(p) && w.begins && w.t0 == 0;       // from the pass before
+        if constexpr (P::kPass) {
+            if (resumes) pass_wait();
+        }
         if (!w.begins || resumes) {                         // the pieces before this one
             // 16 rows: rolled, as short calls take their time fetching code
 #pragma unroll(SIDE ? RW : 1)
@@ -712,6 +716,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         }
         cta_sync();                                          // s.acc and s.q are free again
     }
+    if constexpr (P::kPass) pass_wait();
 }
 
 template <int IN, int D, int ROWS, class P>
@@ -721,8 +726,7 @@ cudaError_t launch_tree_d(P &p, const CUtensorMap &mk, const CUtensorMap &mv, cu
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem((const void *)kern, smem, allowed);
     if (e != cudaSuccess) return e;
-    kern<<<p.ctas, kMThreads, smem, stream>>>(mk, mv, p);
-    e = cudaGetLastError();
+    e = launch_tree_kernel(kern, p, kMThreads, smem, stream, mk, mv, p);
     if (e != cudaSuccess) return e;
     return launch_tree_join<IN, D, ROWS>(p, stream);
 }

@@ -198,7 +198,7 @@ __device__ __forceinline__ uint4 operands(uint32_t x, __half2 hi, __half2 lo) {
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
         const uint32_t y = x >> (4 * j);
-        const uint32_t a = (y & 0x000f000fu) ^ 0x64086408u, b = (y & 0x00f000f0u) ^ 0x64806480u;
+        const uint32_t a = masked_flip(y, 0x000f000fu, 0x64086408u), b = masked_flip(y, 0x00f000f0u, 0x64806480u);
         const __half2 ca = __hadd2(*reinterpret_cast<const __half2 *>(&a), m0);
         const __half2 cb = __hfma2(*reinterpret_cast<const __half2 *>(&b), r16, m1);
         const __half2 ha = __hfma2(ca, hi, __hmul2(ca, lo)), hb = __hfma2(cb, hi, __hmul2(cb, lo));
@@ -840,6 +840,7 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
             bool earlier = !w.begins;
             if constexpr (P::kPass) {                  // the first piece goes on from the pass before, the last leaves its rows there
                 const bool resumes = !p.out_pass && w.begins && w.t0 == 0, leaves = p.out_pass && w.whole;
+                if (resumes) pass_wait();
                 if (live && (resumes || leaves)) {
                     const int64_t o = tree_state<ROWS>(p, w.s.row0, w.mt, w.h, brow);
                     if (resumes) {
@@ -1094,6 +1095,7 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
     }
 
     __syncwarp();
+    if constexpr (P::kPass) pass_wait();
     // no MMA outlives the block, also when it gave up
     if (s.abort_flag) {
         const long long t0 = clock64();
@@ -1115,8 +1117,7 @@ cudaError_t launch_tc(P &p, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem((const void *)kern, smem, allowed);
     if (e != cudaSuccess) return e;
-    kern<<<p.ctas, kTcThreads, smem, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_tree_kernel(kern, p, kTcThreads, smem, stream, p);
     if (e != cudaSuccess) return e;
     return launch_tree_join<IN, D, 128 * NT>(p, stream);
 }

@@ -139,6 +139,12 @@ struct TreeSeq {
     int mt, nt;        // row blocks, tiles
 };
 
+// The second of two passes may begin while the first still runs (its launch says so): nothing but
+// the state is handed on.  Every thread of it waits for the first to end, before it reads the
+// state and at the latest before it exits: what follows on the stream is ordered behind the
+// second pass alone.
+__device__ __forceinline__ void pass_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Is this the pass over the groups' prefixes?
 template <class P>
 __device__ __forceinline__ bool out_pass(const P &p) {
@@ -437,6 +443,7 @@ constexpr int kJoinPerSm = 2;          // blocks: three leave registers for fewe
 template <int IN, int D, int ROWS, class P>
 __global__ void __launch_bounds__(32 * join_warps(ROWS), kJoinPerSm) attn_tree_join_kernel(const __grid_constant__ P p, int turns) {
     constexpr int E = D / 32, RW = join_rows(ROWS), kJoinWarps = join_warps(ROWS);
+    if (out_pass(p)) tree_join_may_begin();                 // here: the second pass
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int begin_row = (blockIdx.y * turns * kJoinWarps + warp) * RW;
     bool there_is = true;                                   // unit c, if blocks have units: its notes are old where it is not
@@ -549,6 +556,22 @@ __global__ void __launch_bounds__(32 * join_warps(ROWS), kJoinPerSm) attn_tree_j
         for (int e = 0; e < E; ++e) store_elem<IN>(p.out, at * D + lane * E + e, acc[i][e]);
     }
     }
+}
+
+// Launches a kernel of the schedule: the second of two passes beside the end of the first.
+template <class P, class... Args>
+cudaError_t launch_tree_kernel(void (*kern)(Args...), const P &p, int threads, size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    if constexpr (P::kPass) cfg.numAttrs = p.out_pass ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int IN, int D, int ROWS, class P>

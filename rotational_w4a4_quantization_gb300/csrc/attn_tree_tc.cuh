@@ -833,7 +833,13 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
             const bool live = brow < rows && done;
             // the pieces before this one: fo times what lies in the slot
             const int64_t at_row = (int64_t)tree_slot(w, begin) * ROWS + brow;
-            float *part = p.part + at_row * D;
+            // The pass over the prefixes leaves a stretch's partial as [D / 4][ROWS] pieces of 4 dims, so that
+            // a warp's 32 rows are stored, and read by its join, side by side: 64 sequences with a prompt
+            // of 8k took 65.6 us for both passes with rows of D, 59.8 so.
+            constexpr bool kSide = P::kPass;
+            const bool aside = kSide && out_pass(p);
+            float *part = aside ? p.part + (int64_t)tree_slot(w, begin) * ROWS * D + 4 * brow : p.part + at_row * D;
+            int part_step = aside ? 4 * ROWS : 4, from_step = part_step;
             float2 *ml = reinterpret_cast<float2 *>(p.part + (int64_t)2 * p.ctas * ROWS * D) + at_row;
             const float *from = part;
             const float2 *from_ml = ml;
@@ -846,9 +852,11 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
                     if (resumes) {
                         from = p.state + o * D;
                         from_ml = p.state_ml + o;
+                        from_step = 4;
                     } else {
                         part = p.state + o * D;
                         ml = p.state_ml + o;
+                        part_step = 4;
                     }
                 }
                 earlier = earlier || resumes;
@@ -885,7 +893,7 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
                 if (fo != 0.f) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(from + 32 * c + i);
+                        const float4 y = *reinterpret_cast<const float4 *>(from + (8 * c + i / 4) * from_step);
                         v[i] += y.x * fo;
                         v[i + 1] += y.y * fo;
                         v[i + 2] += y.z * fo;
@@ -905,7 +913,7 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
                         if (live) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4 *>(part + 32 * c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                                *reinterpret_cast<float4 *>(part + (8 * c + i / 4) * part_step) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                         }
                     }
                 }
@@ -1109,6 +1117,79 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
     }
 }
 
+// The join of the pass over the prefixes: of partials as [D / 4][ROWS] pieces, into the state.  As
+// attn_tree_join_kernel, but a thread has a row, and kPieces pieces of it.
+constexpr int kPieces = 2, kSlots = 4;                      // and four partials at a time
+template <int D, int ROWS>
+__global__ void __launch_bounds__(ROWS) attn_pass_join_kernel(const __grid_constant__ TreePassParams p) {
+    tree_join_may_begin();                                  // here: the second pass
+    bool there_is = true;
+    if (p.per_head) {
+        const int b = blockIdx.x / (p.kv_heads * p.per_head);
+        there_is = (int)(blockIdx.x % p.per_head) < tree_seq<ROWS, kTcTT>(p, b).mt;
+    }
+    pass_wait();                                            // the partials are written
+    TreeJoin u{};
+    if (there_is) u = tree_joins<ROWS, D>(p)[blockIdx.x];
+    const int row = threadIdx.x, c0 = u.slot0 >> 1, c1 = u.c1;
+    if (row >= u.rows) return;
+    const float2 *const ml = reinterpret_cast<const float2 *>(p.part + (int64_t)2 * p.ctas * ROWS * D);
+    // no empty stretch: there are none where each CTA has at least a tile
+    auto there = [&](int c) { return c <= c1 && (u.total >= p.ctas || tree_begin(u.total, p.ctas, c) != tree_begin(u.total, p.ctas, c + 1)); };
+    auto slot = [&](int c) { return (int64_t)(c == c0 ? u.slot0 : 2 * c); };
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c)
+        if (there(c)) top = fmaxf(top, ml[slot(c) * ROWS + row].x);
+    float4 acc[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; c += kSlots) {
+        float2 x[kSlots];
+        float4 v[kSlots][kPieces];
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+            const bool on = there(c + k);
+            const int64_t sl = on ? slot(c + k) : 0;
+            const float4 *const from = reinterpret_cast<const float4 *>(p.part) + (sl * (D / 4) + blockIdx.y * kPieces) * ROWS + row;
+            x[k] = on ? ml[sl * ROWS + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) v[k][i] = on ? from[i * ROWS] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+            const float f = x[k].x == -INFINITY ? 0.f : ex2(x[k].x - top);
+            if (f == 0.f) continue;                         // an empty partial adds nothing
+            sum += x[k].y * f;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                acc[i].x += f * v[k][i].x;
+                acc[i].y += f * v[k][i].y;
+                acc[i].z += f * v[k][i].z;
+                acc[i].w += f * v[k][i].w;
+            }
+        }
+    }
+    const int64_t at = tree_state<ROWS>(p, u.row0, u.mt, u.h, row);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) reinterpret_cast<float4 *>(p.state + at * D)[blockIdx.y * kPieces + i] = acc[i];
+    if (blockIdx.y == 0) p.state_ml[at] = make_float2(top, sum);
+}
+template <int D, int ROWS>
+cudaError_t launch_pass_join(const TreePassParams &p, cudaStream_t stream) {
+    if (p.ctas == 1) return cudaSuccess;                    // every unit lies in it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.per_head ? p.seqs * p.kv_heads * p.per_head : p.ctas - 1), D / 4 / kPieces);
+    cfg.blockDim = dim3(ROWS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_pass_join_kernel<D, ROWS>, p);
+}
+
 template <int IN, int D, int NT, int HV, class P>
 cudaError_t launch_tc(P &p, cudaStream_t stream) {
     auto kern = attn_tree_tc_kernel<IN, D, NT, HV, P>;
@@ -1119,6 +1200,9 @@ cudaError_t launch_tc(P &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_tree_kernel(kern, p, kTcThreads, smem, stream, p);
     if (e != cudaSuccess) return e;
+    if constexpr (P::kPass) {
+        if (p.out_pass) return launch_pass_join<D, 128 * NT>(p, stream);
+    }
     return launch_tree_join<IN, D, 128 * NT>(p, stream);
 }
 

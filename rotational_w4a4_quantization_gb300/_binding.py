@@ -759,7 +759,7 @@ def _attn_paged(entry, q, cache, block_table, context_lens, offsets, seed, flags
             with torch.cuda.device(dev):
                 need = _workspace_bytes[dev, D] = lib.rq_attn_tree_workspace(D)
         if prefix is not None:
-            need = 2 * need + N * Hq * (D + 2) * 4
+            need = 2 * need + N * Hq * (D + 4) * 4
         workspace = _empty(need, torch.uint8, device, stream)
     else:
         if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():

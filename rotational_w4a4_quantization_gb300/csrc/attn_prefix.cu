@@ -9,36 +9,43 @@
 // leaves O, z and l of each row in fp32; the second goes over each sequence's own tokens and
 // begins each row from there.  Both are the kernels of tree attention, which choose their
 // blocks by the rows of the pass.  The second needs the first's rows only where it finishes its
-// own, so it begins beside the first's end, with scratch of its own.
+// own, so it begins beside the first's end, with scratch of its own.  Blocks of few rows join
+// the partials that the first pass has left of each of their rows by themselves: its units
+// note for each row where those are.  Blocks of many rows find them joined in the state.
 //
 // Measured, bf16, heads of 128, one token a sequence: 64 sequences with one prompt of 8k and up to
-// 512 own tokens, 32 heads on 8, 60 us (the first pass 28 us and its join, the second 25 us, which
-// overlap); 256 sequences with two prompts of up to 32k and up to 2k own tokens, 64 heads on 8,
-// 392 us, where 264 + 13 and 114 + 6 us are the passes by themselves.  The first is bound by the
-// softmax of its blocks of 256 rows, the second by reading the codes and widening them.
+// 512 own tokens, 32 heads on 8, 56.7 us (with a join between the passes 62.6; the passes by
+// themselves 28 and 25); 256 sequences with two prompts of up to 32k and up to 2k own tokens,
+// 64 heads on 8, 372 us (381; 264 and 114 less what overlaps).  4 sequences with 1000 + 37
+// tokens, fp16: 19.9 us (24.5).  The first pass is bound by the softmax of its blocks of 256
+// rows, the second by its units' starts and ends, some 8 us each, then by the codes.
 #include "attn_tree_mma.cuh"
 
 namespace rq {
 namespace {
 
-cudaError_t launch_tree_pass(const TreePass &pass, cudaStream_t stream) {
+cudaError_t launch_tree_pass(TreePass &pass, cudaStream_t stream) {
     if (attn_tree_tc_supported(pass.call)) return launch_tree_pass_tc(pass, stream);
     TreePassParams p;
     if (!tree_params(pass, p)) return cudaErrorUnknown;
-    return launch_tree_mma(pass.call, p, stream);
+    const cudaError_t e = launch_tree_mma(pass.call, p, stream);
+    pass.out_rows = p.out_rows;
+    pass.out_ctas = p.ctas;
+    return e;
 }
 
 }  // namespace
 
-// Each pass's scratch (a multiple of 16 bytes), then the state.
+// Each pass's scratch (a multiple of 16 bytes), then the state, then the rows' places.
 int64_t attn_prefix_workspace(int64_t rows, int64_t q_heads, int64_t head_dim) {
-    return 2 * attn_tree_workspace(head_dim) + rows * q_heads * (head_dim + 2) * (int64_t)sizeof(float);
+    return 2 * attn_tree_workspace(head_dim) + rows * q_heads * (int64_t)(sizeof(TreePlace) + (head_dim + 2) * sizeof(float));
 }
 
 cudaError_t launch_attn_prefix(const TreeCall &c, const PrefixCall &prefix, cudaStream_t stream) {
     char *const scratch = static_cast<char *>(c.workspace);
     const int64_t each = attn_tree_workspace(c.head_dim);
     float *const state = reinterpret_cast<float *>(scratch + 2 * each);
+    void *const place = state + c.rows * c.q_heads * (c.head_dim + 2);
     TreePass first{c, prefix.groups, c.seqs, state}, second{c, nullptr, 0, state};
     first.call.table = prefix.table;
     first.call.width = prefix.width;
@@ -47,8 +54,14 @@ cudaError_t launch_attn_prefix(const TreeCall &c, const PrefixCall &prefix, cuda
     first.call.max_nodes = c.rows;
     first.call.mask = nullptr;
     second.call.workspace = scratch + each;
-    const cudaError_t e = launch_tree_pass(first, stream);
-    return e == cudaSuccess ? launch_tree_pass(second, stream) : e;
+    // blocks of few rows join the first pass's partials as they take their rows up
+    if (!attn_tree_tc_supported(second.call)) first.place = second.place = place;
+    cudaError_t e = launch_tree_pass(first, stream);
+    if (e != cudaSuccess) return e;
+    second.out_part = static_cast<const float *>(first.call.workspace);
+    second.out_rows = first.out_rows;
+    second.out_ctas = first.out_ctas;
+    return launch_tree_pass(second, stream);
 }
 
 }  // namespace rq

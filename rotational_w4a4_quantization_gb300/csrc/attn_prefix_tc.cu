@@ -4,10 +4,13 @@
 
 namespace rq {
 
-cudaError_t launch_tree_pass_tc(const TreePass &pass, cudaStream_t stream) {
+cudaError_t launch_tree_pass_tc(TreePass &pass, cudaStream_t stream) {
     TreePassParams p;
     if (!tree_params(pass, p)) return cudaErrorUnknown;
-    return launch_tree_tc(pass.call, p, stream);
+    const cudaError_t e = launch_tree_tc(pass.call, p, stream);
+    pass.out_rows = p.out_rows;
+    pass.out_ctas = p.ctas;
+    return e;
 }
 
 }  // namespace rq

@@ -175,6 +175,9 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     }
     const int64_t total = s.line.prefix[kScan];
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
+    if constexpr (P::kPass) {
+        if (begin == end) tree_empty<ROWS, D>(p);
+    }
     int st = 0;
     uint32_t ph = 0;
 
@@ -214,6 +217,12 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 if (++st == kStages) {
                     st = 0;
                     ph ^= 1;
+                }
+            }
+            if constexpr (P::kPass) {
+                if (p.out_pass && p.place) {
+                    tree_place<ROWS>(p, s.line, w, begin, end);
+                    continue;
                 }
             }
             tree_note<ROWS, D>(p, s.line, w, begin, end, join);
@@ -651,33 +660,47 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             if (resumes) pass_wait();
         }
         if (!w.begins || resumes) {                         // the pieces before this one
-            // 16 rows: rolled, as short calls take their time fetching code
-#pragma unroll(SIDE ? RW : 1)
+            // 16 rows, and rows of a pass: rolled, as short calls take their time fetching code
+#pragma unroll(SIDE && !P::kPass ? RW : 1)
             for (int i = 0; i < RW; ++i) {
                 const int r = i * kCWarps + warp;
+                const float2 *const from_ml = reinterpret_cast<const float2 *>(ml + (slot * ROWS + r) * 2);
+                const float *const from = part + (slot * ROWS + r) * D + lane * E;
                 if constexpr (P::kPass) {
                     if (r >= rows) continue;
-                }
-                const float2 *from_ml = reinterpret_cast<const float2 *>(ml + (slot * ROWS + r) * 2);
-                const float *from = part + (slot * ROWS + r) * D;
-                if constexpr (P::kPass) {
-                    if (resumes) {
-                        const int64_t o = tree_state<ROWS>(p, w.s.row0, w.mt, w.h, r);
-                        from_ml = p.state_ml + o;
-                        from = p.state + o * D;
-                    }
-                }
-                const float2 x = *from_ml;
-                if (r >= rows || x.x == -INFINITY) continue;
+                    const TreeBefore before = resumes ? tree_before<D>(p, tree_state<ROWS>(p, w.s.row0, w.mt, w.h, r))
+                                                      : TreeBefore{from_ml, from_ml, from, from, 0, 0, 1};
+                    float t = top[0], sum = vsum[0], v[E];
 #pragma unroll
-                for (int k = 0; k < RW; ++k)
-                    if (k == i) {
-                        const float t = fmaxf(top[k], x.x), f = ex2(x.x - t), g0 = top[k] == -INFINITY ? 0.f : ex2(top[k] - t);
+                    for (int k = 0; k < RW; ++k)
+                        if (k == i) {
+                            t = top[k];
+                            sum = vsum[k];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) qv[k][e] = (g0 == 0.f ? 0.f : qv[k][e] * g0) + from[lane * E + e] * f;
-                        vsum[k] = (g0 == 0.f ? 0.f : vsum[k] * g0) + x.y * f;
-                        top[k] = t;
-                    }
+                            for (int e = 0; e < E; ++e) v[e] = qv[k][e];
+                        }
+                    tree_onto<E>(before, t, sum, v);
+#pragma unroll
+                    for (int k = 0; k < RW; ++k)
+                        if (k == i) {
+                            top[k] = t;
+                            vsum[k] = sum;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) qv[k][e] = v[e];
+                        }
+                } else {
+                    const float2 x = *from_ml;
+                    if (r >= rows || x.x == -INFINITY) continue;
+#pragma unroll
+                    for (int k = 0; k < RW; ++k)
+                        if (k == i) {
+                            const float t = fmaxf(top[k], x.x), f = ex2(x.x - t), g0 = top[k] == -INFINITY ? 0.f : ex2(top[k] - t);
+#pragma unroll
+                            for (int e = 0; e < E; ++e) qv[k][e] = (g0 == 0.f ? 0.f : qv[k][e] * g0) + from[e] * f;
+                            vsum[k] = (g0 == 0.f ? 0.f : vsum[k] * g0) + x.y * f;
+                            top[k] = t;
+                        }
+                }
             }
         }
         const bool finish = w.whole && !out_pass(p);
@@ -726,8 +749,12 @@ cudaError_t launch_tree_d(P &p, const CUtensorMap &mk, const CUtensorMap &mv, cu
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem((const void *)kern, smem, allowed);
     if (e != cudaSuccess) return e;
+    if constexpr (P::kPass) p.out_rows = p.out_pass ? ROWS : p.out_rows;
     e = launch_tree_kernel(kern, p, kMThreads, smem, stream, mk, mv, p);
     if (e != cudaSuccess) return e;
+    if constexpr (P::kPass) {
+        if (p.out_pass && p.place) return cudaSuccess;      // the pass after it joins
+    }
     return launch_tree_join<IN, D, ROWS>(p, stream);
 }
 

@@ -496,6 +496,9 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
     const uint32_t tO[2] = {tmem + 256, tmem + 256 + (uint32_t)D};
     const int64_t total = s.line.prefix[kScan];
     const int64_t begin = tree_begin(total, p.ctas, blockIdx.x), end = tree_begin(total, p.ctas, blockIdx.x + 1);
+    if constexpr (P::kPass) {
+        if (begin == end) tree_empty<ROWS, D>(p);
+    }
 
     if (warp == 0) {
         // ---------------- scales ----------------
@@ -552,6 +555,12 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
                 }
                 __syncwarp();
                 if (lane == 0) t_mbar_arrive(&s.sc_full[scs]);
+            }
+            if constexpr (P::kPass) {
+                if (p.out_pass && p.place) {
+                    tree_place<ROWS>(p, s.line, w, begin, end);
+                    continue;
+                }
             }
             tree_note<ROWS, D>(p, s.line, w, begin, end, join);
         }
@@ -1198,9 +1207,11 @@ cudaError_t launch_tc(P &p, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem((const void *)kern, smem, allowed);
     if (e != cudaSuccess) return e;
+    if constexpr (P::kPass) p.out_rows = p.out_pass ? 128 * NT : p.out_rows;
     e = launch_tree_kernel(kern, p, kTcThreads, smem, stream, p);
     if (e != cudaSuccess) return e;
     if constexpr (P::kPass) {
+        if (p.out_pass && p.place) return cudaSuccess;      // the pass after it joins
         if (p.out_pass) return launch_pass_join<D, 128 * NT>(p, stream);
     }
     return launch_tree_join<IN, D, 128 * NT>(p, stream);

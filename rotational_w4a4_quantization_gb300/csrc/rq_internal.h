@@ -161,10 +161,13 @@ struct TreePass {
     const int32_t *groups;          // NULL: the pass over the sequences' own tokens
     int64_t group_seqs;             // sequences that the groups may name
     float *state;
+    void *place;                    // for each row and head where its sums are; NULL: in the state
+    const float *out_part;          // the pass over own tokens: the other's scratch, its rows in a block and its CTAs
+    int out_rows, out_ctas;
 };
 int64_t attn_prefix_workspace(int64_t rows, int64_t q_heads, int64_t head_dim);
 cudaError_t launch_attn_prefix(const TreeCall &c, const PrefixCall &prefix, cudaStream_t stream);
-cudaError_t launch_tree_pass_tc(const TreePass &pass, cudaStream_t stream);
+cudaError_t launch_tree_pass_tc(TreePass &pass, cudaStream_t stream);      // sets out_rows and out_ctas
 
 // W4A8 product: INT8 activations, INT4 weights, per-channel (group == K) or
 // per-group (group == 128) weight scales.  Per-channel scales with more than 64

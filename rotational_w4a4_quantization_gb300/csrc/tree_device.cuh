@@ -13,6 +13,7 @@
 #include "paged_device.cuh"
 
 #include <cmath>
+#include <type_traits>
 
 namespace rq {
 namespace {
@@ -39,6 +40,14 @@ struct TreeParams {
     static constexpr bool kPass = false;
 };
 
+// Where the pass over the prefixes has left a row's sums: as partials of its CTAs, as in TreeJoin;
+// in the state, or nowhere.
+struct alignas(8) TreePlace {
+    uint32_t slots;                     // slot0, and the last CTA in the upper half
+    int row;                            // of the block's
+};
+constexpr uint32_t kPlaceState = 0xffffffffu, kPlaceNone = 0xfffffffeu;
+
 // One of two passes over a state (see TreePass): a unit that is finished leaves its rows there
 // (out), or a unit's first tile begins with what they hold (in).
 struct TreePassParams : TreeParams {
@@ -46,6 +55,9 @@ struct TreePassParams : TreeParams {
     int group_seqs;
     float *state;
     float2 *state_ml;
+    TreePlace *place;                   // NULL: a join between the passes leaves every row in the state
+    const float *out_part;              // in: partials of the pass before, of blocks of so many rows, and its CTAs
+    int out_rows, out_ctas;             // (out: set at its launch)
     bool out_pass;
     static constexpr bool kPass = true;
 };
@@ -99,6 +111,10 @@ inline bool tree_params(const TreePass &t, TreePassParams &p) {
     p.group_seqs = (int)t.group_seqs;
     p.state = t.state;
     p.state_ml = reinterpret_cast<float2 *>(t.state + t.call.rows * t.call.q_heads * t.call.head_dim);
+    p.place = static_cast<TreePlace *>(t.place);
+    p.out_part = t.out_part;
+    p.out_rows = t.out_rows;
+    p.out_ctas = t.out_ctas;
     p.out_pass = t.groups != nullptr;
     return true;
 }
@@ -186,7 +202,10 @@ template <int ROWS, int TT>
 __device__ __forceinline__ void tree_clear(const TreePassParams &p) {
     const int64_t heads = (int64_t)p.kv_heads * p.group;
     auto clear = [&](int64_t r0, int64_t r1) {
-        for (int64_t i = r0 * heads + threadIdx.x; i < r1 * heads; i += blockDim.x) p.state_ml[i] = make_float2(-INFINITY, 0.f);
+        for (int64_t i = r0 * heads + threadIdx.x; i < r1 * heads; i += blockDim.x) {
+            if (p.place) p.place[i] = TreePlace{kPlaceNone, 0};
+            else p.state_ml[i] = make_float2(-INFINITY, 0.f);
+        }
     };
     auto row = [&](int g) { return max((int64_t)0, min((int64_t)p.offsets[max(0, min(p.groups[g], p.group_seqs))], p.rows)); };
     if (blockIdx.x == 0) {
@@ -215,6 +234,16 @@ struct TreeLine {
 // each: there the lead would leave some of them without any (one sequence of 512: 16 us
 // without, 18 with 9).
 __device__ __forceinline__ int tree_lead(int64_t tiles, int ctas) { return (int)(tiles / ctas < 8 ? tiles / ctas / 2 : 4); }
+
+// In the passes of shared-prefix attention, whose units are many and short: blocks of few rows
+// give a unit 10 tiles (2, 4, 6, 10, 16 and 28 give 424, 402, 384, 371, 373 and 378 us for
+// 2048 units of up to 17 tiles, 456 CTAs), as far as CTAs are then left with half of their
+// tiles (112 units of up to 24 tiles, 304 CTAs: 3, 5, 7 and 10 give 40.6, 37.0, 39.1 and 42.4).
+template <int ROWS>
+__device__ __forceinline__ int pass_lead(int64_t tiles, int64_t units, int ctas) {
+    constexpr int most = ROWS >= 128 ? 4 : 10;
+    return units >= ctas ? most : (int)min((int64_t)most, tiles / (ctas - units) / 2);
+}
 
 // A unit's length in the line: its tiles, and before them its lead.
 __device__ __forceinline__ int64_t unit_length(int lead, const TreeSeq &s) { return s.nt ? s.nt + lead : 0; }
@@ -246,7 +275,15 @@ __device__ __forceinline__ void tree_scan(const P &p, TreeLine &line) {
         int64_t all = tiles;
 #pragma unroll
         for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        const int lead = tree_lead(all, p.ctas);
+        int lead;
+        if constexpr (P::kPass) {
+            int64_t of = units;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) of += __shfl_xor_sync(0xffffffffu, of, o);
+            lead = pass_lead<ROWS>(all, of, p.ctas);
+        } else {
+            lead = tree_lead(all, p.ctas);
+        }
         const int64_t run = tiles + lead * units;
         int64_t incl = run;
 #pragma unroll
@@ -353,6 +390,91 @@ __device__ __forceinline__ void tree_note(const TreeParams &p, const TreeLine &l
 template <int ROWS, int D>
 __device__ __forceinline__ void tree_noted(const TreeParams &p, const TreeJoin &join) {
     if (!p.per_head && (threadIdx.x & 31) == 0) tree_joins<ROWS, D>(p)[blockIdx.x] = join;
+}
+
+// Instead of both, in the pass over the prefixes: where the pass after it finds the unit's rows.
+template <int ROWS>
+__device__ __forceinline__ void tree_place(const TreePassParams &p, const TreeLine &line, const TreeWork &w, int64_t begin, int64_t end) {
+    if (w.t0 != 0 || w.t1 == 0) return;
+    const int64_t total = line.prefix[kScan], last = w.first + unit_length(line.lead, w.s) - 1;
+    uint32_t slots = kPlaceState;
+    if (last >= end) slots = (uint32_t)tree_slot(w, begin) | (uint32_t)(((last + 1) * p.ctas - 1) / total) << 16;
+    const int rows = min(ROWS, w.s.n * p.group - w.mt * ROWS);
+    for (int r = threadIdx.x & 31; r < rows; r += 32) p.place[tree_state<ROWS>(p, w.s.row0, w.mt, w.h, r)] = TreePlace{slots, r};
+}
+
+// A CTA of that pass without a stretch, where there are more CTAs than tiles: its partials are empty.
+template <int ROWS, int D>
+__device__ __forceinline__ void tree_empty(const TreePassParams &p) {
+    if (!p.out_pass || !p.place) return;
+    float2 *const ml = reinterpret_cast<float2 *>(p.part + (int64_t)2 * p.ctas * ROWS * D) + (int64_t)2 * blockIdx.x * ROWS;
+    for (int r = threadIdx.x; r < ROWS; r += blockDim.x) ml[r] = make_float2(-INFINITY, 0.f);
+}
+
+// What a row's sums are to be joined with: n pairs (reference, sum) at ml + k ml_step, the lane's E
+// dims at from + k step; the first of them by itself.
+struct TreeBefore {
+    const float2 *ml, *ml0;
+    const float *from, *from0;
+    int64_t ml_step, step;
+    int n;
+};
+template <int D>
+__device__ __forceinline__ TreeBefore tree_before(const TreePassParams &p, int64_t at) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const TreePlace u = p.place[at];
+    if (u.slots == kPlaceState) return TreeBefore{p.state_ml + at, p.state_ml + at, p.state + at * D + lane * E, p.state + at * D + lane * E, 0, 0, 1};
+    // within the scratch, whatever groups and offsets that are not in order have left unwritten
+    const int R = p.out_rows, slot0 = min((int)(u.slots & 0xffffu), 2 * p.out_ctas - 1), c0 = slot0 >> 1,
+              c1 = min((int)(u.slots >> 16), p.out_ctas - 1), row = max(0, min(u.row, R - 1));
+    const float2 *const ml = reinterpret_cast<const float2 *>(p.out_part + (int64_t)2 * p.out_ctas * R * D) + row;
+    // blocks of 128 rows and more leave pieces of 4 dims, [D / 4][R]
+    const float *const from = p.out_part + (R >= 128 ? (lane * E / 4 * R + row) * 4 + (lane * E & 3) : row * D + lane * E);
+    return TreeBefore{ml + (int64_t)2 * c0 * R, ml + (int64_t)slot0 * R, from + (int64_t)2 * c0 * R * D, from + (int64_t)slot0 * R * D,
+                      (int64_t)2 * R, (int64_t)2 * R * D, u.slots == kPlaceNone ? 0 : c1 - c0 + 1};
+}
+// By a warp: a row's reference, sum and dims with those before them, in their order.  Few
+// instructions, as each is fetched for the first time here: a version for all rows of a warp at
+// once took 25 us for 20 (4 sequences), 84 for 60 (64 sequences).
+template <int E>
+__device__ __forceinline__ void tree_onto(const TreeBefore &b, float &top, float &sum, float (&acc)[E]) {
+    constexpr int V = E < 4 ? E : 4, KS = 4;                // partials at a time
+    using Vec = typename std::conditional<V == 4, float4, typename std::conditional<V == 2, float2, float>::type>::type;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int base = 0; base < b.n; base += 32) {
+        const int k = base + lane;
+        const float2 x = k < b.n ? (k ? b.ml[k * b.ml_step] : *b.ml0) : make_float2(-INFINITY, 0.f);
+        float t = fmaxf(top, x.x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        const float f = x.x == -INFINITY ? 0.f : ex2(x.x - t), g = top == -INFINITY ? 0.f : ex2(top - t);
+        float add = f == 0.f ? 0.f : x.y * f;               // an empty partial adds nothing
+#pragma unroll
+        for (int o = 16; o; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+        top = t;
+        sum = (g == 0.f ? 0.f : sum * g) + add;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = g == 0.f ? 0.f : acc[e] * g;
+#pragma unroll 1
+        for (int k0 = 0; k0 < min(32, b.n - base); k0 += KS) {
+            Vec y[KS][E / V];
+            float fk[KS];
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                fk[j] = __shfl_sync(0xffffffffu, f, k0 + j);                     // 0: nothing there to read
+                const int kk = base + k0 + j;
+                const float *from = kk ? b.from + kk * b.step : b.from0;
+#pragma unroll
+                for (int v = 0; v < E / V; ++v) y[j][v] = fk[j] != 0.f ? *reinterpret_cast<const Vec *>(from + v * V) : Vec{};
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += fk[j] * reinterpret_cast<const float *>(&y[j][e / V])[e % V];
+        }
+    }
 }
 
 // May query row `r` of the row block see token `t` of the sequence?  Rows past the

@@ -276,3 +276,33 @@ def test_units_of_several_pieces(dtype, seqs, groups, G):
     # a row of such an average is short beside the values that it averages: sum p |v| is below 4 sigma sqrt(D) of them
     err, bound = (got.double() - want).norm(dim=-1), 2 * (8e-6 + 2 * part * (7 / 3)) * 4 * D**0.5 + 2 * paged_ref.UNIT[dtype] * want.norm(dim=-1)
     assert torch.isfinite(want).all() and (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sizes,G", [((2, 1, 3), 4), ((1, 1), 1), ((30, 1, 59), 4), ((300,), 8)])
+@pytest.mark.parametrize("fill", [0, 127, 255])
+def test_tables_wider_than_the_prefixes(dtype, sizes, G, fill):
+    """The launches go by the tables' widths: more blocks than there are tiles, some without any.  Whatever lay in the
+    workspace."""
+    H, D, page = 2, 64, 16
+    seqs = sum(sizes)
+    prefixes, own, counts = [(300, 0, 130)[i] for i in range(len(sizes))], [7 * b % 50 for b in range(seqs)], [1] * seqs
+    cache, table, ptable, groups = batch(list(sizes), prefixes, own, counts, H, page, D, 500)
+    wide = torch.cat([ptable, torch.full((len(sizes), 400), -1, dtype=torch.int32)], 1)
+    ws = torch.full((rq.attn_prefix_workspace(seqs, H * G, D),), fill, dtype=torch.uint8, device=DEV)
+    q = randn(seqs, H * G, D, seed=501, dtype=dtype)
+    got = run(q, cache, table, wide, groups, prefixes, own, counts, workspace=ws)
+    assert torch.equal(got, run(q, cache, table, wide, groups, prefixes, own, counts, workspace=ws))
+    check(q, cache, table, ptable, groups, prefixes, own, counts)
+    check(q, cache, table, wide, groups, prefixes, own, counts, workspace=ws)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("groups,prefix", [(2, 700), (40, 16), (40, 700), (1, 5000)])
+def test_blocks_of_many_own_rows(dtype, groups, prefix):
+    """Trees of 9 nodes and 4 query heads to a KV head: the second pass takes blocks of 128 rows and more too."""
+    H, G, D, n, seqs = 2, 4, 64, 9, 40
+    own, counts = [500 + 3 * b for b in range(seqs)], [n] * seqs
+    cache, table, ptable, bounds = batch([seqs // groups] * groups, [prefix] * groups, own, counts, H, 16, D, 510)
+    q = randn(n * seqs, H * G, D, seed=511, dtype=dtype)
+    check(q, cache, table, ptable, bounds, [prefix] * groups, own, counts, mask=paged_ref.tree_mask(counts, gen(512)), blocks=True)

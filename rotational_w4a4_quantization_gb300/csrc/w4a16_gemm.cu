@@ -18,14 +18,14 @@
 //    rounded to nearest) and are scaled and added in fp32 outside.
 //  * rows that do not fit shared memory, or take long to get there, split K over a cluster of
 //    CTAs, whose sums meet in distributed shared memory; more than 16 rows take the weights
-//    again, from L2 (32 rows at a time spill registers: 61 rows 67 us for 61).
-// Measured, groups of 128: 1 row, 4096 -> 14336, 11.4 us, 2.7 TB/s of weights and scales; 7 rows,
-// 14336 -> 4096, 14.0 us; 16 rows, 8192 -> 28672, 43.2 us, 2.9 TB/s.  What it spends them on there:
+//    again, from L2 (32 rows at a time spill registers: 61 rows 67 us for 60).
+// Measured, groups of 128: 1 row, 4096 -> 14336, 11.2 us, 2.8 TB/s of weights and scales; 7 rows,
+// 14336 -> 4096, 13.5 us; 16 rows, 8192 -> 28672, 42.4 us, 2.9 TB/s.  What it spends them on there:
 // issue slots are 48% busy, 201 instructions for a warp's step of 16 x 128 codes (some 90 to widen
 // them, 16 products, 8 reads of the rows), and 16 warps, all that fit, do not hide the rest.
 // Without the weights' loads it takes 36 us, without products and widening 37, without
 // either 22.  Equal stretches of all steps for each warp, which meet at the end only, were no
-// faster (44.7 us; 1 row 11.9).
+// faster (43.4 us; 1 row 11.9).
 #include "rq.h"
 #include "rq_internal.h"
 #include "paged_device.cuh"
@@ -95,16 +95,21 @@ __device__ __forceinline__ float row_pairs(const RowChunk<IN> &r, uint32_t mask,
         return 1.f;
     } else {
         float x[8];
+        uint32_t top = 0;
         if constexpr (IN == IN_F32) {
             const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
+            for (int j = 0; j < 8; ++j) {
+                x[j] = __uint_as_float(w[j]);
+                top = max(top, w[j] & 0x7fffffffu);
+            }
         } else {
             unpack16<IN_BF16>(r.v[0], x);
+            auto size = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)); };
+            const __nv_bfloat162 m = __hmax2(__hmax2(size(r.v[0].x), size(r.v[0].y)), __hmax2(size(r.v[0].z), size(r.v[0].w)));
+            const uint32_t both = *reinterpret_cast<const uint32_t *>(&m);
+            top = max(both << 16, both & 0xffff0000u);
         }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
         top = __reduce_max_sync(mask, top);
         // 2^ex > the largest; at least what leaves 2^(15 - ex) a float
         const int ex = max(-111, (int)(top >> 23) - 126);

@@ -14,10 +14,10 @@
 // note for each row where those are.  Blocks of many rows find them joined in the state.
 //
 // Measured, bf16, heads of 128, one token a sequence: 64 sequences with one prompt of 8k and up to
-// 512 own tokens, 32 heads on 8, 56.7 us (with a join between the passes 62.6; the passes by
-// themselves 28 and 25); 256 sequences with two prompts of up to 32k and up to 2k own tokens,
-// 64 heads on 8, 372 us (381; 264 and 114 less what overlaps).  4 sequences with 1000 + 37
-// tokens, fp16: 19.9 us (24.5).  The first pass is bound by the softmax of its blocks of 256
+// 512 own tokens, 32 heads on 8, 51.1 us (56.7 with blocks of 256 rows, then with a join between
+// the passes 62.6); 256 sequences with two prompts of up to 32k and up to 2k own tokens,
+// 64 heads on 8, 372 us (with a join 381).  4 sequences with 1000 + 37
+// tokens, fp16: 19.6 us (24.5).  The first pass is bound by the softmax of its blocks of many
 // rows, the second by its units' starts and ends, some 8 us each, then by the codes.
 #include "attn_tree_mma.cuh"
 

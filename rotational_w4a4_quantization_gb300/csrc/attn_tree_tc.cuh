@@ -1224,7 +1224,14 @@ cudaError_t launch_tree_tc(const TreeCall &c, P &p, cudaStream_t stream) {
     if (sms <= 0) return cudaErrorUnknown;
     // two row blocks share each converted tile; fp16 queries keep the second's shared
     // memory for the low parts of q~
-    const int nt = tree_rows(c) > 128 && c.in_type == IN_BF16 ? 2 : 1;
+    int nt = tree_rows(c) > 128 && c.in_type == IN_BF16 ? 2 : 1;
+    // A pass with few tiles for each SM is mostly starts and ends of units, which 128 rows halve: one
+    // prompt, 32 heads on 8, 64 sequences, 256 and 128 rows: 8k tokens (3 tiles of 256 rows for
+    // each SM) 56.7 and 51.3 us, 24k (10) 67 and 66, 32k (13) 74 and 78, 64k (27) 107 and 121.
+    if constexpr (P::kPass) {
+        const int64_t blocks = c.seqs * c.cache.heads * ((tree_rows(c) + 255) / 256);
+        if ((double)blocks * (double)((c.width * c.cache.page_size + kTcTT - 1) / kTcTT) < 10.0 * sms) nt = 1;
+    }
     tree_ctas(c, p, 128 * nt, kTcTT, sms);
     const bool d128 = c.head_dim == 128;
     if (c.in_type == IN_F16)

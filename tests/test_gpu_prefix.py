@@ -306,3 +306,26 @@ def test_blocks_of_many_own_rows(dtype, groups, prefix):
     cache, table, ptable, bounds = batch([seqs // groups] * groups, [prefix] * groups, own, counts, H, 16, D, 510)
     q = randn(n * seqs, H * G, D, seed=511, dtype=dtype)
     check(q, cache, table, ptable, bounds, [prefix] * groups, own, counts, mask=paged_ref.tree_mask(counts, gen(512)), blocks=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("before,sizes,after", [(2, (0, 3, 0, 2), 1), (0, (1, 0), 40), (33, (70, 0, 1), 5)])
+def test_sequences_of_no_group_and_groups_of_none(dtype, before, sizes, after):
+    H, G, D = 2, 4, 64
+    seqs = before + sum(sizes) + after
+    prefixes, own, counts = [130 + 100 * i for i in range(len(sizes))], [11 * b % 160 for b in range(seqs)], [1 + b % 2 for b in range(seqs)]
+    cache, table, ptable, groups = batch(list(sizes), prefixes, own, counts, H, 16, D, 520)
+    check(randn(sum(counts), H * G, D, seed=521, dtype=dtype), cache, table, ptable, groups + before, prefixes, own, counts, pad=2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sizes,prefixes,n", [((300,), (700,), 1), ((70, 40, 90), (2500, 0, 129), 1), ((40, 33), (900, 260), 9)])
+def test_blocks_of_256_rows(D, sizes, prefixes, n):
+    """Tables wide enough for the blocks that long prefixes take; rows that fill the last block in part."""
+    H, G, page, seqs = 2, 4, 16, sum(sizes)
+    own, counts = [(300 if n > 1 else 0) + 13 * b % 200 for b in range(seqs)], [n] * seqs
+    cache, table, ptable, groups = batch(list(sizes), list(prefixes), own, counts, H, page, D, 530)
+    wide = torch.cat([ptable, torch.full((len(sizes), 6200), -1, dtype=torch.int32)], 1)
+    mask = paged_ref.tree_mask(counts, gen(532)) if n > 1 else None
+    check(randn(n * seqs, H * G, D, seed=531, dtype=torch.bfloat16), cache, table, wide, groups, list(prefixes), own, counts,
+          mask=mask, blocks=True)

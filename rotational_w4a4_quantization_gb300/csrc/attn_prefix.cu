@@ -17,7 +17,7 @@
 // 512 own tokens, 32 heads on 8, 51.1 us (56.7 with blocks of 256 rows, then with a join between
 // the passes 62.6); 256 sequences with two prompts of up to 32k and up to 2k own tokens,
 // 64 heads on 8, 372 us (with a join 381).  4 sequences with 1000 + 37
-// tokens, fp16: 19.6 us (24.5).  The first pass is bound by the softmax of its blocks of many
+// tokens, fp16: 17.8 us (24.5).  The first pass is bound by the softmax of its blocks of many
 // rows, the second by its units' starts and ends, some 8 us each, then by the codes.
 #include "attn_tree_mma.cuh"
 

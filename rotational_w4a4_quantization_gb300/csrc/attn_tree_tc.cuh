@@ -1186,7 +1186,7 @@ __global__ void __launch_bounds__(ROWS) attn_pass_join_kernel(const __grid_const
 }
 template <int D, int ROWS>
 cudaError_t launch_pass_join(const TreePassParams &p, cudaStream_t stream) {
-    if (p.ctas == 1) return cudaSuccess;                    // every unit lies in it
+    if (tree_whole(p)) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.per_head ? p.seqs * p.kv_heads * p.per_head : p.ctas - 1), D / 4 / kPieces);
     cfg.blockDim = dim3(ROWS);

@@ -696,9 +696,13 @@ cudaError_t launch_tree_kernel(void (*kern)(Args...), const P &p, int threads, s
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Does every unit lie in one CTA, as there is but one, or no sequence can pass a tile?  Then there
+// is nothing to join (4 sequences with a prompt of 1000 and 37 own tokens: 19.6 to 17.8 us).
+inline bool tree_whole(const TreeParams &p) { return p.ctas == 1 || p.width << p.log_page <= 128; }
+
 template <int IN, int D, int ROWS, class P>
 cudaError_t launch_tree_join(const P &p, cudaStream_t stream) {
-    if (p.ctas == 1) return cudaSuccess;                    // every unit lies in it
+    if (tree_whole(p)) return cudaSuccess;
     const int blocks = p.per_head ? p.seqs * p.kv_heads * p.per_head : p.ctas - 1;
     // one turn per block while the SMs hold them all, counting the rows that there are on
     // average; then blocks take several

@@ -329,3 +329,16 @@ def test_blocks_of_256_rows(D, sizes, prefixes, n):
     mask = paged_ref.tree_mask(counts, gen(532)) if n > 1 else None
     check(randn(n * seqs, H * G, D, seed=531, dtype=torch.bfloat16), cache, table, wide, groups, list(prefixes), own, counts,
           mask=mask, blocks=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seqs,n", [(3, 1), (300, 2), (60, 20)])
+@pytest.mark.parametrize("page,wide", [(128, 1), (16, 8), (16, 9)])
+def test_tables_of_one_tile(dtype, seqs, n, page, wide):
+    """What no sequence can pass is a tile, or one page more; more units than blocks too."""
+    H, G, D = 2, 2, 64
+    own, counts = [(31 * b) % (128 - n + 1) for b in range(seqs)], [n] * seqs
+    cache, table, ptable, groups = batch([seqs], [100], own, counts, H, page, D, 540)
+    table = torch.cat([table, torch.full((seqs, max(0, wide - table.shape[1])), -1, dtype=torch.int32)], 1)
+    mask = paged_ref.tree_mask(counts, gen(542)) if n > 1 else None
+    check(randn(n * seqs, H * G, D, seed=541, dtype=dtype), cache, table, ptable, groups, [100], own, counts, mask=mask, blocks=n > 8)

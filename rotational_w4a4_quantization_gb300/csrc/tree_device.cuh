@@ -155,10 +155,10 @@ struct TreeSeq {
     int mt, nt;        // row blocks, tiles
 };
 
-// The second of two passes may begin while the first still runs (its launch says so): nothing but
-// the state is handed on.  Every thread of it waits for the first to end, before it reads the
-// state and at the latest before it exits: what follows on the stream is ordered behind the
-// second pass alone.
+// The second of two passes may begin while the first still runs (its launch says so): nothing is
+// handed on but the state, the rows' places and the partials.  Every thread of it waits for the
+// first to end, before it reads those and at the latest before it exits: what follows on the
+// stream is ordered behind the second pass alone.
 __device__ __forceinline__ void pass_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Is this the pass over the groups' prefixes?
@@ -392,7 +392,7 @@ __device__ __forceinline__ void tree_noted(const TreeParams &p, const TreeJoin &
     if (!p.per_head && (threadIdx.x & 31) == 0) tree_joins<ROWS, D>(p)[blockIdx.x] = join;
 }
 
-// Instead of both, in the pass over the prefixes: where the pass after it finds the unit's rows.
+// Instead of the join's notes, in the pass over the prefixes: where the pass after it finds the unit's rows.
 template <int ROWS>
 __device__ __forceinline__ void tree_place(const TreePassParams &p, const TreeLine &line, const TreeWork &w, int64_t begin, int64_t end) {
     if (w.t0 != 0 || w.t1 == 0) return;

@@ -198,7 +198,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             int64_t pg = page_of(w.t0);
             for (int tile = w.t0; tile < w.t1; ++tile) {
                 const int64_t next = tile + 1 < w.t1 ? page_of(tile + 1) : -1;
-                const bool go = t_mbar_wait(&s.empty[st], ph ^ 1, &s.abort_flag, p.err);
+                const bool go = t_mbar_wait<P::kPass>(&s.empty[st], ph ^ 1, &s.abort_flag, p.err);
                 const uint32_t valid = __ballot_sync(0xffffffffu, pg >= 0 && go);
                 if (lane == 0) {
                     s.valid[st] = valid;
@@ -332,7 +332,7 @@ attn_tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 
         const uint32_t all = (uint32_t)((1ull << (kTT / min(kTT, 1 << p.log_page))) - 1);
         for (int tile = w.t0; tile < w.t1; ++tile) {
-            const bool ok = __all_sync(0xffffffffu, t_mbar_wait(&s.full[st], ph, &s.abort_flag, p.err));
+            const bool ok = __all_sync(0xffffffffu, t_mbar_wait<false>(&s.full[st], ph, &s.abort_flag, p.err));
             const int tk = warp * 8 * kWT;                            // this warp's tokens of the tile
             const int t_first = tile * kTT + tk;
             if (ok && t_first < w.s.len) {

@@ -239,8 +239,9 @@ __device__ __forceinline__ bool elect_one() {
     return e != 0;
 }
 // t_mbar_wait by a whole warp, with one answer
+template <bool PASS>
 __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag, int *err) {
-    return __all_sync(0xffffffffu, t_mbar_wait(b, parity, abort_flag, err));
+    return __all_sync(0xffffffffu, t_mbar_wait<PASS>(b, parity, abort_flag, err));
 }
 
 // position p of an 8-group of operand columns holds dim kPerm(p) of the group
@@ -543,7 +544,7 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
                 uint32_t chunks = 0;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) chunks |= ((quads >> (4 * c)) & 1) << c;
-                warp_wait(&s.sc_empty[scs], ((sc / kSc) & 1) ^ 1, &s.abort_flag, p.err);
+                warp_wait<P::kPass>(&s.sc_empty[scs], ((sc / kSc) & 1) ^ 1, &s.abort_flag, p.err);
                 if (!FOLD || exact) {
                     const float down = exact ? 1.f : pow2(-ev);
                     reinterpret_cast<float4 *>(s.ks[scs])[lane] = ck;
@@ -581,11 +582,11 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
             const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), J = NT * T;
             at += w.used;
             if (T <= 0) continue;
-            ok = warp_wait(&s.q_full, unit & 1, &s.abort_flag, p.err);
+            ok = warp_wait<P::kPass>(&s.q_full, unit & 1, &s.abort_flag, p.err);
             auto qk = [&](int j) {
                 const int k = NT == 2 ? j >> 1 : j, t = j & 1;
                 const uint32_t i = base + item_of_k<NT>(k), slot = i % kOps;
-                if (NT == 1 || t == 0) ok = ok && warp_wait(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
+                if (NT == 1 || t == 0) ok = ok && warp_wait<P::kPass>(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t b = dk + slot * (S::TILE >> 4);
@@ -608,8 +609,8 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
             for (int j = 0; j < J && ok; ++j) {
                 const int k = NT == 2 ? j >> 1 : j, t = j & 1;
                 const uint32_t i = base + item_of_v<NT>(k, T), slot = i % kOps;
-                if (NT == 1 || t == 0) ok = ok && warp_wait(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
-                ok = ok && warp_wait(&s.p_full[t], pc[t] & 1, &s.abort_flag, p.err);
+                if (NT == 1 || t == 0) ok = ok && warp_wait<P::kPass>(&s.op_full[slot], (i / kOps) & 1, &s.abort_flag, p.err);
+                ok = ok && warp_wait<P::kPass>(&s.p_full[t], pc[t] & 1, &s.abort_flag, p.err);
                 ++pc[t];
                 if (!ok) break;
                 tc_fence_after();
@@ -625,7 +626,7 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
                 // products of different shapes need not run in the order of their issue: the
                 // weights are read before the next scores take their place
                 if (j + 2 < J) {
-                    ok = ok && warp_wait(&s.p_free[t], fc[t] & 1, &s.abort_flag, p.err);
+                    ok = ok && warp_wait<P::kPass>(&s.p_free[t], fc[t] & 1, &s.abort_flag, p.err);
                     ++fc[t];
                     qk(j + 2);
                 }
@@ -743,13 +744,13 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
             for (int j = 0; j < J; ++j) {
                 const int k = NT == 2 ? j >> 1 : j, t = j & 1, blk = NT == 2 ? 128 * t : 0;
                 const uint32_t scs = (sc + k) % kSc, tS = tmem + 128 * t + kHT * team + lanes;
-                bool ok = t_mbar_wait(&s.sc_full[scs], ((sc + k) / kSc) & 1, &s.abort_flag, p.err);
+                bool ok = t_mbar_wait<false>(&s.sc_full[scs], ((sc + k) / kSc) & 1, &s.abort_flag, p.err);
                 const int t0 = (w.t0 + k) * kTcTT + kHT * team;
                 const float2 unit = s.unit[scs];
                 const uint32_t valid = (s.valid[scs] >> (kHT / 16 * team)) & 15u;
                 const float a = unit.x == 0.f ? fac : fac * unit.x, ev = unit.y;
                 const bool plain = unit.x != 0.f && t0 + kHT <= w.s.ctx && valid == 15u;
-                ok = t_mbar_wait(&s.s_full[t], (uses >> t) & 1, &s.abort_flag, p.err) && ok;
+                ok = t_mbar_wait<false>(&s.s_full[t], (uses >> t) & 1, &s.abort_flag, p.err) && ok;
                 ok = __all_sync(0xffffffffu, ok);
                 uses ^= 1u << t;
                 tc_fence_after();
@@ -812,8 +813,8 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
             // ---- the block's sums are complete ----
             const int brow = (NT == 2 ? team * 128 : 0) + row;               // row of the block
             const bool idle = (NT == 2 ? team * 128 : 0) + quarter * 32 >= rows;     // no row of this warp exists
-            bool done = t_mbar_wait(&s.o_full[0], units & 1, &s.abort_flag, p.err);
-            if (J > 1) done = t_mbar_wait(&s.o_full[1], units >> 1, &s.abort_flag, p.err) && done;
+            bool done = t_mbar_wait<false>(&s.o_full[0], units & 1, &s.abort_flag, p.err);
+            if (J > 1) done = t_mbar_wait<false>(&s.o_full[1], units >> 1, &s.abort_flag, p.err) && done;
             units ^= J > 1 ? 3u : 1u;
             done = __all_sync(0xffffffffu, done);
             tc_fence_after();
@@ -1081,8 +1082,8 @@ attn_tree_tc_kernel(const __grid_constant__ P p) {
                 load(i + kConvTeams);
                 pages(i + 2 * kConvTeams);
                 const uint32_t scs = (sc + k) % kSc;
-                bool ok = warp_wait(&s.sc_full[scs], ((sc + k) / kSc) & 1, &s.abort_flag, p.err);
-                ok = warp_wait(&s.op_empty[slot], ((it / kOps) & 1) ^ 1, &s.abort_flag, p.err) && ok;
+                bool ok = warp_wait<P::kPass>(&s.sc_full[scs], ((sc + k) / kSc) & 1, &s.abort_flag, p.err);
+                ok = warp_wait<P::kPass>(&s.op_empty[slot], ((it / kOps) & 1) ^ 1, &s.abort_flag, p.err) && ok;
                 if (ok) {
                     const float2 unit = s.unit[scs];
                     const bool fold = FOLD && unit.x != 0.f;

@@ -520,13 +520,23 @@ constexpr long long kTreeWaitLimit = 4000000000ll;   // ~2 s at 2 GHz
 // Bounded wait.  On expiry it raises the error word and the CTA's abort flag; the
 // caller goes on through its loops (whose later waits return at once), so that
 // barriers between warps still meet.
+// PASS: what is waited for may stand behind warps that are in pass_wait, for as long as the first
+// of two passes takes.  A wait that has run out then stands behind the first pass too, and counts
+// anew from its end (in the first pass nothing is before it).  The warps that go on
+// from the first pass have none of these: they meet at a barrier of theirs before their next wait.
+template <bool PASS>
 __device__ __forceinline__ bool t_mbar_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag, int *err) {
     if (t_mbar_try(b, parity)) return true;
-    const long long t0 = clock64();
+    long long limit = (clock64() + kTreeWaitLimit) & -2ll;         // even: the first count
     while (true) {
         if (t_mbar_try(b, parity)) return true;
         if (*abort_flag) return false;
-        if (clock64() - t0 > kTreeWaitLimit) {
+        if (clock64() > limit) {
+            if (PASS && !(limit & 1)) {
+                pass_wait();
+                limit = (clock64() + kTreeWaitLimit) | 1ll;
+                continue;
+            }
             *abort_flag = 1;
             atomicExch(err, 1);
             return false;

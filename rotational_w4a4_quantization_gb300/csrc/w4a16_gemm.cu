@@ -350,15 +350,20 @@ __global__ void __launch_bounds__(kGThreads, 1) w4a16_kernel(const __grid_consta
             }
 }
 
-// Clusters of 2^log_ks such CTAs that the device holds at once.
+// The current device.
+struct W16Device {
+    int id, sms;
+};
+
+// Clusters of 2^log_ks such CTAs that it holds at once; 0 on error.
 template <int IN, int MT>
-int w16_clusters(int log_ks) {
-    static std::atomic<int> known[4];
-    if (log_ks == 0) return device_sm_count();
-    int n = known[log_ks].load(std::memory_order_relaxed);
-    if (n) return n;
+int w16_clusters(const W16Device &dev, int log_ks) {
+    static std::atomic<int> known[kMaxDevices][4];
+    if (log_ks == 0) return dev.sms;
+    int n = 0;
+    if (dev.id < kMaxDevices && (n = known[dev.id][log_ks].load(std::memory_order_relaxed))) return n;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(device_sm_count() >> log_ks << log_ks);
+    cfg.gridDim = dim3(dev.sms >> log_ks << log_ks);
     cfg.blockDim = dim3(kGThreads);
     cfg.dynamicSmemBytes = kMostBytes;
     cudaLaunchAttribute attr[1];
@@ -370,7 +375,7 @@ int w16_clusters(int log_ks) {
         cudaGetLastError();
         return 0;
     }
-    known[log_ks].store(n, std::memory_order_relaxed);
+    if (dev.id < kMaxDevices) known[dev.id][log_ks].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -379,11 +384,11 @@ int w16_clusters(int log_ks) {
 // way into shared memory (16 KB a step), four steps for a cluster's meeting.  false: the
 // rows fit no cluster's shared memory.
 template <int IN, int MT>
-bool w16_split(W16Params &p, size_t &bytes) {
+bool w16_split(const W16Device &dev, W16Params &p, size_t &bytes) {
     constexpr int RM = 8 * MT, PARTS = IN == IN_F32 ? 2 : 1;
     double least = 1e30;
     for (int log_ks = 0; log_ks <= 3 && (1 << log_ks) <= p.steps; ++log_ks) {
-        const int clusters = w16_clusters<IN, MT>(log_ks), steps = (p.steps + (1 << log_ks) - 1) >> log_ks;
+        const int clusters = w16_clusters<IN, MT>(dev, log_ks), steps = (p.steps + (1 << log_ks) - 1) >> log_ks;
         const int64_t row_bytes = (int64_t)steps * 256 + 64, rows = PARTS * p.rows * row_bytes;
         const int64_t need = (int64_t)sizeof(float) * (2 * kGWarps + (log_ks ? kSumBlocks : 0)) * 16 * RM + rows + (int64_t)steps * RM * sizeof(float);
         if (clusters <= 0 || need > kMostBytes) continue;
@@ -406,7 +411,7 @@ bool w16_split(W16Params &p, size_t &bytes) {
 }
 
 template <int IN, int MT>
-cudaError_t launch_w16_m(W16Params p, cudaStream_t stream) {
+cudaError_t launch_w16_m(const W16Device &dev, W16Params p, cudaStream_t stream) {
     auto kern = w4a16_kernel<IN, MT>;
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem((const void *)kern, kMostBytes, allowed);
@@ -414,12 +419,12 @@ cudaError_t launch_w16_m(W16Params p, cudaStream_t stream) {
     p.steps = (int)(p.K / 128);
     size_t bytes = 0;
     p.rows = (int)(p.M < 8 * MT ? p.M : 8 * MT);
-    while (!w16_split<IN, MT>(p, bytes)) {                                       // fewer rows at a time
-        if constexpr (MT > 1) return launch_w16_m<IN, MT / 2>(p, stream);
+    while (!w16_split<IN, MT>(dev, p, bytes)) {                                       // fewer rows at a time
+        if constexpr (MT > 1) return launch_w16_m<IN, MT / 2>(dev, p, stream);
         if (p.rows == 1) return cudaErrorInvalidValue;
         p.rows /= 2;
     }
-    const int cw = kGWarps >> p.log_kw, most = w16_clusters<IN, MT>(p.log_ks), clusters = p.blocks < most ? p.blocks : most;
+    const int cw = kGWarps >> p.log_kw, most = w16_clusters<IN, MT>(dev, p.log_ks), clusters = p.blocks < most ? p.blocks : most;
     p.block_bytes = p.K / 2 * 16 * cw;
     p.block_scales = (p.grouped ? p.steps : 1) * 16 * cw;
     p.scales4 = p.grouped && p.per == kItem && p.steps % (kItem << p.log_ks) == 0 && reinterpret_cast<uintptr_t>(p.s) % 16 == 0;
@@ -440,7 +445,9 @@ cudaError_t launch_w16_m(W16Params p, cudaStream_t stream) {
 
 template <int IN>
 cudaError_t launch_w16(const W16Params &p, cudaStream_t stream) {
-    return p.M <= 8 ? launch_w16_m<IN, 1>(p, stream) : launch_w16_m<IN, 2>(p, stream);
+    W16Device dev{0, device_sm_count()};
+    if (dev.sms <= 0 || cudaGetDevice(&dev.id) != cudaSuccess) return cudaErrorUnknown;
+    return p.M <= 8 ? launch_w16_m<IN, 1>(dev, p, stream) : launch_w16_m<IN, 2>(dev, p, stream);
 }
 
 }  // namespace

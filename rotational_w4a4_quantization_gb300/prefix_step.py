@@ -11,8 +11,8 @@ projection is:
 3. :func:`rope` turns their queries;
 4. :func:`attn_prefix` attends to the group's prompt, read once for all of it, and to the
    request's own tokens, and leaves the rows in the rotated basis;
-5. :func:`w4a16_gemm` multiplies them with the output weights, into which the heads' rotation
-   is folded (one scale per channel and head).
+5. :func:`w4a16_gemm` multiplies them, 64 at a time, with the output weights, into which the
+   heads' rotation is folded (one scale per channel and head).
 
 Nothing of it waits for the host, so a step can be captured in a CUDA graph and replayed: the
 lengths and the free list's head advance on the device.  Prints the step's time and how far
@@ -83,7 +83,8 @@ class PrefixStep:
         q, _ = rope(self.q, None, at, self.turns, mscale=self.mscale)
         attn_prefix(q, self.cache, self.table, self.contexts, self.offsets, self.prefix_table, self.prefix_lens, self.groups,
                     SEED, RQ_SIGNS_FIRST | RQ_ATTN_ROTATED_OUT, max_nodes=1, out=self.rows, workspace=self.workspace)
-        w4a16_gemm(self.rows.flatten(1), self.w, self.w_scales, out=self.y)
+        for at in range(0, self.seqs, 64):               # as many rows as a product takes
+            w4a16_gemm(self.rows[at:at + 64].flatten(1), self.w, self.w_scales, out=self.y[at:at + 64])
         self.contexts += self.one
         self.head.copy_(head)
         return q, self.rows, self.y

@@ -78,5 +78,6 @@ from ._binding import (  # noqa: F401
 __all__ = ["RQ_A_E4M3", "RQ_ATTN_ROTATED_OUT", "RQ_E4M3_CODES", "RQ_GROUP_SCALES", "RQ_INT4_BYTES", "RQ_INT8_CODES",
            "RQ_KV_ROTATED_OUT", "RQ_ROPE_INTERLEAVED", "RQ_ROPE_INVERSE", "RQ_SIGNS_FIRST", "RQError",
            "attn_decode", "attn_prefix", "attn_prefix_workspace", "attn_tree", "attn_tree_workspace", "fwht_quant",
-           "fwht_quant_gemm", "kv_append", "kv_cache", "kv_plan", "kv_read", "kv_rotate_quant",
-           "library_path", "load_library", "probe_f8_mma", "rope", "rope_turns", "selftest_wait_timeout", "sync_status", "w4a16_gemm", "w4a4_gemm", "w4a8_gemm"]
+           "fwht_quant_gemm", "kv_append", "kv_cache", "kv_plan", "kv_read", "kv_rotate_quant", "library_path",
+           "load_library", "probe_f8_mma", "rope", "rope_turns", "selftest_wait_timeout", "sync_status", "w4a16_gemm",
+           "w4a4_gemm", "w4a8_gemm"]

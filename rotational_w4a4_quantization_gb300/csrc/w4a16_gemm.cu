@@ -170,184 +170,184 @@ __global__ void __launch_bounds__(kGThreads, 1) w4a16_kernel(const __grid_consta
     const int stride = p.per << p.log_kw;                        // steps of an item of all warps
     const int s0 = (int)((int64_t)p.steps * rank >> p.log_ks), ns = (int)((int64_t)p.steps * (rank + 1) >> p.log_ks) - s0;
 
-            // the item on its way: its weights, a step's as soon as the one before it has left their place, and its
-            // scales; steps at .. at + n - 1 of the CTA's, of the block whose lines begin at w0
-            uint4 a[kItem][2];
-            float f[kItem][2];
-            const int at0 = wk * p.per;
-            int at = at0, n, loads = nb;                         // blocks whose items are still to be loaded
-            uint32_t pn = (uint32_t)(blk0 * cw + wc) * 16 + g;
-            const uint8_t *w0;
-            const float *f0;
-            uint32_t w8, f8;                                     // from there to the line 8 channels on
-            auto channels = [&] {                                // past N: the last, never stored
-                const uint32_t ch0 = min(pn, N - 1), next = min(pn + 8, N - 1) - ch0;
-                w0 = p.w + (int64_t)ch0 * (p.K / 2) + (s0 + at0) * 64 + 16 * c;
-                w8 = next * (uint32_t)(p.K / 2);
-                f0 = p.grouped ? p.s + (int64_t)ch0 * p.steps + s0 + at0 : p.s + ch0;
-                f8 = next * (p.grouped ? p.steps : 1);
-            };
-            auto weights = [&](int j) {
+    // the item on its way: its weights, a step's as soon as the one before it has left their place, and its
+    // scales; steps at .. at + n - 1 of the CTA's, of the block whose lines begin at w0
+    uint4 a[kItem][2];
+    float f[kItem][2];
+    const int at0 = wk * p.per;
+    int at = at0, n, loads = nb;                         // blocks whose items are still to be loaded
+    uint32_t pn = (uint32_t)(blk0 * cw + wc) * 16 + g;
+    const uint8_t *w0;
+    const float *f0;
+    uint32_t w8, f8;                                     // from there to the line 8 channels on
+    auto channels = [&] {                                // past N: the last, never stored
+        const uint32_t ch0 = min(pn, N - 1), next = min(pn + 8, N - 1) - ch0;
+        w0 = p.w + (int64_t)ch0 * (p.K / 2) + (s0 + at0) * 64 + 16 * c;
+        w8 = next * (uint32_t)(p.K / 2);
+        f0 = p.grouped ? p.s + (int64_t)ch0 * p.steps + s0 + at0 : p.s + ch0;
+        f8 = next * (p.grouped ? p.steps : 1);
+    };
+    auto weights = [&](int j) {
+        if (j < n) {
+            a[j][0] = ld_weights(w0 + 64 * j);
+            a[j][1] = ld_weights(w0 + w8 + 64 * j);
+        }
+    };
+    auto scales = [&] {
+        if (p.scales4 && n == kItem) {
+            const float4 x = *reinterpret_cast<const float4 *>(f0), y = *reinterpret_cast<const float4 *>(f0 + f8);
+            f[0][0] = x.x; f[1][0] = x.y; f[2][0] = x.z; f[3][0] = x.w;
+            f[0][1] = y.x; f[1][1] = y.y; f[2][1] = y.z; f[3][1] = y.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kItem; ++j)
                 if (j < n) {
-                    a[j][0] = ld_weights(w0 + 64 * j);
-                    a[j][1] = ld_weights(w0 + w8 + 64 * j);
+                    f[j][0] = f0[p.grouped ? j : 0];
+                    f[j][1] = (f0 + f8)[p.grouped ? j : 0];
                 }
-            };
-            auto scales = [&] {
-                if (p.scales4 && n == kItem) {
-                    const float4 x = *reinterpret_cast<const float4 *>(f0), y = *reinterpret_cast<const float4 *>(f0 + f8);
-                    f[0][0] = x.x; f[1][0] = x.y; f[2][0] = x.z; f[3][0] = x.w;
-                    f[0][1] = y.x; f[1][1] = y.y; f[2][1] = y.z; f[3][1] = y.w;
-                } else {
+        }
+    };
+    auto next = [&] {                                    // to the item after this one
+        at += stride;
+        if (at - at0 < ns) {
+            w0 += stride * 64;
+            f0 += p.grouped ? stride : 0;
+        } else {                                         // of the next block
+            w0 += p.block_bytes - (at - stride - at0) * 64;
+            f0 += p.block_scales - (p.grouped ? at - stride - at0 : 0);
+            at = at0;
+            --loads;
+            pn += 16 * cw;
+            if (pn + 8 >= N) channels();
+        }
+        n = loads > 0 ? min(p.per, ns - at) : 0;
+    };
+    channels();
+    n = min(p.per, ns - at);
 #pragma unroll
-                    for (int j = 0; j < kItem; ++j)
-                        if (j < n) {
-                            f[j][0] = f0[p.grouped ? j : 0];
-                            f[j][1] = (f0 + f8)[p.grouped ? j : 0];
-                        }
-                }
-            };
-            auto next = [&] {                                    // to the item after this one
-                at += stride;
-                if (at - at0 < ns) {
-                    w0 += stride * 64;
-                    f0 += p.grouped ? stride : 0;
-                } else {                                         // of the next block
-                    w0 += p.block_bytes - (at - stride - at0) * 64;
-                    f0 += p.block_scales - (p.grouped ? at - stride - at0 : 0);
-                    at = at0;
-                    --loads;
-                    pn += 16 * cw;
-                    if (pn + 8 >= N) channels();
-                }
-                n = loads > 0 ? min(p.per, ns - at) : 0;
-            };
-            channels();
-            n = min(p.per, ns - at);
+    for (int j = 0; j < kItem; ++j) weights(j);
+    scales();
+    // the rows, word by word, while the first items are on their way; 16 threads to a step
+    constexpr int U = IN == IN_F32 ? 4 : 8;
+    for (int ch = threadIdx.x; ch - lane < ns * 16; ch += kGThreads) {       // whole warps
+        const int at = (ch & ~15) + ((ch & 3) << 2) + ((ch >> 2) & 3);       // step, word, lane column
+        const bool there = ch < ns * 16;
+        const char *src = static_cast<const char *>(p.x) + ((int64_t)m0 * p.ldx + (int64_t)s0 * 128 + 8 * (there ? ch : 0)) * ES;
+        for (int mm = 0; mm < M; mm += U) {
+            RowChunk<IN> r[U];
 #pragma unroll
-            for (int j = 0; j < kItem; ++j) weights(j);
-            scales();
-            // the rows, word by word, while the first items are on their way; 16 threads to a step
-            constexpr int U = IN == IN_F32 ? 4 : 8;
-            for (int ch = threadIdx.x; ch - lane < ns * 16; ch += kGThreads) {       // whole warps
-                const int at = (ch & ~15) + ((ch & 3) << 2) + ((ch >> 2) & 3);       // step, word, lane column
-                const bool there = ch < ns * 16;
-                const char *src = static_cast<const char *>(p.x) + ((int64_t)m0 * p.ldx + (int64_t)s0 * 128 + 8 * (there ? ch : 0)) * ES;
-                for (int mm = 0; mm < M; mm += U) {
-                    RowChunk<IN> r[U];
+            for (int u = 0; u < U; ++u)
+                if (mm + u < M) r[u] = row_chunk<IN>(src + (mm + u) * p.ldx * ES, 0);
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (mm + u < M) r[u] = row_chunk<IN>(src + (mm + u) * p.ldx * ES, 0);
+            for (int u = 0; u < U; ++u) {
+                if (mm + u >= M) break;
+                uint4 b[PARTS];
+                const float up = row_pairs<IN, PARTS>(r[u], lane < 16 ? 0x0000ffffu : 0xffff0000u, b);
+                if (!there) continue;
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (mm + u >= M) break;
-                        uint4 b[PARTS];
-                        const float up = row_pairs<IN, PARTS>(r[u], lane < 16 ? 0x0000ffffu : 0xffff0000u, b);
-                        if (!there) continue;
-#pragma unroll
-                        for (int h = 0; h < PARTS; ++h)
-                            *reinterpret_cast<uint4 *>(rows + (h * M + mm + u) * p.row_bytes + at * 16) = b[h];
-                        if (UNIT && (ch & 15) == 0) units[(ch >> 4) * RM + mm + u] = up;
-                    }
-                }
+                for (int h = 0; h < PARTS; ++h)
+                    *reinterpret_cast<uint4 *>(rows + (h * M + mm + u) * p.row_bytes + at * 16) = b[h];
+                if (UNIT && (ch & 15) == 0) units[(ch >> 4) * RM + mm + u] = up;
             }
-            __syncthreads();
+        }
+    }
+    __syncthreads();
 
-            // a lane's row of each n8 tile; what stands for rows that are not there reaches no row that is
-            const uint8_t *row[MT];
+    // a lane's row of each n8 tile; what stands for rows that are not there reaches no row that is
+    const uint8_t *row[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) row[t] = rows + min(8 * t + g, M - 1) * p.row_bytes + 16 * c;
-            float sum[MT][4];
+    for (int t = 0; t < MT; ++t) row[t] = rows + min(8 * t + g, M - 1) * p.row_bytes + 16 * c;
+    float sum[MT][4];
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sum[t][k] = 0.f;
+        for (int k = 0; k < 4; ++k) sum[t][k] = 0.f;
 #pragma unroll 1
-            for (int b = 0; b < nb; ++b) {
+    for (int b = 0; b < nb; ++b) {
 #pragma unroll 1
-                for (int i0 = 0; i0 < ns; i0 += stride) {
-                    float xf[kItem][2];
+        for (int i0 = 0; i0 < ns; i0 += stride) {
+            float xf[kItem][2];
 #pragma unroll
-                    for (int j = 0; j < kItem; ++j)
+            for (int j = 0; j < kItem; ++j)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) xf[j][k] = f[j][k];
-                    const int i1 = i0 + at0, here = n;
-                    next();
-                    scales();
+                for (int k = 0; k < 2; ++k) xf[j][k] = f[j][k];
+            const int i1 = i0 + at0, here = n;
+            next();
+            scales();
 #pragma unroll
-                    for (int j = 0; j < kItem; ++j) {
-                        if (j >= here) {
-                            weights(j);
-                            continue;
-                        }
-                        const uint32_t x0[4] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w}, x1[4] = {a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
-                        float o[MT][4];
+            for (int j = 0; j < kItem; ++j) {
+                if (j >= here) {
+                    weights(j);
+                    continue;
+                }
+                const uint32_t x0[4] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w}, x1[4] = {a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
+                float o[MT][4];
 #pragma unroll
-                        for (int wd = 0; wd < 4; ++wd) {
-                            uint32_t q0[4], q1[4];
-                            code_pairs(x0[wd], q0);
-                            code_pairs(x1[wd], q1);
-                            const uint32_t a0[4] = {q0[0], q1[0], q0[1], q1[1]}, a1[4] = {q0[2], q1[2], q0[3], q1[3]};
+                for (int wd = 0; wd < 4; ++wd) {
+                    uint32_t q0[4], q1[4];
+                    code_pairs(x0[wd], q0);
+                    code_pairs(x1[wd], q1);
+                    const uint32_t a0[4] = {q0[0], q1[0], q0[1], q1[1]}, a1[4] = {q0[2], q1[2], q0[3], q1[3]};
 #pragma unroll
-                            for (int h = PARTS - 1; h >= 0; --h)                 // the small part first
-#pragma unroll
-                                for (int t = 0; t < MT; ++t) {
-                                    const uint4 v = *reinterpret_cast<const uint4 *>(
-                                        row[t] + (uint32_t)i1 * 256u + (uint32_t)(h * M) * p.row_bytes + (j * 256 + wd * 64));
-                                    if (wd == 0 && h == PARTS - 1) mma_w16<true>(o[t], a0, v.x, v.y);
-                                    else mma_w16<false>(o[t], a0, v.x, v.y);
-                                    mma_w16<false>(o[t], a1, v.z, v.w);
-                                }
-                        }
+                    for (int h = PARTS - 1; h >= 0; --h)                 // the small part first
 #pragma unroll
                         for (int t = 0; t < MT; ++t) {
-                            // the weights' scale first: a unit alone may leave fp32's range
-                            float2 e = make_float2(1.f, 1.f);
-                            if constexpr (UNIT) e = *reinterpret_cast<const float2 *>(units + (i1 + j) * RM + 8 * t + 2 * c);
-                            sum[t][0] = fmaf(o[t][0] * xf[j][0], e.x, sum[t][0]);
-                            sum[t][1] = fmaf(o[t][1] * xf[j][0], e.y, sum[t][1]);
-                            sum[t][2] = fmaf(o[t][2] * xf[j][1], e.x, sum[t][2]);
-                            sum[t][3] = fmaf(o[t][3] * xf[j][1], e.y, sum[t][3]);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                row[t] + (uint32_t)i1 * 256u + (uint32_t)(h * M) * p.row_bytes + (j * 256 + wd * 64));
+                            if (wd == 0 && h == PARTS - 1) mma_w16<true>(o[t], a0, v.x, v.y);
+                            else mma_w16<false>(o[t], a0, v.x, v.y);
+                            mma_w16<false>(o[t], a1, v.z, v.w);
                         }
-                        weights(j);
-                    }
                 }
-                // the block's sums, from its warps
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (8 * t + 2 * c + (k & 1) < M) part[b & 1][warp][(8 * t + 2 * c + (k & 1)) * 16 + g + 8 * (k >> 1)] = sum[t][k];
-                        sum[t][k] = 0.f;
-                    }
-                __syncthreads();
-                auto store = [&](int e, int64_t block, float v) {                // element (row, other warp, channel) of a block
-                    const int64_t ch = (block << (log_cw + 4)) + (e & ((16 << log_cw) - 1));
-                    if (ch >= p.N) return;
-                    const int64_t out = (m0 + (e >> (log_cw + 4))) * p.N + ch;
-                    if (p.out == IN_F32) store_elem<IN_F32>(p.y, out, v);
-                    else if (p.out == IN_BF16) store_elem<IN_BF16>(p.y, out, v);
-                    else store_elem<IN_F16>(p.y, out, v);
-                };
-                const int wait = ks > 1 ? kSumBlocks >> log_cw : 1, slot = b % wait, each = M << (log_cw + 4);
-                for (int e = threadIdx.x; e < each; e += kGThreads) {
-                    const float *src = &part[b & 1][((e >> 4) & (cw - 1)) << p.log_kw][(e >> (log_cw + 4)) * 16 + (e & 15)];
-                    float v = 0.f;
-                    for (int w = 0; w < kw; ++w) v += src[w * 16 * RM];
-                    if (ks > 1) sums[slot * each + e] = v;
-                    else store(e, blk0 + b, v);
+                for (int t = 0; t < MT; ++t) {
+                    // the weights' scale first: a unit alone may leave fp32's range
+                    float2 e = make_float2(1.f, 1.f);
+                    if constexpr (UNIT) e = *reinterpret_cast<const float2 *>(units + (i1 + j) * RM + 8 * t + 2 * c);
+                    sum[t][0] = fmaf(o[t][0] * xf[j][0], e.x, sum[t][0]);
+                    sum[t][1] = fmaf(o[t][1] * xf[j][0], e.y, sum[t][1]);
+                    sum[t][2] = fmaf(o[t][2] * xf[j][1], e.x, sum[t][2]);
+                    sum[t][3] = fmaf(o[t][3] * xf[j][1], e.y, sum[t][3]);
                 }
-                if (ks > 1 && (slot == wait - 1 || b == nb - 1)) {               // each CTA adds up its share of the cluster's
-                    cluster_sync();
-                    for (int e = rank * kGThreads + threadIdx.x; e < (slot + 1) * each; e += ks * kGThreads) {
-                        float v = 0.f;
-                        for (int r = 0; r < ks; ++r) v += cluster_load(sums + e, r);
-                        const int bb = e / each;
-                        store(e - bb * each, blk0 + b - slot + bb, v);
-                    }
-                    cluster_sync();
-                }
+                weights(j);
             }
+        }
+        // the block's sums, from its warps
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (8 * t + 2 * c + (k & 1) < M) part[b & 1][warp][(8 * t + 2 * c + (k & 1)) * 16 + g + 8 * (k >> 1)] = sum[t][k];
+                sum[t][k] = 0.f;
+            }
+        __syncthreads();
+        auto store = [&](int e, int64_t block, float v) {                // element (row, other warp, channel) of a block
+            const int64_t ch = (block << (log_cw + 4)) + (e & ((16 << log_cw) - 1));
+            if (ch >= p.N) return;
+            const int64_t out = (m0 + (e >> (log_cw + 4))) * p.N + ch;
+            if (p.out == IN_F32) store_elem<IN_F32>(p.y, out, v);
+            else if (p.out == IN_BF16) store_elem<IN_BF16>(p.y, out, v);
+            else store_elem<IN_F16>(p.y, out, v);
+        };
+        const int wait = ks > 1 ? kSumBlocks >> log_cw : 1, slot = b % wait, each = M << (log_cw + 4);
+        for (int e = threadIdx.x; e < each; e += kGThreads) {
+            const float *src = &part[b & 1][((e >> 4) & (cw - 1)) << p.log_kw][(e >> (log_cw + 4)) * 16 + (e & 15)];
+            float v = 0.f;
+            for (int w = 0; w < kw; ++w) v += src[w * 16 * RM];
+            if (ks > 1) sums[slot * each + e] = v;
+            else store(e, blk0 + b, v);
+        }
+        if (ks > 1 && (slot == wait - 1 || b == nb - 1)) {               // each CTA adds up its share of the cluster's
+            cluster_sync();
+            for (int e = rank * kGThreads + threadIdx.x; e < (slot + 1) * each; e += ks * kGThreads) {
+                float v = 0.f;
+                for (int r = 0; r < ks; ++r) v += cluster_load(sums + e, r);
+                const int bb = e / each;
+                store(e - bb * each, blk0 + b - slot + bb, v);
+            }
+            cluster_sync();
+        }
+    }
 }
 
 // The current device.

@@ -24,8 +24,9 @@ import argparse
 
 import torch
 
-from . import (RQ_ATTN_ROTATED_OUT, RQ_GROUP_SCALES, RQ_SIGNS_FIRST, attn_prefix, attn_prefix_workspace, fwht_quant,
-               kv_append, kv_cache, kv_plan, kv_read, rope, rope_turns, sync_status, w4a16_gemm)
+from . import (RQ_ATTN_ROTATED_OUT, RQ_GROUP_SCALES, RQ_KV_ROTATED_OUT, RQ_SIGNS_FIRST, attn_prefix,
+               attn_prefix_workspace, fwht_quant, kv_append, kv_cache, kv_plan, kv_read, rope, rope_turns, sync_status,
+               w4a16_gemm)
 
 SEED = 0x5EED
 DIM = 128              # a head is a group of 128 weights
@@ -96,7 +97,8 @@ class PrefixStep:
 
         def rows(table, counts):         # dense, in the rotated basis, as the weights are
             offsets = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
-            k, v = kv_read(self.cache, table, None, offsets.to(q.device), sum(counts), SEED, RQ_SIGNS_FIRST | 2, dtype=torch.float32)
+            k, v = kv_read(self.cache, table, None, offsets.to(q.device), sum(counts), SEED, RQ_SIGNS_FIRST | RQ_KV_ROTATED_OUT,
+                           dtype=torch.float32)
             return k.split(counts), v.split(counts)
 
         pk, pv = rows(self.prefix_table, prefixes)

@@ -24,7 +24,7 @@
  *                       sequence) over the paged cache, grouped-query heads;
  *   rq_kv_plan          block tables and slots of that cache from request lengths;
  *   rq_attn_prefix      the same attention where groups of sequences share a prefix,
- *                       which is read once for all of them;
+ *                       which is read for blocks of all their rows;
  *   rq_w4a8_gemm        the W4A8 variant of the linear layer (INT8 activations),
  *                       with per-channel or per-group weight scales;
  *   rq_w4a16_gemm       products of a few unquantised rows with the 4-bit weights.
@@ -465,6 +465,8 @@ rq_status rq_attn_tree(const void *q, int64_t q_token_stride, int64_t q_head_str
  *   offsets [seqs + 1] int32, slots and positions [total] int64, head_out [1] int32: out.  The sum
  *   of new_lens has to fit 31 bits.  Nothing written may overlap anything else (head_out
  *   is not head).  The kept entries of a request are its pages, and no other request's.
+ *   Meant for up to some thousand requests (4 us for 512, 9 for 4096); each block goes over all of
+ *   them, so that 16384 take 64 us and 65536 half a millisecond.
  *   Pointers at boundaries of their elements (4 bytes; slots and positions 8).
  */
 rq_status rq_kv_plan(const int32_t *context_lens, const int32_t *new_lens, const int32_t *base, int64_t seqs,
@@ -479,9 +481,21 @@ rq_status rq_kv_plan(const int32_t *context_lens, const int32_t *new_lens, const
  *   row g before their own.  Their nodes see all of them, then what rq_attn_tree lets them
  *   see: block_table and context_lens speak of a sequence's own tokens alone, which
  *   begin on a page of their own.  The result is that of rq_attn_tree on tables that name the prefix's
- *   pages for each sequence, where the prefix is a whole number of pages, up to rounding;
- *   the prefix is read once for all rows of its group.  Sequences of no group have no prefix.
- *   Roundings as in rq_attn_tree; what the two parts add up is joined in fp32.
+ *   pages for each sequence, where the prefix is a whole number of pages, up to rounding.
+ *   Sequences of no group have no prefix.
+ *   The prefix is read once for each block of its group's rows (query rows times the query heads
+ *   of a KV head): 128 rows, or 256 of bf16 where there are many tokens, if queries are of 16 bits,
+ *   head_dim is 64 or 128, groups have more than 32 rows on average and the tables name more
+ *   tiles (128 tokens of a block and KV head) than there are SMs; else, fp32 queries and other head_dims always, 16 rows
+ *   (8 if groups have 8 rows on average, or fewer).
+ *   Roundings are those of rq_attn_tree for as many rows: prefix and own tokens each go by the
+ *   blocks that meet them, and a prefix that a group of more than 32 rows shares is rounded as for
+ *   more than 32 rows, also where each sequence has one (bf16 rows of one node, 64 sequences,
+ *   prompt of 8k: 1.85e-3 off 64 bits, of which the result's own rounding is 1.64e-3).  What the two parts
+ *   add up is joined in fp32.
+ *   Unlike rq_attn_tree's, the time goes by the tables' widths too, from which the launches are
+ *   worked out before the lengths are known: with tables for 64k tokens 4 sequences with a prompt of 1000
+ *   take 25 us for 16, 64 with one of 8k 53 for 48.
  *
  *   prefix_table [n_groups][prefix_width] int32, prefix_lens [n_groups] int32,
  *   groups [n_groups + 1] int32, not decreasing, within 0 .. seqs.
@@ -513,7 +527,8 @@ rq_status rq_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_s
  *   x         [M][ld_x] of x_dtype (RQ_F32, RQ_BF16, RQ_F16), ld_x >= K, or 0: one row for all; rows at 16-byte
  *             boundaries.  A row that holds a NaN or an infinity has NaN or infinities in y.
  *   w_q       [N][K/2] packed INT4 codes, one output channel per row.
- *   w_scales  [N] fp32 (group == K) or [N][K/128] fp32 (group == 128).
+ *   w_scales  [N] fp32 (group == K) or [N][K/128] fp32 (group == 128), below 2^100 in size: a
+ *             step's sum, up to 2^25, is scaled first.
  *   M <= 64 rows (RQ_ERR_UNSUPPORTED above: that is work for rq_w4a8_gemm and
  *   rq_w4a4_gemm); N any; K a multiple of 128, <= 262144.
  *   y         [M][N] of y_dtype (RQ_F32, RQ_BF16, RQ_F16).

@@ -30,7 +30,7 @@ Entry points (same names as the C ABI):
 * :func:`kv_plan` -- block tables and slots of that cache from the requests'
   lengths;
 * :func:`attn_prefix` -- the same attention where groups of sequences share a
-  prefix, which is read once for all of them;
+  prefix, which is read for blocks of all their rows;
 * :func:`w4a16_gemm` -- products of a few unquantised rows with the 4-bit
   weights, per-channel or per-group weight scales;
 * :func:`sync_status` -- drain a stream and read (and clear) the device error

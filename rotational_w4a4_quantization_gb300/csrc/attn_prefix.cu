@@ -4,7 +4,7 @@
 //   out = softmax([e_prefix, e_own]) [v^_prefix; v^_own] R^T
 // with the scores of attn_tree_mma.cuh.  The softmax over both is that of either with its
 // reference z and sum l, joined:  z = max(z1, z2), l = l1 2^(z1 - z) + l2 2^(z2 - z), and O
-// alike.  So the prefix is read once for all rows of its group: a first pass takes the groups
+// alike.  So the prefix is read once for a block of all its group's rows: a first pass takes the groups
 // for sequences, with the rows of all their sequences as nodes that see every token, and
 // leaves O, z and l of each row in fp32; the second goes over each sequence's own tokens and
 // begins each row from there.  Both are the kernels of tree attention, which choose their
@@ -13,12 +13,16 @@
 // the partials that the first pass has left of each of their rows by themselves: its units
 // note for each row where those are.  Blocks of many rows find them joined in the state.
 //
-// Measured, bf16, heads of 128, one token a sequence: 64 sequences with one prompt of 8k and up to
-// 512 own tokens, 32 heads on 8, 51.1 us (56.7 with blocks of 256 rows, then with a join between
-// the passes 62.6); 256 sequences with two prompts of up to 32k and up to 2k own tokens,
-// 64 heads on 8, 372 us (with a join 381).  4 sequences with 1000 + 37
-// tokens, fp16: 17.8 us (24.5).  The first pass is bound by the softmax of its blocks of many
-// rows, the second by its units' starts and ends, some 8 us each, then by the codes.
+// Measured, bf16, heads of 128, one token a sequence, in a graph on the same inputs (and after a
+// flush of L2, which takes the kernels' code with it): 64 sequences with one prompt of 8k and up to
+// 512 own tokens, 32 heads on 8, 48 us (61); 256 sequences with two prompts of up to 32k and up to
+// 2k own tokens, 64 heads on 8, 372 us (375); 4 sequences with 1000 + 37 tokens, fp16, 16 us (26).
+// Those are with tables of the longest sequence's width; with tables for 64k tokens the first take
+// 53 us, on blocks of 256 rows, the last 25, with a join behind the second pass.  The first pass is
+// bound by the softmax of its blocks of many rows, the second by its units' starts and ends, some 8 us
+// each, then by the codes.  Both wait for registers now and then: with 168 or 128 of them the
+// instances for heads of 128 spill 36 to 72 bytes a thread (fp32 68 to 136), those on tensor
+// cores, of 96, 20 to 52; tree attention's own 12 to 68, fp32 32 to 96, and 20 to 40.
 #include "attn_tree_mma.cuh"
 
 namespace rq {

@@ -46,9 +46,9 @@
 //    output).
 //
 // Measured (bf16, D = 128): 64 sequences of up to 8k, 8 query heads to each of 8 KV
-// heads, one node: 103 us, 3.7 TB/s of cache, where 56 us is the reading alone (130 with
-// blocks of 16 rows, half empty); two sequences of 256k, 4 query heads to a KV head: 135
-// us, 4.2 TB/s (167).  What bounds it is instructions (operands, softmax, fragments), so
+// heads, one node: 83 us, 4.6 TB/s of cache, where 56 us is the reading alone (103 when a
+// mask and a flip of codes took two instructions, and 130 then with blocks of 16 rows, half empty);
+// two sequences of 256k, 4 query heads to a KV head: 106 us, 5.4 TB/s (135 and 167).  What bounds it is instructions (operands, softmax, fragments), so
 // memory waits.  One sequence of 514 tokens takes the 16 us of its latencies and 7 of the
 // join, which overlap in part.
 #pragma once

@@ -34,8 +34,8 @@
 // A tile keeps exact codes if a scale of it is not finite or they lie too far apart (values
 // by more than 2^8, keys 2^12), and applies them to scores and weights, so that a large
 // scale costs the others no bits and what an unseen token holds (a NaN scale, say) reaches
-// nobody.  Where every tile does so, 64 nodes of 16 sequences of 16k take 766 us (bf16) for
-// 330, 16 nodes of 4k 155 (fp16) for 104.  fp16 queries, whose outputs resolve an 11-bit rounding of q~, k^ and v^, keep q~
+// nobody.  Where every tile does so, 64 nodes of 16 sequences of 16k take 737 us (bf16) for
+// 303, 16 nodes of 4k 128 (fp16) for 75.  fp16 queries, whose outputs resolve an 11-bit rounding of q~, k^ and v^, keep q~
 // in two fp16 parts (Q K^T runs twice) and the scales out of the operands; the weights with
 // vs in them round once (16 sequences of up to 4k: outputs 3.0e-4 off; with the scales of V
 // folded 3.3e-4, and 2 us slower).
@@ -47,17 +47,17 @@
 // arrival that delivers P, when no MMA touches it).  fp16 keeps 11 bits down to 2^-14, so
 // of tokens at least 23 bits below the largest, and something down to 2^-25.
 //
-// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 426 us, 0.69
-// PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 5,000 cycles
+// Measured (D = 128): 256 rows (bf16, 16 sequences of up to 32k, 8 KV heads): 411 us, 0.71
+// PFLOP/s of Q K^T and P V, where the products alone take 153; a tile takes 4,800 cycles
 // of which the MMAs run 2,048.  The softmax bounds it: 1,800 cycles for half a tile, most
 // of it latency of tensor-memory loads, exponentials and the exchange between a row's
 // threads (issue slots are two fifths full), and 800 from one half to the next.  Slower
-// were, with one limit of 96 registers for all warps: one pass over the scores with the old
+// than the 426 us of that time were, with one limit of 96 registers for all warps: one pass over the scores with the old
 // reference, weights kept back in registers (431 us); scores kept in registers (457,
 // spills); 32 columns a load (433); buffers of 64 columns (423, as Q K^T with N = 64 takes
-// 48 cycles for 32's work).  64 rows (fp16, 16 sequences of up to 4k): 72 us, where the
+// 48 cycles for 32's work).  64 rows (fp16, 16 sequences of up to 4k): 68 us, where the
 // bytes take 9: starts and ends of units; with a buffer per softmax team, 128 columns to a
-// thread, 86 (and the 256 rows 404).
+// thread, 86 for 72 (and the 256 rows 404 for 426).
 #pragma once
 
 #include "rq.h"
@@ -1226,9 +1226,11 @@ cudaError_t launch_tree_tc(const TreeCall &c, P &p, cudaStream_t stream) {
     // two row blocks share each converted tile; fp16 queries keep the second's shared
     // memory for the low parts of q~
     int nt = tree_rows(c) > 128 && c.in_type == IN_BF16 ? 2 : 1;
-    // A pass with few tiles for each SM is mostly starts and ends of units, which 128 rows halve: one
-    // prompt, 32 heads on 8, 64 sequences, 256 and 128 rows: 8k tokens (3 tiles of 256 rows for
-    // each SM) 56.7 and 51.3 us, 24k (10) 67 and 66, 32k (13) 74 and 78, 64k (27) 107 and 121.
+    // A pass with few tiles for each SM is mostly starts and ends of units, which 128 rows halve.  One
+    // prompt, 128 own tokens, 3, 6, 10, 13 and 20 tiles of 256 rows for each SM, in us on 256 and 128 rows:
+    // 64 sequences, 32 heads of 128 on 8: 52 60 69 77 93 and 47 57 69 79 102; on 2: 56 62 71 78 93 and
+    // 47 56 69 78 100; heads of 64, on 8: 44 50 58 64 79 and 39 47 56 64 81; 200 sequences, 16 heads of
+    // 64 on 16: 84 90 98 104 119 and 78 85 95 102 119.  So even at 10 to 13, heads of 64 up to 20.
     if constexpr (P::kPass) {
         const int64_t blocks = c.seqs * c.cache.heads * ((tree_rows(c) + 255) / 256);
         if ((double)blocks * (double)((c.width * c.cache.page_size + kTcTT - 1) / kTcTT) < 10.0 * sms) nt = 1;

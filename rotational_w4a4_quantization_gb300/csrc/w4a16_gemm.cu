@@ -19,8 +19,9 @@
 //  * rows that do not fit shared memory, or take long to get there, split K over a cluster of
 //    CTAs, whose sums meet in distributed shared memory; more than 16 rows take the weights
 //    again, from L2 (32 rows at a time spill registers: 61 rows 67 us for 60).
-// Measured, groups of 128: 1 row, 4096 -> 14336, 11.2 us, 2.8 TB/s of weights and scales; 7 rows,
-// 14336 -> 4096, 13.5 us; 16 rows, 8192 -> 28672, 42.4 us, 2.9 TB/s.  What it spends them on there:
+// Measured, groups of 128, weights from HBM (L2 flushed) and in brackets on the same inputs, where those of
+// the first two lie in L2: 1 row, 4096 -> 14336, 11.8 us (9.6), 2.6 TB/s of weights and scales; 7 rows,
+// 14336 -> 4096, 14.1 us (11.6); 16 rows, 8192 -> 28672, 42.5 us (40.5), 3.0 TB/s.  What it spends them on there:
 // issue slots are 48% busy, 201 instructions for a warp's step of 16 x 128 codes (some 90 to widen
 // them, 16 products, 8 reads of the rows), and 16 warps, all that fit, do not hide the rest.
 // Without the weights' loads it takes 36 us, without products and widening 37, without

@@ -9,8 +9,8 @@ projection is:
 1. :func:`kv_plan` gives each request's new token its page and slot;
 2. :func:`kv_append` writes the tokens' keys, turned to their positions, and values there;
 3. :func:`rope` turns their queries;
-4. :func:`attn_prefix` attends to the group's prompt, read once for all of it, and to the
-   request's own tokens, and leaves the rows in the rotated basis;
+4. :func:`attn_prefix` attends to the group's prompt, read for blocks of all its rows, and to
+   the request's own tokens, and leaves the rows in the rotated basis;
 5. :func:`w4a16_gemm` multiplies them, 64 at a time, with the output weights, into which the
    heads' rotation is folded (one scale per channel and head).
 

@@ -493,6 +493,9 @@ rq_status rq_kv_plan(const int32_t *context_lens, const int32_t *new_lens, const
  *   more than 32 rows, also where each sequence has one (bf16 rows of one node, 64 sequences,
  *   prompt of 8k: 1.85e-3 off 64 bits, of which the result's own rounding is 1.64e-3).  What the two parts
  *   add up is joined in fp32.
+ *   The pass over the prefix pays where several sequences have it and each has few rows; where a
+ *   sequence's own rows fill blocks (prompts behind a prefix; fp32 trees of 16 nodes), rq_attn_tree
+ *   with the prefix's pages in its tables is the faster.
  *   Unlike rq_attn_tree's, the time goes by the tables' widths too, from which the launches are
  *   worked out before the lengths are known: with tables for 64k tokens 4 sequences with a prompt of 1000
  *   take 25 us for 16, 64 with one of 8k 53 for 48.

@@ -803,7 +803,8 @@ def attn_prefix(q: torch.Tensor, cache: dict, block_table: torch.Tensor, context
     (int32 [n_groups][width]) before their own, and every node sees them.  block_table and context_lens name a
     sequence's own tokens, on pages of its own; so do the places of its nodes.  Rotary positions count the prefix
     (:func:`kv_plan`'s base).  Sequences of no group have no prefix.  The launches go by the tables' widths: tables not
-    much wider than the longest sequence are the fastest.  The other arguments and the result are those of
+    much wider than the longest sequence are the fastest.  Where each sequence has as many rows as a prompt, attn_tree
+    with the prefix's pages in its tables is the faster.  The other arguments and the result are those of
     :func:`attn_tree`."""
     return _attn_paged("rq_attn_prefix", q, cache, block_table, context_lens, offsets, seed, flags, tree_mask, max_nodes,
                        softmax_scale, out, workspace, stream, (prefix_table, prefix_lens, groups))
